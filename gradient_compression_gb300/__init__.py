@@ -92,6 +92,15 @@ def lib() -> C.CDLL:
         L.gc_sparse_decompress_accumulate_quantized.argtypes = [LP, LP, I32, I32, I32, P, P, P, P, P, P, SZ, P]
         L.gc_dense_decompress_accumulate.argtypes = [LP, LP, I32, I32, I32, P, P, P, P, SZ, P]
         L.gc_get_device_status.argtypes = [P, SZ, P, C.POINTER(gc_diag)]
+        L.gc_act_compress.argtypes = [P, I64, I32, I64, I64, P, P, P]
+        L.gc_act_decompress.argtypes = [P, P, I64, I64, P, I64, I32, P]
+        L.gc_rmsnorm.argtypes = [P, I64, P, I64, I32, P, I32, F, I64, I64, P, I64, P, I64, P, P, P, P]
+        L.gc_rmsnorm_backward_workspace_size.argtypes = [I64, I64, C.POINTER(SZ)]
+        L.gc_rmsnorm_backward.argtypes = [P, I64, P, I64, I32, P, P, P, P, I32, I64, I64, P, I64, P, U32, P, SZ, P]
+        L.gc_gated_act.argtypes = [I32, P, I64, P, I64, I32, I64, I64, P, I64, P, P, P, P, P]
+        L.gc_gated_act_backward.argtypes = [I32, P, I64, I32, P, P, P, P, I64, I64, P, I64, P, I64, P, P, P]
+        L.gc_act_weight_grad_workspace_size.argtypes = [I64, I64, I64, I32, C.POINTER(SZ)]
+        L.gc_act_weight_grad.argtypes = [P, I64, I32, I64, I64, P, P, I64, P, I32, P, I64, U32, P, SZ, P]
         L.gc_status_string.argtypes = [I32]
         L.gc_status_string.restype = C.c_char_p
         L.gc_version.restype = I32
@@ -107,7 +116,10 @@ def lib() -> C.CDLL:
                      "gc_sign_compress", "gc_quantize_stochastic", "gc_sparse_decompress_accumulate",
                      "gc_sparse_decompress_accumulate_quantized",
                      "gc_dense_decompress_accumulate", "gc_get_device_status",
-                     "gc_ef_topk_compress_dev_iter", "gc_quantize_stochastic_dev_iter"):
+                     "gc_ef_topk_compress_dev_iter", "gc_quantize_stochastic_dev_iter",
+                     "gc_act_compress", "gc_act_decompress", "gc_rmsnorm", "gc_rmsnorm_backward_workspace_size",
+                     "gc_rmsnorm_backward", "gc_gated_act", "gc_gated_act_backward",
+                     "gc_act_weight_grad_workspace_size", "gc_act_weight_grad"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -508,3 +520,11 @@ class TopkCompressor:
         ef_topk_compress(self.layout, g, e, self.idx, self.val, self.q, self.scale, seed, it, self.flags,
                          self.workspace, stream)
         return self.idx, self.val, self.q, self.scale
+
+
+# ---------------------------------------------------------------------------- activation checkpoints
+
+from .activations import (ACT_GROUP, GC_ACCUMULATE, GC_BF16, GC_F16, GC_F32, GC_GATE_GELU_TANH,  # noqa: E402,F401
+                          GC_GATE_SILU, ActCheckpoint, act_compress, act_decompress, act_weight_grad,
+                          act_weight_grad_workspace, gated_act, gated_act_backward, rmsnorm, rmsnorm_backward,
+                          rmsnorm_backward_workspace)

@@ -44,6 +44,26 @@ inline gc_status validate_layout(const gc_layout* h, bool sparse) {
   return GC_OK;
 }
 
+// Matrix and checkpoint arguments of the activation entry points.
+inline bool valid_dtype(int32_t d) { return d == GC_F32 || d == GC_BF16 || d == GC_F16; }
+inline size_t dtype_bytes(int32_t d) { return d == GC_F32 ? 4 : 2; }
+inline gc_status validate_matrix(int64_t rows, int64_t cols, int32_t dtype) {
+  if (rows < 0 || cols < 1 || rows > INT64_C(2147483647) || cols > INT64_C(2147483647)) return GC_ERR_LAYOUT;
+  return valid_dtype(dtype) ? GC_OK : GC_ERR_INVALID_ARG;
+}
+inline gc_status check_matrix(const void* p, int64_t ld, int64_t cols, int32_t dtype) {
+  if (!p) return GC_ERR_INVALID_ARG;
+  if (ld < cols) return GC_ERR_LAYOUT;
+  return ((uintptr_t)p & (dtype_bytes(dtype) - 1)) ? GC_ERR_ALIGNMENT : GC_OK;
+}
+inline gc_status check_codes(const int8_t* codes, const uint8_t* steps) {
+  if (!codes || !steps) return GC_ERR_INVALID_ARG;
+  return aligned16(codes) ? GC_OK : GC_ERR_ALIGNMENT;
+}
+inline gc_status check_workspace(const void* ws, size_t have, size_t need) {
+  return need > 0 && (!ws || have < need || ((uintptr_t)ws & 255u)) ? GC_ERR_WORKSPACE : GC_OK;
+}
+
 // Defined by the operation files.
 size_t topk_workspace_bytes(const gc_layout* h, bool sampled);
 size_t dense_workspace_bytes(const gc_layout* h);

@@ -548,6 +548,109 @@ gc_status gc_dense_decompress_accumulate(const gc_layout* dev, const gc_layout* 
                                          const float* const* scale, float* out, void* workspace,
                                          size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------- 8-bit activation checkpoints
+ * The backward pass that fills the gradient arena reads activations that
+ * the forward pass kept.  These entry points keep them in 8 bits, take the
+ * gradients of the operators around them from the 8-bit form, and put the
+ * weight gradients into the arena.
+ *
+ * Matrices.  A matrix m[rows, cols] of `dtype` is row-major: row r starts
+ * `ld` elements after row r - 1 (ld >= cols), its columns are consecutive.
+ * Any base address, ld and width of whole elements are accepted.  0 <= rows
+ * and 1 <= cols, both < 2^31; offsets inside a matrix are 64-bit.
+ *
+ * Checkpoint.  x[rows, cols] is held as int8 codes[rows, ldc], ldc = 32 *
+ * ceil(cols / 32), pad codes 0, and uint8 steps[rows, ldc / 32], one step
+ * per group of 32 consecutive columns of a row (a row's last group may be
+ * short).  With m the largest magnitude of the group, the step is the least
+ * power of two 2^(b - 127), 1 <= b <= 248, for which m / step rounds to at
+ * most 127; code = round-to-nearest-even(x / step), clamped to +-127 (only
+ * magnitudes from 2^128 (1 - 2^-8) on need the clamp); value = code * step.
+ * A group of zeros has b = 1.  A group holding a NaN or an infinity has
+ * b = 255 and codes 0 and reads back as NaN.  Every finite value is exact
+ * in bf16 and in fp32.  codes: 16-byte aligned.
+ *
+ * Arithmetic is fp32 whatever the dtype, each output rounded to its type
+ * once; sums are fp32 with a fixed order, so results are bit-identical from
+ * run to run.  Unless stated otherwise buffers must not overlap. */
+typedef enum gc_dtype { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
+
+#define GC_ACCUMULATE 0x1u /* flags: add to dw instead of writing it */
+
+/* Gated activations act(g) = g * sigmoid(p(g)). */
+#define GC_GATE_SILU 0      /* p = g */
+#define GC_GATE_GELU_TANH 1 /* p = 2 sqrt(2/pi) (g + 0.044715 g^3): the tanh form of GELU */
+
+/* Checkpoint of x[rows, cols]. */
+gc_status gc_act_compress(const void* x, int64_t ld, int32_t dtype, int64_t rows, int64_t cols,
+                          int8_t* codes, uint8_t* steps, void* stream);
+
+/* out[rows, cols] = the checkpoint's values in `dtype`. */
+gc_status gc_act_decompress(const int8_t* codes, const uint8_t* steps, int64_t rows, int64_t cols,
+                            void* out, int64_t ldo, int32_t dtype, void* stream);
+
+/* RMS norm with the residual's addition, row by row:
+ *   h = x + residual (x without one), rstd = 1 / sqrt(mean(h^2) + eps),
+ *   xh = h * rstd, y = xh * weight.
+ * residual, weight (ones), y, h, rstd (fp32[rows]) and the checkpoint
+ * codes / steps of xh (both or neither) are optional; x, residual, y and h
+ * are of `dtype`, weight[cols] of `weight_dtype`.  eps >= 0.  h or y may be
+ * x or residual itself (the same pointer and ld). */
+gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
+                     const void* weight, int32_t weight_dtype, float eps, int64_t rows,
+                     int64_t cols, void* y, int64_t ldy, void* h, int64_t ldh, float* rstd,
+                     int8_t* codes, uint8_t* steps, void* stream);
+
+/* Bytes of workspace of gc_rmsnorm_backward with dw. */
+gc_status gc_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradient of gc_rmsnorm at the checkpoint's values q of xh:
+ *   gw = dy * weight, dx = rstd * (gw - q * mean(gw * q)) + dh,
+ *   dw[c] = sum over rows of dy * q   (fp32; added to dw with GC_ACCUMULATE).
+ * dx is the gradient of x and of the residual alike; dh, the gradient that
+ * arrives at h, weight (ones) and dw are optional.  dy, dh, dx are of
+ * `dtype`; dx may be dy or dh itself.  The workspace (256-byte aligned) is
+ * needed with dw only. */
+gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const void* dh, int64_t lddh,
+                              int32_t dtype, const int8_t* codes, const uint8_t* steps,
+                              const float* rstd, const void* weight, int32_t weight_dtype,
+                              int64_t rows, int64_t cols, void* dx, int64_t lddx, float* dw,
+                              uint32_t flags, void* workspace, size_t ws_bytes, void* stream);
+
+/* out = act(gate) * up, and the checkpoints of gate and up (all four arrays
+ * or none).  gate, up and out are of `dtype`; out may be gate or up itself. */
+gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, const void* up, int64_t ldu,
+                       int32_t dtype, int64_t rows, int64_t cols, void* out, int64_t ldo,
+                       int8_t* gate_codes, uint8_t* gate_steps, int8_t* up_codes,
+                       uint8_t* up_steps, void* stream);
+
+/* Gradient of gc_gated_act at the checkpoints' values G and U:
+ *   dgate = dout * U * act'(G), dup = dout * act(G),
+ * and, with out_codes and out_steps (both or neither), the checkpoint of
+ * act(G) * U for the weight gradient of the product that follows.  dout,
+ * dgate and dup are of `dtype`; dgate or dup may be dout itself. */
+gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
+                                const int8_t* gate_codes, const uint8_t* gate_steps,
+                                const int8_t* up_codes, const uint8_t* up_steps, int64_t rows,
+                                int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu,
+                                int8_t* out_codes, uint8_t* out_steps, void* stream);
+
+/* Bytes of workspace of gc_act_weight_grad. */
+gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dtype,
+                                            size_t* bytes);
+
+/* Weight gradient of y = x W^T from the checkpoint q of x[rows, k]:
+ *   dw[n, k] = col_scale[k] * sum over rows of dy[rows, n] * q[rows, k],
+ * fp32 into the arena (added to dw with GC_ACCUMULATE), row r of dw at
+ * r * lddw.  col_scale (ones) is the norm's weight where q is gc_rmsnorm's
+ * checkpoint.  Products are exact (an fp16 or fp32 dy is split into two or
+ * three bf16 terms) and summed in fp32.  Workspace 256-byte aligned. */
+gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t rows, int64_t n,
+                             const int8_t* codes, const uint8_t* steps, int64_t k,
+                             const void* col_scale, int32_t col_scale_dtype, float* dw,
+                             int64_t lddw, uint32_t flags, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 /* Waits for `stream`, then reads the diagnostics that the last call using
  * `workspace` left there.  Returns GC_ERR_DEVICE if an error bit is set. */
 gc_status gc_get_device_status(const void* workspace, size_t ws_bytes, void* stream, gc_diag* out);
