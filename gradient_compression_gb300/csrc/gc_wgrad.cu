@@ -2,6 +2,8 @@
 // tensor cores: dw[n, k] = sum_t dy[t, n] * q[t, k], q = code * step.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "gc_act.cuh"
 #include "gc_host.h"
 
@@ -73,6 +75,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // Shared-memory operand descriptor of an MN-major tile under the 128-byte
 // swizzle: 64-wide blocks `block` bytes apart, groups of 8 t 1024 bytes apart.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
@@ -105,15 +111,27 @@ __device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t addr) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Two codes (bytes of p in the low byte of each half, 0x43 above) as bf16:
-// with s the sign bit and l the low 7 bits, code = l - 128 s =
-// bf16(0x4300 | l) - bf16(0x4300 | 128 s), 0x4300 | l being 128 + l.
-__device__ __forceinline__ uint32_t codes2_bf16(uint32_t p, __nv_bfloat162 scale) {
-  const uint32_t lo = p & 0xFF7FFF7Fu, hi = p & 0xFF80FF80u;
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
-  v = __hmul2(v, scale);
-  return *reinterpret_cast<uint32_t*>(&v);
+// The codes in bytes 0 and 2 of w (the low byte of each half) as bf16 times
+// their step.  With s a code's sign bit and l its low 7 bits, code = l - 128 s
+// = (128 + l) - 128 (1 + s); as bf16 0x4300 | l is 128 + l and 0x4300 | 128 s
+// is 128 (1 + s).  `lead` is 0x4300 with the step added to its exponent,
+// `minus` the step negated, so one fused multiply-add gives the value, exactly.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t lead, uint32_t minus) {
+  const uint32_t lo = (w & 0x007F007Fu) | lead, hi = (w & 0x00800080u) | 0x43004300u;
+  uint32_t v;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(hi), "r"(minus), "r"(lo));
+  return v;
 }
+// Two codes by way of fp32, for the steps whose lead would leave bf16's
+// exponents (0, 248 and 255, the step of a group that is not finite).
+__device__ __forceinline__ uint32_t codes_bf16_any(uint32_t w, uint32_t step) {
+  const float sc = act_scale(step);
+  const float a = __fmul_rn((float)(int8_t)(w & 255u), sc), b = __fmul_rn((float)(int8_t)((w >> 16) & 255u), sc);
+  return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+}
+// The bytes of a word come out in the order 0, 2, 1, 3: column 4 q + p of the
+// tile holds column 4 q + (0, 2, 1, 3)[p] of q, which the result undoes.
+__device__ __forceinline__ int wg_column(int c) { return (c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1); }
 
 // 8 elements of dy from column c on, as fp32; 0 outside [0, n).
 template <typename T, bool VEC>
@@ -137,13 +155,15 @@ __device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float 
 // TMA: dy is bf16 and its rows start on 16-byte boundaries, so that its
 // tiles come by bulk tensor copies; else the unpacking warps load it too,
 // split into PARTS bf16 terms.
-template <typename T, int PARTS, bool TMA, bool VEC>
+// WIDE: the rows of q in a stage may span 2^32 bytes.
+template <typename T, int PARTS, bool TMA, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_constant__ CUtensorMap map, const WgArgs a) {
   constexpr int KT = TMA ? 64 : 32;                     // t of a stage
   constexpr int BLOCK = KT * 128;                       // bytes of a 64-wide column block
   constexpr int A_BYTES = 4 * BLOCK, B_BYTES = 4 * BLOCK, STAGE = PARTS * A_BYTES + B_BYTES;
   constexpr int STAGES = WG_SMEM / STAGE;
   constexpr int ROWS = KT / WG_CONV;                    // t per unpacking warp and stage
+  constexpr int AHEAD = 3;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[3 * 8 + 1];
   __shared__ uint32_t tmem_base;
@@ -185,26 +205,45 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
 
   if (warp < WG_CONV) {
     // ------------------------------------------------ unpack q (and split dy)
-    const int64_t kc = k0 + 8 * lane;
-    const bool kin = kc < a.ldc;
-    const int8_t* cp = a.codes + (t0 + warp) * a.ldc + kc;
-    const uint8_t* sp = a.steps + (t0 + warp) * (a.ldc >> 5) + (kc >> 5);
-    uint2 code[2][ROWS];
-    uint32_t step[2][ROWS];
-    auto fetch = [&](int it, int u) {
+    // Lanes past q's last column read the last columns again: what they put
+    // into the tile reaches only columns of the accumulators that are not
+    // written out.
+    using Off = typename std::conditional<WIDE, int64_t, uint32_t>::type;
+    const int64_t kc = min(k0 + 8 * lane, a.ldc - 8), groups = a.ldc >> 5;
+    const int8_t* cp = a.codes + t0 * a.ldc;
+    const uint8_t* sp = a.steps + t0 * groups;
+    Off co[ROWS], so[ROWS];
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const int64_t dt = (int64_t)it * KT + 8 * i;
-        const bool in = kin && t0 + warp + dt < t1;
-        code[u][i] = in ? __ldg(reinterpret_cast<const uint2*>(cp + dt * a.ldc)) : make_uint2(0u, 0u);
-        step[u][i] = in ? __ldg(sp + dt * (a.ldc >> 5)) : 0u;
+    for (int i = 0; i < ROWS; ++i) {
+      co[i] = (Off)((warp + 8 * i) * a.ldc + kc);
+      so[i] = (Off)((warp + 8 * i) * groups + (kc >> 5));
+    }
+    uint2 code[AHEAD][ROWS];
+    uint32_t step[AHEAD][ROWS];
+    auto fetch = [&](int it, int u) {
+      if ((int64_t)(it + 1) * KT <= t1 - t0) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          code[u][i] = __ldg(reinterpret_cast<const uint2*>(cp + co[i]));
+          step[u][i] = __ldg(sp + so[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {  // rows past the split's end: zeros
+          const bool in = (int64_t)it * KT + 8 * i + warp < t1 - t0;
+          code[u][i] = in ? __ldg(reinterpret_cast<const uint2*>(cp + co[i])) : make_uint2(0u, 0u);
+          step[u][i] = in ? __ldg(sp + so[i]) : 1u;
+        }
       }
+      cp += KT * a.ldc;
+      sp += KT * groups;
     };
     const uint32_t off = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)warp * 128u + (uint32_t)(((lane & 7) ^ warp) << 4);
+    int slot = 0;
+    uint32_t phase = 1;
     auto put = [&](int it, int u) -> bool {
-      const int s = it % STAGES;
-      if (!mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1)) return false;
-      const uint32_t st = base + (uint32_t)s * STAGE;
+      if (!mbar_wait(empty(slot), phase)) return false;
+      const uint32_t st = base + (uint32_t)slot * STAGE + off;
       if constexpr (!TMA) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
@@ -231,38 +270,47 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
                 }
               }
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st + p * A_BYTES + off + 1024u * i), "r"(w[0]),
-                         "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
+            st_shared16(st + p * A_BYTES + 1024u * i, w[0], w[1], w[2], w[3]);
           }
         }
       }
+      uint32_t odd = 0u;
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const uint32_t sc = (step[u][i] << 7) | (step[u][i] << 23);
-        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&sc);
-        const uint2 c = code[u][i];
-        const uint32_t w0 = codes2_bf16(__byte_perm(c.x, 0x43434343u, 0x4140), scale);
-        const uint32_t w1 = codes2_bf16(__byte_perm(c.x, 0x43434343u, 0x4342), scale);
-        const uint32_t w2 = codes2_bf16(__byte_perm(c.y, 0x43434343u, 0x4140), scale);
-        const uint32_t w3 = codes2_bf16(__byte_perm(c.y, 0x43434343u, 0x4342), scale);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st + PARTS * A_BYTES + off + 1024u * i), "r"(w0),
-                     "r"(w1), "r"(w2), "r"(w3)
-                     : "memory");
+      for (int i = 0; i < ROWS; ++i) odd = max(odd, step[u][i] - 1u);
+      if (__any_sync(FULL, odd >= 247u)) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          const uint32_t b = step[u][i];
+          const uint2 c = code[u][i];
+          st_shared16(st + PARTS * A_BYTES + 1024u * i, codes_bf16_any(c.x, b), codes_bf16_any(c.x >> 8, b),
+                      codes_bf16_any(c.y, b), codes_bf16_any(c.y >> 8, b));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          const uint32_t lead = step[u][i] * 0x00800080u + 0x03800380u, minus = step[u][i] * 0x00800080u + 0x80008000u;
+          const uint2 c = code[u][i];
+          st_shared16(st + PARTS * A_BYTES + 1024u * i, codes_bf16(c.x, lead, minus), codes_bf16(c.x >> 8, lead, minus),
+                      codes_bf16(c.y, lead, minus), codes_bf16(c.y >> 8, lead, minus));
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(full_b(s));
+      if (lane == 0) mbar_arrive(full_b(slot));
+      if (++slot == STAGES) slot = 0, phase ^= 1u;
       return true;
     };
+    // codes are fetched AHEAD - 1 stages before they are unpacked
     bool ok = true;
-    if (iters > 0) fetch(0, 0);
-    for (int it = 0; ok && it < iters; it += 2) {
-      if (it + 1 < iters) fetch(it + 1, 1);
-      ok = put(it, 0);
-      if (!ok || it + 1 >= iters) break;
-      if (it + 2 < iters) fetch(it + 2, 0);
-      ok = put(it + 1, 1);
+#pragma unroll
+    for (int u = 0; u + 1 < AHEAD; ++u)
+      if (u < iters) fetch(u, u);
+    for (int it = 0; ok && it < iters;) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (it + AHEAD - 1 < iters) fetch(it + AHEAD - 1, (u + AHEAD - 1) % AHEAD);
+        if (!(ok = put(it, u)) || ++it >= iters) break;
+      }
     }
     if (!ok) fail();
   } else if (warp == WG_CONV) {
@@ -342,7 +390,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
           const int rows = (int)min((int64_t)32, a.n - r0);
           for (int r = 0; r < rows; ++r) {
             float* o = out + (r0 + r) * a.lddw + c;
-            const float x = __fmul_rn(buf[r * 33 + lane], cs);
+            const float x = __fmul_rn(buf[r * 33 + wg_column(lane)], cs);
             *o = a.splits == 1 && a.accumulate ? __fadd_rn(*o, x) : x;
           }
         }
@@ -404,9 +452,9 @@ static bool make_dy_map(CUtensorMap* m, const void* dy, int64_t lddy, int64_t ro
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int PARTS, bool TMA, bool VEC>
+template <typename T, int PARTS, bool TMA, bool VEC, bool WIDE = false>
 static bool launch_wg(const CUtensorMap& map, const WgArgs& a, unsigned grid, cudaStream_t s) {
-  auto kern = k_weight_grad<T, PARTS, TMA, VEC>;
+  auto kern = k_weight_grad<T, PARTS, TMA, VEC, WIDE>;
   static const bool ready = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) == cudaSuccess;
   if (!ready) return false;
   launch_chained(kern, grid, WG_THREADS, WG_SMEM, s, map, a);
@@ -459,7 +507,11 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
   const bool vec = aligned16(dy) && lddy % 8 == 0;
   CUtensorMap map = {};
   bool ok;
-  if (dtype == GC_BF16 && vec && rows > 0) {
+  if (a.ldc >= (int64_t(1) << 25)) {  // 64 rows of q span 2^31 bytes
+    ok = dtype == GC_BF16  ? launch_wg<__nv_bfloat16, 1, false, false, true>(map, a, grid, s)
+         : dtype == GC_F16 ? launch_wg<__half, 2, false, false, true>(map, a, grid, s)
+                           : launch_wg<float, 3, false, false, true>(map, a, grid, s);
+  } else if (dtype == GC_BF16 && vec && rows > 0) {
     ok = make_dy_map(&map, dy, lddy, rows, n) && launch_wg<__nv_bfloat16, 1, true, true>(map, a, grid, s);
   } else if (dtype == GC_BF16) {
     ok = launch_wg<__nv_bfloat16, 1, false, false>(map, a, grid, s);
