@@ -26,7 +26,11 @@ namespace gc {
 // one t, 16-byte chunk c of row t at chunk c ^ (t & 7) (the 128-byte
 // swizzle), 64-wide column blocks one after another.
 constexpr int WG_M = 256, WG_N = 256;      // n and k of a CTA's tile
-constexpr int WG_CONV = 8;                 // warps that unpack codes, then write the result
+// The unpacking warps work in teams, each on every WG_TEAMS-th stage: a team
+// has as many stages' time for its own, so the latency of its loads of codes
+// is hidden without keeping several stages' codes in registers.
+constexpr int WG_TEAMS = 3, WG_TEAM = 4;   // teams, warps of a team
+constexpr int WG_CONV = WG_TEAMS * WG_TEAM;     // warps that unpack codes, then write the result
 constexpr int WG_THREADS = (WG_CONV + 2) * 32;  // + one warp issuing TMA loads, one issuing MMAs
 constexpr int WG_SMEM = 192 * 1024;
 
@@ -162,8 +166,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
   constexpr int BLOCK = KT * 128;                       // bytes of a 64-wide column block
   constexpr int A_BYTES = 4 * BLOCK, B_BYTES = 4 * BLOCK, STAGE = PARTS * A_BYTES + B_BYTES;
   constexpr int STAGES = WG_SMEM / STAGE;
-  constexpr int ROWS = KT / WG_CONV;                    // t per unpacking warp and stage
-  constexpr int AHEAD = 3;
+  constexpr int ROWS = KT / WG_TEAM;                    // t per unpacking warp and stage
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[3 * 8 + 1];
   __shared__ uint32_t tmem_base;
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
   const uint32_t done = bar0 + 192u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(full_a(s), 1), mbar_init(full_b(s), WG_CONV), mbar_init(empty(s), 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(full_a(s), 1), mbar_init(full_b(s), WG_TEAM), mbar_init(empty(s), 1);
     mbar_init(done, 1);
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -209,45 +212,40 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
     // into the tile reaches only columns of the accumulators that are not
     // written out.
     using Off = typename std::conditional<WIDE, int64_t, uint32_t>::type;
+    const int team = warp / WG_TEAM, w = warp % WG_TEAM;  // rows w, w + 4, ...
     const int64_t kc = min(k0 + 8 * lane, a.ldc - 8), groups = a.ldc >> 5;
-    const int8_t* cp = a.codes + t0 * a.ldc;
-    const uint8_t* sp = a.steps + t0 * groups;
-    Off co[ROWS], so[ROWS];
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      co[i] = (Off)((warp + 8 * i) * a.ldc + kc);
-      so[i] = (Off)((warp + 8 * i) * groups + (kc >> 5));
-    }
-    uint2 code[AHEAD][ROWS];
-    uint32_t step[AHEAD][ROWS];
-    auto fetch = [&](int it, int u) {
+    const int8_t* cp = a.codes + (t0 + (int64_t)team * KT) * a.ldc;
+    const uint8_t* sp = a.steps + (t0 + (int64_t)team * KT) * groups;
+    const Off co = (Off)(w * a.ldc + kc), so = (Off)(w * groups + (kc >> 5));
+    const uint32_t off0 = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + (uint32_t)(((lane & 7) ^ w) << 4);
+    const uint32_t off1 = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + 512u + (uint32_t)(((lane & 7) ^ (w + 4)) << 4);
+    bool ok = true;
+    for (int it = team; it < iters; it += WG_TEAMS) {
+      uint2 code[ROWS];
+      uint32_t step[ROWS];
       if ((int64_t)(it + 1) * KT <= t1 - t0) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          code[u][i] = __ldg(reinterpret_cast<const uint2*>(cp + co[i]));
-          step[u][i] = __ldg(sp + so[i]);
+          code[i] = __ldg(reinterpret_cast<const uint2*>(cp + (co + (Off)(WG_TEAM * i) * (Off)a.ldc)));
+          step[i] = __ldg(sp + (so + (Off)(WG_TEAM * i) * (Off)groups));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {  // rows past the split's end: zeros
-          const bool in = (int64_t)it * KT + 8 * i + warp < t1 - t0;
-          code[u][i] = in ? __ldg(reinterpret_cast<const uint2*>(cp + co[i])) : make_uint2(0u, 0u);
-          step[u][i] = in ? __ldg(sp + so[i]) : 1u;
+          const bool in = (int64_t)it * KT + WG_TEAM * i + w < t1 - t0;
+          code[i] = in ? __ldg(reinterpret_cast<const uint2*>(cp + (co + (Off)(WG_TEAM * i) * (Off)a.ldc))) : make_uint2(0u, 0u);
+          step[i] = in ? __ldg(sp + (so + (Off)(WG_TEAM * i) * (Off)groups)) : 1u;
         }
       }
-      cp += KT * a.ldc;
-      sp += KT * groups;
-    };
-    const uint32_t off = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)warp * 128u + (uint32_t)(((lane & 7) ^ warp) << 4);
-    int slot = 0;
-    uint32_t phase = 1;
-    auto put = [&](int it, int u) -> bool {
-      if (!mbar_wait(empty(slot), phase)) return false;
-      const uint32_t st = base + (uint32_t)slot * STAGE + off;
+      cp += WG_TEAMS * KT * a.ldc;
+      sp += WG_TEAMS * KT * groups;
+      const int slot = it % STAGES;
+      if (!(ok = mbar_wait(empty(slot), ((it / STAGES) & 1) ^ 1))) break;
+      const uint32_t st = base + (uint32_t)slot * STAGE;
       if constexpr (!TMA) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          const int64_t t = t0 + (int64_t)it * KT + 8 * i + warp;
+          const int64_t t = t0 + (int64_t)it * KT + WG_TEAM * i + w;
           float v[8];
           if (t < t1) {
             load8<T, VEC>(static_cast<const T*>(a.dy) + t * a.lddy, n0 + 8 * lane, a.n, v);
@@ -257,11 +255,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
           }
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            uint32_t w[4];
+            uint32_t x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               // the upper halves: truncation to bf16, so that nothing overflows
-              w[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+              x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
               if (p + 1 < PARTS) {
 #pragma unroll
                 for (int e = 2 * j; e < 2 * j + 2; ++e) {
@@ -270,47 +268,31 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
                 }
               }
             }
-            st_shared16(st + p * A_BYTES + 1024u * i, w[0], w[1], w[2], w[3]);
+            st_shared16(st + p * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), x[0], x[1], x[2], x[3]);
           }
         }
       }
       uint32_t odd = 0u;
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) odd = max(odd, step[u][i] - 1u);
+      for (int i = 0; i < ROWS; ++i) odd = max(odd, step[i] - 1u);
       if (__any_sync(FULL, odd >= 247u)) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const uint32_t b = step[u][i];
-          const uint2 c = code[u][i];
-          st_shared16(st + PARTS * A_BYTES + 1024u * i, codes_bf16_any(c.x, b), codes_bf16_any(c.x >> 8, b),
-                      codes_bf16_any(c.y, b), codes_bf16_any(c.y >> 8, b));
-        }
+        for (int i = 0; i < ROWS; ++i)
+          st_shared16(st + PARTS * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16_any(code[i].x, step[i]),
+                      codes_bf16_any(code[i].x >> 8, step[i]), codes_bf16_any(code[i].y, step[i]),
+                      codes_bf16_any(code[i].y >> 8, step[i]));
       } else {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-          const uint32_t lead = step[u][i] * 0x00800080u + 0x03800380u, minus = step[u][i] * 0x00800080u + 0x80008000u;
-          const uint2 c = code[u][i];
-          st_shared16(st + PARTS * A_BYTES + 1024u * i, codes_bf16(c.x, lead, minus), codes_bf16(c.x >> 8, lead, minus),
-                      codes_bf16(c.y, lead, minus), codes_bf16(c.y >> 8, lead, minus));
+          const uint32_t lead = step[i] * 0x00800080u + 0x03800380u, minus = step[i] * 0x00800080u + 0x80008000u;
+          st_shared16(st + PARTS * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16(code[i].x, lead, minus),
+                      codes_bf16(code[i].x >> 8, lead, minus), codes_bf16(code[i].y, lead, minus),
+                      codes_bf16(code[i].y >> 8, lead, minus));
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(full_b(slot));
-      if (++slot == STAGES) slot = 0, phase ^= 1u;
-      return true;
-    };
-    // codes are fetched AHEAD - 1 stages before they are unpacked
-    bool ok = true;
-#pragma unroll
-    for (int u = 0; u + 1 < AHEAD; ++u)
-      if (u < iters) fetch(u, u);
-    for (int it = 0; ok && it < iters;) {
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        if (it + AHEAD - 1 < iters) fetch(it + AHEAD - 1, (u + AHEAD - 1) % AHEAD);
-        if (!(ok = put(it, u)) || ++it >= iters) break;
-      }
     }
     if (!ok) fail();
   } else if (warp == WG_CONV) {
@@ -366,14 +348,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
 
   if (warp < WG_CONV && !failed) {
     // -------------------------------------------------- the result, row by row
-    if (mbar_wait(done, 0)) {
+    const bool finished = mbar_wait(done, 0);
+    __syncwarp();
+    if (__all_sync(FULL, finished)) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float* buf = reinterpret_cast<float*>(smem) + warp * 32 * 33;
-      const int h = warp >> 2;
-      const int64_t r0 = n0 + 128 * h + 32 * (warp & 3);
       float* out = a.dw + (a.splits > 1 ? (int64_t)split * a.n * a.lddw : 0);
-      for (int c0 = 0; c0 < WG_N; c0 += 32) {
-        if (k0 + c0 >= a.k || r0 >= a.n) break;
+      for (int item = warp / 4; item < 2 * (WG_N / 32); item += WG_TEAMS) {  // 32 columns of an accumulator
+        const int h = item / (WG_N / 32), c0 = item % (WG_N / 32) * 32;
+        const int64_t r0 = n0 + 128 * h + 32 * (warp & 3);
+        if (k0 + c0 >= a.k || r0 >= a.n) continue;
         float v[32];
         if (iters > 0) {
           tmem_load32(v, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256u * h + c0);
