@@ -2,8 +2,6 @@
 // tensor cores: dw[n, k] = sum_t dy[t, n] * q[t, k], q = code * step.
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "gc_act.cuh"
 #include "gc_host.h"
 
@@ -17,33 +15,50 @@ namespace gc {
 // Tile.  A CTA computes 256 (n) x 256 (k) of dw: two accumulators of 128 x
 // 256 fp32, all 512 columns of the SM's tensor memory.  q has to be unpacked
 // from codes by ordinary instructions, and the unpacked tile serves both
-// accumulators: 16 codes per clock at the tensor cores' full rate, about 45%
-// of the SM's issue slots at 2.5 instructions each.  A 128 x 256 tile would
-// need 32 codes per clock.
+// accumulators: 16 codes per clock at the tensor cores' full rate.  Shared
+// memory bounds the loop: per 64 t the MMAs read 96 KB and the copies of dy
+// and the unpacked q write 32 KB each, 1280 clocks at 128 bytes each, where
+// the MMAs alone would take 1024.  With several terms of dy the tile is 128 x
+// 256: the leading terms go into one accumulator, the others, 2^-8 of their
+// size, into the second, where the truncation below costs them nothing.
+//
+// Chains.  The tensor cores truncate what they add to an accumulator, a bias
+// towards zero that grows with the number of additions: 8192 rows in one
+// chain end with a relative error of 3.0e-6, 2048 rows with 4.8e-7 (fp32
+// additions that round: 5e-7).  An accumulator is therefore added to the
+// result, in fp32 that rounds, after at most WG_CHAIN rows, by warps of their
+// own.  The two accumulators' chains end half a chain apart, so that the
+// other one's MMAs go on with the stages at hand meanwhile; and CTAs end them
+// at different times, so that they do not all write at once.
 //
 // Both operands have the summed index t as their slow dimension in memory,
 // so both are staged "MN-major": 128-byte rows of 64 consecutive n (or k) of
 // one t, 16-byte chunk c of row t at chunk c ^ (t & 7) (the 128-byte
 // swizzle), 64-wide column blocks one after another.
-constexpr int WG_M = 256, WG_N = 256;      // n and k of a CTA's tile
+constexpr int WG_N = 256;                  // k of a CTA's tile
 // The unpacking warps work in teams, each on every WG_TEAMS-th stage: a team
 // has as many stages' time for its own, so the latency of its loads of codes
 // is hidden without keeping several stages' codes in registers.
-constexpr int WG_TEAMS = 3, WG_TEAM = 4;   // teams, warps of a team
-constexpr int WG_CONV = WG_TEAMS * WG_TEAM;     // warps that unpack codes, then write the result
-constexpr int WG_THREADS = (WG_CONV + 2) * 32;  // + one warp issuing TMA loads, one issuing MMAs
-constexpr int WG_SMEM = 192 * 1024;
+constexpr int WG_TEAMS = 2, WG_TEAM = 4;   // teams, warps of a team
+constexpr int WG_CONV = WG_TEAMS * WG_TEAM;
+constexpr int WG_OUT = 8;                  // warps that write the result
+constexpr int WG_TMA = WG_CONV + WG_OUT, WG_MMA = WG_TMA + 1;  // the warps that issue loads of dy, MMAs
+constexpr int WG_THREADS = (WG_CONV + WG_OUT + 4) * 32;        // two warps idle: registers go by groups of four
+constexpr int WG_REGS = 96;                // registers per thread at launch
+constexpr int WG_RING = 192 * 1024;        // shared memory of the stages
+constexpr int WG_SMEM = WG_RING + WG_OUT * 4096;  // + a 32 x 32 tile of the result per writing warp
+constexpr int WG_CHAIN = 3200;             // rows of a chain
 
 struct WgArgs {
   const void* dy;
   int64_t lddy, rows, n, k, ldc;
   const int8_t* codes;
   const uint8_t* steps;
-  const void* cscale;
-  int ctype, accumulate;
-  float* dw;       // or the partial sums, one [n, k] after another
-  int64_t lddw;
-  int splits, tiles_n;          // tiles along k
+  const void* cscale;           // of the result; NULL where it is a split's sums
+  int ctype, accumulate, bulk;  // bulk: rows of the result start on 16-byte boundaries
+  float* out;                   // dw, or the splits' sums one [n, ldo] after another
+  int64_t ldo;
+  int splits, tiles_n, items;   // tiles along k; tiles * splits
   int64_t span;                 // rows of a split, a multiple of 64
   uint32_t* diag;
 };
@@ -58,10 +73,11 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+constexpr int WG_POLLS = 1 << 22;  // limit of every wait
 // Waits for the phase of the given parity to complete, a bounded number of
 // polls (each suspended by the hardware for at most about a microsecond).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 22); ++i) {
+  for (int i = 0; i < WG_POLLS; ++i) {
     uint32_t done;
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.b32 %0, 1, 0, p;\n}\n"
@@ -83,6 +99,32 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// A 32 x 32 tile of the result, 128-byte rows under the 128-byte swizzle, to
+// global memory: stored, or added to it.  Whoever issued it may then wait
+// until its source may be written again, or until it is complete.
+__device__ __forceinline__ void tma_put(const CUtensorMap* map, int x, int y, int z, uint32_t src, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(src)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_put_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_put_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// One float of the result: stored, or added to what is there, which nobody
+// else changes meanwhile, without waiting for it.
+__device__ __forceinline__ void put1(float* o, float v, bool add) {
+  if (add)
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(o), "f"(v) : "memory");
+  else
+    *o = v;
+}
+
 // Shared-memory operand descriptor of an MN-major tile under the 128-byte
 // swizzle: 64-wide blocks `block` bytes apart, groups of 8 t 1024 bytes apart.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t block) {
@@ -99,20 +141,35 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t addr) {
+// 32 consecutive columns of the 32 lanes of tensor memory at `addr`.
+__device__ __forceinline__ void tmem_load32(float* v, uint32_t addr) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Adds 16 consecutive columns of the 32 lanes of tensor memory at `addr` to v.
+__device__ __forceinline__ void tmem_add16(float* v, uint32_t addr) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\ntcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], __uint_as_float(r[i]));
 }
 
 // The codes in bytes 0 and 2 of w (the low byte of each half) as bf16 times
@@ -133,58 +190,192 @@ __device__ __forceinline__ uint32_t codes_bf16_any(uint32_t w, uint32_t step) {
   const float a = __fmul_rn((float)(int8_t)(w & 255u), sc), b = __fmul_rn((float)(int8_t)((w >> 16) & 255u), sc);
   return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
 }
-// The bytes of a word come out in the order 0, 2, 1, 3: column 4 q + p of the
-// tile holds column 4 q + (0, 2, 1, 3)[p] of q, which the result undoes.
-__device__ __forceinline__ int wg_column(int c) { return (c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1); }
+// The bytes of a word come out in the order 0, 2, 1, 3, so accumulator columns
+// 4 q + 1 and 4 q + 2 hold columns 4 q + 2 and 4 q + 1; the result undoes it.
 
-// 8 elements of dy from column c on, as fp32; 0 outside [0, n).
+// 8 elements of dy from column c on, as they are; 0 outside [0, n).
+template <typename T>
+struct Dy8 {
+  T e[8];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float (&v)[8]) {
+__device__ __forceinline__ Dy8<T> load8(const T* row, int64_t c, int64_t n) {
+  Dy8<T> v;
   if (VEC && c + 8 <= n) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(row + c), b = *reinterpret_cast<const float4*>(row + c + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(row + c);
-      const T* e = reinterpret_cast<const T*>(&a);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4*>(v.e)[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(row[c + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) v.e[i] = c + i < n ? row[c + i] : from_f32<T>(0.0f);
   }
+  return v;
+}
+
+template <int PARTS, bool TMA>
+struct WgShape {
+  static constexpr int M = PARTS == 1 ? 256 : 128;      // n of a tile
+  static constexpr int KT = TMA ? 64 : 32;              // t of a stage
+  static constexpr int BLOCK = KT * 128;                // bytes of a 64-wide column block
+  static constexpr int A_BYTES = M / 64 * BLOCK, B_BYTES = WG_N / 64 * BLOCK, STAGE = PARTS * A_BYTES + B_BYTES;
+  static constexpr int STAGES = WG_RING / STAGE < 6 ? WG_RING / STAGE : 6;
+  static constexpr int CHAIN = WG_CHAIN / KT;           // stages of a chain
+  // Registers per thread as the roles share out those of the launch, so that
+  // none keeps its variables in memory: unpacking, writing, the rest.
+  static constexpr int REGS_CONV = TMA ? 80 : 96, REGS_OUT = TMA ? 120 : 112, REGS_REST = TMA ? 80 : 64;
+  static_assert(WG_CONV * REGS_CONV + WG_OUT * REGS_OUT + 4 * REGS_REST <= WG_THREADS / 32 * WG_REGS, "registers");
+};
+
+// A tile and a split of the rows.
+struct WgItem {
+  int split, iters, halves;  // iters: stages; halves: accumulators with rows of their own
+  int64_t n0, k0, t0, t1;
+};
+template <typename S>
+__device__ __forceinline__ WgItem wg_item(const WgArgs& a, int i) {
+  WgItem m;
+  m.split = i % a.splits;
+  const int tile = i / a.splits;
+  m.n0 = (int64_t)(tile / a.tiles_n) * S::M, m.k0 = (int64_t)(tile % a.tiles_n) * WG_N;
+  m.t0 = m.split * a.span, m.t1 = min(m.t0 + a.span, a.rows);
+  m.iters = (int)((m.t1 - m.t0 + S::KT - 1) / S::KT);
+  m.halves = S::M == 256 && m.n0 + 128 < a.n ? 2 : 1;
+  return m;
+}
+// Where the chain of accumulator h that is at stage `pos` ends.
+template <typename S>
+__device__ __forceinline__ int wg_chain_end(int iters, int h, int pos) {
+  if (iters <= S::CHAIN) return iters;
+  const int off = (int)(blockIdx.x % 8u) * (S::CHAIN / 16) + h * (S::CHAIN / 2);
+  return min(iters, pos + S::CHAIN - (pos + off) % S::CHAIN);
+}
+
+// The role of the writing warps.  A warp reads the 32 lanes of tensor
+// memory that its number gives, and 128 of their columns in four tiles of 32.
+// What it may write out at once goes at the rate of the SM's writes, 4000
+// clocks for an accumulator; the accumulator is given back as soon as its
+// last tile is in registers, with one tile written and one on its way.
+template <typename S>
+__device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map, uint32_t tiles, uint32_t full, uint32_t empty,
+                                      uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, side = (warp - WG_CONV) >> 2;
+  const uint32_t tile = tiles + (uint32_t)(side * 4 + quad) * 4096u;
+  const uint32_t columns = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)side * (WG_N / 2);
+  bool ok = true;
+  uint32_t used0 = 0u, used1 = 0u;
+  for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+    const WgItem m = wg_item<S>(a, i);
+    int pos0 = 0, pos1 = m.halves == 2 ? 0 : m.iters;
+    while (ok && (pos0 < m.iters || pos1 < m.iters)) {
+      // the chains in the order of their ends
+      const int end0 = pos0 < m.iters ? wg_chain_end<S>(m.iters, 0, pos0) : m.iters + 1;
+      const int end1 = pos1 < m.iters ? wg_chain_end<S>(m.iters, 1, pos1) : m.iters + 1;
+      const int h = end1 < end0 ? 1 : 0;
+      const bool later = (h ? pos1 : pos0) > 0, add = later || a.accumulate;
+      ok = __all_sync(FULL, mbar_wait(full + 8u * h, (h ? used1 : used0) & 1));
+      if (!ok) break;
+      if (h)
+        ++used1, pos1 = end1;
+      else
+        ++used0, pos0 = end0;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int64_t r0 = m.n0 + 128 * h + 32 * quad, k0 = m.k0 + side * (WG_N / 2);
+      const int rows = (int)max((int64_t)0, min((int64_t)32, a.n - r0));
+      float v[64];
+      auto fetch = [&](int c, float* x) {  // tile c
+        __syncwarp();
+        tmem_load32(x, columns + 256u * h + 32u * c);
+        if (S::M == 128) {
+          tmem_add16(x, columns + 256u + 32u * c);
+          tmem_add16(x + 16, columns + 256u + 32u * c + 16u);
+        }
+      };
+      auto put = [&](int c, float* x) {
+        const int64_t c0 = k0 + 32 * c;
+        if (rows == 0 || c0 >= a.k) return;  // uniform in the warp
+        if (a.bulk && lane == 0) tma_put_read();
+        if (a.cscale) {
+          const float cs = c0 + lane < a.k ? load_as_f32(a.cscale, a.ctype, c0 + lane) : 0.0f;
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            x[q] = __fmul_rn(x[q], __shfl_sync(FULL, cs, (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1)));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared16(tile + (uint32_t)lane * 128u + (uint32_t)((q ^ (lane & 7)) << 4), __float_as_uint(x[4 * q]),
+                      __float_as_uint(x[4 * q + 2]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 3]));
+        if (a.bulk) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tma_put(map, (int)c0, (int)r0, m.split, tile, add);
+        } else {
+          __syncwarp();
+          if (c0 + lane < a.k) {
+            float* o = a.out + ((int64_t)m.split * a.n + r0) * a.ldo + c0 + lane;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r, o += a.ldo) {
+              float y;
+              asm volatile("ld.shared.f32 %0, [%1];"
+                           : "=f"(y)
+                           : "r"(tile + (uint32_t)r * 128u + (uint32_t)(((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4u)
+                           : "memory");
+              put1(o, y, add);
+            }
+          }
+        }
+      };
+      if (a.bulk && later && lane == 0) tma_put_done();  // the chain before is in the result
+      fetch(0, v);
+      put(0, v);
+      fetch(1, v);
+      if (S::M == 256) fetch(2, v + 32);
+      put(1, v);
+      if (S::M == 128) {
+        fetch(2, v + 32);
+        put(2, v + 32);
+      }
+      fetch(3, v);
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8u * h);
+      if (S::M == 256) put(2, v + 32);
+      put(3, v);
+    }
+  }
+  if (lane == 0) tma_put_done();
+  return ok;
 }
 
 // TMA: dy is bf16 and its rows start on 16-byte boundaries, so that its
 // tiles come by bulk tensor copies; else the unpacking warps load it too,
-// split into PARTS bf16 terms.
-// WIDE: the rows of q in a stage may span 2^32 bytes.
-template <typename T, int PARTS, bool TMA, bool VEC, bool WIDE>
-__global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_constant__ CUtensorMap map, const WgArgs a) {
-  constexpr int KT = TMA ? 64 : 32;                     // t of a stage
-  constexpr int BLOCK = KT * 128;                       // bytes of a 64-wide column block
-  constexpr int A_BYTES = 4 * BLOCK, B_BYTES = 4 * BLOCK, STAGE = PARTS * A_BYTES + B_BYTES;
-  constexpr int STAGES = WG_SMEM / STAGE;
+// split into PARTS bf16 terms.  A CTA takes every gridDim.x-th item (a tile and
+// a split of the rows); all roles walk the same items, and `g` counts the
+// stages.
+template <typename T, int PARTS, bool TMA, bool VEC>
+__global__ void __launch_bounds__(WG_THREADS, 1)
+    k_weight_grad(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap out_map,
+                  const __grid_constant__ WgArgs a) {
+  using S = WgShape<PARTS, TMA>;
+  constexpr int KT = S::KT, BLOCK = S::BLOCK, A_BYTES = S::A_BYTES, STAGES = S::STAGES, CHAIN = S::CHAIN;
   constexpr int ROWS = KT / WG_TEAM;                    // t per unpacking warp and stage
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[3 * 8 + 1];
+  __shared__ __align__(8) uint64_t bars[3 * 8 + 4];
   __shared__ uint32_t tmem_base;
-  __shared__ volatile int failed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
   auto full_a = [&](int s) { return bar0 + 8u * s; };
   auto full_b = [&](int s) { return bar0 + 64u + 8u * s; };
   auto empty = [&](int s) { return bar0 + 128u + 8u * s; };
-  const uint32_t done = bar0 + 192u;
+  auto acc_full = [&](int h) { return bar0 + 192u + 8u * h; };   // a chain's MMAs are done
+  auto acc_empty = [&](int h) { return bar0 + 208u + 8u * h; };  // its sums have been read out
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(full_a(s), 1), mbar_init(full_b(s), WG_TEAM), mbar_init(empty(s), 1);
-    mbar_init(done, 1);
-    failed = 0;
+    for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), WG_OUT);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == WG_CONV + 1) {
+  if (warp == WG_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -195,211 +386,240 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_weight_grad(const __grid_cons
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.diag = 0u;
 
-  const int split = blockIdx.x % a.splits;
-  const int tile = blockIdx.x / a.splits;
-  const int64_t n0 = (int64_t)(tile / a.tiles_n) * WG_M, k0 = (int64_t)(tile % a.tiles_n) * WG_N;
-  const int64_t t0 = split * a.span, t1 = min(t0 + a.span, a.rows);
-  const int iters = t1 > t0 ? (int)((t1 - t0 + KT - 1) / KT) : 0;
-  const int halves = n0 + 128 < a.n ? 2 : 1;
-  auto fail = [&]() {
-    failed = 1;
-    atomicOr(a.diag, GC_DIAG_TIMEOUT);
-  };
+  auto item_at = [&](int i) { return wg_item<S>(a, i); };
+  bool ok = true;
+  int g = 0;
 
   if (warp < WG_CONV) {
     // ------------------------------------------------ unpack q (and split dy)
+    if (S::REGS_CONV < WG_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_CONV));
     // Lanes past q's last column read the last columns again: what they put
     // into the tile reaches only columns of the accumulators that are not
     // written out.
-    using Off = typename std::conditional<WIDE, int64_t, uint32_t>::type;
-    const int team = warp / WG_TEAM, w = warp % WG_TEAM;  // rows w, w + 4, ...
-    const int64_t kc = min(k0 + 8 * lane, a.ldc - 8), groups = a.ldc >> 5;
-    const int8_t* cp = a.codes + (t0 + (int64_t)team * KT) * a.ldc;
-    const uint8_t* sp = a.steps + (t0 + (int64_t)team * KT) * groups;
-    const Off co = (Off)(w * a.ldc + kc), so = (Off)(w * groups + (kc >> 5));
-    const uint32_t off0 = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + (uint32_t)(((lane & 7) ^ w) << 4);
-    const uint32_t off1 = (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + 512u + (uint32_t)(((lane & 7) ^ (w + 4)) << 4);
-    bool ok = true;
-    for (int it = team; it < iters; it += WG_TEAMS) {
-      uint2 code[ROWS];
-      uint32_t step[ROWS];
-      if ((int64_t)(it + 1) * KT <= t1 - t0) {
+    const int team = warp / WG_TEAM, w = warp % WG_TEAM;  // rows w, w + 4, ... of q
+    const int64_t groups = a.ldc >> 5;
+    const uint32_t off0 = PARTS * A_BYTES + (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + (uint32_t)(((lane & 7) ^ w) << 4);
+    const uint32_t off1 =
+        PARTS * A_BYTES + (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + 512u + (uint32_t)(((lane & 7) ^ (w + 4)) << 4);
+    // dy: a row takes AL lanes
+    constexpr int AL = S::M / 8, AR = 32 / AL, AN = ROWS / AR;  // lanes per row, rows at a time, times
+    for (int i0 = blockIdx.x; ok && i0 < a.items; i0 += gridDim.x) {
+      const WgItem m = item_at(i0);
+      const int64_t kc = min(m.k0 + 8 * lane, a.ldc - 8), span = m.t1 - m.t0;
+      int it = (team + WG_TEAMS - g % WG_TEAMS) % WG_TEAMS;  // this team's first stage of the item
+      const int8_t* cp = a.codes + (m.t0 + (int64_t)it * KT + w) * a.ldc + kc;
+      const uint8_t* sp = a.steps + (m.t0 + (int64_t)it * KT + w) * groups + (kc >> 5);
+      for (; it < m.iters; it += WG_TEAMS) {
+        uint2 code[ROWS];
+        uint32_t step[ROWS];
+        {
+          // row by row: with its multiples of the stride kept at hand the loop
+          // would take 32 registers more
+          int64_t down = WG_TEAM * a.ldc, down_steps = WG_TEAM * groups;
+          asm volatile("" : "+l"(down), "+l"(down_steps));
+          const int8_t* c = cp;
+          const uint8_t* b = sp;
+          if ((int64_t)(it + 1) * KT <= span) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          code[i] = __ldg(reinterpret_cast<const uint2*>(cp + (co + (Off)(WG_TEAM * i) * (Off)a.ldc)));
-          step[i] = __ldg(sp + (so + (Off)(WG_TEAM * i) * (Off)groups));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {  // rows past the split's end: zeros
-          const bool in = (int64_t)it * KT + WG_TEAM * i + w < t1 - t0;
-          code[i] = in ? __ldg(reinterpret_cast<const uint2*>(cp + (co + (Off)(WG_TEAM * i) * (Off)a.ldc))) : make_uint2(0u, 0u);
-          step[i] = in ? __ldg(sp + (so + (Off)(WG_TEAM * i) * (Off)groups)) : 1u;
-        }
-      }
-      cp += WG_TEAMS * KT * a.ldc;
-      sp += WG_TEAMS * KT * groups;
-      const int slot = it % STAGES;
-      if (!(ok = mbar_wait(empty(slot), ((it / STAGES) & 1) ^ 1))) break;
-      const uint32_t st = base + (uint32_t)slot * STAGE;
-      if constexpr (!TMA) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const int64_t t = t0 + (int64_t)it * KT + WG_TEAM * i + w;
-          float v[8];
-          if (t < t1) {
-            load8<T, VEC>(static_cast<const T*>(a.dy) + t * a.lddy, n0 + 8 * lane, a.n, v);
+            for (int i = 0; i < ROWS; ++i, c += down, b += down_steps) {
+              code[i] = __ldg(reinterpret_cast<const uint2*>(c));
+              step[i] = __ldg(b);
+            }
           } else {
+            const int left = (int)(span - (int64_t)it * KT) - w;  // rows past the split's end: zeros
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            for (int i = 0; i < ROWS; ++i, c += down, b += down_steps) {
+              code[i] = WG_TEAM * i < left ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
+              step[i] = WG_TEAM * i < left ? __ldg(b) : 1u;
+            }
           }
+        }
+        cp += WG_TEAMS * KT * a.ldc;
+        sp += WG_TEAMS * KT * groups;
+        const int slot = (g + it) % STAGES;
+        const uint32_t st = base + (uint32_t)slot * S::STAGE;
+        if constexpr (TMA) {
+          if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
+        } else {
+          Dy8<T> d[AN];
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            uint32_t x[4];
+          for (int i = 0; i < AN; ++i) {
+            const int64_t t = m.t0 + (int64_t)it * KT + WG_TEAM * (AR * i + lane / AL) + w;
+            const bool in = t < m.t1;  // rows past the split's end: zeros
+            d[i] = load8<T, VEC>(static_cast<const T*>(a.dy) + (in ? t : m.t0) * a.lddy, m.n0 + 8 * (lane % AL), in ? a.n : 0);
+          }
+          if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // the upper halves: truncation to bf16, so that nothing overflows
-              x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
-              if (p + 1 < PARTS) {
+          for (int i = 0; i < AN; ++i) {
+            const int t = WG_TEAM * (AR * i + lane / AL) + w;
+            float v[8];
 #pragma unroll
-                for (int e = 2 * j; e < 2 * j + 2; ++e) {
-                  const float h = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
-                  v[e] = isinf(v[e]) ? 0.0f : __fsub_rn(v[e], h);
+            for (int j = 0; j < 8; ++j) v[j] = to_f32(d[i].e[j]);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+              uint32_t x[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // the upper halves: truncation to bf16, so that nothing overflows
+                x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+                if (p + 1 < PARTS) {
+#pragma unroll
+                  for (int e = 2 * j; e < 2 * j + 2; ++e) {
+                    const float top = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
+                    v[e] = isinf(v[e]) ? 0.0f : __fsub_rn(v[e], top);
+                  }
                 }
               }
+              st_shared16(st + p * A_BYTES + (uint32_t)(lane % AL / 8) * BLOCK + (uint32_t)t * 128u +
+                              (uint32_t)(((lane & 7) ^ (t & 7)) << 4),
+                          x[0], x[1], x[2], x[3]);
             }
-            st_shared16(st + p * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), x[0], x[1], x[2], x[3]);
           }
         }
-      }
-      uint32_t odd = 0u;
+        uint32_t odd = 0u;
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) odd = max(odd, step[i] - 1u);
-      if (__any_sync(FULL, odd >= 247u)) {
+        for (int i = 0; i < ROWS; ++i) odd = max(odd, step[i] - 1u);
+        if (__any_sync(FULL, odd >= 247u)) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-          st_shared16(st + PARTS * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16_any(code[i].x, step[i]),
-                      codes_bf16_any(code[i].x >> 8, step[i]), codes_bf16_any(code[i].y, step[i]),
-                      codes_bf16_any(code[i].y >> 8, step[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const uint32_t lead = step[i] * 0x00800080u + 0x03800380u, minus = step[i] * 0x00800080u + 0x80008000u;
-          st_shared16(st + PARTS * A_BYTES + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16(code[i].x, lead, minus),
-                      codes_bf16(code[i].x >> 8, lead, minus), codes_bf16(code[i].y, lead, minus),
-                      codes_bf16(code[i].y >> 8, lead, minus));
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full_b(slot));
-    }
-    if (!ok) fail();
-  } else if (warp == WG_CONV) {
-    // ------------------------------------------------ dy tiles by TMA
-    if (TMA && lane == 0) {
-      bool ok = true;
-      int it = 0;
-      for (; it < iters; ++it) {
-        const int s = it % STAGES;
-        if (!(ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1))) break;
-        mbar_expect(full_a(s), A_BYTES);
-        const uint32_t st = base + (uint32_t)s * STAGE;
-        const int y = (int)(t0 + (int64_t)it * KT);
-        for (int b = 0; b < 4; ++b) tma_load_2d(st + b * BLOCK, &map, (int)n0 + 64 * b, y, full_a(s));
-      }
-      if (!ok) {
-        fail();
-        for (int j = max(0, it - STAGES); j < it; ++j) mbar_wait(full_a(j % STAGES), (j / STAGES) & 1);
-      }
-    }
-    __syncwarp();
-  } else if (lane == 0) {
-    // ------------------------------------------------ MMA
-    const int kw = (int)min((int64_t)WG_N, a.k - k0);
-    const uint32_t nd = (uint32_t)((kw + 15) / 16 * 16);
-    // fp32 accumulator, bf16 operands, both MN-major, N, M = 128
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((nd >> 3) << 17) | (8u << 24);
-    bool ok = true;
-    for (int it = 0; it < iters; ++it) {
-      const int s = it % STAGES;
-      const uint32_t ph = (it / STAGES) & 1;
-      if (!(ok = (!TMA || mbar_wait(full_a(s), ph)) && mbar_wait(full_b(s), ph))) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t st = base + (uint32_t)s * STAGE;
-#pragma unroll
-      for (int j = 0; j < KT / 16; ++j) {
-        const uint64_t db = mn_desc(st + PARTS * A_BYTES + j * 2048, BLOCK);
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-          for (int h = 0; h < halves; ++h)
-            mma_bf16(tmem + 256u * h, mn_desc(st + p * A_BYTES + h * 2 * BLOCK + j * 2048, BLOCK), db, idesc,
-                     it > 0 || j > 0 || p > 0);
-      }
-      mma_commit(empty(s));
-    }
-    mma_commit(done);
-    if (!ok) {
-      fail();
-      mbar_wait(done, 0);
-    }
-  }
-  __syncwarp();
-
-  if (warp < WG_CONV && !failed) {
-    // -------------------------------------------------- the result, row by row
-    const bool finished = mbar_wait(done, 0);
-    __syncwarp();
-    if (__all_sync(FULL, finished)) {
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float* buf = reinterpret_cast<float*>(smem) + warp * 32 * 33;
-      float* out = a.dw + (a.splits > 1 ? (int64_t)split * a.n * a.lddw : 0);
-      for (int item = warp / 4; item < 2 * (WG_N / 32); item += WG_TEAMS) {  // 32 columns of an accumulator
-        const int h = item / (WG_N / 32), c0 = item % (WG_N / 32) * 32;
-        const int64_t r0 = n0 + 128 * h + 32 * (warp & 3);
-        if (k0 + c0 >= a.k || r0 >= a.n) continue;
-        float v[32];
-        if (iters > 0) {
-          tmem_load32(v, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256u * h + c0);
+          for (int i = 0; i < ROWS; ++i)
+            st_shared16(st + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16_any(code[i].x, step[i]),
+                        codes_bf16_any(code[i].x >> 8, step[i]), codes_bf16_any(code[i].y, step[i]),
+                        codes_bf16_any(code[i].y >> 8, step[i]));
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) buf[lane * 33 + j] = v[j];
-        __syncwarp();
-        const int64_t c = k0 + c0 + lane;
-        if (c < a.k) {
-          const float cs = a.splits == 1 && a.cscale ? load_as_f32(a.cscale, a.ctype, c) : 1.0f;
-          const int rows = (int)min((int64_t)32, a.n - r0);
-          for (int r = 0; r < rows; ++r) {
-            float* o = out + (r0 + r) * a.lddw + c;
-            const float x = __fmul_rn(buf[r * 33 + wg_column(lane)], cs);
-            *o = a.splits == 1 && a.accumulate ? __fadd_rn(*o, x) : x;
+          for (int i = 0; i < ROWS; ++i) {
+            const uint32_t lead = step[i] * 0x00800080u + 0x03800380u, minus = step[i] * 0x00800080u + 0x80008000u;
+            st_shared16(st + ((i & 1) ? off1 : off0) + 1024u * (i >> 1), codes_bf16(code[i].x, lead, minus),
+                        codes_bf16(code[i].x >> 8, lead, minus), codes_bf16(code[i].y, lead, minus),
+                        codes_bf16(code[i].y >> 8, lead, minus));
           }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+        if (lane == 0) mbar_arrive(full_b(slot));
       }
-    } else {
-      fail();
+      g += m.iters;
+    }
+  } else if (warp < WG_TMA) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_OUT));
+    ok = wg_write<S>(a, &out_map, base + WG_RING, acc_full(0), acc_empty(0), tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_REST));
+    if (warp == WG_TMA) {
+    // ------------------------------------------------ dy tiles by TMA
+    if (TMA && lane == 0) {
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+        const WgItem m = item_at(i);
+        for (int it = 0; it < m.iters; ++it, ++g) {
+          const int s = g % STAGES;
+          if (!(ok = mbar_wait(empty(s), ((g / STAGES) & 1) ^ 1))) break;
+          mbar_expect(full_a(s), A_BYTES);
+          const uint32_t st = base + (uint32_t)s * S::STAGE;
+          const int y = (int)(m.t0 + (int64_t)it * KT);
+          for (int b = 0; b < S::M / 64; ++b) tma_load_2d(st + b * BLOCK, &dy_map, (int)m.n0 + 64 * b, y, full_a(s));
+        }
+      }
+      // its copies in flight write this CTA's memory: see them land
+      if (!ok)
+        for (int j = max(0, g - STAGES); j < g; ++j) mbar_wait(full_a(j % STAGES), (j / STAGES) & 1);
+    }
+    } else if (warp == WG_MMA) {
+    // ------------------------------------------------ MMA
+    if (lane == 0) {
+      uint32_t used0 = 0u, used1 = 0u;  // chains so far of each accumulator
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+        const WgItem m = item_at(i);
+        const uint32_t nd = (uint32_t)((min((int64_t)WG_N, a.k - m.k0) + 15) / 16 * 16);
+        // fp32 accumulator, bf16 operands, both MN-major, N, M = 128
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((nd >> 3) << 17) | (8u << 24);
+        auto arrived = [&](int q) {
+          const int s = q % STAGES;
+          const uint32_t ph = (q / STAGES) & 1;
+          const bool in = (!TMA || mbar_wait(full_a(s), ph)) && mbar_wait(full_b(s), ph);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          return in;
+        };
+        // a chain begins where the one before has been read out
+        auto vacant = [&](int h) {
+          const bool in = mbar_wait(acc_empty(h), ((h ? used1++ : used0++) & 1) ^ 1);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          return in;
+        };
+        auto multiply = [&](int q, int h, bool first) {
+          const uint32_t st = base + (uint32_t)(q % STAGES) * S::STAGE;
+#pragma unroll
+          for (int j = 0; j < KT / 16; ++j) {
+            const uint64_t db = mn_desc(st + PARTS * A_BYTES + j * 2048, BLOCK);
+            if (PARTS == 1) {
+              mma_bf16(tmem + 256u * h, mn_desc(st + h * 2 * BLOCK + j * 2048, BLOCK), db, idesc, !first || j > 0);
+            } else {
+#pragma unroll
+              for (int p = 0; p < PARTS; ++p)
+                mma_bf16(tmem + (p ? 256u : 0u), mn_desc(st + p * A_BYTES + j * 2048, BLOCK), db, idesc, !first || j > 0 || p > 1);
+            }
+          }
+        };
+        int end0 = wg_chain_end<S>(m.iters, 0, 0), end1 = m.halves == 2 ? wg_chain_end<S>(m.iters, 1, 0) : m.iters + 1;
+        bool new0 = true, new1 = m.halves == 2;
+        for (int pos = 0; ok && pos < m.iters;) {
+          const int stop = min(end0, end1);
+          if (new0 || new1) {
+            // the other accumulator goes on with the stages at hand while
+            // the one whose chain begins is still read out, which catches up
+            const int lead = min(stop - pos, STAGES), h = new0 && !new1 && m.halves == 2 ? 1 : 0;
+            ok = !(h ? new1 : new0) || vacant(h);
+            for (int q = 0; ok && q < lead; ++q) {
+              if (!(ok = arrived(g + pos + q))) break;
+              multiply(g + pos + q, h, (h ? new1 : new0) && q == 0);
+              if (m.halves == 1) mma_commit(empty((g + pos + q) % STAGES));
+            }
+            if (m.halves == 2) {
+              ok = ok && vacant(1 - h);
+              for (int q = 0; ok && q < lead; ++q) {
+                multiply(g + pos + q, 1 - h, q == 0);
+                mma_commit(empty((g + pos + q) % STAGES));
+              }
+            }
+            pos += lead;
+          }
+          for (; ok && pos < stop; ++pos) {
+            if (!(ok = arrived(g + pos))) break;
+            multiply(g + pos, 0, false);
+            if (m.halves == 2) multiply(g + pos, 1, false);
+            mma_commit(empty((g + pos) % STAGES));
+          }
+          new0 = end0 == stop, new1 = end1 == stop;
+          if (new0) mma_commit(acc_full(0)), end0 = wg_chain_end<S>(m.iters, 0, pos);
+          if (new1) mma_commit(acc_full(1)), end1 = wg_chain_end<S>(m.iters, 1, pos);
+        }
+        g += m.iters;
+      }
+      if (!ok) {
+        // MMAs in flight read this CTA's memory: see them end
+        mma_commit(acc_full(0));
+        mbar_wait(acc_full(0), (used0 - 1) & 1);
+      }
+    }
     }
   }
+  if (!ok) atomicOr(a.diag, GC_DIAG_TIMEOUT);
+  __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == WG_CONV + 1)
+  if (warp == WG_MMA)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // dw = (dw +) cscale * the splits' sums in their order.
-__global__ void __launch_bounds__(256) k_weight_grad_join(const float* part, int splits, int64_t n, int64_t k,
+__global__ void __launch_bounds__(256) k_weight_grad_join(const float* part, int splits, int64_t n, int64_t k, int64_t ldp,
                                                           const void* cscale, int ctype, float* dw, int64_t lddw,
                                                           int accumulate) {
   chain_wait();
   const int64_t total = n * k;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    float s = part[i];
-    for (int p = 1; p < splits; ++p) s = __fadd_rn(s, part[p * total + i]);
     const int64_t r = i / k, c = i - r * k;
+    float s = 0.0f;
+    for (int p = 0; p < splits; ++p) s = __fadd_rn(s, part[(p * n + r) * ldp + c]);
     if (cscale) s = __fmul_rn(s, load_as_f32(cscale, ctype, c));
     float* o = dw + r * lddw + c;
     *o = accumulate ? __fadd_rn(*o, s) : s;
@@ -409,39 +629,67 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const float* part, int
 constexpr int WG_SMS = 152;  // of a GB300
 
 // Splits of the rows: as many as keep every SM busy when there are few
-// tiles, each of at least 256 rows.
-static int wg_splits(int64_t rows, int64_t n, int64_t k) {
-  const int64_t tiles = ((n + WG_M - 1) / WG_M) * ((k + WG_N - 1) / WG_N);
+// tiles, each of at least 256 rows.  A split has a multiple of 64 rows.
+static int64_t wg_span(int64_t rows, int64_t splits) { return ((rows + splits - 1) / splits + 63) / 64 * 64; }
+static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
+  const int m = dtype == GC_BF16 ? WgShape<1, true>::M : WgShape<2, false>::M;
+  return (n + m - 1) / m;
+}
+static int wg_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
+  const int64_t tiles = wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N);
   int64_t s = WG_SMS / tiles;
   if (s > rows / 256) s = rows / 256;
-  return (int)(s < 1 ? 1 : s);
+  if (s < 2) return 1;
+  const int64_t span = wg_span(rows, s);
+  return (int)((rows + span - 1) / span);
 }
+static int64_t wg_ldp(int64_t k) { return (k + 3) / 4 * 4; }  // row stride of the splits' sums
 
-// dy as a 2-D tensor of 64 x 64 boxes under the 128-byte swizzle.
-static bool make_dy_map(CUtensorMap* m, const void* dy, int64_t lddy, int64_t rows, int64_t n) {
-  using Encode = decltype(&cuTensorMapEncodeTiled);
-  static const Encode encode = [] {
+using TensorMapEncode = decltype(&cuTensorMapEncodeTiled);
+static TensorMapEncode tensor_map_encode() {
+  static const TensorMapEncode encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess)
       f = nullptr;
-    return reinterpret_cast<Encode>(f);
+    return reinterpret_cast<TensorMapEncode>(f);
   }();
-  if (!encode) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)lddy * 2};
+  return encode;
+}
+// dy (bf16) as a 2-D tensor of 64 x 64 boxes under the 128-byte swizzle.
+static bool make_dy_map(CUtensorMap* m, const WgArgs& a) {
+  const TensorMapEncode encode = tensor_map_encode();
+  const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.lddy * 2};
   const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(dy), dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.dy), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The result as a 3-D tensor (k, n, split) of 32 x 32 boxes.
+static bool make_out_map(CUtensorMap* m, const WgArgs& a) {
+  const TensorMapEncode encode = tensor_map_encode();
+  const cuuint64_t dims[3] = {(cuuint64_t)a.k, (cuuint64_t)a.n, (cuuint64_t)a.splits};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.ldo * 4, (cuuint64_t)a.ldo * 4 * (cuuint64_t)a.n};
+  const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
+  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.out, dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int PARTS, bool TMA, bool VEC, bool WIDE = false>
-static bool launch_wg(const CUtensorMap& map, const WgArgs& a, unsigned grid, cudaStream_t s) {
-  auto kern = k_weight_grad<T, PARTS, TMA, VEC, WIDE>;
-  static const bool ready = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) == cudaSuccess;
-  if (!ready) return false;
-  launch_chained(kern, grid, WG_THREADS, WG_SMEM, s, map, a);
+template <typename T, int PARTS, bool TMA, bool VEC>
+static bool launch_wg(const WgArgs& a, cudaStream_t s) {
+  auto kern = k_weight_grad<T, PARTS, TMA, VEC>;
+  // the registers that the groups share out are those of the launch: with
+  // fewer the kernel would wait for more
+  static const bool ready = [=] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs == WG_REGS &&
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) == cudaSuccess;
+  }();
+  CUtensorMap dy_map = {}, out_map = {};
+  if (!ready || (TMA && !make_dy_map(&dy_map, a)) || (a.bulk && !make_out_map(&out_map, a))) return false;
+  launch_chained(kern, (unsigned)(a.items < WG_SMS ? a.items : WG_SMS), WG_THREADS, WG_SMEM, s, dy_map, out_map, a);
   return true;
 }
 
@@ -455,8 +703,8 @@ extern "C" gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, 
   if (st == GC_OK) st = validate_matrix(rows, k, dtype);
   if (st != GC_OK) return st;
   if (!bytes) return GC_ERR_INVALID_ARG;
-  const int splits = wg_splits(rows, n, k);
-  *bytes = DIAG_BYTES + (splits > 1 ? (size_t)splits * (size_t)n * (size_t)k * sizeof(float) : 0);
+  const int splits = wg_splits(rows, n, k, dtype);
+  *bytes = DIAG_BYTES + (splits > 1 ? (size_t)splits * (size_t)n * (size_t)wg_ldp(k) * sizeof(float) : 0);
   return GC_OK;
 }
 
@@ -474,41 +722,35 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
   if (rows > 0 && ((st = check_matrix(dy, lddy, n, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK))
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int splits = wg_splits(rows, n, k);
-  const int64_t tiles_n = (k + WG_N - 1) / WG_N, tiles = (n + WG_M - 1) / WG_M * tiles_n;
-  if (tiles * splits > INT64_C(2147483647)) return GC_ERR_LAYOUT;
-  WgArgs a;
-  a.dy = dy, a.lddy = lddy, a.rows = rows, a.n = n, a.k = k, a.ldc = act_ldc(k);
-  a.codes = codes, a.steps = steps, a.cscale = col_scale, a.ctype = col_scale_dtype;
-  a.accumulate = (flags & GC_ACCUMULATE) ? 1 : 0;
+  const int splits = wg_splits(rows, n, k, dtype), acc = (flags & GC_ACCUMULATE) ? 1 : 0;
+  const int64_t tiles_n = (k + WG_N - 1) / WG_N, items = wg_tiles_m(n, dtype) * tiles_n * splits;
+  if (items > INT64_C(1073741823)) return GC_ERR_LAYOUT;
   float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + DIAG_BYTES);
-  a.dw = splits > 1 ? part : dw;
-  a.lddw = splits > 1 ? k : lddw;
-  a.splits = splits, a.tiles_n = (int)tiles_n;
-  a.span = ((rows + splits - 1) / splits + 63) / 64 * 64;
-  a.diag = static_cast<uint32_t*>(workspace);
-  const unsigned grid = (unsigned)(tiles * splits);
-  const bool vec = aligned16(dy) && lddy % 8 == 0;
-  CUtensorMap map = {};
-  bool ok;
-  if (a.ldc >= (int64_t(1) << 25)) {  // 64 rows of q span 2^31 bytes
-    ok = dtype == GC_BF16  ? launch_wg<__nv_bfloat16, 1, false, false, true>(map, a, grid, s)
-         : dtype == GC_F16 ? launch_wg<__half, 2, false, false, true>(map, a, grid, s)
-                           : launch_wg<float, 3, false, false, true>(map, a, grid, s);
-  } else if (dtype == GC_BF16 && vec && rows > 0) {
-    ok = make_dy_map(&map, dy, lddy, rows, n) && launch_wg<__nv_bfloat16, 1, true, true>(map, a, grid, s);
-  } else if (dtype == GC_BF16) {
-    ok = launch_wg<__nv_bfloat16, 1, false, false>(map, a, grid, s);
-  } else if (dtype == GC_F16) {
-    ok = vec ? launch_wg<__half, 2, false, true>(map, a, grid, s) : launch_wg<__half, 2, false, false>(map, a, grid, s);
-  } else {
-    ok = vec ? launch_wg<float, 3, false, true>(map, a, grid, s) : launch_wg<float, 3, false, false>(map, a, grid, s);
+  if (rows > 0) {
+    WgArgs a;
+    a.dy = dy, a.lddy = lddy, a.rows = rows, a.n = n, a.k = k, a.ldc = act_ldc(k);
+    a.codes = codes, a.steps = steps;
+    a.cscale = splits > 1 ? nullptr : col_scale, a.ctype = col_scale_dtype;
+    a.accumulate = splits > 1 ? 0 : acc;
+    a.out = splits > 1 ? part : dw, a.ldo = splits > 1 ? wg_ldp(k) : lddw;
+    a.bulk = aligned16(a.out) && a.ldo % 4 == 0;
+    a.splits = splits, a.tiles_n = (int)tiles_n, a.items = (int)items;
+    a.span = wg_span(rows, splits);
+    a.diag = static_cast<uint32_t*>(workspace);
+    const bool vec = aligned16(dy) && lddy % 8 == 0;
+    bool ok;
+    if (dtype == GC_BF16)
+      ok = vec ? launch_wg<__nv_bfloat16, 1, true, true>(a, s) : launch_wg<__nv_bfloat16, 1, false, false>(a, s);
+    else if (dtype == GC_F16)
+      ok = vec ? launch_wg<__half, 2, false, true>(a, s) : launch_wg<__half, 2, false, false>(a, s);
+    else
+      ok = vec ? launch_wg<float, 3, false, true>(a, s) : launch_wg<float, 3, false, false>(a, s);
+    if (!ok) return GC_ERR_CUDA;
   }
-  if (!ok) return GC_ERR_CUDA;
-  if (splits > 1) {
+  if (splits > 1 || rows == 0) {
     const int64_t blocks = (n * k + 255) / 256;
     launch_chained(k_weight_grad_join, (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, s, (const float*)part,
-                   splits, n, k, col_scale, (int)col_scale_dtype, dw, lddw, a.accumulate);
+                   rows == 0 ? 0 : splits, n, k, wg_ldp(k), col_scale, (int)col_scale_dtype, dw, lddw, acc);
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
