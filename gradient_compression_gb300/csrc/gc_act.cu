@@ -4,31 +4,53 @@
 
 namespace gc {
 
-// One warp per group of 32 columns, a lane per column.
-template <typename T>
-__global__ void __launch_bounds__(256) k_act_compress(const T* x, int64_t ld, int64_t rows, int64_t cols,
-                                                      int64_t groups, int8_t* codes, uint8_t* steps) {
+constexpr int UNROLL = 4;  // chunks of a thread: their loads are issued before any is used
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_act_compress(const T* x, int64_t ld, int64_t cols, Walk w, int8_t* codes,
+                                                      uint8_t* steps) {
   chain_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t total = rows * groups, stride = (int64_t)gridDim.x * 8;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += stride) {
-    const int64_t r = i / groups, c = (i - r * groups) * 32 + lane;
-    const float v = c < cols ? to_f32(x[r * ld + c]) : 0.0f;
-    const uint32_t b = act_step(__reduce_max_sync(FULL, __float_as_uint(fabsf(v))));
-    codes[i * 32 + lane] = (int8_t)act_code(v, act_inverse(b));
-    if (lane == 0) steps[i] = (uint8_t)b;
+  const int64_t groups = w.c8s / 4;
+  Chunk at[UNROLL];
+  Raw8<T> raw[UNROLL];
+  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * UNROLL) + threadIdx.x);
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
+    raw[i] = load_chunk<T, VEC>(x + at[i].r * ld + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols));
+  }
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    float v[CHUNK];
+    unpack(raw[i], v);
+    const uint32_t b = chunk_step(v);
+    const uint2 c = chunk_codes(v, b);
+    if (at[i].r < w.rows) store_codes(codes, steps, groups, at[i].r, at[i].c8, c, b);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_act_decompress(const int8_t* codes, const uint8_t* steps, int64_t rows,
-                                                        int64_t cols, int64_t groups, T* out, int64_t ld) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_act_decompress(const int8_t* codes, const uint8_t* steps, int64_t cols, Walk w,
+                                                        T* out, int64_t ld) {
+  __shared__ float4 stage[VEC ? 1 : 512];
   chain_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t total = rows * groups, stride = (int64_t)gridDim.x * 8;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += stride) {
-    const int64_t r = i / groups, c = (i - r * groups) * 32 + lane;
-    if (c < cols) out[r * ld + c] = from_f32<T>(__fmul_rn((float)codes[i * 32 + lane], act_scale(steps[i])));
+  const int64_t groups = w.c8s / 4;
+  Chunk at[UNROLL];
+  uint2 c[UNROLL];
+  uint32_t b[UNROLL];
+  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * UNROLL) + threadIdx.x);
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
+    c[i] = make_uint2(0u, 0u), b[i] = 1u;
+    if (at[i].r < w.rows) c[i] = load_codes(codes, groups, at[i].r, at[i].c8), b[i] = steps[at[i].r * groups + (at[i].c8 >> 2)];
+  }
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) {
+    float v[CHUNK];
+    chunk_values(c[i], b[i], v);
+    store_chunk<T, VEC>(out + at[i].r * ld + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols), v,
+                        reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256);
   }
 }
 
@@ -40,7 +62,11 @@ __global__ void __launch_bounds__(256) k_act_decompress(const int8_t* codes, con
 // applied as exp(-(p + low)) = exp(-p) (1 - low).
 // Below -80, where 1 + exp(-p) is exp(-p) and soon overflows, the sigmoid is
 // exp(p).
-template <int KIND>
+// PRECISE (fp32 results): correctly rounded division and CUDA's expf.  For
+// 16-bit results the hardware's exponential and reciprocal, a few 2^-23 off
+// (and |p| 2^-24 from the argument), are 2^-10 of the result's own rounding
+// and a third of the instructions, which bound these kernels next to memory.
+template <int KIND, bool PRECISE>
 __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
   float p = g, low = 0.0f;
   *dp = 1.0f;
@@ -55,64 +81,131 @@ __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
     *dp = __fmaf_rn(2.0f * CA, t2, w);
   }
   const bool far = p < -80.0f;
-  float e = expf(far ? p : -p);
+  const float z = far ? p : -p;
+  float e;
+  if (PRECISE) {
+    e = expf(z);
+  } else {
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(z, 1.4426950408889634f)));
+  }
   if (KIND == GC_GATE_GELU_TANH) e = __fmaf_rn(e, far ? low : -low, e);
-  return far ? e : __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
+  const float one = __fadd_rn(1.0f, e);
+  float s;
+  if (PRECISE) {
+    s = __fdiv_rn(1.0f, one);
+  } else {
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(one));
+  }
+  return far ? e : s;
 }
 
-template <typename T, int KIND>
+// The loads of one chunk are issued together; two chunks per thread leave 32
+// warps per SM and put 128 bytes per thread in flight.
+constexpr int GATED_UNROLL = 2;
+
+template <typename T, int KIND, bool VEC>
 __global__ void __launch_bounds__(256)
-    k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, int64_t rows, int64_t cols, int64_t groups,
-            T* out, int64_t ldo, int8_t* gcodes, uint8_t* gsteps, int8_t* ucodes, uint8_t* usteps) {
+    k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, int64_t cols, Walk w, T* out, int64_t ldo, int8_t* gcodes,
+            uint8_t* gsteps, int8_t* ucodes, uint8_t* usteps) {
+  __shared__ float4 stage[VEC ? 1 : 512];
   chain_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t total = rows * groups, stride = (int64_t)gridDim.x * 8;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += stride) {
-    const int64_t r = i / groups, c = (i - r * groups) * 32 + lane;
-    const float g = c < cols ? to_f32(gate[r * ldg + c]) : 0.0f, u = c < cols ? to_f32(up[r * ldu + c]) : 0.0f;
-    float dp;
-    if (c < cols) out[r * ldo + c] = from_f32<T>(__fmul_rn(__fmul_rn(g, gate_sigmoid<KIND>(g, &dp)), u));
+  const int64_t groups = w.c8s / 4;
+  Chunk at[GATED_UNROLL];
+  Raw8<T> rg[GATED_UNROLL], ru[GATED_UNROLL];
+  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * GATED_UNROLL) + threadIdx.x);
+#pragma unroll
+  for (int i = 0; i < GATED_UNROLL; ++i) {
+    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
+    const int n = chunk_len(w, at[i], cols);
+    const int64_t c = (int64_t)at[i].c8 * CHUNK;
+    rg[i] = load_chunk<T, VEC>(gate + at[i].r * ldg + c, n);
+    ru[i] = load_chunk<T, VEC>(up + at[i].r * ldu + c, n);
+  }
+#pragma unroll
+  for (int i = 0; i < GATED_UNROLL; ++i) {
+    float g[CHUNK], u[CHUNK], v[CHUNK];
+    unpack(rg[i], g);
+    unpack(ru[i], u);
     if (gcodes) {
-      const uint32_t bg = act_step(__reduce_max_sync(FULL, __float_as_uint(fabsf(g))));
-      const uint32_t bu = act_step(__reduce_max_sync(FULL, __float_as_uint(fabsf(u))));
-      gcodes[i * 32 + lane] = (int8_t)act_code(g, act_inverse(bg));
-      ucodes[i * 32 + lane] = (int8_t)act_code(u, act_inverse(bu));
-      if (lane == 0) gsteps[i] = (uint8_t)bg, usteps[i] = (uint8_t)bu;
+      const uint32_t bg = chunk_step(g), bu = chunk_step(u);
+      const uint2 cg = chunk_codes(g, bg), cu = chunk_codes(u, bu);
+      if (at[i].r < w.rows) {
+        store_codes(gcodes, gsteps, groups, at[i].r, at[i].c8, cg, bg);
+        store_codes(ucodes, usteps, groups, at[i].r, at[i].c8, cu, bu);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < CHUNK; ++e) {
+      float dp;
+      v[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp)), u[e]);
+    }
+    store_chunk<T, VEC>(out + at[i].r * ldo + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols), v,
+                        reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256);
   }
 }
 
-template <typename T, int KIND>
+template <typename T, int KIND, bool VEC>
 __global__ void __launch_bounds__(256)
-    k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps,
-                     const int8_t* ucodes, const uint8_t* usteps, int64_t rows, int64_t cols, int64_t groups, T* dgate,
-                     int64_t lddg, T* dup, int64_t lddu, int8_t* ocodes, uint8_t* osteps) {
+    k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
+                     const uint8_t* usteps, int64_t cols, Walk w, T* dgate, int64_t lddg, T* dup, int64_t lddu,
+                     int8_t* ocodes, uint8_t* osteps) {
+  __shared__ float4 stage[VEC ? 1 : 512];
+  float* const buf = reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256;
   chain_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t total = rows * groups, stride = (int64_t)gridDim.x * 8;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += stride) {
-    const int64_t r = i / groups, c = (i - r * groups) * 32 + lane;
-    const float g = __fmul_rn((float)gcodes[i * 32 + lane], act_scale(gsteps[i]));
-    const float u = __fmul_rn((float)ucodes[i * 32 + lane], act_scale(usteps[i]));
-    float dp;
-    const float s = gate_sigmoid<KIND>(g, &dp), a = __fmul_rn(g, s);
-    if (c < cols) {
-      const float d = to_f32(dout[r * lddo + c]);
-      dgate[r * lddg + c] = from_f32<T>(d * u * __fmaf_rn(a * (1.0f - s), dp, s));
-      dup[r * lddu + c] = from_f32<T>(d * a);
+  const int64_t groups = w.c8s / 4;
+  Chunk at[GATED_UNROLL];
+  Raw8<T> rd[GATED_UNROLL];
+  uint2 cg[GATED_UNROLL], cu[GATED_UNROLL];
+  uint32_t bg[GATED_UNROLL], bu[GATED_UNROLL];
+  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * GATED_UNROLL) + threadIdx.x);
+#pragma unroll
+  for (int i = 0; i < GATED_UNROLL; ++i) {
+    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
+    rd[i] = load_chunk<T, VEC>(dout + at[i].r * lddo + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols));
+    cg[i] = cu[i] = make_uint2(0u, 0u), bg[i] = bu[i] = 1u;
+    if (at[i].r < w.rows) {
+      const int64_t s = at[i].r * groups + (at[i].c8 >> 2);
+      cg[i] = load_codes(gcodes, groups, at[i].r, at[i].c8), bg[i] = gsteps[s];
+      cu[i] = load_codes(ucodes, groups, at[i].r, at[i].c8), bu[i] = usteps[s];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < GATED_UNROLL; ++i) {
+    float g[CHUNK], u[CHUNK], d[CHUNK], a[CHUNK];
+    chunk_values(cg[i], bg[i], g);
+    chunk_values(cu[i], bu[i], u);
+    unpack(rd[i], d);
+#pragma unroll
+    for (int e = 0; e < CHUNK; ++e) {
+      float dp;
+      const float s = gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp), act = __fmul_rn(g[e], s);
+      const float slope = __fmaf_rn(__fmul_rn(act, __fsub_rn(1.0f, s)), dp, s);
+      g[e] = __fmul_rn(__fmul_rn(d[e], u[e]), slope);  // dgate
+      a[e] = __fmul_rn(act, u[e]);
+      u[e] = __fmul_rn(d[e], act);  // dup
+    }
+    const int n = chunk_len(w, at[i], cols);
+    const int64_t c = (int64_t)at[i].c8 * CHUNK;
+    store_chunk<T, VEC>(dgate + at[i].r * lddg + c, n, g, buf);
+    store_chunk<T, VEC>(dup + at[i].r * lddu + c, n, u, buf);
     if (ocodes) {
-      const float v = __fmul_rn(a, u);
-      const uint32_t b = act_step(__reduce_max_sync(FULL, __float_as_uint(fabsf(v))));
-      ocodes[i * 32 + lane] = (int8_t)act_code(v, act_inverse(b));
-      if (lane == 0) osteps[i] = (uint8_t)b;
+      const uint32_t b = chunk_step(a);
+      const uint2 q = chunk_codes(a, b);
+      if (at[i].r < w.rows) store_codes(ocodes, osteps, groups, at[i].r, at[i].c8, q, b);
     }
   }
 }
 
-static unsigned groups_grid(int64_t total) {
-  const int64_t blocks = (total + 7) / 8;
-  return (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
+static Walk make_walk(int64_t rows, int64_t cols) {
+  Walk w;
+  w.rows = rows, w.c8s = (int32_t)(act_ldc(cols) / CHUNK);
+  w.dr = 256 / w.c8s, w.dc = 256 % w.c8s;
+  return w;
+}
+// CTAs for `unroll` chunks per thread; 0 if a grid cannot hold them.
+static unsigned walk_grid(const Walk& w, int unroll) {
+  const int64_t blocks = (w.rows * w.c8s + 256 * unroll - 1) / (256 * unroll);
+  return blocks <= INT64_C(2147483647) ? (unsigned)blocks : 0u;
 }
 
 }  // namespace gc
@@ -126,10 +219,13 @@ extern "C" gc_status gc_act_compress(const void* x, int64_t ld, int32_t dtype, i
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_matrix(x, ld, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK) return st;
-  const int64_t groups = act_ldc(cols) / 32;
-  GC_BY_DTYPE(dtype, T, launch_chained(k_act_compress<T>, groups_grid(rows * groups), 256, 0,
-                                       static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, rows, cols,
-                                       groups, codes, steps));
+  const Walk w = make_walk(rows, cols);
+  const unsigned grid = walk_grid(w, UNROLL);
+  if (!grid) return GC_ERR_LAYOUT;
+  const bool vec = chunk_aligned(x, ld, dtype);
+  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_compress<T, true> : k_act_compress<T, false>, grid, 256, 0,
+                                       static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, cols, w, codes,
+                                       steps));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -140,10 +236,13 @@ extern "C" gc_status gc_act_decompress(const int8_t* codes, const uint8_t* steps
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_codes(codes, steps)) != GC_OK || (st = check_matrix(out, ldo, cols, dtype)) != GC_OK) return st;
-  const int64_t groups = act_ldc(cols) / 32;
-  GC_BY_DTYPE(dtype, T, launch_chained(k_act_decompress<T>, groups_grid(rows * groups), 256, 0,
-                                       static_cast<cudaStream_t>(stream), codes, steps, rows, cols, groups,
-                                       static_cast<T*>(out), ldo));
+  const Walk w = make_walk(rows, cols);
+  const unsigned grid = walk_grid(w, UNROLL);
+  if (!grid) return GC_ERR_LAYOUT;
+  const bool vec = chunk_aligned(out, ldo, dtype);
+  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_decompress<T, true> : k_act_decompress<T, false>, grid, 256, 0,
+                                       static_cast<cudaStream_t>(stream), codes, steps, cols, w, static_cast<T*>(out),
+                                       ldo));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -162,11 +261,17 @@ extern "C" gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, c
   if (gate_codes || gate_steps || up_codes || up_steps)
     if ((st = check_codes(gate_codes, gate_steps)) != GC_OK || (st = check_codes(up_codes, up_steps)) != GC_OK)
       return st;
-  const int64_t groups = act_ldc(cols) / 32;
-  GC_BY_DTYPE(dtype, T, launch_chained(kind == GC_GATE_SILU ? k_gated<T, GC_GATE_SILU> : k_gated<T, GC_GATE_GELU_TANH>,
-                                       groups_grid(rows * groups), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
-                                       static_cast<const T*>(up), ldu, rows, cols, groups, static_cast<T*>(out), ldo,
-                                       gate_codes, gate_steps, up_codes, up_steps));
+  const Walk w = make_walk(rows, cols);
+  const unsigned grid = walk_grid(w, GATED_UNROLL);
+  if (!grid) return GC_ERR_LAYOUT;
+  const bool vec = chunk_aligned(gate, ldg, dtype) && chunk_aligned(up, ldu, dtype) && chunk_aligned(out, ldo, dtype);
+  GC_BY_DTYPE(dtype, T, {
+    auto kern = kind == GC_GATE_SILU ? (vec ? k_gated<T, GC_GATE_SILU, true> : k_gated<T, GC_GATE_SILU, false>)
+                                     : (vec ? k_gated<T, GC_GATE_GELU_TANH, true> : k_gated<T, GC_GATE_GELU_TANH, false>);
+    launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
+                   static_cast<const T*>(up), ldu, cols, w, static_cast<T*>(out), ldo, gate_codes, gate_steps, up_codes,
+                   up_steps);
+  });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -186,12 +291,17 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
     return st;
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
-  const int64_t groups = act_ldc(cols) / 32;
-  GC_BY_DTYPE(dtype, T, launch_chained(kind == GC_GATE_SILU ? k_gated_backward<T, GC_GATE_SILU>
-                                                            : k_gated_backward<T, GC_GATE_GELU_TANH>,
-                                       groups_grid(rows * groups), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo,
-                                       gate_codes, gate_steps, up_codes, up_steps, rows, cols, groups,
-                                       static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu, out_codes,
-                                       out_steps));
+  const Walk w = make_walk(rows, cols);
+  const unsigned grid = walk_grid(w, GATED_UNROLL);
+  if (!grid) return GC_ERR_LAYOUT;
+  const bool vec = chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype);
+  GC_BY_DTYPE(dtype, T, {
+    auto kern = kind == GC_GATE_SILU
+                    ? (vec ? k_gated_backward<T, GC_GATE_SILU, true> : k_gated_backward<T, GC_GATE_SILU, false>)
+                    : (vec ? k_gated_backward<T, GC_GATE_GELU_TANH, true> : k_gated_backward<T, GC_GATE_GELU_TANH, false>);
+    launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
+                   gate_steps, up_codes, up_steps, cols, w, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
+                   out_codes, out_steps);
+  });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }

@@ -54,6 +54,164 @@ __device__ __forceinline__ int act_code(float x, float inverse) {
   return inverse == 0.0f ? 0 : __float2int_rn(v);
 }
 
+// ---------------------------------------------------------------- chunks
+// The streaming kernels give a lane 8 consecutive columns (16 bytes of a
+// 16-bit type, 8 bytes of codes), four lanes a group of 32; a group's lanes
+// are always four of one warp, from a multiple of four on.
+constexpr int CHUNK = 8;
+
+// 8 elements as they are in memory.
+template <typename T>
+struct alignas(16) Raw8 {
+  T e[CHUNK];
+};
+
+// `n` of the 8 elements from p on, zeros after them.  VEC: p is 16-byte
+// aligned.  Read past L1, which keeps what is used again.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> load_chunk(const T* p, int n) {
+  Raw8<T> r;
+  if (VEC && n == CHUNK) {
+    uint4* w = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(r) / 16; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(reinterpret_cast<const uint4*>(p) + i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) r.e[i] = i < n ? p[i] : from_f32<T>(0.0f);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[CHUNK]) {
+#pragma unroll
+  for (int i = 0; i < CHUNK; ++i) v[i] = to_f32(r.e[i]);
+}
+
+// Writes n of the 8 values.  Without VEC a warp's chunks go through `buf`
+// (256 floats of its own): stores of one element per lane at 8 elements'
+// distance would be eight times the sectors.  All lanes of the warp take part.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[CHUNK], float* buf) {
+  if (VEC) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) r.e[i] = from_f32<T>(v[i]);
+    if (n == CHUNK) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(r) / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&r)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < CHUNK; ++i)
+        if (i < n) p[i] = r.e[i];
+    }
+  } else {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    reinterpret_cast<float4*>(buf)[2 * lane] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(buf)[2 * lane + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) {
+      const int from = 4 * j + (lane >> 3);
+      T* q = reinterpret_cast<T*>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(p), from));
+      if ((lane & 7) < __shfl_sync(FULL, n, from)) q[lane & 7] = from_f32<T>(buf[32 * j + lane]);
+    }
+  }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The step byte of the group that this lane's 8 values belong to.
+__device__ __forceinline__ uint32_t chunk_step(const float (&v)[CHUNK]) {
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < CHUNK; ++i) top = max_nan(top, fabsf(v[i]));
+  top = max_nan(top, __shfl_xor_sync(FULL, top, 1));
+  top = max_nan(top, __shfl_xor_sync(FULL, top, 2));
+  return act_step(__float_as_uint(top));
+}
+// The 8 codes under step b.  Adding 1.5 * 2^23 rounds to an integer in the low
+// bits.  Only the largest finite step (b = 248) can meet magnitudes that round
+// past 127.
+__device__ __forceinline__ uint2 chunk_codes(const float (&v)[CHUNK], uint32_t b) {
+  const float inverse = act_inverse(b);
+  uint32_t w[CHUNK];
+#pragma unroll
+  for (int i = 0; i < CHUNK; ++i) {
+    float x = v[i];
+    if (b >= 248u) x = fminf(fmaxf(x, -127.0f * 0x1p121f), 127.0f * 0x1p121f);
+    w[i] = __float_as_uint(__fmaf_rn(x, inverse, 12582912.0f));
+  }
+  uint2 c;
+  c.x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  c.y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
+  return b == 255u ? make_uint2(0u, 0u) : c;
+}
+// The values of 8 codes: code + 128 in the low byte of 2^23's significand.
+__device__ __forceinline__ void chunk_values(uint2 c, uint32_t b, float (&v)[CHUNK]) {
+  const float scale = act_scale(b);
+  const uint32_t x = c.x ^ 0x80808080u, y = c.y ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440 + i)), 8388736.0f), scale);
+    v[4 + i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(y, 0x4B000000u, 0x7440 + i)), 8388736.0f), scale);
+  }
+}
+
+// A checkpoint's codes and step of chunk c8 of row r; groups = ldc / 32.
+__device__ __forceinline__ uint2 load_codes(const int8_t* codes, int64_t groups, int64_t r, int c8) {
+  uint2 c;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(c.x), "=r"(c.y)
+               : "l"(codes + r * groups * ACT_GROUP + (int64_t)c8 * CHUNK)
+               : "memory");
+  return c;
+}
+__device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* steps, int64_t groups, int64_t r, int c8, uint2 c,
+                                            uint32_t b) {
+  *reinterpret_cast<uint2*>(codes + r * groups * ACT_GROUP + (int64_t)c8 * CHUNK) = c;
+  if ((c8 & 3) == 0) steps[r * groups + (c8 >> 2)] = (uint8_t)b;
+}
+
+// A thread's chunks of a matrix: chunk tid + 256 i of its CTA's share.
+struct Walk {
+  int64_t rows;
+  int32_t c8s, dr, dc;  // chunks per row; 256 chunks on: rows and chunks
+};
+struct Chunk {
+  int64_t r;
+  int c8;
+};
+__device__ __forceinline__ Chunk first_chunk(const Walk& w, int64_t id) {
+  Chunk k;
+  if (id < (int64_t(1) << 32)) {
+    k.r = (uint32_t)id / (uint32_t)w.c8s;
+  } else {
+    k.r = id / w.c8s;
+  }
+  k.c8 = (int)(id - k.r * w.c8s);
+  return k;
+}
+__device__ __forceinline__ void next_chunk(const Walk& w, Chunk& k) {
+  k.r += w.dr;
+  k.c8 += w.dc;
+  if (k.c8 >= w.c8s) k.c8 -= w.c8s, ++k.r;
+}
+// Elements of the chunk inside a row of `cols` (0 past the last row).
+__device__ __forceinline__ int chunk_len(const Walk& w, const Chunk& k, int64_t cols) {
+  const int64_t left = cols - (int64_t)k.c8 * CHUNK;
+  return k.r < w.rows ? (int)(left < CHUNK ? (left < 0 ? 0 : left) : CHUNK) : 0;
+}
+
 }  // namespace gc
 
 // Runs a statement with T the element type of a valid dtype.

@@ -4,8 +4,243 @@
 
 namespace gc {
 
+// A row is held in registers by W warps, N chunks of 8 columns per lane (chunk
+// (j W + w) 32 + lane), so that it is read once; a CTA of 8 warps (16 for the
+// widest rows) works on 8 / W rows at a time and walks over the rows.  Rows
+// wider than 16384 are read twice (the _wide kernels).
 constexpr int NTHREADS = 256;
+constexpr int64_t NORM_WIDEST = 16384;
 
+struct RowShape {
+  int warps;    // W
+  int threads;  // of a CTA
+};
+
+// The sum over a row's warps of each thread's v, the same bits in all of its
+// threads.  `red` holds 2 x 16 floats and is used alternately: one barrier.
+__device__ __forceinline__ float row_sum(float v, int W, float (&red)[2][16], int& turn) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
+  if (W == 1) return v;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
+  __syncthreads();
+  const int first = warp & ~(W - 1);
+  float s = red[turn][first];
+  for (int i = 1; i < W; ++i) s = __fadd_rn(s, red[turn][first + i]);
+  turn ^= 1;
+  return s;
+}
+
+__device__ __forceinline__ float rms_inverse(float ss, int64_t cols, float eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)cols), eps)));
+}
+
+// 8 weights from column c on (n of them; ones without weights).
+__device__ __forceinline__ void load_weights(const void* weight, int wtype, int64_t c, int n, bool vec, float (&w)[CHUNK]) {
+  if (!weight) {
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) w[i] = 1.0f;
+  } else if (vec && n == CHUNK) {
+    if (wtype == GC_F32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(weight) + c));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(weight) + c) + 1);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(weight) + c));
+      if (wtype == GC_BF16)
+        unpack(*reinterpret_cast<const Raw8<__nv_bfloat16>*>(&a), w);
+      else
+        unpack(*reinterpret_cast<const Raw8<__half>*>(&a), w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) w[i] = i < n ? load_as_f32(weight, wtype, c + i) : 0.0f;
+  }
+}
+
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 4 : 1)
+    k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, bool wvec, float eps,
+              int64_t rows, int64_t cols, int64_t groups, RowShape shape, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd,
+              int8_t* codes, uint8_t* steps) {
+  __shared__ float red[2][16];
+  extern __shared__ float4 stage[];  // without VEC: 256 floats per warp
+  chain_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = shape.warps;
+  const int per = (int)blockDim.x / 32 / W, sub = warp / W;  // rows at a time, this warp's among them
+  float* const buf = reinterpret_cast<float*>(stage) + warp * 256;
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
+    const int64_t r = base + sub;
+    float v[N][CHUNK];
+    float ss = 0.0f;
+    {
+      Raw8<T> a[N], b[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int64_t c = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
+        const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - c)) : 0;
+        a[j] = load_chunk<T, VEC>(x + r * ldx + c, n);
+        if (res) b[j] = load_chunk<T, VEC>(res + r * ldr + c, n);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        unpack(a[j], v[j]);
+        if (res) {
+          float t[CHUNK];
+          unpack(b[j], t);
+#pragma unroll
+          for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
+      }
+    }
+    const float rs = rms_inverse(row_sum(ss, W, red, turn), cols, eps);
+    if (rstd && r < rows && warp % W == 0 && lane == 0) rstd[r] = rs;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c8 = (j * W + warp % W) * 32 + lane;
+      const int64_t c = (int64_t)c8 * CHUNK;
+      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - c)) : 0;
+      if (h) store_chunk<T, VEC>(h + r * ldh + c, n, v[j], buf);
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) v[j][e] = __fmul_rn(v[j][e], rs);
+      if (codes) {
+        // past the row's end the values are 0 * rstd, which a rstd that is
+        // not finite would turn into NaN
+        if (n < CHUNK)
+#pragma unroll
+          for (int e = 0; e < CHUNK; ++e)
+            if (e >= n) v[j][e] = 0.0f;
+        const uint32_t b = chunk_step(v[j]);
+        const uint2 q = chunk_codes(v[j], b);
+        if (r < rows && c8 < 4 * groups) store_codes(codes, steps, groups, r, c8, q, b);
+      }
+      if (y) {
+        float w[CHUNK];
+        load_weights(weight, wtype, c, n, wvec, w);
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) w[e] = __fmul_rn(v[j][e], w[e]);
+        store_chunk<T, VEC>(y + r * ldy + c, n, w, buf);
+      }
+    }
+  }
+}
+
+// Gradient: gw = dy * weight, dx = rstd (gw - q mean(gw q)) + dh, and each
+// thread's share of dw = sum dy q of its columns over the rows that its CTA
+// walks over, one partial sum per CTA and row at a time.
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
+    k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
+                       const float* rstd, const void* weight, int wtype, bool wvec, int64_t rows, int64_t cols,
+                       int64_t groups, RowShape shape, T* dx, int64_t lddx, float* part) {
+  __shared__ float red[2][16];
+  extern __shared__ float4 stage[];
+  chain_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = shape.warps;
+  const int per = (int)blockDim.x / 32 / W, sub = warp / W;
+  float* const buf = reinterpret_cast<float*>(stage) + warp * 256;
+  int turn = 0;
+  float dw[N][CHUNK];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < CHUNK; ++e) dw[j][e] = 0.0f;
+  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
+    const int64_t r = base + sub;
+    Raw8<T> d[N], up[N];
+    uint2 c[N];
+    uint32_t b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c8 = (j * W + warp % W) * 32 + lane;
+      const int64_t col = (int64_t)c8 * CHUNK;
+      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - col)) : 0;
+      d[j] = load_chunk<T, VEC>(dy + r * lddy + col, n);
+      if (dh) up[j] = load_chunk<T, VEC>(dh + r * lddh + col, n);
+      c[j] = make_uint2(0u, 0u), b[j] = 1u;
+      if (r < rows && c8 < 4 * groups) c[j] = load_codes(codes, groups, r, c8), b[j] = steps[r * groups + (c8 >> 2)];
+    }
+    const float rs = r < rows ? rstd[r] : 0.0f;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
+      const int n = (int)max((int64_t)0, min((int64_t)CHUNK, cols - col));
+      float q[CHUNK], w[CHUNK], t[CHUNK];
+      // past the row's end dy is 0 and so are the codes, but a NaN's step
+      // would make them NaN
+      if (n <= 0) b[j] = 1u;
+      chunk_values(c[j], b[j], q);
+      load_weights(weight, wtype, col, n, wvec, w);
+      unpack(d[j], t);
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) {
+        if (n < CHUNK && e >= n) q[e] = 0.0f;
+        dw[j][e] = __fmaf_rn(t[e], q[e], dw[j][e]);
+        s = __fmaf_rn(__fmul_rn(t[e], w[e]), q[e], s);
+      }
+    }
+    const float mean = __fdiv_rn(row_sum(s, W, red, turn), (float)cols);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
+      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - col)) : 0;
+      float q[CHUNK], w[CHUNK], t[CHUNK], v[CHUNK];
+      chunk_values(c[j], b[j], q);
+      load_weights(weight, wtype, col, n, wvec, w);
+      unpack(d[j], v);
+      if (dh) unpack(up[j], t);
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) {
+        v[e] = __fmul_rn(rs, __fmaf_rn(-q[e], mean, __fmul_rn(v[e], w[e])));
+        if (dh) v[e] = __fadd_rn(v[e], t[e]);
+      }
+      store_chunk<T, VEC>(dx + r * lddx + col, n, v, buf);
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
+    float* o = part + ((int64_t)blockIdx.x * per + sub) * groups * ACT_GROUP + col;  // rows of ldc floats
+    if (col < groups * ACT_GROUP) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    }
+  }
+}
+
+// dw[c] = (dw[c] +) the partial sums in a fixed order: 32 columns per CTA,
+// eight warps each over every eighth of them.
+__global__ void __launch_bounds__(NTHREADS) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, int64_t ldp,
+                                                              float* dw, int accumulate) {
+  __shared__ float sum[8][32];
+  chain_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < cols) {
+    int p = warp;
+    for (; p + 24 < parts; p += 32) {  // four loads at a time
+      const float a = part[p * ldp + c], b = part[(p + 8) * ldp + c], d = part[(p + 16) * ldp + c], e = part[(p + 24) * ldp + c];
+      s = __fadd_rn(s, __fadd_rn(__fadd_rn(a, b), __fadd_rn(d, e)));
+    }
+    for (; p < parts; p += 8) s = __fadd_rn(s, part[p * ldp + c]);
+  }
+  sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s = __fadd_rn(s, sum[i][lane]);
+    dw[c] = accumulate ? __fadd_rn(dw[c], s) : s;
+  }
+}
+
+// ---------------------------------------------------------------- wide rows
 // The sum over the CTA, the same bits in every thread.
 __device__ __forceinline__ float cta_sum(float v, float* red) {
   for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
@@ -20,9 +255,9 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 // One CTA per row: the sum of squares, then the outputs, a warp per group.
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS)
-    k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps,
-              int64_t rows, int64_t cols, int64_t groups, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd,
-              int8_t* codes, uint8_t* steps) {
+    k_rmsnorm_wide(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps,
+                   int64_t rows, int64_t cols, int64_t groups, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd,
+                   int8_t* codes, uint8_t* steps) {
   __shared__ float red[NTHREADS / 32];
   chain_wait();
   const int lane = threadIdx.x & 31;
@@ -36,8 +271,7 @@ __global__ void __launch_bounds__(NTHREADS)
       const float v = sum_at(c);
       ss = __fmaf_rn(v, v, ss);
     }
-    ss = cta_sum(ss, red);
-    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)cols), eps)));
+    const float rs = rms_inverse(cta_sum(ss, red), cols, eps);
     if (rstd && threadIdx.x == 0) rstd[r] = rs;
     for (int64_t g = threadIdx.x >> 5; g < groups; g += NTHREADS / 32) {
       const int64_t c = g * 32 + lane;
@@ -58,9 +292,9 @@ __global__ void __launch_bounds__(NTHREADS)
 
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS)
-    k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
-                       const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
-                       T* dx, int64_t lddx) {
+    k_rmsnorm_backward_wide(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes,
+                            const uint8_t* steps, const float* rstd, const void* weight, int wtype, int64_t rows,
+                            int64_t cols, int64_t groups, T* dx, int64_t lddx) {
   __shared__ float red[NTHREADS / 32];
   chain_wait();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -90,8 +324,8 @@ __global__ void __launch_bounds__(NTHREADS)
 // dw[c] over rows [p * span, (p + 1) * span) of part p: a thread per column.
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS)
-    k_rmsnorm_dw(const T* dy, int64_t lddy, const int8_t* codes, const uint8_t* steps, int64_t rows, int64_t cols,
-                 int64_t groups, int64_t span, float* part) {
+    k_rmsnorm_dw_wide(const T* dy, int64_t lddy, const int8_t* codes, const uint8_t* steps, int64_t rows, int64_t cols,
+                      int64_t groups, int64_t span, float* part) {
   chain_wait();
   const int64_t c = (int64_t)blockIdx.x * NTHREADS + threadIdx.x;
   if (c >= cols) return;
@@ -100,20 +334,34 @@ __global__ void __launch_bounds__(NTHREADS)
   for (int64_t r = r0; r < r1; ++r)
     s = __fmaf_rn(to_f32(dy[r * lddy + c]),
                   __fmul_rn((float)codes[r * groups * 32 + c], act_scale(steps[r * groups + c / 32])), s);
-  part[blockIdx.y * cols + c] = s;
+  part[blockIdx.y * groups * 32 + c] = s;
 }
 
-__global__ void __launch_bounds__(NTHREADS) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, float* dw,
-                                                              int accumulate) {
-  chain_wait();
-  const int64_t c = (int64_t)blockIdx.x * NTHREADS + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s = __fadd_rn(s, part[p * cols + c]);
-  dw[c] = accumulate ? __fadd_rn(dw[c], s) : s;
-}
+// ---------------------------------------------------------------- shapes
+constexpr int NORM_SMS = 152;  // of a GB300
 
-static int dw_parts(int64_t rows) { return (int)(rows < 64 ? (rows < 1 ? 1 : rows) : 64); }
+// Warps per row for two chunks per lane, four beyond 4096 columns.
+static int norm_chunks(int64_t cols) { return cols <= 4096 ? 2 : 4; }
+static RowShape norm_shape(int64_t cols) {
+  RowShape s;
+  s.warps = 1;
+  while ((int64_t)s.warps * norm_chunks(cols) * 256 < cols) s.warps *= 2;
+  s.threads = s.warps == 16 ? 512 : 256;
+  return s;
+}
+// CTAs: one per set of rows, at most `per_sm` per SM.
+static int norm_grid(int64_t rows, const RowShape& s, int per_sm) {
+  const int per = s.threads / 32 / s.warps;
+  const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * per_sm * 256 / s.threads;
+  return (int)(ctas < most ? ctas : most);
+}
+constexpr int FORWARD_PER_SM = 4, BACKWARD_PER_SM = 3;  // CTAs of 256 threads
+static int dw_parts(int64_t rows, int64_t cols) {
+  if (rows < 1) return 1;
+  if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
+  const RowShape s = norm_shape(cols);
+  return norm_grid(rows, s, BACKWARD_PER_SM) * (s.threads / 32 / s.warps);
+}
 
 }  // namespace gc
 
@@ -135,11 +383,24 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
       ((codes || steps) && (st = check_codes(codes, steps)) != GC_OK))
     return st;
   const int64_t groups = act_ldc(cols) / 32;
-  const unsigned grid = (unsigned)(rows < 152 * 64 ? rows : 152 * 64);
-  GC_BY_DTYPE(dtype, T, launch_chained(k_rmsnorm<T>, grid, NTHREADS, 0, static_cast<cudaStream_t>(stream),
-                                       static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight,
-                                       weight_dtype, eps, rows, cols, groups, static_cast<T*>(y), ldy,
-                                       static_cast<T*>(h), ldh, rstd, codes, steps));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cols > NORM_WIDEST) {
+    const unsigned grid = (unsigned)(rows < 152 * 64 ? rows : 152 * 64);
+    GC_BY_DTYPE(dtype, T, launch_chained(k_rmsnorm_wide<T>, grid, NTHREADS, 0, s, static_cast<const T*>(x), ldx,
+                                         static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows, cols,
+                                         groups, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps));
+    return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+  }
+  const RowShape shape = norm_shape(cols);
+  const bool vec = chunk_aligned(x, ldx, dtype) && (!residual || chunk_aligned(residual, ldr, dtype)) &&
+                   (!y || chunk_aligned(y, ldy, dtype)) && (!h || chunk_aligned(h, ldh, dtype));
+  const bool wvec = aligned16(weight), two = norm_chunks(cols) == 2;
+  GC_BY_DTYPE(dtype, T, {
+    auto kern = two ? (vec ? k_rmsnorm<T, 2, true> : k_rmsnorm<T, 2, false>) : (vec ? k_rmsnorm<T, 4, true> : k_rmsnorm<T, 4, false>);
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, vec ? 0 : shape.threads * 32, s,
+                   static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, wvec, eps,
+                   rows, cols, groups, shape, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
+  });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -147,7 +408,7 @@ extern "C" gc_status gc_rmsnorm_backward_workspace_size(int64_t rows, int64_t co
   const gc_status st = validate_matrix(rows, cols, GC_F32);
   if (st != GC_OK) return st;
   if (!bytes) return GC_ERR_INVALID_ARG;
-  *bytes = (size_t)dw_parts(rows) * (size_t)cols * sizeof(float);
+  *bytes = (size_t)dw_parts(rows, cols) * (size_t)act_ldc(cols) * sizeof(float);
   return GC_OK;
 }
 
@@ -167,28 +428,45 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
     if ((uintptr_t)dw & 3u) return GC_ERR_ALIGNMENT;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned cgrid = (unsigned)((cols + NTHREADS - 1) / NTHREADS);
+  const int64_t groups = act_ldc(cols) / 32;
   const int acc = (flags & GC_ACCUMULATE) ? 1 : 0;
+  float* part = dw ? static_cast<float*>(workspace) : nullptr;
+  auto join = [&](int parts) {
+    launch_chained(k_rmsnorm_dw_join, (unsigned)groups, NTHREADS, 0, s, (const float*)part, parts, cols, groups * 32, dw, acc);
+  };
   if (rows == 0) {
-    if (dw && !acc) launch_chained(k_rmsnorm_dw_join, cgrid, NTHREADS, 0, s, (const float*)nullptr, 0, cols, dw, 0);
+    if (dw && !acc) join(0);
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
   if ((st = check_matrix(dy, lddy, cols, dtype)) != GC_OK || (dh && (st = check_matrix(dh, lddh, cols, dtype)) != GC_OK) ||
       (st = check_matrix(dx, lddx, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK)
     return st;
   if (!rstd) return GC_ERR_INVALID_ARG;
-  const int64_t groups = act_ldc(cols) / 32;
-  const unsigned grid = (unsigned)(rows < 152 * 64 ? rows : 152 * 64);
-  if (dw) {  // before dx, which may overwrite dy
-    float* part = static_cast<float*>(workspace);
-    const int parts = dw_parts(rows);
-    GC_BY_DTYPE(dtype, T, launch_chained(k_rmsnorm_dw<T>, dim3(cgrid, parts), NTHREADS, 0, s,
-                                         static_cast<const T*>(dy), lddy, codes, steps, rows, cols, groups,
-                                         (rows + parts - 1) / parts, part));
-    launch_chained(k_rmsnorm_dw_join, cgrid, NTHREADS, 0, s, (const float*)part, parts, cols, dw, acc);
+  const int parts = dw_parts(rows, cols);
+  if (cols > NORM_WIDEST) {
+    const unsigned grid = (unsigned)(rows < 152 * 64 ? rows : 152 * 64);
+    GC_BY_DTYPE(dtype, T, {
+      if (dw) {  // before dx, which may overwrite dy
+        launch_chained(k_rmsnorm_dw_wide<T>, dim3((unsigned)((cols + NTHREADS - 1) / NTHREADS), parts), NTHREADS, 0, s,
+                       static_cast<const T*>(dy), lddy, codes, steps, rows, cols, groups, (rows + parts - 1) / parts, part);
+        join(parts);
+      }
+      launch_chained(k_rmsnorm_backward_wide<T>, grid, NTHREADS, 0, s, static_cast<const T*>(dy), lddy,
+                     static_cast<const T*>(dh), lddh, codes, steps, rstd, weight, weight_dtype, rows, cols, groups,
+                     static_cast<T*>(dx), lddx);
+    });
+    return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
-  GC_BY_DTYPE(dtype, T, launch_chained(k_rmsnorm_backward<T>, grid, NTHREADS, 0, s, static_cast<const T*>(dy), lddy,
-                                       static_cast<const T*>(dh), lddh, codes, steps, rstd, weight, weight_dtype, rows,
-                                       cols, groups, static_cast<T*>(dx), lddx));
+  const RowShape shape = norm_shape(cols);
+  const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
+  const bool wvec = aligned16(weight), two = norm_chunks(cols) == 2;
+  GC_BY_DTYPE(dtype, T, {
+    auto kern = two ? (vec ? k_rmsnorm_backward<T, 2, true> : k_rmsnorm_backward<T, 2, false>)
+                    : (vec ? k_rmsnorm_backward<T, 4, true> : k_rmsnorm_backward<T, 4, false>);
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, vec ? 0 : shape.threads * 32, s,
+                   static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
+                   weight_dtype, wvec, rows, cols, groups, shape, static_cast<T*>(dx), lddx, part);
+  });
+  if (dw) join(parts);
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
