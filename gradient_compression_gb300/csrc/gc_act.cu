@@ -4,53 +4,94 @@
 
 namespace gc {
 
-constexpr int UNROLL = 4;  // chunks of a thread: their loads are issued before any is used
-
+// The loops keep AHEAD rows' loads in flight while they work on one: with
+// rows on 16-byte boundaries (VEC) through rings in shared memory.  Four CTAs
+// per SM with 128 bytes per thread in flight are 128 KB; the two dies'
+// memories are 1.5 us away under load, and 6.7 TB/s is 44 KB per SM and us.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_act_compress(const T* x, int64_t ld, int64_t cols, Walk w, int8_t* codes,
-                                                      uint8_t* steps) {
+__global__ void __launch_bounds__(256, 4) k_act_compress(const T* x, int64_t ld, Tiling t, int8_t* codes, uint8_t* steps) {
+  constexpr int AHEAD = 8 / (int)(sizeof(T) / 2);
+  __shared__ float4 shared[VEC ? Ring<T>::bytes(AHEAD, 256) / 16 : 1];
   chain_wait();
-  const int64_t groups = w.c8s / 4;
-  Chunk at[UNROLL];
-  Raw8<T> raw[UNROLL];
-  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * UNROLL) + threadIdx.x);
+  const Place p = place(t);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
+  const T* px = x + p.r * ld + (int64_t)p.c8 * CHUNK;  // the next row to load
+  int8_t* pc = codes + p.r * ldc + (int64_t)p.c8 * CHUNK;
+  uint8_t* ps = steps + p.r * groups + (p.c8 >> 2);
+  const int64_t dx = p.step * ld, dc = p.step * ldc, ds = p.step * groups;
+  const Ring<T> ring(shared, 256);
+  int64_t r = p.r, next = p.r;
+  auto copy = [&](int slot) {
+    if (VEC) {
+      if (next < p.end && p.n > 0) ring.copy(slot, px, p.n);
+      copy_group();
+      px += dx, next += p.step;
+    }
+  };
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
-    raw[i] = load_chunk<T, VEC>(x + at[i].r * ld + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols));
-  }
-#pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
+  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
+  int slot = 0;
+  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step, pc += dc, ps += ds) {
+    const int n = r < p.end ? p.n : 0;
+    Raw8<T> raw;
+    if (VEC) {
+      wait_groups<AHEAD - 2>();
+      raw = ring.take(slot);
+      copy((slot + AHEAD - 1) % AHEAD);
+      slot = (slot + 1) % AHEAD;
+    } else {
+      raw = load_chunk<T, false>(px, n);
+      px += dx;
+    }
     float v[CHUNK];
-    unpack(raw[i], v);
+    unpack(raw, v);
+    if (n == 0) {  // nothing was copied
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) v[e] = 0.0f;
+    }
     const uint32_t b = chunk_step(v);
     const uint2 c = chunk_codes(v, b);
-    if (at[i].r < w.rows) store_codes(codes, steps, groups, at[i].r, at[i].c8, c, b);
+    if (p.in && r < p.end) {
+      *reinterpret_cast<uint2*>(pc) = c;
+      if ((p.c8 & 3) == 0) *ps = (uint8_t)b;
+    }
   }
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_act_decompress(const int8_t* codes, const uint8_t* steps, int64_t cols, Walk w,
-                                                        T* out, int64_t ld) {
+template <typename T, bool VEC, int ROWS>
+__global__ void __launch_bounds__(256, VEC ? 4 : 3) k_act_decompress(const int8_t* codes, const uint8_t* steps, Tiling t, T* out, int64_t ld) {
   __shared__ float4 stage[VEC ? 1 : 512];
+  float* const buf = reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256;
   chain_wait();
-  const int64_t groups = w.c8s / 4;
-  Chunk at[UNROLL];
-  uint2 c[UNROLL];
-  uint32_t b[UNROLL];
-  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * UNROLL) + threadIdx.x);
+  const Place p = place(t);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
+  const int8_t* pc = codes + p.r * ldc + (int64_t)p.c8 * CHUNK;
+  const uint8_t* ps = steps + p.r * groups + (p.c8 >> 2);
+  T* po = out + p.r * ld + (int64_t)p.c8 * CHUNK;
+  const int64_t dx = p.step * ld, dc = p.step * ldc, ds = p.step * groups;
+  uint2 c[ROWS];
+  uint32_t b[ROWS];
+  auto fetch = [&](int64_t r) {
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
-    c[i] = make_uint2(0u, 0u), b[i] = 1u;
-    if (at[i].r < w.rows) c[i] = load_codes(codes, groups, at[i].r, at[i].c8), b[i] = steps[at[i].r * groups + (at[i].c8 >> 2)];
-  }
+    for (int i = 0; i < ROWS; ++i, r += p.step, pc += dc, ps += ds) {
+      c[i] = make_uint2(0u, 0u), b[i] = 1u;
+      if (p.in && r < p.end) c[i] = load_codes(pc), b[i] = __ldg(ps);
+    }
+  };
+  int64_t r = p.r, lead = (int64_t)blockIdx.y * t.slab;
+  fetch(r);
+  for (; lead < p.end; lead += ROWS * p.step) {
+    uint2 cn[ROWS];
+    uint32_t bn[ROWS];
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    float v[CHUNK];
-    chunk_values(c[i], b[i], v);
-    store_chunk<T, VEC>(out + at[i].r * ld + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols), v,
-                        reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256);
+    for (int i = 0; i < ROWS; ++i) cn[i] = c[i], bn[i] = b[i];
+    if (lead + ROWS * p.step < p.end) fetch(r + ROWS * p.step);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i, r += p.step, po += dx) {
+      float v[CHUNK];
+      chunk_values(cn[i], bn[i], v);
+      store_chunk<T, VEC>(po, r < p.end ? p.n : 0, v, buf);
+    }
   }
 }
 
@@ -80,6 +121,14 @@ __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
     low = __fmaf_rn(CA * __fmaf_rn(t, t, -t2), t, __fmaf_rn(w, t, -p));
     *dp = __fmaf_rn(2.0f * CA, t2, w);
   }
+  if (KIND == GC_GATE_SILU && !PRECISE) {
+    // far out on the left the exponential is infinite and the sigmoid 0,
+    // where it would be below 2^-126
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
+    return s;
+  }
   const bool far = p < -80.0f;
   const float z = far ? p : -p;
   float e;
@@ -94,119 +143,183 @@ __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
   if (PRECISE) {
     s = __fdiv_rn(1.0f, one);
   } else {
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(one));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(one));
   }
   return far ? e : s;
 }
 
-// The loads of one chunk are issued together; two chunks per thread leave 32
-// warps per SM and put 128 bytes per thread in flight.
-constexpr int GATED_UNROLL = 2;
-
 template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(256)
-    k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, int64_t cols, Walk w, T* out, int64_t ldo, int8_t* gcodes,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
+    k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, Tiling t, T* out, int64_t ldo, int8_t* gcodes,
             uint8_t* gsteps, int8_t* ucodes, uint8_t* usteps) {
-  __shared__ float4 stage[VEC ? 1 : 512];
+  constexpr int AHEAD = 4 / (int)(sizeof(T) / 2);
+  // the ring, or the warps' staging
+  __shared__ float4 shared[VEC ? Ring<T>::bytes(2 * AHEAD, 256) / 16 : 512];
+  float* const buf = reinterpret_cast<float*>(shared) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
   chain_wait();
-  const int64_t groups = w.c8s / 4;
-  Chunk at[GATED_UNROLL];
-  Raw8<T> rg[GATED_UNROLL], ru[GATED_UNROLL];
-  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * GATED_UNROLL) + threadIdx.x);
+  const Place p = place(t);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4, col = (int64_t)p.c8 * CHUNK;
+  const T *pg = gate + p.r * ldg + col, *pu = up + p.r * ldu + col;  // the next row to load
+  T* po = out + p.r * ldo + col;
+  int64_t ac = p.r * ldc + col, as = p.r * groups + (p.c8 >> 2);  // offsets of codes and steps
+  const int64_t dg = p.step * ldg, du = p.step * ldu, dd = p.step * ldo, dc = p.step * ldc, ds = p.step * groups;
+  const Ring<T> ring(shared, 256);
+  int64_t r = p.r, next = p.r;
+  auto copy = [&](int slot) {
+    if (VEC) {
+      if (next < p.end && p.n > 0) ring.copy(2 * slot, pg, p.n), ring.copy(2 * slot + 1, pu, p.n);
+      copy_group();
+      pg += dg, pu += du, next += p.step;
+    }
+  };
 #pragma unroll
-  for (int i = 0; i < GATED_UNROLL; ++i) {
-    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
-    const int n = chunk_len(w, at[i], cols);
-    const int64_t c = (int64_t)at[i].c8 * CHUNK;
-    rg[i] = load_chunk<T, VEC>(gate + at[i].r * ldg + c, n);
-    ru[i] = load_chunk<T, VEC>(up + at[i].r * ldu + c, n);
-  }
+  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
+  int slot = 0;
+  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step) {
+    const int n = r < p.end ? p.n : 0;
+    Raw8<T> rg, ru;
+    if (VEC) {
+      wait_groups<AHEAD - 2>();
+      rg = ring.take(2 * slot), ru = ring.take(2 * slot + 1);
+      copy((slot + AHEAD - 1) % AHEAD);
+      slot = (slot + 1) % AHEAD;
+    } else {
+      rg = load_chunk<T, false>(pg, n), ru = load_chunk<T, false>(pu, n);
+      pg += dg, pu += du;
+    }
+    float g[CHUNK], u[CHUNK];
+    unpack(rg, g);
+    unpack(ru, u);
+    if (n == 0) {  // nothing was copied
 #pragma unroll
-  for (int i = 0; i < GATED_UNROLL; ++i) {
-    float g[CHUNK], u[CHUNK], v[CHUNK];
-    unpack(rg[i], g);
-    unpack(ru[i], u);
+      for (int e = 0; e < CHUNK; ++e) g[e] = u[e] = 0.0f;
+    }
     if (gcodes) {
       const uint32_t bg = chunk_step(g), bu = chunk_step(u);
       const uint2 cg = chunk_codes(g, bg), cu = chunk_codes(u, bu);
-      if (at[i].r < w.rows) {
-        store_codes(gcodes, gsteps, groups, at[i].r, at[i].c8, cg, bg);
-        store_codes(ucodes, usteps, groups, at[i].r, at[i].c8, cu, bu);
+      if (p.in && r < p.end) {
+        *reinterpret_cast<uint2*>(gcodes + ac) = cg;
+        *reinterpret_cast<uint2*>(ucodes + ac) = cu;
+        if ((p.c8 & 3) == 0) gsteps[as] = (uint8_t)bg, usteps[as] = (uint8_t)bu;
       }
+      ac += dc, as += ds;
     }
 #pragma unroll
     for (int e = 0; e < CHUNK; ++e) {
       float dp;
-      v[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp)), u[e]);
+      g[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp)), u[e]);
     }
-    store_chunk<T, VEC>(out + at[i].r * ldo + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols), v,
-                        reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256);
+    store_chunk<T, VEC>(po, n, g, buf);
+    po += dd;
   }
 }
 
 template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
     k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
-                     const uint8_t* usteps, int64_t cols, Walk w, T* dgate, int64_t lddg, T* dup, int64_t lddu,
-                     int8_t* ocodes, uint8_t* osteps) {
-  __shared__ float4 stage[VEC ? 1 : 512];
-  float* const buf = reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256;
+                     const uint8_t* usteps, Tiling t, T* dgate, int64_t lddg, T* dup, int64_t lddu, int8_t* ocodes,
+                     uint8_t* osteps) {
+  constexpr int AHEAD = 4;
+  __shared__ float4 shared[VEC ? Ring<T>::bytes(AHEAD, 256) / 16 : 512];
+  __shared__ uint2 code_slots[2 * AHEAD * 256];
+  float* const buf = reinterpret_cast<float*>(shared) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
   chain_wait();
-  const int64_t groups = w.c8s / 4;
-  Chunk at[GATED_UNROLL];
-  Raw8<T> rd[GATED_UNROLL];
-  uint2 cg[GATED_UNROLL], cu[GATED_UNROLL];
-  uint32_t bg[GATED_UNROLL], bu[GATED_UNROLL];
-  at[0] = first_chunk(w, (int64_t)blockIdx.x * (256 * GATED_UNROLL) + threadIdx.x);
-#pragma unroll
-  for (int i = 0; i < GATED_UNROLL; ++i) {
-    if (i) at[i] = at[i - 1], next_chunk(w, at[i]);
-    rd[i] = load_chunk<T, VEC>(dout + at[i].r * lddo + (int64_t)at[i].c8 * CHUNK, chunk_len(w, at[i], cols));
-    cg[i] = cu[i] = make_uint2(0u, 0u), bg[i] = bu[i] = 1u;
-    if (at[i].r < w.rows) {
-      const int64_t s = at[i].r * groups + (at[i].c8 >> 2);
-      cg[i] = load_codes(gcodes, groups, at[i].r, at[i].c8), bg[i] = gsteps[s];
-      cu[i] = load_codes(ucodes, groups, at[i].r, at[i].c8), bu[i] = usteps[s];
+  const Place p = place(t);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4, col = (int64_t)p.c8 * CHUNK;
+  T *pg = dgate + p.r * lddg + col, *pu = dup + p.r * lddu + col;
+  int64_t ac = p.r * ldc + col, as = p.r * groups + (p.c8 >> 2), r = p.r;
+  const int64_t dg = p.step * lddg, du = p.step * lddu, dc = p.step * ldc, ds = p.step * groups;
+  const Ring<T> ring(shared, 256);
+  const CodeRing code(code_slots, 256);
+  // the next row to load
+  const T* pd = dout + p.r * lddo + col;
+  const int64_t dd = p.step * lddo;
+  int64_t next = p.r, nc = ac;
+  auto copy = [&](int slot) {
+    if (next < p.end && p.in) {
+      if (VEC && p.n > 0) ring.copy(slot, pd, p.n);
+      code.copy(2 * slot, gcodes + nc, true), code.copy(2 * slot + 1, ucodes + nc, true);
     }
-  }
+    copy_group();
+    if (VEC) pd += dd;
+    next += p.step, nc += dc;
+  };
+  // step bytes of AHEAD rows, loaded as many rows earlier
+  uint32_t bg[AHEAD], bu[AHEAD];
+  auto fetch_steps = [&](int64_t row, int64_t at) {
 #pragma unroll
-  for (int i = 0; i < GATED_UNROLL; ++i) {
-    float g[CHUNK], u[CHUNK], d[CHUNK], a[CHUNK];
-    chunk_values(cg[i], bg[i], g);
-    chunk_values(cu[i], bu[i], u);
-    unpack(rd[i], d);
-#pragma unroll
-    for (int e = 0; e < CHUNK; ++e) {
-      float dp;
-      const float s = gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp), act = __fmul_rn(g[e], s);
-      const float slope = __fmaf_rn(__fmul_rn(act, __fsub_rn(1.0f, s)), dp, s);
-      g[e] = __fmul_rn(__fmul_rn(d[e], u[e]), slope);  // dgate
-      a[e] = __fmul_rn(act, u[e]);
-      u[e] = __fmul_rn(d[e], act);  // dup
+    for (int i = 0; i < AHEAD; ++i, row += p.step, at += ds) {
+      bg[i] = bu[i] = 1u;
+      if (p.in && row < p.end) bg[i] = __ldg(gsteps + at), bu[i] = __ldg(usteps + at);
     }
-    const int n = chunk_len(w, at[i], cols);
-    const int64_t c = (int64_t)at[i].c8 * CHUNK;
-    store_chunk<T, VEC>(dgate + at[i].r * lddg + c, n, g, buf);
-    store_chunk<T, VEC>(dup + at[i].r * lddu + c, n, u, buf);
-    if (ocodes) {
-      const uint32_t b = chunk_step(a);
-      const uint2 q = chunk_codes(a, b);
-      if (at[i].r < w.rows) store_codes(ocodes, osteps, groups, at[i].r, at[i].c8, q, b);
+  };
+  fetch_steps(r, as);
+#pragma unroll
+  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
+  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end;) {
+    uint32_t ng[AHEAD], nu[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ng[i] = bg[i], nu[i] = bu[i];
+    if (lead + AHEAD * p.step < p.end) fetch_steps(r + AHEAD * p.step, as + AHEAD * ds);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (lead >= p.end) break;
+      const int n = r < p.end ? p.n : 0;
+      wait_groups<AHEAD - 2>();
+      Raw8<T> rd;
+      if (VEC) {
+        rd = ring.take(i);
+      } else {
+        rd = load_chunk<T, false>(pd, n);
+        pd += dd;
+      }
+      const uint2 cg = code.take(2 * i), cu = code.take(2 * i + 1);
+      copy((i + AHEAD - 1) % AHEAD);
+      float g[CHUNK], u[CHUNK], d[CHUNK], a[CHUNK];
+      chunk_values(cg, ng[i], g);
+      chunk_values(cu, nu[i], u);
+      unpack(rd, d);
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) {
+        float dp;
+        const float s = gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp), act = __fmul_rn(g[e], s);
+        const float slope = __fmaf_rn(__fmul_rn(act, __fsub_rn(1.0f, s)), dp, s);
+        g[e] = __fmul_rn(__fmul_rn(d[e], u[e]), slope);  // dgate
+        a[e] = __fmul_rn(act, u[e]);
+        u[e] = __fmul_rn(d[e], act);  // dup
+      }
+      store_chunk<T, VEC>(pg, n, g, buf);
+      store_chunk<T, VEC>(pu, n, u, buf);
+      if (ocodes) {
+        const uint32_t b = chunk_step(a);
+        const uint2 q = chunk_codes(a, b);
+        if (p.in && r < p.end) {
+          *reinterpret_cast<uint2*>(ocodes + ac) = q;
+          if ((p.c8 & 3) == 0) osteps[as] = (uint8_t)b;
+        }
+      }
+      pg += dg, pu += du, ac += dc, as += ds, r += p.step, lead += p.step;
     }
   }
 }
 
-static Walk make_walk(int64_t rows, int64_t cols) {
-  Walk w;
-  w.rows = rows, w.c8s = (int32_t)(act_ldc(cols) / CHUNK);
-  w.dr = 256 / w.c8s, w.dc = 256 % w.c8s;
-  return w;
+// The widest tile (256 chunks to 4) that leaves at most a sixteenth of its
+// lanes past the rows' end, and about `ctas` CTAs.
+static Tiling make_tiling(int64_t rows, int64_t cols, int64_t ctas, dim3* grid) {
+  Tiling t;
+  t.rows = rows, t.cols = (int32_t)cols, t.c8s = (int32_t)(act_ldc(cols) / CHUNK);
+  t.wide = 8;
+  while (t.wide > 2 && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
+  const int64_t across = ((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide, at_once = 256 >> t.wide;
+  int64_t slabs = (ctas + across - 1) / across;
+  const int64_t most = (rows + at_once - 1) / at_once;
+  if (slabs > most) slabs = most;
+  if (slabs > 65535) slabs = 65535;
+  t.slab = ((rows + slabs - 1) / slabs + at_once - 1) / at_once * at_once;
+  *grid = dim3((unsigned)across, (unsigned)((rows + t.slab - 1) / t.slab));
+  return t;
 }
-// CTAs for `unroll` chunks per thread; 0 if a grid cannot hold them.
-static unsigned walk_grid(const Walk& w, int unroll) {
-  const int64_t blocks = (w.rows * w.c8s + 256 * unroll - 1) / (256 * unroll);
-  return blocks <= INT64_C(2147483647) ? (unsigned)blocks : 0u;
-}
+constexpr int64_t ACT_CTAS = 152 * 8;  // two waves of four CTAs per SM
 
 }  // namespace gc
 
@@ -219,12 +332,11 @@ extern "C" gc_status gc_act_compress(const void* x, int64_t ld, int32_t dtype, i
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_matrix(x, ld, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK) return st;
-  const Walk w = make_walk(rows, cols);
-  const unsigned grid = walk_grid(w, UNROLL);
-  if (!grid) return GC_ERR_LAYOUT;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
   const bool vec = chunk_aligned(x, ld, dtype);
   GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_compress<T, true> : k_act_compress<T, false>, grid, 256, 0,
-                                       static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, cols, w, codes,
+                                       static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, t, codes,
                                        steps));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
@@ -236,12 +348,11 @@ extern "C" gc_status gc_act_decompress(const int8_t* codes, const uint8_t* steps
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_codes(codes, steps)) != GC_OK || (st = check_matrix(out, ldo, cols, dtype)) != GC_OK) return st;
-  const Walk w = make_walk(rows, cols);
-  const unsigned grid = walk_grid(w, UNROLL);
-  if (!grid) return GC_ERR_LAYOUT;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
   const bool vec = chunk_aligned(out, ldo, dtype);
-  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_decompress<T, true> : k_act_decompress<T, false>, grid, 256, 0,
-                                       static_cast<cudaStream_t>(stream), codes, steps, cols, w, static_cast<T*>(out),
+  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_decompress<T, true, 4> : k_act_decompress<T, false, 4>, grid, 256, 0,
+                                       static_cast<cudaStream_t>(stream), codes, steps, t, static_cast<T*>(out),
                                        ldo));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
@@ -261,15 +372,14 @@ extern "C" gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, c
   if (gate_codes || gate_steps || up_codes || up_steps)
     if ((st = check_codes(gate_codes, gate_steps)) != GC_OK || (st = check_codes(up_codes, up_steps)) != GC_OK)
       return st;
-  const Walk w = make_walk(rows, cols);
-  const unsigned grid = walk_grid(w, GATED_UNROLL);
-  if (!grid) return GC_ERR_LAYOUT;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
   const bool vec = chunk_aligned(gate, ldg, dtype) && chunk_aligned(up, ldu, dtype) && chunk_aligned(out, ldo, dtype);
   GC_BY_DTYPE(dtype, T, {
     auto kern = kind == GC_GATE_SILU ? (vec ? k_gated<T, GC_GATE_SILU, true> : k_gated<T, GC_GATE_SILU, false>)
                                      : (vec ? k_gated<T, GC_GATE_GELU_TANH, true> : k_gated<T, GC_GATE_GELU_TANH, false>);
     launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
-                   static_cast<const T*>(up), ldu, cols, w, static_cast<T*>(out), ldo, gate_codes, gate_steps, up_codes,
+                   static_cast<const T*>(up), ldu, t, static_cast<T*>(out), ldo, gate_codes, gate_steps, up_codes,
                    up_steps);
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
@@ -291,16 +401,15 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
     return st;
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
-  const Walk w = make_walk(rows, cols);
-  const unsigned grid = walk_grid(w, GATED_UNROLL);
-  if (!grid) return GC_ERR_LAYOUT;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
   const bool vec = chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype);
   GC_BY_DTYPE(dtype, T, {
     auto kern = kind == GC_GATE_SILU
                     ? (vec ? k_gated_backward<T, GC_GATE_SILU, true> : k_gated_backward<T, GC_GATE_SILU, false>)
                     : (vec ? k_gated_backward<T, GC_GATE_GELU_TANH, true> : k_gated_backward<T, GC_GATE_GELU_TANH, false>);
     launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
-                   gate_steps, up_codes, up_steps, cols, w, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
+                   gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
                    out_codes, out_steps);
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;

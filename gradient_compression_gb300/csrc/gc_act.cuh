@@ -146,10 +146,11 @@ __device__ __forceinline__ uint2 chunk_codes(const float (&v)[CHUNK], uint32_t b
   const float inverse = act_inverse(b);
   uint32_t w[CHUNK];
 #pragma unroll
-  for (int i = 0; i < CHUNK; ++i) {
-    float x = v[i];
-    if (b >= 248u) x = fminf(fmaxf(x, -127.0f * 0x1p121f), 127.0f * 0x1p121f);
-    w[i] = __float_as_uint(__fmaf_rn(x, inverse, 12582912.0f));
+  for (int i = 0; i < CHUNK; ++i) w[i] = __float_as_uint(__fmaf_rn(v[i], inverse, 12582912.0f));
+  if (__builtin_expect(b >= 248u, 0)) {
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i)
+      w[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fmul_rn(v[i], inverse), -127.0f), 127.0f), 12582912.0f));
   }
   uint2 c;
   c.x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
@@ -167,49 +168,95 @@ __device__ __forceinline__ void chunk_values(uint2 c, uint32_t b, float (&v)[CHU
   }
 }
 
-// A checkpoint's codes and step of chunk c8 of row r; groups = ldc / 32.
-__device__ __forceinline__ uint2 load_codes(const int8_t* codes, int64_t groups, int64_t r, int c8) {
+__device__ __forceinline__ uint2 load_codes(const int8_t* p) {
   uint2 c;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(c.x), "=r"(c.y)
-               : "l"(codes + r * groups * ACT_GROUP + (int64_t)c8 * CHUNK)
-               : "memory");
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "l"(p) : "memory");
   return c;
 }
-__device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* steps, int64_t groups, int64_t r, int c8, uint2 c,
-                                            uint32_t b) {
-  *reinterpret_cast<uint2*>(codes + r * groups * ACT_GROUP + (int64_t)c8 * CHUNK) = c;
-  if ((c8 & 3) == 0) steps[r * groups + (c8 >> 2)] = (uint8_t)b;
-}
 
-// A thread's chunks of a matrix: chunk tid + 256 i of its CTA's share.
-struct Walk {
-  int64_t rows;
-  int32_t c8s, dr, dc;  // chunks per row; 256 chunks on: rows and chunks
-};
-struct Chunk {
-  int64_t r;
-  int c8;
-};
-__device__ __forceinline__ Chunk first_chunk(const Walk& w, int64_t id) {
-  Chunk k;
-  if (id < (int64_t(1) << 32)) {
-    k.r = (uint32_t)id / (uint32_t)w.c8s;
-  } else {
-    k.r = id / w.c8s;
+// ---------------------------------------------------------------- rings
+// Loads in flight without registers for them: each thread copies its own
+// chunks of the rows ahead into slots of shared memory that only it reads, so
+// that no barrier is needed.  Each copy_group() closes what was copied since
+// the last; wait_groups<N>() leaves the newest N groups in flight.
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A thread's slots of 8 elements: the threads' 16-byte words side by side.
+template <typename T>
+struct Ring {
+  static constexpr int WORDS = (int)sizeof(Raw8<T>) / 16;
+  uint32_t at;      // shared address of this thread's word of slot 0
+  uint32_t stride;  // bytes from word to word: 16 per thread
+  __device__ __forceinline__ Ring(void* shared, int threads)
+      : at((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16u), stride((uint32_t)threads * 16u) {}
+  static constexpr size_t bytes(int slots, int threads) { return (size_t)slots * WORDS * threads * 16; }
+  // n elements from p on (16-byte aligned, and valid even for n = 0), zeros after them.
+  __device__ __forceinline__ void copy(int slot, const T* p, int n) const {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      const int b = min(max(n * (int)sizeof(T) - 16 * i, 0), 16);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (uint32_t)(slot * WORDS + i) * stride),
+                   "l"(reinterpret_cast<const char*>(p) + (b > 0 ? 16 * i : 0)), "r"(b)
+                   : "memory");
+    }
   }
-  k.c8 = (int)(id - k.r * w.c8s);
-  return k;
-}
-__device__ __forceinline__ void next_chunk(const Walk& w, Chunk& k) {
-  k.r += w.dr;
-  k.c8 += w.dc;
-  if (k.c8 >= w.c8s) k.c8 -= w.c8s, ++k.r;
-}
-// Elements of the chunk inside a row of `cols` (0 past the last row).
-__device__ __forceinline__ int chunk_len(const Walk& w, const Chunk& k, int64_t cols) {
-  const int64_t left = cols - (int64_t)k.c8 * CHUNK;
-  return k.r < w.rows ? (int)(left < CHUNK ? (left < 0 ? 0 : left) : CHUNK) : 0;
+  __device__ __forceinline__ Raw8<T> take(int slot) const {
+    Raw8<T> r;
+    uint4* w = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "r"(at + (uint32_t)(slot * WORDS + i) * stride)
+                   : "memory");
+    return r;
+  }
+};
+// The same for 8 codes.
+struct CodeRing {
+  uint32_t at, stride;
+  __device__ __forceinline__ CodeRing(void* shared, int threads)
+      : at((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 8u), stride((uint32_t)threads * 8u) {}
+  static constexpr size_t bytes(int slots, int threads) { return (size_t)slots * threads * 8; }
+  __device__ __forceinline__ void copy(int slot, const int8_t* p, bool in) const {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at + (uint32_t)slot * stride), "l"(p), "r"(in ? 8 : 0)
+                 : "memory");
+  }
+  __device__ __forceinline__ uint2 take(int slot) const {
+    uint2 c;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(at + (uint32_t)slot * stride) : "memory");
+    return c;
+  }
+};
+
+// How the streaming kernels of gc_act.cu cut a matrix: a CTA of 256 threads
+// takes 2^wide chunks of 256 / 2^wide rows at a time, from row blockIdx.y *
+// slab on to the end of its slab.  A thread's columns never change, so the
+// loop over the rows only adds the strides.
+struct Tiling {
+  int64_t rows, slab;
+  int32_t wide, c8s, cols;  // c8s: chunks per row, pad included
+};
+struct Place {
+  int64_t r, end;   // this thread's row, the slab's end
+  int32_t step;     // rows to the next
+  int32_t c8, n;    // its chunk, elements of it inside the row
+  bool in;          // the chunk exists (its row may still be past the end)
+};
+__device__ __forceinline__ Place place(const Tiling& t) {
+  Place p;
+  const int rb = threadIdx.x >> t.wide;
+  p.step = 256 >> t.wide;
+  p.c8 = (int)(blockIdx.x << t.wide) + (int)(threadIdx.x & ((1u << t.wide) - 1u));
+  p.r = (int64_t)blockIdx.y * t.slab + rb;
+  p.end = min((int64_t)(blockIdx.y + 1) * t.slab, t.rows);
+  p.in = p.c8 < t.c8s;
+  const int64_t left = (int64_t)t.cols - (int64_t)p.c8 * CHUNK;
+  p.n = left < 0 ? 0 : (left < CHUNK ? (int)left : CHUNK);
+  return p;
 }
 
 }  // namespace gc

@@ -25,64 +25,78 @@ __device__ __forceinline__ float row_sum(float v, int W, float (&red)[2][16], in
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
   __syncthreads();
-  const int first = warp & ~(W - 1);
-  float s = red[turn][first];
-  for (int i = 1; i < W; ++i) s = __fadd_rn(s, red[turn][first + i]);
+  const float* of = &red[turn][warp & ~(W - 1)];
+  float s = __fadd_rn(of[0], of[1]);
+  for (int i = 2; i < W; i += 2) s = __fadd_rn(s, __fadd_rn(of[i], of[i + 1]));
   turn ^= 1;
   return s;
 }
 
-__device__ __forceinline__ float rms_inverse(float ss, int64_t cols, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)cols), eps)));
+// share = 1 / cols
+__device__ __forceinline__ float rms_inverse(float ss, float share, float eps) {
+  return __frsqrt_rn(__fadd_rn(__fmul_rn(ss, share), eps));
 }
 
-// 8 weights from column c on (n of them; ones without weights).
-__device__ __forceinline__ void load_weights(const void* weight, int wtype, int64_t c, int n, bool vec, float (&w)[CHUNK]) {
-  if (!weight) {
-#pragma unroll
-    for (int i = 0; i < CHUNK; ++i) w[i] = 1.0f;
-  } else if (vec && n == CHUNK) {
-    if (wtype == GC_F32) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(weight) + c));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(weight) + c) + 1);
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    } else {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(weight) + c));
-      if (wtype == GC_BF16)
-        unpack(*reinterpret_cast<const Raw8<__nv_bfloat16>*>(&a), w);
-      else
-        unpack(*reinterpret_cast<const Raw8<__half>*>(&a), w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < CHUNK; ++i) w[i] = i < n ? load_as_f32(weight, wtype, c + i) : 0.0f;
-  }
+// The weights as fp32 in shared memory, once per CTA: the first and the last
+// four of every chunk apart, so that a warp's 16-byte loads meet no bank
+// twice.  Ones without weights, zeros past the row's end.
+__device__ __forceinline__ void stage_weights(float4* ws, const void* weight, int wtype, int64_t cols, int chunks) {
+  float* f = reinterpret_cast<float*>(ws);
+  for (int c = threadIdx.x; c < chunks * CHUNK; c += blockDim.x)
+    f[((c >> 2) & 1) * 4 * chunks + (c >> 3) * 4 + (c & 3)] = c < cols ? (weight ? load_as_f32(weight, wtype, c) : 1.0f) : 0.0f;
+  __syncthreads();
 }
+__device__ __forceinline__ void load_weights(const float4* ws, int chunks, int c8, float (&w)[CHUNK]) {
+  const int c = min(c8, chunks - 1);  // lanes past the row's end have nothing to weigh
+  const float4 a = ws[c], b = ws[chunks + c];
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// A thread's N chunks of a row.
+template <int N>
+struct RowChunks {
+  int c8[N], n[N];  // chunk, elements of it inside the row
+  int sub, per;     // this warp's row of those that the CTA takes at a time
+  int W;            // warps per row
+  __device__ __forceinline__ RowChunks(int warps, int64_t cols) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    W = warps, per = (int)(blockDim.x >> 5) / warps, sub = warp / warps;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      c8[j] = (j * warps + warp % warps) * 32 + lane;
+      const int left = (int)cols - c8[j] * CHUNK;  // cols <= NORM_WIDEST
+      n[j] = left < 0 ? 0 : (left < CHUNK ? left : CHUNK);
+    }
+  }
+};
 
 template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 4 : 1)
-    k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, bool wvec, float eps,
-              int64_t rows, int64_t cols, int64_t groups, RowShape shape, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd,
-              int8_t* codes, uint8_t* steps) {
+__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? (sizeof(T) == 2 ? 4 : 3) : 1)
+    k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
+              int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
+              uint8_t* steps) {
   __shared__ float red[2][16];
-  extern __shared__ float4 stage[];  // without VEC: 256 floats per warp
+  extern __shared__ float4 shared[];  // the weights; without VEC also 256 floats per warp
   chain_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = shape.warps;
-  const int per = (int)blockDim.x / 32 / W, sub = warp / W;  // rows at a time, this warp's among them
-  float* const buf = reinterpret_cast<float*>(stage) + warp * 256;
+  const RowChunks<N> at(warps, cols);
+  const int chunks = 4 * (int)groups;
+  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (threadIdx.x >> 5) * 256;
+  if (y) stage_weights(shared, weight, wtype, cols, chunks);
+  const float share = __fdiv_rn(1.0f, (float)cols);
+  const int64_t stride = (int64_t)gridDim.x * at.per;
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
-    const int64_t r = base + sub;
+  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
+  for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
+    const bool in = r < rows;
     float v[N][CHUNK];
     float ss = 0.0f;
     {
       Raw8<T> a[N], b[N];
+      const T *px = x + r * ldx, *pr = res + r * ldr;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int64_t c = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
-        const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - c)) : 0;
-        a[j] = load_chunk<T, VEC>(x + r * ldx + c, n);
-        if (res) b[j] = load_chunk<T, VEC>(res + r * ldr + c, n);
+        a[j] = load_chunk<T, VEC>(px + at.c8[j] * CHUNK, in ? at.n[j] : 0);
+        if (res) b[j] = load_chunk<T, VEC>(pr + at.c8[j] * CHUNK, in ? at.n[j] : 0);
       }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
@@ -97,33 +111,42 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 4 : 1)
         for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
       }
     }
-    const float rs = rms_inverse(row_sum(ss, W, red, turn), cols, eps);
-    if (rstd && r < rows && warp % W == 0 && lane == 0) rstd[r] = rs;
+    if (h) {
+      T* ph = h + r * ldh;
+#pragma unroll
+      for (int j = 0; j < N; ++j) store_chunk<T, VEC>(ph + at.c8[j] * CHUNK, in ? at.n[j] : 0, v[j], buf);
+    }
+    const float rs = rms_inverse(row_sum(ss, at.W, red, turn), share, eps);
+    if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
+    int8_t* pc = codes + r * groups * ACT_GROUP;
+    uint8_t* ps = steps + r * groups;
+    T* py = y + r * ldy;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int c8 = (j * W + warp % W) * 32 + lane;
-      const int64_t c = (int64_t)c8 * CHUNK;
-      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - c)) : 0;
-      if (h) store_chunk<T, VEC>(h + r * ldh + c, n, v[j], buf);
+      const int n = in ? at.n[j] : 0;
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) v[j][e] = __fmul_rn(v[j][e], rs);
       if (codes) {
         // past the row's end the values are 0 * rstd, which a rstd that is
         // not finite would turn into NaN
-        if (n < CHUNK)
+        if (n < CHUNK) {
 #pragma unroll
           for (int e = 0; e < CHUNK; ++e)
             if (e >= n) v[j][e] = 0.0f;
+        }
         const uint32_t b = chunk_step(v[j]);
         const uint2 q = chunk_codes(v[j], b);
-        if (r < rows && c8 < 4 * groups) store_codes(codes, steps, groups, r, c8, q, b);
+        if (in && at.c8[j] < chunks) {
+          *reinterpret_cast<uint2*>(pc + at.c8[j] * CHUNK) = q;
+          if ((at.c8[j] & 3) == 0) ps[at.c8[j] >> 2] = (uint8_t)b;
+        }
       }
       if (y) {
-        float w[CHUNK];
-        load_weights(weight, wtype, c, n, wvec, w);
+        float t[CHUNK];
+        load_weights(shared, chunks, at.c8[j], t);
 #pragma unroll
-        for (int e = 0; e < CHUNK; ++e) w[e] = __fmul_rn(v[j][e], w[e]);
-        store_chunk<T, VEC>(y + r * ldy + c, n, w, buf);
+        for (int e = 0; e < CHUNK; ++e) t[e] = __fmul_rn(v[j][e], t[e]);
+        store_chunk<T, VEC>(py + at.c8[j] * CHUNK, n, t, buf);
       }
     }
   }
@@ -135,79 +158,86 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 4 : 1)
 template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
-                       const float* rstd, const void* weight, int wtype, bool wvec, int64_t rows, int64_t cols,
-                       int64_t groups, RowShape shape, T* dx, int64_t lddx, float* part) {
+                       const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
+                       int warps, T* dx, int64_t lddx, float* part) {
   __shared__ float red[2][16];
-  extern __shared__ float4 stage[];
+  extern __shared__ float4 shared[];
   chain_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = shape.warps;
-  const int per = (int)blockDim.x / 32 / W, sub = warp / W;
-  float* const buf = reinterpret_cast<float*>(stage) + warp * 256;
+  const RowChunks<N> at(warps, cols);
+  const int chunks = 4 * (int)groups;
+  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (threadIdx.x >> 5) * 256;
+  stage_weights(shared, weight, wtype, cols, chunks);
+  const float share = __fdiv_rn(1.0f, (float)cols);
+  const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP;
   int turn = 0;
   float dw[N][CHUNK];
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < CHUNK; ++e) dw[j][e] = 0.0f;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
-    const int64_t r = base + sub;
-    Raw8<T> d[N], up[N];
-    uint2 c[N];
-    uint32_t b[N];
+  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
+  for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
+    const bool in = r < rows;
+    Raw8<T> up[N];
+    float gw[N][CHUNK], q[N][CHUNK];
+    float s = 0.0f, rs;
+    {
+      Raw8<T> d[N];
+      uint2 c[N];
+      uint32_t b[N];
+      const T *pd = dy + r * lddy, *ph = dh + r * lddh;
+      const int8_t* pc = codes + r * ldc;
+      const uint8_t* ps = steps + r * groups;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c8 = (j * W + warp % W) * 32 + lane;
-      const int64_t col = (int64_t)c8 * CHUNK;
-      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - col)) : 0;
-      d[j] = load_chunk<T, VEC>(dy + r * lddy + col, n);
-      if (dh) up[j] = load_chunk<T, VEC>(dh + r * lddh + col, n);
-      c[j] = make_uint2(0u, 0u), b[j] = 1u;
-      if (r < rows && c8 < 4 * groups) c[j] = load_codes(codes, groups, r, c8), b[j] = steps[r * groups + (c8 >> 2)];
-    }
-    const float rs = r < rows ? rstd[r] : 0.0f;
-    float s = 0.0f;
+      for (int j = 0; j < N; ++j) {
+        d[j] = load_chunk<T, VEC>(pd + at.c8[j] * CHUNK, in ? at.n[j] : 0);
+        c[j] = make_uint2(0u, 0u), b[j] = 1u;
+        if (in && at.c8[j] < chunks) c[j] = load_codes(pc + at.c8[j] * CHUNK), b[j] = __ldg(ps + (at.c8[j] >> 2));
+      }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
-      const int n = (int)max((int64_t)0, min((int64_t)CHUNK, cols - col));
-      float q[CHUNK], w[CHUNK], t[CHUNK];
-      // past the row's end dy is 0 and so are the codes, but a NaN's step
-      // would make them NaN
-      if (n <= 0) b[j] = 1u;
-      chunk_values(c[j], b[j], q);
-      load_weights(weight, wtype, col, n, wvec, w);
-      unpack(d[j], t);
+      for (int j = 0; j < N; ++j)
+        if (dh) up[j] = load_chunk<T, VEC>(ph + at.c8[j] * CHUNK, in ? at.n[j] : 0);
+      rs = in ? __ldg(rstd + r) : 0.0f;
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) {
-        if (n < CHUNK && e >= n) q[e] = 0.0f;
-        dw[j][e] = __fmaf_rn(t[e], q[e], dw[j][e]);
-        s = __fmaf_rn(__fmul_rn(t[e], w[e]), q[e], s);
+      for (int j = 0; j < N; ++j) {
+        float w[CHUNK];
+        chunk_values(c[j], b[j], q[j]);
+        unpack(d[j], gw[j]);
+        load_weights(shared, chunks, at.c8[j], w);
+        // past the row's end dy and the codes are 0, but a NaN's step would
+        // make 0 * q NaN
+        if (at.n[j] < CHUNK) {
+#pragma unroll
+          for (int e = 0; e < CHUNK; ++e)
+            if (e >= at.n[j]) q[j][e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) {
+          dw[j][e] = __fmaf_rn(gw[j][e], q[j][e], dw[j][e]);
+          gw[j][e] = __fmul_rn(gw[j][e], w[e]);
+          s = __fmaf_rn(gw[j][e], q[j][e], s);
+        }
       }
     }
-    const float mean = __fdiv_rn(row_sum(s, W, red, turn), (float)cols);
+    const float mean = __fmul_rn(row_sum(s, at.W, red, turn), share);
+    T* px = dx + r * lddx;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
-      const int n = r < rows ? (int)max((int64_t)0, min((int64_t)CHUNK, cols - col)) : 0;
-      float q[CHUNK], w[CHUNK], t[CHUNK], v[CHUNK];
-      chunk_values(c[j], b[j], q);
-      load_weights(weight, wtype, col, n, wvec, w);
-      unpack(d[j], v);
+      float t[CHUNK];
       if (dh) unpack(up[j], t);
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
-        v[e] = __fmul_rn(rs, __fmaf_rn(-q[e], mean, __fmul_rn(v[e], w[e])));
-        if (dh) v[e] = __fadd_rn(v[e], t[e]);
+        const float v = __fmul_rn(rs, __fmaf_rn(-q[j][e], mean, gw[j][e]));
+        gw[j][e] = dh ? __fadd_rn(v, t[e]) : v;
       }
-      store_chunk<T, VEC>(dx + r * lddx + col, n, v, buf);
+      store_chunk<T, VEC>(px + at.c8[j] * CHUNK, in ? at.n[j] : 0, gw[j], buf);
     }
   }
   if (!part) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int64_t col = (int64_t)((j * W + warp % W) * 32 + lane) * CHUNK;
-    float* o = part + ((int64_t)blockIdx.x * per + sub) * groups * ACT_GROUP + col;  // rows of ldc floats
-    if (col < groups * ACT_GROUP) {
+    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + at.c8[j] * CHUNK;  // rows of ldc floats
+    if (at.c8[j] < chunks) {
       reinterpret_cast<float4*>(o)[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
       reinterpret_cast<float4*>(o)[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
@@ -271,7 +301,7 @@ __global__ void __launch_bounds__(NTHREADS)
       const float v = sum_at(c);
       ss = __fmaf_rn(v, v, ss);
     }
-    const float rs = rms_inverse(cta_sum(ss, red), cols, eps);
+    const float rs = rms_inverse(cta_sum(ss, red), __fdiv_rn(1.0f, (float)cols), eps);
     if (rstd && threadIdx.x == 0) rstd[r] = rs;
     for (int64_t g = threadIdx.x >> 5; g < groups; g += NTHREADS / 32) {
       const int64_t c = g * 32 + lane;
@@ -355,6 +385,14 @@ static int norm_grid(int64_t rows, const RowShape& s, int per_sm) {
   const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * per_sm * 256 / s.threads;
   return (int)(ctas < most ? ctas : most);
 }
+// Shared memory: the weights, and without VEC the warps' staging.
+static size_t norm_shared(int64_t cols, const RowShape& s, bool vec) {
+  return (size_t)act_ldc(cols) * sizeof(float) + (vec ? 0 : (size_t)s.threads * 32);
+}
+template <typename K>
+static bool allow_shared(K kern) {  // up to 16384 weights and 16 warps' staging
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024) == cudaSuccess;
+}
 constexpr int FORWARD_PER_SM = 4, BACKWARD_PER_SM = 3;  // CTAs of 256 threads
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
@@ -394,12 +432,14 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
   const RowShape shape = norm_shape(cols);
   const bool vec = chunk_aligned(x, ldx, dtype) && (!residual || chunk_aligned(residual, ldr, dtype)) &&
                    (!y || chunk_aligned(y, ldy, dtype)) && (!h || chunk_aligned(h, ldh, dtype));
-  const bool wvec = aligned16(weight), two = norm_chunks(cols) == 2;
+  const bool two = norm_chunks(cols) == 2;
   GC_BY_DTYPE(dtype, T, {
+    static const bool ready = allow_shared(k_rmsnorm<T, 4, true>) && allow_shared(k_rmsnorm<T, 4, false>);
+    if (!ready) return GC_ERR_CUDA;
     auto kern = two ? (vec ? k_rmsnorm<T, 2, true> : k_rmsnorm<T, 2, false>) : (vec ? k_rmsnorm<T, 4, true> : k_rmsnorm<T, 4, false>);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, vec ? 0 : shape.threads * 32, s,
-                   static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, wvec, eps,
-                   rows, cols, groups, shape, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec), s,
+                   static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows,
+                   cols, groups, shape.warps, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
@@ -459,13 +499,15 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   }
   const RowShape shape = norm_shape(cols);
   const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
-  const bool wvec = aligned16(weight), two = norm_chunks(cols) == 2;
+  const bool two = norm_chunks(cols) == 2;
   GC_BY_DTYPE(dtype, T, {
+    static const bool ready = allow_shared(k_rmsnorm_backward<T, 4, true>) && allow_shared(k_rmsnorm_backward<T, 4, false>);
+    if (!ready) return GC_ERR_CUDA;
     auto kern = two ? (vec ? k_rmsnorm_backward<T, 2, true> : k_rmsnorm_backward<T, 2, false>)
                     : (vec ? k_rmsnorm_backward<T, 4, true> : k_rmsnorm_backward<T, 4, false>);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, vec ? 0 : shape.threads * 32, s,
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec), s,
                    static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
-                   weight_dtype, wvec, rows, cols, groups, shape, static_cast<T*>(dx), lddx, part);
+                   weight_dtype, rows, cols, groups, shape.warps, static_cast<T*>(dx), lddx, part);
   });
   if (dw) join(parts);
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
