@@ -70,46 +70,88 @@ struct RowChunks {
   }
 };
 
+// Rows ahead come through rings in shared memory where two slots of them fit:
+// SLOTS - 1 rows are in flight while one is worked on.  (Registers for the
+// rows ahead cost the warps that hide the latency: 0.5 of the copy rate.)
 template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? (sizeof(T) == 2 ? 4 : 3) : 1)
+struct RowRing {
+  static constexpr bool USED = VEC && N * sizeof(T) <= 8;
+  static constexpr int FORWARD = USED ? (N * sizeof(T) <= 4 ? 3 : 2) : 0, BACKWARD = USED ? 2 : 0;  // slots
+  static size_t forward_bytes(int threads) { return Ring<T>::bytes(2 * N * FORWARD, threads); }
+  static size_t backward_bytes(int threads) {
+    return Ring<T>::bytes(2 * N * BACKWARD, threads) + CodeRing::bytes(N * BACKWARD, threads);
+  }
+};
+
+template <typename T, int N, bool VEC>
+__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
               int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
               uint8_t* steps) {
+  constexpr int SLOTS = RowRing<T, N, VEC>::FORWARD;
   __shared__ float red[2][16];
-  extern __shared__ float4 shared[];  // the weights; without VEC also 256 floats per warp
+  extern __shared__ float4 shared[];  // the weights, then the ring, or without VEC 256 floats per warp
   chain_wait();
   const RowChunks<N> at(warps, cols);
   const int chunks = 4 * (int)groups;
-  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (threadIdx.x >> 5) * 256;
+  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  const Ring<T> ring(shared + 2 * chunks, (int)blockDim.x);
+  const int64_t stride = (int64_t)gridDim.x * at.per;
+  int64_t r = (int64_t)blockIdx.x * at.per + at.sub, next = r;
+  auto copy = [&](int slot) {
+    if (next < rows) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (at.n[j] > 0) {
+          ring.copy((slot * N + j) * 2, x + next * ldx + at.c8[j] * CHUNK, at.n[j]);
+          if (res) ring.copy((slot * N + j) * 2 + 1, res + next * ldr + at.c8[j] * CHUNK, at.n[j]);
+        }
+    }
+    copy_group();
+    next += stride;
+  };
+  if constexpr (SLOTS > 0) {
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) copy(i);
+  }
   if (y) stage_weights(shared, weight, wtype, cols, chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
-  const int64_t stride = (int64_t)gridDim.x * at.per;
-  int turn = 0;
-  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
+  int turn = 0, slot = 0;
   for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
     const bool in = r < rows;
     float v[N][CHUNK];
     float ss = 0.0f;
-    {
-      Raw8<T> a[N], b[N];
-      const T *px = x + r * ldx, *pr = res + r * ldr;
+    if constexpr (SLOTS > 0) {
+      wait_groups<SLOTS - 2>();
+    }
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        a[j] = load_chunk<T, VEC>(px + at.c8[j] * CHUNK, in ? at.n[j] : 0);
-        if (res) b[j] = load_chunk<T, VEC>(pr + at.c8[j] * CHUNK, in ? at.n[j] : 0);
+    for (int j = 0; j < N; ++j) {
+      const int n = in ? at.n[j] : 0;
+      Raw8<T> a, b;
+      if constexpr (SLOTS > 0) {
+        a = ring.take((slot * N + j) * 2);
+        if (res) b = ring.take((slot * N + j) * 2 + 1);
+      } else {
+        a = load_chunk<T, VEC>(x + r * ldx + at.c8[j] * CHUNK, n);
+        if (res) b = load_chunk<T, VEC>(res + r * ldr + at.c8[j] * CHUNK, n);
+      }
+      unpack(a, v[j]);
+      if (res) {
+        float t[CHUNK];
+        unpack(b, t);
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
+      }
+      if (SLOTS > 0 && n == 0) {  // nothing was copied
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) v[j][e] = 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        unpack(a[j], v[j]);
-        if (res) {
-          float t[CHUNK];
-          unpack(b[j], t);
-#pragma unroll
-          for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
-      }
+      for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
+    }
+    if constexpr (SLOTS > 0) {
+      copy(slot == 0 ? SLOTS - 1 : slot - 1);
+      slot = slot == SLOTS - 1 ? 0 : slot + 1;
     }
     if (h) {
       T* ph = h + r * ldh;
@@ -160,78 +202,114 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
                        const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
                        int warps, T* dx, int64_t lddx, float* part) {
+  constexpr int SLOTS = RowRing<T, N, VEC>::BACKWARD;
   __shared__ float red[2][16];
   extern __shared__ float4 shared[];
   chain_wait();
   const RowChunks<N> at(warps, cols);
   const int chunks = 4 * (int)groups;
-  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (threadIdx.x >> 5) * 256;
+  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  const Ring<T> ring(shared + 2 * chunks, (int)blockDim.x);
+  const CodeRing code(shared + 2 * chunks + Ring<T>::bytes(2 * N * SLOTS, 1) / 16 * blockDim.x, (int)blockDim.x);
+  const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP;
+  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
+  auto copy = [&](int slot, int64_t row) {
+    if (row < rows) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (at.n[j] > 0) {
+          ring.copy((slot * N + j) * 2, dy + row * lddy + at.c8[j] * CHUNK, at.n[j]);
+          if (dh) ring.copy((slot * N + j) * 2 + 1, dh + row * lddh + at.c8[j] * CHUNK, at.n[j]);
+        }
+        if (at.c8[j] < chunks) code.copy(slot * N + j, codes + row * ldc + at.c8[j] * CHUNK, true);
+      }
+    }
+    copy_group();
+  };
+  // step bytes and rstd of the row ahead
+  uint32_t b[N];
+  float rs;
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      b[j] = 1u;
+      if (row < rows && at.c8[j] < chunks) b[j] = __ldg(steps + row * groups + (at.c8[j] >> 2));
+    }
+    rs = row < rows ? __ldg(rstd + row) : 0.0f;
+  };
+  if constexpr (SLOTS > 0) copy(0, r);
+  fetch(r);
   stage_weights(shared, weight, wtype, cols, chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
-  const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP;
-  int turn = 0;
+  int turn = 0, slot = 0;
   float dw[N][CHUNK];
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < CHUNK; ++e) dw[j][e] = 0.0f;
-  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
   for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
     const bool in = r < rows;
-    Raw8<T> up[N];
-    float gw[N][CHUNK], q[N][CHUNK];
-    float s = 0.0f, rs;
-    {
-      Raw8<T> d[N];
-      uint2 c[N];
-      uint32_t b[N];
-      const T *pd = dy + r * lddy, *ph = dh + r * lddh;
-      const int8_t* pc = codes + r * ldc;
-      const uint8_t* ps = steps + r * groups;
+    uint32_t step[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        d[j] = load_chunk<T, VEC>(pd + at.c8[j] * CHUNK, in ? at.n[j] : 0);
-        c[j] = make_uint2(0u, 0u), b[j] = 1u;
-        if (in && at.c8[j] < chunks) c[j] = load_codes(pc + at.c8[j] * CHUNK), b[j] = __ldg(ps + (at.c8[j] >> 2));
+    for (int j = 0; j < N; ++j) step[j] = b[j];
+    const float inverse = rs;
+    if constexpr (SLOTS > 0) {
+      wait_groups<0>();
+      if (lead + stride < rows) copy(slot ^ 1, r + stride);
+    }
+    if (lead + stride < rows) fetch(r + stride);
+    float gw[N][CHUNK], q[N][CHUNK];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int n = in ? at.n[j] : 0;
+      Raw8<T> d;
+      uint2 c = make_uint2(0u, 0u);
+      if constexpr (SLOTS > 0) {
+        d = ring.take((slot * N + j) * 2);
+        c = code.take(slot * N + j);
+      } else {
+        d = load_chunk<T, VEC>(dy + r * lddy + at.c8[j] * CHUNK, n);
+        if (in && at.c8[j] < chunks) c = load_codes(codes + r * ldc + at.c8[j] * CHUNK);
+      }
+      float w[CHUNK];
+      chunk_values(c, step[j], q[j]);
+      unpack(d, gw[j]);
+      load_weights(shared, chunks, at.c8[j], w);
+      // past the row's end dy and q are nothing (what was not copied, or a
+      // NaN's step)
+      if (n < CHUNK) {
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e)
+          if (e >= n) q[j][e] = gw[j][e] = 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (dh) up[j] = load_chunk<T, VEC>(ph + at.c8[j] * CHUNK, in ? at.n[j] : 0);
-      rs = in ? __ldg(rstd + r) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float w[CHUNK];
-        chunk_values(c[j], b[j], q[j]);
-        unpack(d[j], gw[j]);
-        load_weights(shared, chunks, at.c8[j], w);
-        // past the row's end dy and the codes are 0, but a NaN's step would
-        // make 0 * q NaN
-        if (at.n[j] < CHUNK) {
-#pragma unroll
-          for (int e = 0; e < CHUNK; ++e)
-            if (e >= at.n[j]) q[j][e] = 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < CHUNK; ++e) {
-          dw[j][e] = __fmaf_rn(gw[j][e], q[j][e], dw[j][e]);
-          gw[j][e] = __fmul_rn(gw[j][e], w[e]);
-          s = __fmaf_rn(gw[j][e], q[j][e], s);
-        }
+      for (int e = 0; e < CHUNK; ++e) {
+        dw[j][e] = __fmaf_rn(gw[j][e], q[j][e], dw[j][e]);
+        gw[j][e] = __fmul_rn(gw[j][e], w[e]);
+        s = __fmaf_rn(gw[j][e], q[j][e], s);
       }
     }
     const float mean = __fmul_rn(row_sum(s, at.W, red, turn), share);
     T* px = dx + r * lddx;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+      const int n = in ? at.n[j] : 0;
       float t[CHUNK];
-      if (dh) unpack(up[j], t);
+      if (dh) {
+        if constexpr (SLOTS > 0)
+          unpack(ring.take((slot * N + j) * 2 + 1), t);
+        else
+          unpack(load_chunk<T, VEC>(dh + r * lddh + at.c8[j] * CHUNK, n), t);
+      }
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
-        const float v = __fmul_rn(rs, __fmaf_rn(-q[j][e], mean, gw[j][e]));
+        const float v = __fmul_rn(inverse, __fmaf_rn(-q[j][e], mean, gw[j][e]));
         gw[j][e] = dh ? __fadd_rn(v, t[e]) : v;
       }
-      store_chunk<T, VEC>(px + at.c8[j] * CHUNK, in ? at.n[j] : 0, gw[j], buf);
+      store_chunk<T, VEC>(px + at.c8[j] * CHUNK, n, gw[j], buf);
     }
+    slot ^= 1;
   }
   if (!part) return;
 #pragma unroll
@@ -385,15 +463,15 @@ static int norm_grid(int64_t rows, const RowShape& s, int per_sm) {
   const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * per_sm * 256 / s.threads;
   return (int)(ctas < most ? ctas : most);
 }
-// Shared memory: the weights, and without VEC the warps' staging.
-static size_t norm_shared(int64_t cols, const RowShape& s, bool vec) {
-  return (size_t)act_ldc(cols) * sizeof(float) + (vec ? 0 : (size_t)s.threads * 32);
+// Shared memory: the weights, and the ring or without VEC the warps' staging.
+static size_t norm_shared(int64_t cols, const RowShape& s, bool vec, size_t ring) {
+  return (size_t)act_ldc(cols) * sizeof(float) + (vec ? ring : (size_t)s.threads * 32);
 }
 template <typename K>
-static bool allow_shared(K kern) {  // up to 16384 weights and 16 warps' staging
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024) == cudaSuccess;
+static bool allow_shared(K kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) == cudaSuccess;
 }
-constexpr int FORWARD_PER_SM = 4, BACKWARD_PER_SM = 3;  // CTAs of 256 threads
+constexpr int FORWARD_PER_SM = 3, BACKWARD_PER_SM = 3;  // CTAs of 256 threads
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
   if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
@@ -434,10 +512,12 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
                    (!y || chunk_aligned(y, ldy, dtype)) && (!h || chunk_aligned(h, ldh, dtype));
   const bool two = norm_chunks(cols) == 2;
   GC_BY_DTYPE(dtype, T, {
-    static const bool ready = allow_shared(k_rmsnorm<T, 4, true>) && allow_shared(k_rmsnorm<T, 4, false>);
+    static const bool ready = allow_shared(k_rmsnorm<T, 2, true>) && allow_shared(k_rmsnorm<T, 4, true>) &&
+                              allow_shared(k_rmsnorm<T, 4, false>);
     if (!ready) return GC_ERR_CUDA;
     auto kern = two ? (vec ? k_rmsnorm<T, 2, true> : k_rmsnorm<T, 2, false>) : (vec ? k_rmsnorm<T, 4, true> : k_rmsnorm<T, 4, false>);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec), s,
+    const size_t ring = two ? RowRing<T, 2, true>::forward_bytes(shape.threads) : RowRing<T, 4, true>::forward_bytes(shape.threads);
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec, ring), s,
                    static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows,
                    cols, groups, shape.warps, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
   });
@@ -501,11 +581,13 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
   const bool two = norm_chunks(cols) == 2;
   GC_BY_DTYPE(dtype, T, {
-    static const bool ready = allow_shared(k_rmsnorm_backward<T, 4, true>) && allow_shared(k_rmsnorm_backward<T, 4, false>);
+    static const bool ready = allow_shared(k_rmsnorm_backward<T, 2, true>) && allow_shared(k_rmsnorm_backward<T, 4, true>) &&
+                              allow_shared(k_rmsnorm_backward<T, 4, false>);
     if (!ready) return GC_ERR_CUDA;
     auto kern = two ? (vec ? k_rmsnorm_backward<T, 2, true> : k_rmsnorm_backward<T, 2, false>)
                     : (vec ? k_rmsnorm_backward<T, 4, true> : k_rmsnorm_backward<T, 4, false>);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec), s,
+    const size_t ring = two ? RowRing<T, 2, true>::backward_bytes(shape.threads) : RowRing<T, 4, true>::backward_bytes(shape.threads);
+    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec, ring), s,
                    static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
                    weight_dtype, rows, cols, groups, shape.warps, static_cast<T*>(dx), lddx, part);
   });
