@@ -203,6 +203,13 @@ struct Ring {
                    : "memory");
     }
   }
+  __device__ __forceinline__ void copy(int slot, const T* p) const {  // all 8
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (uint32_t)(slot * WORDS + i) * stride),
+                   "l"(reinterpret_cast<const char*>(p) + 16 * i)
+                   : "memory");
+  }
   __device__ __forceinline__ Raw8<T> take(int slot) const {
     Raw8<T> r;
     uint4* w = reinterpret_cast<uint4*>(&r);

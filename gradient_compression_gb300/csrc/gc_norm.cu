@@ -47,75 +47,95 @@ __device__ __forceinline__ void stage_weights(float4* ws, const void* weight, in
   __syncthreads();
 }
 __device__ __forceinline__ void load_weights(const float4* ws, int chunks, int c8, float (&w)[CHUNK]) {
-  const int c = min(c8, chunks - 1);  // lanes past the row's end have nothing to weigh
+  const int c = min(c8, chunks - 1);  // a lane past the row's end weighs nothing
   const float4 a = ws[c], b = ws[chunks + c];
   w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
-// A thread's N chunks of a row.
-template <int N>
+// How a row lies on its warps.
+constexpr int ROW_SCALAR = 0;  // rows not on 16-byte boundaries
+constexpr int ROW_VEC = 1;
+constexpr int ROW_FULL = 2;    // and every lane has N whole chunks: no bounds inside a row
+
+// A thread's N chunks of a row: the first, and the others 32 W chunks apart.
+template <int N, int MODE>
 struct RowChunks {
-  int c8[N], n[N];  // chunk, elements of it inside the row
-  int sub, per;     // this warp's row of those that the CTA takes at a time
-  int W;            // warps per row
-  __device__ __forceinline__ RowChunks(int warps, int64_t cols) {
+  int first, apart;  // chunks
+  int len[N];        // elements of each inside the row
+  int chunks;        // of a row, pad included
+  int sub, per;      // this warp's row of those that the CTA takes at a time
+  int W;             // warps per row
+  __device__ __forceinline__ RowChunks(int warps, int64_t cols, int64_t groups) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     W = warps, per = (int)(blockDim.x >> 5) / warps, sub = warp / warps;
+    first = warp % warps * 32 + lane, apart = warps * 32, chunks = 4 * (int)groups;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      c8[j] = (j * warps + warp % warps) * 32 + lane;
-      const int left = (int)cols - c8[j] * CHUNK;  // cols <= NORM_WIDEST
-      n[j] = left < 0 ? 0 : (left < CHUNK ? left : CHUNK);
+      const int left = (int)cols - c8(j) * CHUNK;  // cols <= NORM_WIDEST
+      len[j] = left < 0 ? 0 : (left < CHUNK ? left : CHUNK);
     }
   }
+  __device__ __forceinline__ int c8(int j) const { return first + j * apart; }
+  __device__ __forceinline__ int n(int j) const { return MODE == ROW_FULL ? CHUNK : len[j]; }
+  __device__ __forceinline__ bool held(int j) const { return MODE == ROW_FULL || c8(j) < chunks; }  // in the checkpoint
 };
 
 // Rows ahead come through rings in shared memory where two slots of them fit:
 // SLOTS - 1 rows are in flight while one is worked on.  (Registers for the
 // rows ahead cost the warps that hide the latency: 0.5 of the copy rate.)
-template <typename T, int N, bool VEC>
+// Three or four slots instead of two, with 12 warps fewer, measured no faster.
+template <typename T, int N, int MODE>
 struct RowRing {
-  static constexpr bool USED = VEC && N * sizeof(T) <= 8;
-  static constexpr int FORWARD = USED ? (N * sizeof(T) <= 4 ? 3 : 2) : 0, BACKWARD = USED ? 2 : 0;  // slots
-  static size_t forward_bytes(int threads) { return Ring<T>::bytes(2 * N * FORWARD, threads); }
+  static constexpr bool USED = MODE != ROW_SCALAR && N * sizeof(T) <= 8;
+  static constexpr int SLOTS = USED ? 2 : 0;
+  static size_t forward_bytes(int threads) { return Ring<T>::bytes(2 * N * SLOTS, threads); }
   static size_t backward_bytes(int threads) {
-    return Ring<T>::bytes(2 * N * BACKWARD, threads) + CodeRing::bytes(N * BACKWARD, threads);
+    return Ring<T>::bytes(2 * N * SLOTS, threads) + CodeRing::bytes(N * SLOTS, threads);
   }
 };
 
-template <typename T, int N, bool VEC>
+template <typename T, int N, int MODE>
 __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
               int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
               uint8_t* steps) {
-  constexpr int SLOTS = RowRing<T, N, VEC>::FORWARD;
+  constexpr bool VEC = MODE != ROW_SCALAR;
+  constexpr int SLOTS = RowRing<T, N, MODE>::SLOTS;
   __shared__ float red[2][16];
   extern __shared__ float4 shared[];  // the weights, then the ring, or without VEC 256 floats per warp
   chain_wait();
-  const RowChunks<N> at(warps, cols);
-  const int chunks = 4 * (int)groups;
-  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
-  const Ring<T> ring(shared + 2 * chunks, (int)blockDim.x);
-  const int64_t stride = (int64_t)gridDim.x * at.per;
+  const RowChunks<N, MODE> at(warps, cols, groups);
+  float* const buf = reinterpret_cast<float*>(shared + 2 * at.chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  const Ring<T> ring(shared + 2 * at.chunks, (int)blockDim.x);
+  const int64_t stride = (int64_t)gridDim.x * at.per, start = at.first * CHUNK;
+  const int jump = at.apart * CHUNK;  // elements from chunk to chunk
   int64_t r = (int64_t)blockIdx.x * at.per + at.sub, next = r;
+  const T *px = x + r * ldx + start, *pr = res + r * ldr + start;  // the next row to load
   auto copy = [&](int slot) {
     if (next < rows) {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (at.n[j] > 0) {
-          ring.copy((slot * N + j) * 2, x + next * ldx + at.c8[j] * CHUNK, at.n[j]);
-          if (res) ring.copy((slot * N + j) * 2 + 1, res + next * ldr + at.c8[j] * CHUNK, at.n[j]);
+      for (int j = 0; j < N; ++j) {
+        if (MODE == ROW_FULL) {
+          ring.copy((slot * N + j) * 2, px + j * jump);
+          if (res) ring.copy((slot * N + j) * 2 + 1, pr + j * jump);
+        } else if (at.n(j) > 0) {
+          ring.copy((slot * N + j) * 2, px + j * jump, at.n(j));
+          if (res) ring.copy((slot * N + j) * 2 + 1, pr + j * jump, at.n(j));
         }
+      }
     }
     copy_group();
-    next += stride;
+    next += stride, px += stride * ldx, pr += stride * ldr;
   };
   if constexpr (SLOTS > 0) {
 #pragma unroll
     for (int i = 0; i < SLOTS - 1; ++i) copy(i);
   }
-  if (y) stage_weights(shared, weight, wtype, cols, chunks);
+  if (y) stage_weights(shared, weight, wtype, cols, at.chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
+  T *ph = h + r * ldh + start, *py = y + r * ldy + start;
+  int8_t* pc = codes + r * groups * ACT_GROUP + start;
+  uint8_t* ps = steps + r * groups + (at.first >> 2);
   int turn = 0, slot = 0;
   for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
     const bool in = r < rows;
@@ -126,14 +146,14 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int n = in ? at.n[j] : 0;
+      const int n = in ? at.n(j) : 0;
       Raw8<T> a, b;
       if constexpr (SLOTS > 0) {
         a = ring.take((slot * N + j) * 2);
         if (res) b = ring.take((slot * N + j) * 2 + 1);
       } else {
-        a = load_chunk<T, VEC>(x + r * ldx + at.c8[j] * CHUNK, n);
-        if (res) b = load_chunk<T, VEC>(res + r * ldr + at.c8[j] * CHUNK, n);
+        a = load_chunk<T, VEC>(px + j * jump, n);
+        if (res) b = load_chunk<T, VEC>(pr + j * jump, n);
       }
       unpack(a, v[j]);
       if (res) {
@@ -142,7 +162,7 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
       }
-      if (SLOTS > 0 && n == 0) {  // nothing was copied
+      if (SLOTS > 0 && MODE != ROW_FULL && n == 0) {  // nothing was copied
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e) v[j][e] = 0.0f;
       }
@@ -152,95 +172,107 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     if constexpr (SLOTS > 0) {
       copy(slot == 0 ? SLOTS - 1 : slot - 1);
       slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    } else {
+      px += stride * ldx, pr += stride * ldr;
     }
     if (h) {
-      T* ph = h + r * ldh;
 #pragma unroll
-      for (int j = 0; j < N; ++j) store_chunk<T, VEC>(ph + at.c8[j] * CHUNK, in ? at.n[j] : 0, v[j], buf);
+      for (int j = 0; j < N; ++j) store_chunk<T, VEC>(ph + j * jump, in ? at.n(j) : 0, v[j], buf);
+      ph += stride * ldh;
     }
     const float rs = rms_inverse(row_sum(ss, at.W, red, turn), share, eps);
     if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
-    int8_t* pc = codes + r * groups * ACT_GROUP;
-    uint8_t* ps = steps + r * groups;
-    T* py = y + r * ldy;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int n = in ? at.n[j] : 0;
+      const int n = in ? at.n(j) : 0;
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) v[j][e] = __fmul_rn(v[j][e], rs);
       if (codes) {
         // past the row's end the values are 0 * rstd, which a rstd that is
         // not finite would turn into NaN
-        if (n < CHUNK) {
+        if (MODE != ROW_FULL && n < CHUNK) {
 #pragma unroll
           for (int e = 0; e < CHUNK; ++e)
             if (e >= n) v[j][e] = 0.0f;
         }
         const uint32_t b = chunk_step(v[j]);
         const uint2 q = chunk_codes(v[j], b);
-        if (in && at.c8[j] < chunks) {
-          *reinterpret_cast<uint2*>(pc + at.c8[j] * CHUNK) = q;
-          if ((at.c8[j] & 3) == 0) ps[at.c8[j] >> 2] = (uint8_t)b;
+        if (in && at.held(j)) {
+          *reinterpret_cast<uint2*>(pc + j * jump) = q;
+          if ((at.first & 3) == 0) ps[j * (at.apart >> 2)] = (uint8_t)b;
         }
       }
       if (y) {
         float t[CHUNK];
-        load_weights(shared, chunks, at.c8[j], t);
+        load_weights(shared, at.chunks, at.c8(j), t);
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e) t[e] = __fmul_rn(v[j][e], t[e]);
-        store_chunk<T, VEC>(py + at.c8[j] * CHUNK, n, t, buf);
+        store_chunk<T, VEC>(py + j * jump, n, t, buf);
       }
     }
+    py += stride * ldy, pc += stride * groups * ACT_GROUP, ps += stride * groups;
   }
 }
 
 // Gradient: gw = dy * weight, dx = rstd (gw - q mean(gw q)) + dh, and each
 // thread's share of dw = sum dy q of its columns over the rows that its CTA
 // walks over, one partial sum per CTA and row at a time.
-template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
+template <typename T, int N, int MODE>
+__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
                        const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
                        int warps, T* dx, int64_t lddx, float* part) {
-  constexpr int SLOTS = RowRing<T, N, VEC>::BACKWARD;
+  constexpr bool VEC = MODE != ROW_SCALAR;
+  constexpr int SLOTS = RowRing<T, N, MODE>::SLOTS;
   __shared__ float red[2][16];
   extern __shared__ float4 shared[];
   chain_wait();
-  const RowChunks<N> at(warps, cols);
-  const int chunks = 4 * (int)groups;
-  float* const buf = reinterpret_cast<float*>(shared + 2 * chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
-  const Ring<T> ring(shared + 2 * chunks, (int)blockDim.x);
-  const CodeRing code(shared + 2 * chunks + Ring<T>::bytes(2 * N * SLOTS, 1) / 16 * blockDim.x, (int)blockDim.x);
-  const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP;
-  int64_t r = (int64_t)blockIdx.x * at.per + at.sub;
-  auto copy = [&](int slot, int64_t row) {
-    if (row < rows) {
+  const RowChunks<N, MODE> at(warps, cols, groups);
+  float* const buf = reinterpret_cast<float*>(shared + 2 * at.chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  const Ring<T> ring(shared + 2 * at.chunks, (int)blockDim.x);
+  const CodeRing code(shared + 2 * at.chunks + Ring<T>::bytes(2 * N * SLOTS, 1) / 16 * blockDim.x, (int)blockDim.x);
+  const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP, start = at.first * CHUNK;
+  const int jump = at.apart * CHUNK;
+  int64_t r = (int64_t)blockIdx.x * at.per + at.sub, next = r;
+  // the next row to load
+  const T *pd = dy + r * lddy + start, *ph = dh + r * lddh + start;
+  const int8_t* pc = codes + r * ldc + start;
+  const uint8_t* ps = steps + r * groups + (at.first >> 2);
+  auto copy = [&](int slot) {
+    if (next < rows) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (at.n[j] > 0) {
-          ring.copy((slot * N + j) * 2, dy + row * lddy + at.c8[j] * CHUNK, at.n[j]);
-          if (dh) ring.copy((slot * N + j) * 2 + 1, dh + row * lddh + at.c8[j] * CHUNK, at.n[j]);
+        if (MODE == ROW_FULL) {
+          ring.copy((slot * N + j) * 2, pd + j * jump);
+          if (dh) ring.copy((slot * N + j) * 2 + 1, ph + j * jump);
+        } else if (at.n(j) > 0) {
+          ring.copy((slot * N + j) * 2, pd + j * jump, at.n(j));
+          if (dh) ring.copy((slot * N + j) * 2 + 1, ph + j * jump, at.n(j));
         }
-        if (at.c8[j] < chunks) code.copy(slot * N + j, codes + row * ldc + at.c8[j] * CHUNK, true);
+        if (at.held(j)) code.copy(slot * N + j, pc + j * jump, true);
       }
     }
     copy_group();
+    next += stride, pd += stride * lddy, ph += stride * lddh, pc += stride * ldc;
   };
-  // step bytes and rstd of the row ahead
+  // step bytes and rstd, a row ahead
   uint32_t b[N];
   float rs;
   auto fetch = [&](int64_t row) {
+    const bool in = row < rows;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      b[j] = 1u;
-      if (row < rows && at.c8[j] < chunks) b[j] = __ldg(steps + row * groups + (at.c8[j] >> 2));
-    }
-    rs = row < rows ? __ldg(rstd + row) : 0.0f;
+    for (int j = 0; j < N; ++j) b[j] = in && at.held(j) ? __ldg(ps + j * (at.apart >> 2)) : 1u;
+    rs = in ? __ldg(rstd + row) : 0.0f;
+    ps += stride * groups;
   };
-  if constexpr (SLOTS > 0) copy(0, r);
+  if constexpr (SLOTS > 0) {
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) copy(i);
+  }
   fetch(r);
-  stage_weights(shared, weight, wtype, cols, chunks);
+  stage_weights(shared, weight, wtype, cols, at.chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
+  T* px = dx + r * lddx + start;
   int turn = 0, slot = 0;
   float dw[N][CHUNK];
 #pragma unroll
@@ -254,34 +286,34 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     for (int j = 0; j < N; ++j) step[j] = b[j];
     const float inverse = rs;
     if constexpr (SLOTS > 0) {
-      wait_groups<0>();
-      if (lead + stride < rows) copy(slot ^ 1, r + stride);
+      wait_groups<SLOTS - 2>();
+      copy(slot == 0 ? SLOTS - 1 : slot - 1);
     }
     if (lead + stride < rows) fetch(r + stride);
     float gw[N][CHUNK], q[N][CHUNK];
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int n = in ? at.n[j] : 0;
+      const int n = in ? at.n(j) : 0;
       Raw8<T> d;
       uint2 c = make_uint2(0u, 0u);
       if constexpr (SLOTS > 0) {
         d = ring.take((slot * N + j) * 2);
         c = code.take(slot * N + j);
       } else {
-        d = load_chunk<T, VEC>(dy + r * lddy + at.c8[j] * CHUNK, n);
-        if (in && at.c8[j] < chunks) c = load_codes(codes + r * ldc + at.c8[j] * CHUNK);
+        d = load_chunk<T, VEC>(pd + j * jump, n);
+        if (in && at.held(j)) c = load_codes(pc + j * jump);
       }
       float w[CHUNK];
       chunk_values(c, step[j], q[j]);
       unpack(d, gw[j]);
-      load_weights(shared, chunks, at.c8[j], w);
+      load_weights(shared, at.chunks, at.c8(j), w);
       // past the row's end dy and q are nothing (what was not copied, or a
       // NaN's step)
       if (n < CHUNK) {
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e)
-          if (e >= n) q[j][e] = gw[j][e] = 0.0f;
+          if (MODE == ROW_FULL || e >= n) q[j][e] = gw[j][e] = 0.0f;
       }
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
@@ -291,60 +323,63 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
       }
     }
     const float mean = __fmul_rn(row_sum(s, at.W, red, turn), share);
-    T* px = dx + r * lddx;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int n = in ? at.n[j] : 0;
+      const int n = in ? at.n(j) : 0;
       float t[CHUNK];
       if (dh) {
         if constexpr (SLOTS > 0)
           unpack(ring.take((slot * N + j) * 2 + 1), t);
         else
-          unpack(load_chunk<T, VEC>(dh + r * lddh + at.c8[j] * CHUNK, n), t);
+          unpack(load_chunk<T, VEC>(ph + j * jump, n), t);
       }
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
         const float v = __fmul_rn(inverse, __fmaf_rn(-q[j][e], mean, gw[j][e]));
         gw[j][e] = dh ? __fadd_rn(v, t[e]) : v;
       }
-      store_chunk<T, VEC>(px + at.c8[j] * CHUNK, n, gw[j], buf);
+      store_chunk<T, VEC>(px + j * jump, n, gw[j], buf);
     }
-    slot ^= 1;
+    px += stride * lddx;
+    if (SLOTS == 0)
+      pd += stride * lddy, ph += stride * lddh, pc += stride * ldc;
+    else
+      slot = slot == SLOTS - 1 ? 0 : slot + 1;
   }
   if (!part) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + at.c8[j] * CHUNK;  // rows of ldc floats
-    if (at.c8[j] < chunks) {
+    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + start + j * jump;  // rows of ldc floats
+    if (at.held(j)) {
       reinterpret_cast<float4*>(o)[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
       reinterpret_cast<float4*>(o)[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
   }
 }
 
-// dw[c] = (dw[c] +) the partial sums in a fixed order: 32 columns per CTA,
-// eight warps each over every eighth of them.
-__global__ void __launch_bounds__(NTHREADS) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, int64_t ldp,
-                                                              float* dw, int accumulate) {
-  __shared__ float sum[8][32];
+// dw[c] = (dw[c] +) the partial sums in a fixed order: 32 columns per CTA, 32
+// warps each over every 32nd sum, its loads issued eight at a time.
+__global__ void __launch_bounds__(1024) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, int64_t ldp, float* dw,
+                                                          int accumulate) {
+  __shared__ float sum[32][33];
   chain_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // ldp columns exist
   float s = 0.0f;
-  if (c < cols) {
-    int p = warp;
-    for (; p + 24 < parts; p += 32) {  // four loads at a time
-      const float a = part[p * ldp + c], b = part[(p + 8) * ldp + c], d = part[(p + 16) * ldp + c], e = part[(p + 24) * ldp + c];
-      s = __fadd_rn(s, __fadd_rn(__fadd_rn(a, b), __fadd_rn(d, e)));
-    }
-    for (; p < parts; p += 8) s = __fadd_rn(s, part[p * ldp + c]);
+  for (int p = warp; p < parts; p += 256) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p + 32 * i < parts ? __ldg(part + (int64_t)(p + 32 * i) * ldp + c) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __fadd_rn(s, v[i]);
   }
   sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < cols) {
+    float t = sum[0][lane];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s = __fadd_rn(s, sum[i][lane]);
-    dw[c] = accumulate ? __fadd_rn(dw[c], s) : s;
+    for (int i = 1; i < 32; ++i) t = __fadd_rn(t, sum[i][lane]);
+    dw[c] = accumulate ? __fadd_rn(dw[c], t) : t;
   }
 }
 
@@ -471,7 +506,18 @@ template <typename K>
 static bool allow_shared(K kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) == cudaSuccess;
 }
-constexpr int FORWARD_PER_SM = 3, BACKWARD_PER_SM = 3;  // CTAs of 256 threads
+static int row_mode(int64_t cols, const RowShape& s, bool vec) {
+  if (!vec) return ROW_SCALAR;
+  return cols == (int64_t)s.warps * norm_chunks(cols) * 256 ? ROW_FULL : ROW_VEC;
+}
+template <int N>
+struct Chunks {
+  static constexpr int value = N;
+};
+// CTAs of 256 threads per SM in a grid: two waves of three forward (110 us for
+// 16384 x 4096 in bf16; one wave 116), one of two backward, whose sums of dw
+// grow with the CTAs.
+constexpr int FORWARD_PER_SM = 6, BACKWARD_PER_SM = 2;
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
   if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
@@ -510,16 +556,21 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
   const RowShape shape = norm_shape(cols);
   const bool vec = chunk_aligned(x, ldx, dtype) && (!residual || chunk_aligned(residual, ldr, dtype)) &&
                    (!y || chunk_aligned(y, ldy, dtype)) && (!h || chunk_aligned(h, ldh, dtype));
-  const bool two = norm_chunks(cols) == 2;
+  const int mode = row_mode(cols, shape, vec);
   GC_BY_DTYPE(dtype, T, {
-    static const bool ready = allow_shared(k_rmsnorm<T, 2, true>) && allow_shared(k_rmsnorm<T, 4, true>) &&
-                              allow_shared(k_rmsnorm<T, 4, false>);
-    if (!ready) return GC_ERR_CUDA;
-    auto kern = two ? (vec ? k_rmsnorm<T, 2, true> : k_rmsnorm<T, 2, false>) : (vec ? k_rmsnorm<T, 4, true> : k_rmsnorm<T, 4, false>);
-    const size_t ring = two ? RowRing<T, 2, true>::forward_bytes(shape.threads) : RowRing<T, 4, true>::forward_bytes(shape.threads);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec, ring), s,
-                   static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows,
-                   cols, groups, shape.warps, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
+    auto go = [&](auto chunks) -> bool {
+      constexpr int N = decltype(chunks)::value;
+      static const bool ready = allow_shared(k_rmsnorm<T, N, ROW_SCALAR>) && allow_shared(k_rmsnorm<T, N, ROW_VEC>) &&
+                                allow_shared(k_rmsnorm<T, N, ROW_FULL>);
+      auto kern = mode == ROW_FULL ? k_rmsnorm<T, N, ROW_FULL> : mode == ROW_VEC ? k_rmsnorm<T, N, ROW_VEC> : k_rmsnorm<T, N, ROW_SCALAR>;
+      if (ready)
+        launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads,
+                       norm_shared(cols, shape, vec, RowRing<T, N, ROW_VEC>::forward_bytes(shape.threads)), s,
+                       static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows,
+                       cols, groups, shape.warps, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
+      return ready;
+    };
+    if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
@@ -552,7 +603,7 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   const int acc = (flags & GC_ACCUMULATE) ? 1 : 0;
   float* part = dw ? static_cast<float*>(workspace) : nullptr;
   auto join = [&](int parts) {
-    launch_chained(k_rmsnorm_dw_join, (unsigned)groups, NTHREADS, 0, s, (const float*)part, parts, cols, groups * 32, dw, acc);
+    launch_chained(k_rmsnorm_dw_join, (unsigned)groups, 1024, 0, s, (const float*)part, parts, cols, groups * 32, dw, acc);
   };
   if (rows == 0) {
     if (dw && !acc) join(0);
@@ -579,17 +630,24 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   }
   const RowShape shape = norm_shape(cols);
   const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
-  const bool two = norm_chunks(cols) == 2;
+  const int mode = row_mode(cols, shape, vec);
   GC_BY_DTYPE(dtype, T, {
-    static const bool ready = allow_shared(k_rmsnorm_backward<T, 2, true>) && allow_shared(k_rmsnorm_backward<T, 4, true>) &&
-                              allow_shared(k_rmsnorm_backward<T, 4, false>);
-    if (!ready) return GC_ERR_CUDA;
-    auto kern = two ? (vec ? k_rmsnorm_backward<T, 2, true> : k_rmsnorm_backward<T, 2, false>)
-                    : (vec ? k_rmsnorm_backward<T, 4, true> : k_rmsnorm_backward<T, 4, false>);
-    const size_t ring = two ? RowRing<T, 2, true>::backward_bytes(shape.threads) : RowRing<T, 4, true>::backward_bytes(shape.threads);
-    launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads, norm_shared(cols, shape, vec, ring), s,
-                   static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
-                   weight_dtype, rows, cols, groups, shape.warps, static_cast<T*>(dx), lddx, part);
+    auto go = [&](auto chunks) -> bool {
+      constexpr int N = decltype(chunks)::value;
+      static const bool ready = allow_shared(k_rmsnorm_backward<T, N, ROW_SCALAR>) &&
+                                allow_shared(k_rmsnorm_backward<T, N, ROW_VEC>) &&
+                                allow_shared(k_rmsnorm_backward<T, N, ROW_FULL>);
+      auto kern = mode == ROW_FULL  ? k_rmsnorm_backward<T, N, ROW_FULL>
+                  : mode == ROW_VEC ? k_rmsnorm_backward<T, N, ROW_VEC>
+                                    : k_rmsnorm_backward<T, N, ROW_SCALAR>;
+      if (ready)
+        launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads,
+                       norm_shared(cols, shape, vec, RowRing<T, N, ROW_VEC>::backward_bytes(shape.threads)), s,
+                       static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
+                       weight_dtype, rows, cols, groups, shape.warps, static_cast<T*>(dx), lddx, part);
+      return ready;
+    };
+    if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });
   if (dw) join(parts);
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
