@@ -4,51 +4,38 @@
 
 namespace gc {
 
-// The loops keep AHEAD rows' loads in flight while they work on one: with
-// rows on 16-byte boundaries (VEC) through rings in shared memory.  Four CTAs
-// per SM with 128 bytes per thread in flight are 128 KB; the two dies'
-// memories are 1.5 us away under load, and 6.7 TB/s is 44 KB per SM and us.
-template <typename T, bool VEC>
+// The loops keep AHEAD - 1 rows' loads in flight while they work on one, in
+// rings of shared memory.  Four CTAs per SM with 112 bytes per thread in
+// flight are 114 KB; the two dies' memories are about 1.5 us away under load,
+// and 6.7 TB/s is 44 KB per SM and us.
+template <typename T, bool SPAN>
 __global__ void __launch_bounds__(256, 4) k_act_compress(const T* x, int64_t ld, Tiling t, int8_t* codes, uint8_t* steps) {
   constexpr int AHEAD = 8 / (int)(sizeof(T) / 2);
-  __shared__ float4 shared[VEC ? Ring<T>::bytes(AHEAD, 256) / 16 : 1];
+  __shared__ float4 shared[Rows<T, SPAN>::bytes(AHEAD, 256) / 16];
   chain_wait();
   const Place p = place(t);
   const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
-  const T* px = x + p.r * ld + (int64_t)p.c8 * CHUNK;  // the next row to load
+  Rows<T, SPAN> in(shared, 256, x + p.r * ld, p.step * ld, p.c8, p.n, t.cols);
   int8_t* pc = codes + p.r * ldc + (int64_t)p.c8 * CHUNK;
   uint8_t* ps = steps + p.r * groups + (p.c8 >> 2);
-  const int64_t dx = p.step * ld, dc = p.step * ldc, ds = p.step * groups;
-  const Ring<T> ring(shared, 256);
+  const int64_t dc = p.step * ldc, ds = p.step * groups;
   int64_t r = p.r, next = p.r;
   auto copy = [&](int slot) {
-    if (VEC) {
-      if (next < p.end && p.n > 0) ring.copy(slot, px, p.n);
-      copy_group();
-      px += dx, next += p.step;
-    }
+    in.copy(slot, next < p.end);
+    copy_group();
+    next += p.step;
   };
 #pragma unroll
   for (int i = 0; i < AHEAD - 1; ++i) copy(i);
   int slot = 0;
   for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step, pc += dc, ps += ds) {
-    const int n = r < p.end ? p.n : 0;
-    Raw8<T> raw;
-    if (VEC) {
-      wait_groups<AHEAD - 2>();
-      raw = ring.take(slot);
-      copy((slot + AHEAD - 1) % AHEAD);
-      slot = (slot + 1) % AHEAD;
-    } else {
-      raw = load_chunk<T, false>(px, n);
-      px += dx;
-    }
     float v[CHUNK];
-    unpack(raw, v);
-    if (n == 0) {  // nothing was copied
-#pragma unroll
-      for (int e = 0; e < CHUNK; ++e) v[e] = 0.0f;
-    }
+    wait_groups<AHEAD - 2>();
+    in.landed();
+    in.take(slot, r < p.end ? p.n : 0, v);
+    in.done();
+    copy((slot + AHEAD - 1) % AHEAD);
+    slot = (slot + 1) % AHEAD;
     const uint32_t b = chunk_step(v);
     const uint2 c = chunk_codes(v, b);
     if (p.in && r < p.end) {
@@ -58,17 +45,20 @@ __global__ void __launch_bounds__(256, 4) k_act_compress(const T* x, int64_t ld,
   }
 }
 
-template <typename T, bool VEC, int ROWS>
-__global__ void __launch_bounds__(256, VEC ? 4 : 3) k_act_decompress(const int8_t* codes, const uint8_t* steps, Tiling t, T* out, int64_t ld) {
-  __shared__ float4 stage[VEC ? 1 : 512];
-  float* const buf = reinterpret_cast<float*>(stage) + (threadIdx.x >> 5) * 256;
+// Codes and steps take three registers a row: four rows ahead stay there.
+template <typename T, bool SPAN>
+__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
+    k_act_decompress(const int8_t* codes, const uint8_t* steps, Tiling t, T* out, int64_t ld) {
+  constexpr int ROWS = 4;
+  __shared__ float4 stage[SPAN ? 8 * RowsOut<T, SPAN>::STAGE : 1];
   chain_wait();
   const Place p = place(t);
   const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
   const int8_t* pc = codes + p.r * ldc + (int64_t)p.c8 * CHUNK;
   const uint8_t* ps = steps + p.r * groups + (p.c8 >> 2);
-  T* po = out + p.r * ld + (int64_t)p.c8 * CHUNK;
-  const int64_t dx = p.step * ld, dc = p.step * ldc, ds = p.step * groups;
+  RowsOut<T, SPAN> to(out + p.r * ld, p.step * ld, p.c8, t.cols);
+  float4* const own = stage + (SPAN ? (threadIdx.x >> 5) * RowsOut<T, SPAN>::STAGE : 0);
+  const int64_t dc = p.step * ldc, ds = p.step * groups;
   uint2 c[ROWS];
   uint32_t b[ROWS];
   auto fetch = [&](int64_t r) {
@@ -87,10 +77,10 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 3) k_act_decompress(const int8_
     for (int i = 0; i < ROWS; ++i) cn[i] = c[i], bn[i] = b[i];
     if (lead + ROWS * p.step < p.end) fetch(r + ROWS * p.step);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i, r += p.step, po += dx) {
+    for (int i = 0; i < ROWS; ++i, r += p.step) {
       float v[CHUNK];
       chunk_values(cn[i], bn[i], v);
-      store_chunk<T, VEC>(po, r < p.end ? p.n : 0, v, buf);
+      to.put(v, p.n, r < p.end, own);
     }
   }
 }
@@ -148,52 +138,40 @@ __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
   return far ? e : s;
 }
 
-template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
+template <typename T, int KIND, bool SPAN>
+__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
     k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, Tiling t, T* out, int64_t ldo, int8_t* gcodes,
             uint8_t* gsteps, int8_t* ucodes, uint8_t* usteps) {
   constexpr int AHEAD = 4 / (int)(sizeof(T) / 2);
-  // the ring, or the warps' staging
-  __shared__ float4 shared[VEC ? Ring<T>::bytes(2 * AHEAD, 256) / 16 : 512];
-  float* const buf = reinterpret_cast<float*>(shared) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  constexpr size_t RING = Rows<T, SPAN>::bytes(AHEAD, 256) / 16;
+  __shared__ float4 shared[2 * RING + (SPAN ? 8 * RowsOut<T, SPAN>::STAGE : 0)];
   chain_wait();
   const Place p = place(t);
-  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4, col = (int64_t)p.c8 * CHUNK;
-  const T *pg = gate + p.r * ldg + col, *pu = up + p.r * ldu + col;  // the next row to load
-  T* po = out + p.r * ldo + col;
-  int64_t ac = p.r * ldc + col, as = p.r * groups + (p.c8 >> 2);  // offsets of codes and steps
-  const int64_t dg = p.step * ldg, du = p.step * ldu, dd = p.step * ldo, dc = p.step * ldc, ds = p.step * groups;
-  const Ring<T> ring(shared, 256);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
+  Rows<T, SPAN> gin(shared, 256, gate + p.r * ldg, p.step * ldg, p.c8, p.n, t.cols);
+  Rows<T, SPAN> uin(shared + RING, 256, up + p.r * ldu, p.step * ldu, p.c8, p.n, t.cols);
+  RowsOut<T, SPAN> to(out + p.r * ldo, p.step * ldo, p.c8, t.cols);
+  float4* const own = shared + 2 * RING + (SPAN ? (threadIdx.x >> 5) * RowsOut<T, SPAN>::STAGE : 0);
+  int64_t ac = p.r * ldc + (int64_t)p.c8 * CHUNK, as = p.r * groups + (p.c8 >> 2);  // offsets of codes and steps
+  const int64_t dc = p.step * ldc, ds = p.step * groups;
   int64_t r = p.r, next = p.r;
   auto copy = [&](int slot) {
-    if (VEC) {
-      if (next < p.end && p.n > 0) ring.copy(2 * slot, pg, p.n), ring.copy(2 * slot + 1, pu, p.n);
-      copy_group();
-      pg += dg, pu += du, next += p.step;
-    }
+    gin.copy(slot, next < p.end), uin.copy(slot, next < p.end);
+    copy_group();
+    next += p.step;
   };
 #pragma unroll
   for (int i = 0; i < AHEAD - 1; ++i) copy(i);
   int slot = 0;
   for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step) {
     const int n = r < p.end ? p.n : 0;
-    Raw8<T> rg, ru;
-    if (VEC) {
-      wait_groups<AHEAD - 2>();
-      rg = ring.take(2 * slot), ru = ring.take(2 * slot + 1);
-      copy((slot + AHEAD - 1) % AHEAD);
-      slot = (slot + 1) % AHEAD;
-    } else {
-      rg = load_chunk<T, false>(pg, n), ru = load_chunk<T, false>(pu, n);
-      pg += dg, pu += du;
-    }
     float g[CHUNK], u[CHUNK];
-    unpack(rg, g);
-    unpack(ru, u);
-    if (n == 0) {  // nothing was copied
-#pragma unroll
-      for (int e = 0; e < CHUNK; ++e) g[e] = u[e] = 0.0f;
-    }
+    wait_groups<AHEAD - 2>();
+    gin.landed();
+    gin.take(slot, n, g), uin.take(slot, n, u);
+    gin.done(), uin.done();
+    copy((slot + AHEAD - 1) % AHEAD);
+    slot = (slot + 1) % AHEAD;
     if (gcodes) {
       const uint32_t bg = chunk_step(g), bu = chunk_step(u);
       const uint2 cg = chunk_codes(g, bg), cu = chunk_codes(u, bu);
@@ -209,39 +187,33 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
       float dp;
       g[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp)), u[e]);
     }
-    store_chunk<T, VEC>(po, n, g, buf);
-    po += dd;
+    to.put(g, n, r < p.end, own);
   }
 }
 
-template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
+template <typename T, int KIND, bool SPAN>
+__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
     k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
                      const uint8_t* usteps, Tiling t, T* dgate, int64_t lddg, T* dup, int64_t lddu, int8_t* ocodes,
                      uint8_t* osteps) {
-  constexpr int AHEAD = 4;
-  __shared__ float4 shared[VEC ? Ring<T>::bytes(AHEAD, 256) / 16 : 512];
+  constexpr int AHEAD = sizeof(T) == 2 ? 4 : 2;
+  constexpr size_t RING = Rows<T, SPAN>::bytes(AHEAD, 256) / 16;
+  __shared__ float4 shared[RING + (SPAN ? 8 * RowsOut<T, SPAN>::STAGE : 0)];
   __shared__ uint2 code_slots[2 * AHEAD * 256];
-  float* const buf = reinterpret_cast<float*>(shared) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
   chain_wait();
   const Place p = place(t);
-  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4, col = (int64_t)p.c8 * CHUNK;
-  T *pg = dgate + p.r * lddg + col, *pu = dup + p.r * lddu + col;
-  int64_t ac = p.r * ldc + col, as = p.r * groups + (p.c8 >> 2), r = p.r;
-  const int64_t dg = p.step * lddg, du = p.step * lddu, dc = p.step * ldc, ds = p.step * groups;
-  const Ring<T> ring(shared, 256);
+  const int64_t ldc = (int64_t)t.c8s * CHUNK, groups = t.c8s / 4;
+  Rows<T, SPAN> din(shared, 256, dout + p.r * lddo, p.step * lddo, p.c8, p.n, t.cols);
+  RowsOut<T, SPAN> gto(dgate + p.r * lddg, p.step * lddg, p.c8, t.cols), uto(dup + p.r * lddu, p.step * lddu, p.c8, t.cols);
+  float4* const own = shared + RING + (SPAN ? (threadIdx.x >> 5) * RowsOut<T, SPAN>::STAGE : 0);
   const CodeRing code(code_slots, 256);
-  // the next row to load
-  const T* pd = dout + p.r * lddo + col;
-  const int64_t dd = p.step * lddo;
+  int64_t ac = p.r * ldc + (int64_t)p.c8 * CHUNK, as = p.r * groups + (p.c8 >> 2), r = p.r;
+  const int64_t dc = p.step * ldc, ds = p.step * groups;
   int64_t next = p.r, nc = ac;
   auto copy = [&](int slot) {
-    if (next < p.end && p.in) {
-      if (VEC && p.n > 0) ring.copy(slot, pd, p.n);
-      code.copy(2 * slot, gcodes + nc, true), code.copy(2 * slot + 1, ucodes + nc, true);
-    }
+    din.copy(slot, next < p.end);
+    if (next < p.end && p.in) code.copy(2 * slot, gcodes + nc), code.copy(2 * slot + 1, ucodes + nc);
     copy_group();
-    if (VEC) pd += dd;
     next += p.step, nc += dc;
   };
   // step bytes of AHEAD rows, loaded as many rows earlier
@@ -265,20 +237,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
     for (int i = 0; i < AHEAD; ++i) {
       if (lead >= p.end) break;
       const int n = r < p.end ? p.n : 0;
-      wait_groups<AHEAD - 2>();
-      Raw8<T> rd;
-      if (VEC) {
-        rd = ring.take(i);
-      } else {
-        rd = load_chunk<T, false>(pd, n);
-        pd += dd;
-      }
-      const uint2 cg = code.take(2 * i), cu = code.take(2 * i + 1);
-      copy((i + AHEAD - 1) % AHEAD);
       float g[CHUNK], u[CHUNK], d[CHUNK], a[CHUNK];
-      chunk_values(cg, ng[i], g);
-      chunk_values(cu, nu[i], u);
-      unpack(rd, d);
+      wait_groups<AHEAD - 2>();
+      din.landed();
+      din.take(i, n, d);
+      din.done();
+      chunk_values(code.take(2 * i), ng[i], g);
+      chunk_values(code.take(2 * i + 1), nu[i], u);
+      copy((i + AHEAD - 1) % AHEAD);
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
         float dp;
@@ -288,8 +254,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
         a[e] = __fmul_rn(act, u[e]);
         u[e] = __fmul_rn(d[e], act);  // dup
       }
-      store_chunk<T, VEC>(pg, n, g, buf);
-      store_chunk<T, VEC>(pu, n, u, buf);
+      gto.put(g, n, r < p.end, own);
+      uto.put(u, n, r < p.end, own);
       if (ocodes) {
         const uint32_t b = chunk_step(a);
         const uint2 q = chunk_codes(a, b);
@@ -298,20 +264,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && VEC ? 4 : 3)
           if ((p.c8 & 3) == 0) osteps[as] = (uint8_t)b;
         }
       }
-      pg += dg, pu += du, ac += dc, as += ds, r += p.step, lead += p.step;
+      ac += dc, as += ds, r += p.step, lead += p.step;
     }
   }
 }
 
-// The widest tile (256 chunks to 4) that leaves at most a sixteenth of its
-// lanes past the rows' end, and about `ctas` CTAs.
-static Tiling make_tiling(int64_t rows, int64_t cols, int64_t ctas, dim3* grid) {
+// The widest tile (256 chunks to 4, or to 32 where a warp takes a span of one
+// row) that leaves at most a sixteenth of its lanes past the rows' end, and
+// about ACT_CTAS CTAs.
+constexpr int64_t ACT_CTAS = 152 * 8;  // two waves of four CTAs per SM
+static Tiling make_tiling(int64_t rows, int64_t cols, bool span, dim3* grid) {
   Tiling t;
   t.rows = rows, t.cols = (int32_t)cols, t.c8s = (int32_t)(act_ldc(cols) / CHUNK);
   t.wide = 8;
-  while (t.wide > 2 && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
+  while (t.wide > (span ? 5 : 2) && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
   const int64_t across = ((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide, at_once = 256 >> t.wide;
-  int64_t slabs = (ctas + across - 1) / across;
+  int64_t slabs = (ACT_CTAS + across - 1) / across;
   const int64_t most = (rows + at_once - 1) / at_once;
   if (slabs > most) slabs = most;
   if (slabs > 65535) slabs = 65535;
@@ -319,7 +287,13 @@ static Tiling make_tiling(int64_t rows, int64_t cols, int64_t ctas, dim3* grid) 
   *grid = dim3((unsigned)across, (unsigned)((rows + t.slab - 1) / t.slab));
   return t;
 }
-constexpr int64_t ACT_CTAS = 152 * 8;  // two waves of four CTAs per SM
+// The kernel for rows on 16-byte boundaries, or for any.  (fp32 takes spans
+// always: 8 fp32 per lane are 32 bytes, and copies of every other 16 bytes
+// reached 0.6 of the copy rate.)
+template <typename K>
+static K row_kernel(bool span, K aligned, K any) {
+  return span ? any : aligned;
+}
 
 }  // namespace gc
 
@@ -332,10 +306,10 @@ extern "C" gc_status gc_act_compress(const void* x, int64_t ld, int32_t dtype, i
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_matrix(x, ld, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK) return st;
+  const bool span = !chunk_aligned(x, ld, dtype);
   dim3 grid;
-  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
-  const bool vec = chunk_aligned(x, ld, dtype);
-  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_compress<T, true> : k_act_compress<T, false>, grid, 256, 0,
+  const Tiling t = make_tiling(rows, cols, span, &grid);
+  GC_BY_DTYPE(dtype, T, launch_chained(row_kernel(span, k_act_compress<T, sizeof(T) == 4>, k_act_compress<T, true>), grid, 256, 0,
                                        static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, t, codes,
                                        steps));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
@@ -348,10 +322,10 @@ extern "C" gc_status gc_act_decompress(const int8_t* codes, const uint8_t* steps
   if (st != GC_OK) return st;
   if (rows == 0) return GC_OK;
   if ((st = check_codes(codes, steps)) != GC_OK || (st = check_matrix(out, ldo, cols, dtype)) != GC_OK) return st;
+  const bool span = !chunk_aligned(out, ldo, dtype);
   dim3 grid;
-  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
-  const bool vec = chunk_aligned(out, ldo, dtype);
-  GC_BY_DTYPE(dtype, T, launch_chained(vec ? k_act_decompress<T, true, 4> : k_act_decompress<T, false, 4>, grid, 256, 0,
+  const Tiling t = make_tiling(rows, cols, span, &grid);
+  GC_BY_DTYPE(dtype, T, launch_chained(row_kernel(span, k_act_decompress<T, sizeof(T) == 4>, k_act_decompress<T, true>), grid, 256, 0,
                                        static_cast<cudaStream_t>(stream), codes, steps, t, static_cast<T*>(out),
                                        ldo));
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
@@ -372,12 +346,13 @@ extern "C" gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, c
   if (gate_codes || gate_steps || up_codes || up_steps)
     if ((st = check_codes(gate_codes, gate_steps)) != GC_OK || (st = check_codes(up_codes, up_steps)) != GC_OK)
       return st;
+  const bool span = !(chunk_aligned(gate, ldg, dtype) && chunk_aligned(up, ldu, dtype) && chunk_aligned(out, ldo, dtype));
   dim3 grid;
-  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
-  const bool vec = chunk_aligned(gate, ldg, dtype) && chunk_aligned(up, ldu, dtype) && chunk_aligned(out, ldo, dtype);
+  const Tiling t = make_tiling(rows, cols, span, &grid);
   GC_BY_DTYPE(dtype, T, {
-    auto kern = kind == GC_GATE_SILU ? (vec ? k_gated<T, GC_GATE_SILU, true> : k_gated<T, GC_GATE_SILU, false>)
-                                     : (vec ? k_gated<T, GC_GATE_GELU_TANH, true> : k_gated<T, GC_GATE_GELU_TANH, false>);
+    constexpr bool S = sizeof(T) == 4;
+    auto kern = kind == GC_GATE_SILU ? row_kernel(span, k_gated<T, GC_GATE_SILU, S>, k_gated<T, GC_GATE_SILU, true>)
+                                     : row_kernel(span, k_gated<T, GC_GATE_GELU_TANH, S>, k_gated<T, GC_GATE_GELU_TANH, true>);
     launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
                    static_cast<const T*>(up), ldu, t, static_cast<T*>(out), ldo, gate_codes, gate_steps, up_codes,
                    up_steps);
@@ -401,13 +376,14 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
     return st;
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
+  const bool span = !(chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype));
   dim3 grid;
-  const Tiling t = make_tiling(rows, cols, ACT_CTAS, &grid);
-  const bool vec = chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype);
+  const Tiling t = make_tiling(rows, cols, span, &grid);
   GC_BY_DTYPE(dtype, T, {
+    constexpr bool S = sizeof(T) == 4;
     auto kern = kind == GC_GATE_SILU
-                    ? (vec ? k_gated_backward<T, GC_GATE_SILU, true> : k_gated_backward<T, GC_GATE_SILU, false>)
-                    : (vec ? k_gated_backward<T, GC_GATE_GELU_TANH, true> : k_gated_backward<T, GC_GATE_GELU_TANH, false>);
+                    ? row_kernel(span, k_gated_backward<T, GC_GATE_SILU, S>, k_gated_backward<T, GC_GATE_SILU, true>)
+                    : row_kernel(span, k_gated_backward<T, GC_GATE_GELU_TANH, S>, k_gated_backward<T, GC_GATE_GELU_TANH, true>);
     launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
                    gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
                    out_codes, out_steps);

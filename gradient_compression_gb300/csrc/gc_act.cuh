@@ -66,63 +66,10 @@ struct alignas(16) Raw8 {
   T e[CHUNK];
 };
 
-// `n` of the 8 elements from p on, zeros after them.  VEC: p is 16-byte
-// aligned.  Read past L1, which keeps what is used again.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> load_chunk(const T* p, int n) {
-  Raw8<T> r;
-  if (VEC && n == CHUNK) {
-    uint4* w = reinterpret_cast<uint4*>(&r);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(r) / 16; ++i)
-      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "l"(reinterpret_cast<const uint4*>(p) + i)
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < CHUNK; ++i) r.e[i] = i < n ? p[i] : from_f32<T>(0.0f);
-  }
-  return r;
-}
-
 template <typename T>
 __device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[CHUNK]) {
 #pragma unroll
   for (int i = 0; i < CHUNK; ++i) v[i] = to_f32(r.e[i]);
-}
-
-// Writes n of the 8 values.  Without VEC a warp's chunks go through `buf`
-// (256 floats of its own): stores of one element per lane at 8 elements'
-// distance would be eight times the sectors.  All lanes of the warp take part.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[CHUNK], float* buf) {
-  if (VEC) {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < CHUNK; ++i) r.e[i] = from_f32<T>(v[i]);
-    if (n == CHUNK) {
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(r) / 16; ++i)
-        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&r)[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < CHUNK; ++i)
-        if (i < n) p[i] = r.e[i];
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-    reinterpret_cast<float4*>(buf)[2 * lane] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(buf)[2 * lane + 1] = make_float4(v[4], v[5], v[6], v[7]);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < CHUNK; ++j) {
-      const int from = 4 * j + (lane >> 3);
-      T* q = reinterpret_cast<T*>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(p), from));
-      if ((lane & 7) < __shfl_sync(FULL, n, from)) q[lane & 7] = from_f32<T>(buf[32 * j + lane]);
-    }
-  }
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -175,62 +122,212 @@ __device__ __forceinline__ uint2 load_codes(const int8_t* p) {
 }
 
 // ---------------------------------------------------------------- rings
-// Loads in flight without registers for them: each thread copies its own
-// chunks of the rows ahead into slots of shared memory that only it reads, so
-// that no barrier is needed.  Each copy_group() closes what was copied since
-// the last; wait_groups<N>() leaves the newest N groups in flight.
+// Loads in flight without registers for them: asynchronous copies of the rows
+// ahead into slots of shared memory.  Each copy_group() closes what was copied
+// since the last; wait_groups<N>() leaves the newest N groups in flight.
 __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A thread's slots of 8 elements: the threads' 16-byte words side by side.
-template <typename T>
-struct Ring {
-  static constexpr int WORDS = (int)sizeof(Raw8<T>) / 16;
-  uint32_t at;      // shared address of this thread's word of slot 0
-  uint32_t stride;  // bytes from word to word: 16 per thread
-  __device__ __forceinline__ Ring(void* shared, int threads)
-      : at((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16u), stride((uint32_t)threads * 16u) {}
-  static constexpr size_t bytes(int slots, int threads) { return (size_t)slots * WORDS * threads * 16; }
-  // n elements from p on (16-byte aligned, and valid even for n = 0), zeros after them.
-  __device__ __forceinline__ void copy(int slot, const T* p, int n) const {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {  // zeros after `bytes`
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// OUT words from byte `off` (0 to 15) on of OUT + 4 words.
+template <int OUT>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[OUT + 4], int off) {
+  if (off & 8) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      const int b = min(max(n * (int)sizeof(T) - 16 * i, 0), 16);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (uint32_t)(slot * WORDS + i) * stride),
-                   "l"(reinterpret_cast<const char*>(p) + (b > 0 ? 16 * i : 0)), "r"(b)
-                   : "memory");
+    for (int i = 0; i < OUT + 2; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < OUT + 1; ++i) w[i] = w[i + 1];
+  }
+  if (off & 3) {
+#pragma unroll
+    for (int i = 0; i < OUT; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
+  }
+}
+
+// A matrix's rows as the streaming kernels read them, a thread's chunk of
+// each row to come in a slot of its own.
+//  SPAN = false (16-bit types, rows on 16-byte boundaries): each thread copies
+//    and reads its own 16 bytes, no barrier is needed.
+//  SPAN = true (any rows): a warp's 32 chunks of a row are one span of 256
+//    elements; its 16-byte granules are copied as they lie in memory, whole
+//    lines at a time, and a lane shifts its elements out of the granules
+//    around them.  Every granule read holds an element of the span (only
+//    bytes before the first may be a neighbour's, and are not used).
+template <typename T, bool SPAN>
+struct Rows {
+  static constexpr int WORDS = SPAN ? 16 * (int)sizeof(T) + 1 : 1;  // granules of a warp's span, or of a lane
+  static constexpr size_t bytes(int slots, int threads) {
+    return SPAN ? (size_t)slots * (threads / 32) * WORDS * 16 : (size_t)slots * threads * 16;
+  }
+  uint32_t at, slot_bytes;
+  const T* next;     // the next row's chunk or span
+  int64_t step;      // elements from row to row
+  int len;           // elements of the chunk or span inside the row
+  uint32_t off, doff;  // SPAN: the current row's misalignment in bytes, its change from row to row
+  // c8: this thread's chunk; n: its elements inside the row
+  __device__ __forceinline__ Rows(void* shared, int threads, const T* row, int64_t stride, int c8, int n, int cols) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(shared);
+    step = stride;
+    if (SPAN) {
+      at = base + (threadIdx.x >> 5) * (WORDS * 16u);
+      slot_bytes = (uint32_t)(threads / 32) * (WORDS * 16u);
+      next = row + (int64_t)(c8 - lane) * CHUNK;
+      len = (int)min(max((int64_t)cols - (int64_t)(c8 - lane) * CHUNK, (int64_t)0), (int64_t)(32 * CHUNK));
+      off = (uint32_t)((uintptr_t)next & 15u), doff = (uint32_t)((uint64_t)stride * sizeof(T) & 15u);
+    } else {
+      at = base + threadIdx.x * 16u, slot_bytes = (uint32_t)threads * 16u;
+      next = row + (int64_t)c8 * CHUNK, len = n;
     }
   }
-  __device__ __forceinline__ void copy(int slot, const T* p) const {  // all 8
+  // Starts the next row's copy (nothing for a row that is not there).
+  __device__ __forceinline__ void copy(int slot, bool in) {
+    if (in && len > 0) {
+      const uint32_t to = at + (uint32_t)slot * slot_bytes;
+      if (SPAN) {
+        const int lane = threadIdx.x & 31, skip = (int)((uintptr_t)next & 15u), total = skip + len * (int)sizeof(T);
+        const char* from = reinterpret_cast<const char*>(next) - skip;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (uint32_t)(slot * WORDS + i) * stride),
-                   "l"(reinterpret_cast<const char*>(p) + 16 * i)
-                   : "memory");
+        for (int g = 0; g < WORDS; g += 32) {
+          const int i = g + lane, b = min(total - 16 * i, 16);
+          if (i < WORDS && b > 0) copy16(to + 16u * i, from + 16 * i, b);
+        }
+      } else {
+        copy16(to, next, len * (int)sizeof(T));
+      }
+    }
+    next += step;
   }
-  __device__ __forceinline__ Raw8<T> take(int slot) const {
-    Raw8<T> r;
-    uint4* w = reinterpret_cast<uint4*>(&r);
+  // All 8 elements of a chunk inside a row that is there (SPAN = false).
+  __device__ __forceinline__ void copy_whole(int slot) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (uint32_t)slot * slot_bytes), "l"(next) : "memory");
+    next += step;
+  }
+  // Before the first take of a row, after the wait: the other lanes' copies.
+  __device__ __forceinline__ void landed() const {
+    if (SPAN) __syncwarp();
+  }
+  // The current row's chunk as fp32; zeros from element n on.
+  __device__ __forceinline__ void take(int slot, int n, float (&v)[CHUNK]) const {
+    const uint32_t from = at + (uint32_t)slot * slot_bytes;
+    constexpr int W = CHUNK * (int)sizeof(T) / 4;
+    uint32_t w[W + 4];
+    if (SPAN) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "r"(at + (uint32_t)(slot * WORDS + i) * stride)
-                   : "memory");
-    return r;
+      for (int i = 0; i <= W / 4; ++i) {
+        const uint4 x = shared16(from + ((threadIdx.x & 31) * (W / 4) + i) * 16u);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+      shift_words<W>(w, (int)off);
+    } else {
+      const uint4 x = shared16(from);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    }
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(&r)[i] = w[i];
+    unpack(r, v);
+    if (n < CHUNK) {
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e)
+        if (e >= n) v[e] = 0.0f;
+    }
+  }
+  // After the last take of a row: on to the next, whose slot's predecessor may
+  // be copied over.
+  __device__ __forceinline__ void done() {
+    if (SPAN) off = (off + doff) & 15u, __syncwarp();
   }
 };
-// The same for 8 codes.
+
+// A matrix's rows as they are written.  SPAN: through `stage` (the warp's own),
+// shifted to whole granules; the ends element by element.
+template <typename T, bool SPAN>
+struct RowsOut {
+  static constexpr int STAGE = 16 * (int)sizeof(T) + 2;  // 16-byte words of a warp's stage
+  T* next;
+  int64_t step;
+  int len;
+  __device__ __forceinline__ RowsOut(T* row, int64_t stride, int c8, int cols) : step(stride) {
+    const int lane = threadIdx.x & 31;
+    next = row + (int64_t)(SPAN ? c8 - lane : c8) * CHUNK;
+    len = SPAN ? (int)min(max((int64_t)cols - (int64_t)(c8 - lane) * CHUNK, (int64_t)0), (int64_t)(32 * CHUNK)) : 0;
+  }
+  // n elements of the chunk; in: the row is there.  All lanes of the warp.
+  __device__ __forceinline__ void put(const float (&v)[CHUNK], int n, bool in, float4* stage) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) r.e[i] = from_f32<T>(v[i]);
+    if (SPAN) {
+      constexpr int W = CHUNK * (int)sizeof(T) / 16;
+      const int lane = threadIdx.x & 31;
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(stage);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(&r)[i];
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (1 + lane * W + i) * 16u), "r"(x.x), "r"(x.y),
+                     "r"(x.z), "r"(x.w)
+                     : "memory");
+      }
+      __syncwarp();
+      const int skip = (int)((uintptr_t)next & 15u), total = skip + (in ? len : 0) * (int)sizeof(T);
+      char* const to = reinterpret_cast<char*>(next) - skip;
+      if (in && len > 0)
+        for (int g = lane; 16 * g < total; g += 32) {
+          uint32_t w[8];
+          const uint4 a = shared16(at + (uint32_t)(g + (skip ? 0 : 1)) * 16u), b = shared16(at + (uint32_t)(g + 1) * 16u);
+          w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+          shift_words<4>(w, (16 - skip) & 15);
+          if (16 * g >= skip && 16 * g + 16 <= total) {
+            *reinterpret_cast<uint4*>(to + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            T* q = reinterpret_cast<T*>(to + 16 * g);
+#pragma unroll
+            for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
+              const int byte = 16 * g + e * (int)sizeof(T);
+              if (byte >= skip && byte < total) {
+                if (sizeof(T) == 4)
+                  reinterpret_cast<uint32_t*>(q)[e] = w[e % 4];
+                else
+                  reinterpret_cast<uint16_t*>(q)[e] = (uint16_t)(w[e / 2 % 4] >> (16 * (e & 1)));
+              }
+            }
+          }
+        }
+    } else if (in) {
+      if (n == CHUNK) {
+        *reinterpret_cast<uint4*>(next) = *reinterpret_cast<const uint4*>(&r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; ++i)
+          if (i < n) next[i] = r.e[i];
+      }
+    }
+    next += step;
+  }
+};
+
+// A thread's 8 codes of the rows ahead, in slots of its own.
 struct CodeRing {
   uint32_t at, stride;
   __device__ __forceinline__ CodeRing(void* shared, int threads)
       : at((uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 8u), stride((uint32_t)threads * 8u) {}
   static constexpr size_t bytes(int slots, int threads) { return (size_t)slots * threads * 8; }
-  __device__ __forceinline__ void copy(int slot, const int8_t* p, bool in) const {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at + (uint32_t)slot * stride), "l"(p), "r"(in ? 8 : 0)
-                 : "memory");
+  __device__ __forceinline__ void copy(int slot, const int8_t* p) const {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + (uint32_t)slot * stride), "l"(p) : "memory");
   }
   __device__ __forceinline__ uint2 take(int slot) const {
     uint2 c;

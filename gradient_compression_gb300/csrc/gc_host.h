@@ -56,9 +56,9 @@ inline gc_status check_matrix(const void* p, int64_t ld, int64_t cols, int32_t d
   if (ld < cols) return GC_ERR_LAYOUT;
   return ((uintptr_t)p & (dtype_bytes(dtype) - 1)) ? GC_ERR_ALIGNMENT : GC_OK;
 }
-// Rows that start on 16-byte boundaries.
+// 16-bit rows that start on 16-byte boundaries.
 inline bool chunk_aligned(const void* p, int64_t ld, int32_t dtype) {
-  return aligned16(p) && ld * (int64_t)dtype_bytes(dtype) % 16 == 0;
+  return dtype != GC_F32 && aligned16(p) && ld % 8 == 0;
 }
 inline gc_status check_codes(const int8_t* codes, const uint8_t* steps) {
   if (!codes || !steps) return GC_ERR_INVALID_ARG;

@@ -53,8 +53,8 @@ __device__ __forceinline__ void load_weights(const float4* ws, int chunks, int c
 }
 
 // How a row lies on its warps.
-constexpr int ROW_SCALAR = 0;  // rows not on 16-byte boundaries
-constexpr int ROW_VEC = 1;
+constexpr int ROW_SPAN = 0;    // any rows: a warp's 32 chunks as a span
+constexpr int ROW_CHUNKS = 1;  // 16-bit rows on 16-byte boundaries: each lane its own
 constexpr int ROW_FULL = 2;    // and every lane has N whole chunks: no bounds inside a row
 
 // A thread's N chunks of a row: the first, and the others 32 W chunks apart.
@@ -80,18 +80,71 @@ struct RowChunks {
   __device__ __forceinline__ bool held(int j) const { return MODE == ROW_FULL || c8(j) < chunks; }  // in the checkpoint
 };
 
-// Rows ahead come through rings in shared memory where two slots of them fit:
-// SLOTS - 1 rows are in flight while one is worked on.  (Registers for the
-// rows ahead cost the warps that hide the latency: 0.5 of the copy rate.)
-// Three or four slots instead of two, with 12 warps fewer, measured no faster.
+// Rows ahead come through rings in shared memory: SLOTS - 1 rows are in flight
+// while one is worked on (none for the widest rows that are spans or fp32,
+// whose second slot does not fit).  Registers for the rows ahead cost the warps that hide the
+// latency: 0.5 of the copy rate; three or four slots measured no faster.
 template <typename T, int N, int MODE>
-struct RowRing {
-  static constexpr bool USED = MODE != ROW_SCALAR && N * sizeof(T) <= 8;
-  static constexpr int SLOTS = USED ? 2 : 0;
-  static size_t forward_bytes(int threads) { return Ring<T>::bytes(2 * N * SLOTS, threads); }
-  static size_t backward_bytes(int threads) {
-    return Ring<T>::bytes(2 * N * SLOTS, threads) + CodeRing::bytes(N * SLOTS, threads);
+struct RowShared {
+  static constexpr bool SPAN = MODE == ROW_SPAN;
+  static constexpr int SLOTS = N * sizeof(T) <= 8 && !(SPAN && N == 4) ? 2 : 1;
+  static constexpr size_t rows(int threads) { return N * Rows<T, SPAN>::bytes(SLOTS, threads); }  // of one matrix
+  static constexpr size_t stage(int threads) { return SPAN ? (size_t)(threads / 32) * RowsOut<T, SPAN>::STAGE * 16 : 0; }
+  static constexpr size_t forward(int threads) { return 2 * rows(threads) + stage(threads); }
+  static constexpr size_t backward(int threads) {
+    return 2 * rows(threads) + stage(threads) + CodeRing::bytes(N * SLOTS, threads);
   }
+};
+
+// The N chunks of a matrix's rows.
+template <typename T, int N, int MODE>
+struct RowIn {
+  static constexpr bool SPAN = MODE == ROW_SPAN;
+  Rows<T, SPAN> in;
+  int64_t jump;  // elements from chunk to chunk
+  int len[N];    // of each chunk, or of each span
+  __device__ __forceinline__ RowIn(char* shared, const T* row, int64_t stride, const RowChunks<N, MODE>& at, int cols)
+      : in(shared, (int)blockDim.x, row, stride, at.first, at.n(0), cols), jump((int64_t)at.apart * CHUNK) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      len[j] = SPAN ? min(max(cols - (at.c8(j) - (int)(threadIdx.x & 31)) * CHUNK, 0), 32 * CHUNK) : at.n(j);
+  }
+  __device__ __forceinline__ void copy(int slot, bool there) {
+    const T* row = in.next;
+    if (there) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        in.next = row + j * jump, in.len = len[j];
+        if (MODE == ROW_FULL)
+          in.copy_whole(slot * N + j);
+        else
+          in.copy(slot * N + j, true);
+      }
+    }
+    in.next = row + in.step;
+  }
+  // a span's columns are whole lines apart: all N share the row's misalignment
+  __device__ __forceinline__ void take(int slot, int j, int n, float (&v)[CHUNK]) const { in.take(slot * N + j, n, v); }
+};
+template <typename T, int N, int MODE>
+struct RowTo {
+  static constexpr bool SPAN = MODE == ROW_SPAN;
+  RowsOut<T, SPAN> to;
+  int64_t jump;
+  int len[N];
+  __device__ __forceinline__ RowTo(T* row, int64_t stride, const RowChunks<N, MODE>& at, int cols)
+      : to(row, stride, at.first, cols), jump((int64_t)at.apart * CHUNK) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) len[j] = SPAN ? min(max(cols - (at.c8(j) - (int)(threadIdx.x & 31)) * CHUNK, 0), 32 * CHUNK) : 0;
+  }
+  // chunk j of the current row
+  __device__ __forceinline__ void put(int j, const float (&v)[CHUNK], int n, bool there, float4* stage) {
+    T* row = to.next;
+    to.next = row + j * jump, to.len = len[j];
+    to.put(v, n, there, stage);
+    to.next = row;
+  }
+  __device__ __forceinline__ void done() { to.next += to.step; }
 };
 
 template <typename T, int N, int MODE>
@@ -99,41 +152,29 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
               int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
               uint8_t* steps) {
-  constexpr bool VEC = MODE != ROW_SCALAR;
-  constexpr int SLOTS = RowRing<T, N, MODE>::SLOTS;
+  using S = RowShared<T, N, MODE>;
+  constexpr int SLOTS = S::SLOTS;
   __shared__ float red[2][16];
-  extern __shared__ float4 shared[];  // the weights, then the ring, or without VEC 256 floats per warp
+  extern __shared__ float4 shared[];  // the weights, then the rings and the warps' staging
   chain_wait();
   const RowChunks<N, MODE> at(warps, cols, groups);
-  float* const buf = reinterpret_cast<float*>(shared + 2 * at.chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
-  const Ring<T> ring(shared + 2 * at.chunks, (int)blockDim.x);
+  char* const rings = reinterpret_cast<char*>(shared + 2 * at.chunks);
+  const size_t one = S::rows((int)blockDim.x);
+  float4* const own = reinterpret_cast<float4*>(rings + 2 * one) + (threadIdx.x >> 5) * RowsOut<T, S::SPAN>::STAGE;
   const int64_t stride = (int64_t)gridDim.x * at.per, start = at.first * CHUNK;
-  const int jump = at.apart * CHUNK;  // elements from chunk to chunk
   int64_t r = (int64_t)blockIdx.x * at.per + at.sub, next = r;
-  const T *px = x + r * ldx + start, *pr = res + r * ldr + start;  // the next row to load
+  RowIn<T, N, MODE> xin(rings, x + r * ldx, stride * ldx, at, (int)cols);
+  RowIn<T, N, MODE> rin(rings + one, res + r * ldr, stride * ldr, at, (int)cols);
+  RowTo<T, N, MODE> hto(h + r * ldh, stride * ldh, at, (int)cols), yto(y + r * ldy, stride * ldy, at, (int)cols);
   auto copy = [&](int slot) {
-    if (next < rows) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (MODE == ROW_FULL) {
-          ring.copy((slot * N + j) * 2, px + j * jump);
-          if (res) ring.copy((slot * N + j) * 2 + 1, pr + j * jump);
-        } else if (at.n(j) > 0) {
-          ring.copy((slot * N + j) * 2, px + j * jump, at.n(j));
-          if (res) ring.copy((slot * N + j) * 2 + 1, pr + j * jump, at.n(j));
-        }
-      }
-    }
+    xin.copy(slot, next < rows);
+    if (res) rin.copy(slot, next < rows);
     copy_group();
-    next += stride, px += stride * ldx, pr += stride * ldr;
+    next += stride;
   };
-  if constexpr (SLOTS > 0) {
-#pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) copy(i);
-  }
+  if (SLOTS == 2) copy(0);
   if (y) stage_weights(shared, weight, wtype, cols, at.chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
-  T *ph = h + r * ldh + start, *py = y + r * ldy + start;
   int8_t* pc = codes + r * groups * ACT_GROUP + start;
   uint8_t* ps = steps + r * groups + (at.first >> 2);
   int turn = 0, slot = 0;
@@ -141,44 +182,32 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
     const bool in = r < rows;
     float v[N][CHUNK];
     float ss = 0.0f;
-    if constexpr (SLOTS > 0) {
-      wait_groups<SLOTS - 2>();
-    }
+    if (SLOTS == 1) copy(0);
+    wait_groups<0>();
+    xin.in.landed();
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
-      Raw8<T> a, b;
-      if constexpr (SLOTS > 0) {
-        a = ring.take((slot * N + j) * 2);
-        if (res) b = ring.take((slot * N + j) * 2 + 1);
-      } else {
-        a = load_chunk<T, VEC>(px + j * jump, n);
-        if (res) b = load_chunk<T, VEC>(pr + j * jump, n);
-      }
-      unpack(a, v[j]);
+      xin.take(slot, j, n, v[j]);
       if (res) {
         float t[CHUNK];
-        unpack(b, t);
+        rin.take(slot, j, n, t);
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
-      }
-      if (SLOTS > 0 && MODE != ROW_FULL && n == 0) {  // nothing was copied
-#pragma unroll
-        for (int e = 0; e < CHUNK; ++e) v[j][e] = 0.0f;
       }
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
     }
-    if constexpr (SLOTS > 0) {
-      copy(slot == 0 ? SLOTS - 1 : slot - 1);
-      slot = slot == SLOTS - 1 ? 0 : slot + 1;
-    } else {
-      px += stride * ldx, pr += stride * ldr;
+    xin.in.done();
+    if (res) rin.in.done();
+    if (SLOTS == 2) {
+      copy(slot ^ 1);
+      slot ^= 1;
     }
     if (h) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) store_chunk<T, VEC>(ph + j * jump, in ? at.n(j) : 0, v[j], buf);
-      ph += stride * ldh;
+      for (int j = 0; j < N; ++j) hto.put(j, v[j], at.n(j), in, own);
+      hto.done();
     }
     const float rs = rms_inverse(row_sum(ss, at.W, red, turn), share, eps);
     if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
         const uint32_t b = chunk_step(v[j]);
         const uint2 q = chunk_codes(v[j], b);
         if (in && at.held(j)) {
-          *reinterpret_cast<uint2*>(pc + j * jump) = q;
+          *reinterpret_cast<uint2*>(pc + j * at.apart * CHUNK) = q;
           if ((at.first & 3) == 0) ps[j * (at.apart >> 2)] = (uint8_t)b;
         }
       }
@@ -207,10 +236,11 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
         load_weights(shared, at.chunks, at.c8(j), t);
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e) t[e] = __fmul_rn(v[j][e], t[e]);
-        store_chunk<T, VEC>(py + j * jump, n, t, buf);
+        yto.put(j, t, at.n(j), in, own);
       }
     }
-    py += stride * ldy, pc += stride * groups * ACT_GROUP, ps += stride * groups;
+    yto.done();
+    pc += stride * groups * ACT_GROUP, ps += stride * groups;
   }
 }
 
@@ -222,38 +252,33 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
                        const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
                        int warps, T* dx, int64_t lddx, float* part) {
-  constexpr bool VEC = MODE != ROW_SCALAR;
-  constexpr int SLOTS = RowRing<T, N, MODE>::SLOTS;
+  using S = RowShared<T, N, MODE>;
+  constexpr int SLOTS = S::SLOTS;
   __shared__ float red[2][16];
   extern __shared__ float4 shared[];
   chain_wait();
   const RowChunks<N, MODE> at(warps, cols, groups);
-  float* const buf = reinterpret_cast<float*>(shared + 2 * at.chunks) + (VEC ? 0 : (threadIdx.x >> 5) * 256);
-  const Ring<T> ring(shared + 2 * at.chunks, (int)blockDim.x);
-  const CodeRing code(shared + 2 * at.chunks + Ring<T>::bytes(2 * N * SLOTS, 1) / 16 * blockDim.x, (int)blockDim.x);
+  char* const rings = reinterpret_cast<char*>(shared + 2 * at.chunks);
+  const size_t one = S::rows((int)blockDim.x);
+  float4* const own = reinterpret_cast<float4*>(rings + 2 * one) + (threadIdx.x >> 5) * RowsOut<T, S::SPAN>::STAGE;
+  const CodeRing code(rings + 2 * one + S::stage((int)blockDim.x), (int)blockDim.x);
   const int64_t stride = (int64_t)gridDim.x * at.per, ldc = groups * ACT_GROUP, start = at.first * CHUNK;
-  const int jump = at.apart * CHUNK;
   int64_t r = (int64_t)blockIdx.x * at.per + at.sub, next = r;
-  // the next row to load
-  const T *pd = dy + r * lddy + start, *ph = dh + r * lddh + start;
+  RowIn<T, N, MODE> din(rings, dy + r * lddy, stride * lddy, at, (int)cols);
+  RowIn<T, N, MODE> hin(rings + one, dh + r * lddh, stride * lddh, at, (int)cols);
+  RowTo<T, N, MODE> to(dx + r * lddx, stride * lddx, at, (int)cols);
   const int8_t* pc = codes + r * ldc + start;
   const uint8_t* ps = steps + r * groups + (at.first >> 2);
   auto copy = [&](int slot) {
+    din.copy(slot, next < rows);
+    if (dh) hin.copy(slot, next < rows);
     if (next < rows) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (MODE == ROW_FULL) {
-          ring.copy((slot * N + j) * 2, pd + j * jump);
-          if (dh) ring.copy((slot * N + j) * 2 + 1, ph + j * jump);
-        } else if (at.n(j) > 0) {
-          ring.copy((slot * N + j) * 2, pd + j * jump, at.n(j));
-          if (dh) ring.copy((slot * N + j) * 2 + 1, ph + j * jump, at.n(j));
-        }
-        if (at.held(j)) code.copy(slot * N + j, pc + j * jump, true);
-      }
+      for (int j = 0; j < N; ++j)
+        if (at.held(j)) code.copy(slot * N + j, pc + j * at.apart * CHUNK);
     }
     copy_group();
-    next += stride, pd += stride * lddy, ph += stride * lddh, pc += stride * ldc;
+    next += stride, pc += stride * ldc;
   };
   // step bytes and rstd, a row ahead
   uint32_t b[N];
@@ -265,14 +290,10 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     rs = in ? __ldg(rstd + row) : 0.0f;
     ps += stride * groups;
   };
-  if constexpr (SLOTS > 0) {
-#pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) copy(i);
-  }
+  if (SLOTS == 2) copy(0);
   fetch(r);
   stage_weights(shared, weight, wtype, cols, at.chunks);
   const float share = __fdiv_rn(1.0f, (float)cols);
-  T* px = dx + r * lddx + start;
   int turn = 0, slot = 0;
   float dw[N][CHUNK];
 #pragma unroll
@@ -285,35 +306,25 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
 #pragma unroll
     for (int j = 0; j < N; ++j) step[j] = b[j];
     const float inverse = rs;
-    if constexpr (SLOTS > 0) {
-      wait_groups<SLOTS - 2>();
-      copy(slot == 0 ? SLOTS - 1 : slot - 1);
-    }
+    if (SLOTS == 1) copy(0);
+    wait_groups<0>();
+    din.in.landed();
+    if (SLOTS == 2) copy(slot ^ 1);
     if (lead + stride < rows) fetch(r + stride);
     float gw[N][CHUNK], q[N][CHUNK];
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
-      Raw8<T> d;
-      uint2 c = make_uint2(0u, 0u);
-      if constexpr (SLOTS > 0) {
-        d = ring.take((slot * N + j) * 2);
-        c = code.take(slot * N + j);
-      } else {
-        d = load_chunk<T, VEC>(pd + j * jump, n);
-        if (in && at.held(j)) c = load_codes(pc + j * jump);
-      }
       float w[CHUNK];
-      chunk_values(c, step[j], q[j]);
-      unpack(d, gw[j]);
+      din.take(slot, j, n, gw[j]);
+      chunk_values(code.take(slot * N + j), step[j], q[j]);
       load_weights(shared, at.chunks, at.c8(j), w);
-      // past the row's end dy and q are nothing (what was not copied, or a
-      // NaN's step)
+      // past the row's end q is nothing (what was not copied, or a NaN's step)
       if (n < CHUNK) {
 #pragma unroll
         for (int e = 0; e < CHUNK; ++e)
-          if (MODE == ROW_FULL || e >= n) q[j][e] = gw[j][e] = 0.0f;
+          if (MODE == ROW_FULL || e >= n) q[j][e] = 0.0f;
       }
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
@@ -327,29 +338,23 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
       float t[CHUNK];
-      if (dh) {
-        if constexpr (SLOTS > 0)
-          unpack(ring.take((slot * N + j) * 2 + 1), t);
-        else
-          unpack(load_chunk<T, VEC>(ph + j * jump, n), t);
-      }
+      if (dh) hin.take(slot, j, n, t);
 #pragma unroll
       for (int e = 0; e < CHUNK; ++e) {
         const float v = __fmul_rn(inverse, __fmaf_rn(-q[j][e], mean, gw[j][e]));
         gw[j][e] = dh ? __fadd_rn(v, t[e]) : v;
       }
-      store_chunk<T, VEC>(px + j * jump, n, gw[j], buf);
+      to.put(j, gw[j], at.n(j), in, own);
     }
-    px += stride * lddx;
-    if (SLOTS == 0)
-      pd += stride * lddy, ph += stride * lddh, pc += stride * ldc;
-    else
-      slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    to.done();
+    din.in.done();
+    if (dh) hin.in.done();
+    if (SLOTS == 2) slot ^= 1;
   }
   if (!part) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + start + j * jump;  // rows of ldc floats
+    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + start + j * at.apart * CHUNK;  // rows of ldc floats
     if (at.held(j)) {
       reinterpret_cast<float4*>(o)[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
       reinterpret_cast<float4*>(o)[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
@@ -498,17 +503,15 @@ static int norm_grid(int64_t rows, const RowShape& s, int per_sm) {
   const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * per_sm * 256 / s.threads;
   return (int)(ctas < most ? ctas : most);
 }
-// Shared memory: the weights, and the ring or without VEC the warps' staging.
-static size_t norm_shared(int64_t cols, const RowShape& s, bool vec, size_t ring) {
-  return (size_t)act_ldc(cols) * sizeof(float) + (vec ? ring : (size_t)s.threads * 32);
-}
-template <typename K>
-static bool allow_shared(K kern) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) == cudaSuccess;
+// Shared memory for the widest rows, asked for once per kernel.
+template <auto KERN>
+static bool allow_shared() {
+  static const bool ok = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 232192) == cudaSuccess;
+  return ok;
 }
 static int row_mode(int64_t cols, const RowShape& s, bool vec) {
-  if (!vec) return ROW_SCALAR;
-  return cols == (int64_t)s.warps * norm_chunks(cols) * 256 ? ROW_FULL : ROW_VEC;
+  if (!vec) return ROW_SPAN;
+  return cols == (int64_t)s.warps * norm_chunks(cols) * 256 ? ROW_FULL : ROW_CHUNKS;
 }
 template <int N>
 struct Chunks {
@@ -560,15 +563,18 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
   GC_BY_DTYPE(dtype, T, {
     auto go = [&](auto chunks) -> bool {
       constexpr int N = decltype(chunks)::value;
-      static const bool ready = allow_shared(k_rmsnorm<T, N, ROW_SCALAR>) && allow_shared(k_rmsnorm<T, N, ROW_VEC>) &&
-                                allow_shared(k_rmsnorm<T, N, ROW_FULL>);
-      auto kern = mode == ROW_FULL ? k_rmsnorm<T, N, ROW_FULL> : mode == ROW_VEC ? k_rmsnorm<T, N, ROW_VEC> : k_rmsnorm<T, N, ROW_SCALAR>;
-      if (ready)
+      constexpr bool ANY = sizeof(T) == 4;  // fp32 rows are spans always
+      auto run = [&](auto kern, size_t ring) -> bool {
         launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads,
-                       norm_shared(cols, shape, vec, RowRing<T, N, ROW_VEC>::forward_bytes(shape.threads)), s,
-                       static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows,
-                       cols, groups, shape.warps, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
-      return ready;
+                       (size_t)groups * ACT_GROUP * sizeof(float) + ring, s, static_cast<const T*>(x), ldx,
+                       static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows, cols, groups, shape.warps,
+                       static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
+        return true;
+      };
+      constexpr int FULL = ANY ? ROW_SPAN : ROW_FULL, LANES = ANY ? ROW_SPAN : ROW_CHUNKS;
+      if (mode == ROW_FULL) return allow_shared<k_rmsnorm<T, N, FULL>>() && run(k_rmsnorm<T, N, FULL>, RowShared<T, N, FULL>::forward(shape.threads));
+      if (mode == ROW_CHUNKS) return allow_shared<k_rmsnorm<T, N, LANES>>() && run(k_rmsnorm<T, N, LANES>, RowShared<T, N, LANES>::forward(shape.threads));
+      return allow_shared<k_rmsnorm<T, N, ROW_SPAN>>() && run(k_rmsnorm<T, N, ROW_SPAN>, RowShared<T, N, ROW_SPAN>::forward(shape.threads));
     };
     if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });
@@ -634,18 +640,18 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   GC_BY_DTYPE(dtype, T, {
     auto go = [&](auto chunks) -> bool {
       constexpr int N = decltype(chunks)::value;
-      static const bool ready = allow_shared(k_rmsnorm_backward<T, N, ROW_SCALAR>) &&
-                                allow_shared(k_rmsnorm_backward<T, N, ROW_VEC>) &&
-                                allow_shared(k_rmsnorm_backward<T, N, ROW_FULL>);
-      auto kern = mode == ROW_FULL  ? k_rmsnorm_backward<T, N, ROW_FULL>
-                  : mode == ROW_VEC ? k_rmsnorm_backward<T, N, ROW_VEC>
-                                    : k_rmsnorm_backward<T, N, ROW_SCALAR>;
-      if (ready)
+      constexpr bool ANY = sizeof(T) == 4;  // fp32 rows are spans always
+      auto run = [&](auto kern, size_t ring) -> bool {
         launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads,
-                       norm_shared(cols, shape, vec, RowRing<T, N, ROW_VEC>::backward_bytes(shape.threads)), s,
-                       static_cast<const T*>(dy), lddy, static_cast<const T*>(dh), lddh, codes, steps, rstd, weight,
-                       weight_dtype, rows, cols, groups, shape.warps, static_cast<T*>(dx), lddx, part);
-      return ready;
+                       (size_t)groups * ACT_GROUP * sizeof(float) + ring, s, static_cast<const T*>(dy), lddy,
+                       static_cast<const T*>(dh), lddh, codes, steps, rstd, weight, weight_dtype, rows, cols, groups,
+                       shape.warps, static_cast<T*>(dx), lddx, part);
+        return true;
+      };
+      constexpr int FULL = ANY ? ROW_SPAN : ROW_FULL, LANES = ANY ? ROW_SPAN : ROW_CHUNKS;
+      if (mode == ROW_FULL) return allow_shared<k_rmsnorm_backward<T, N, FULL>>() && run(k_rmsnorm_backward<T, N, FULL>, RowShared<T, N, FULL>::backward(shape.threads));
+      if (mode == ROW_CHUNKS) return allow_shared<k_rmsnorm_backward<T, N, LANES>>() && run(k_rmsnorm_backward<T, N, LANES>, RowShared<T, N, LANES>::backward(shape.threads));
+      return allow_shared<k_rmsnorm_backward<T, N, ROW_SPAN>>() && run(k_rmsnorm_backward<T, N, ROW_SPAN>, RowShared<T, N, ROW_SPAN>::backward(shape.threads));
     };
     if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });

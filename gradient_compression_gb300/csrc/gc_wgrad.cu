@@ -193,21 +193,35 @@ __device__ __forceinline__ uint32_t codes_bf16_any(uint32_t w, uint32_t step) {
 // The bytes of a word come out in the order 0, 2, 1, 3, so accumulator columns
 // 4 q + 1 and 4 q + 2 hold columns 4 q + 2 and 4 q + 1; the result undoes it.
 
-// 8 elements of dy from column c on, as they are; 0 outside [0, n).
-template <typename T>
-struct Dy8 {
-  T e[8];
-};
+// 8 elements of dy from column c on, as they are; 0 outside [0, n).  Without
+// VEC the row may start anywhere: the 16-byte granules that hold an element of
+// the 8 are read as they lie, and the elements shifted out of them.
 template <typename T, bool VEC>
-__device__ __forceinline__ Dy8<T> load8(const T* row, int64_t c, int64_t n) {
-  Dy8<T> v;
-  if (VEC && c + 8 <= n) {
+__device__ __forceinline__ Raw8<T> load8(const T* row, int64_t c, int64_t n) {
+  constexpr int W = CHUNK * (int)sizeof(T) / 4;
+  const int in = (int)max((int64_t)0, min((int64_t)CHUNK, n - c));
+  Raw8<T> v;
+  uint4* out = reinterpret_cast<uint4*>(&v);
+  if (VEC && in == CHUNK) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(v.e)[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
-  } else {
+    for (int i = 0; i < W / 4; ++i) out[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+    return v;
+  }
+  const int skip = (int)((uintptr_t)(row + c) & 15u), total = in > 0 ? skip + in * (int)sizeof(T) : 0;
+  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + c) - skip);
+  uint32_t w[W + 4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v.e[i] = c + i < n ? row[c + i] : from_f32<T>(0.0f);
+  for (int i = 0; i <= W / 4; ++i) {
+    const uint4 x = 16 * i < total ? __ldg(from + i) : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+  }
+  shift_words<W>(w, skip);
+#pragma unroll
+  for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(&v)[i] = w[i];
+  if (in < CHUNK) {
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i)
+      if (i >= in) v.e[i] = from_f32<T>(0.0f);
   }
   return v;
 }
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         if constexpr (TMA) {
           if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
         } else {
-          Dy8<T> d[AN];
+          Raw8<T> d[AN];
 #pragma unroll
           for (int i = 0; i < AN; ++i) {
             const int64_t t = m.t0 + (int64_t)it * KT + WG_TEAM * (AR * i + lane / AL) + w;
