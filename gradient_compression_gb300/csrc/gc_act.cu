@@ -269,24 +269,6 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
   }
 }
 
-// The widest tile (256 chunks to 4, or to 32 where a warp takes a span of one
-// row) that leaves at most a sixteenth of its lanes past the rows' end, and
-// about ACT_CTAS CTAs.
-constexpr int64_t ACT_CTAS = 152 * 8;  // two waves of four CTAs per SM
-static Tiling make_tiling(int64_t rows, int64_t cols, bool span, dim3* grid) {
-  Tiling t;
-  t.rows = rows, t.cols = (int32_t)cols, t.c8s = (int32_t)(act_ldc(cols) / CHUNK);
-  t.wide = 8;
-  while (t.wide > (span ? 5 : 2) && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
-  const int64_t across = ((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide, at_once = 256 >> t.wide;
-  int64_t slabs = (ACT_CTAS + across - 1) / across;
-  const int64_t most = (rows + at_once - 1) / at_once;
-  if (slabs > most) slabs = most;
-  if (slabs > 65535) slabs = 65535;
-  t.slab = ((rows + slabs - 1) / slabs + at_once - 1) / at_once * at_once;
-  *grid = dim3((unsigned)across, (unsigned)((rows + t.slab - 1) / t.slab));
-  return t;
-}
 // The kernel for rows on 16-byte boundaries, or for any.  (fp32 takes spans
 // always: 8 fp32 per lane are 32 bytes, and copies of every other 16 bytes
 // reached 0.6 of the copy rate.)

@@ -271,7 +271,7 @@ struct RowsOut {
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i) r.e[i] = from_f32<T>(v[i]);
     if (SPAN) {
-      constexpr int W = CHUNK * (int)sizeof(T) / 16;
+      constexpr int W = CHUNK * (int)sizeof(T) / 16, E = 16 / (int)sizeof(T);  // granules per lane, elements per granule
       const int lane = threadIdx.x & 31;
       const uint32_t at = (uint32_t)__cvta_generic_to_shared(stage);
       __syncwarp();
@@ -283,30 +283,36 @@ struct RowsOut {
                      : "memory");
       }
       __syncwarp();
-      const int skip = (int)((uintptr_t)next & 15u), total = skip + (in ? len : 0) * (int)sizeof(T);
+      const int skip = (int)((uintptr_t)next & 15u), total = in && len > 0 ? skip + len * (int)sizeof(T) : 0;
       char* const to = reinterpret_cast<char*>(next) - skip;
-      if (in && len > 0)
-        for (int g = lane; 16 * g < total; g += 32) {
-          uint32_t w[8];
-          const uint4 a = shared16(at + (uint32_t)(g + (skip ? 0 : 1)) * 16u), b = shared16(at + (uint32_t)(g + 1) * 16u);
-          w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-          shift_words<4>(w, (16 - skip) & 15);
-          if (16 * g >= skip && 16 * g + 16 <= total) {
-            *reinterpret_cast<uint4*>(to + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
-            T* q = reinterpret_cast<T*>(to + 16 * g);
 #pragma unroll
-            for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
-              const int byte = 16 * g + e * (int)sizeof(T);
-              if (byte >= skip && byte < total) {
-                if (sizeof(T) == 4)
-                  reinterpret_cast<uint32_t*>(q)[e] = w[e % 4];
-                else
-                  reinterpret_cast<uint16_t*>(q)[e] = (uint16_t)(w[e / 2 % 4] >> (16 * (e & 1)));
-              }
-            }
+      for (int i = 0; i < W; ++i) {  // whole granules
+        const int g = lane + 32 * i;
+        uint32_t w[8];
+        const uint4 a = shared16(at + (uint32_t)(g + (skip ? 0 : 1)) * 16u), b = shared16(at + (uint32_t)(g + 1) * 16u);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        shift_words<4>(w, (16 - skip) & 15);
+        if (16 * g >= skip && 16 * g + 16 <= total) *reinterpret_cast<uint4*>(to + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      // the first granule's elements and the last one's where they are not
+      // whole, a lane for each
+      if (skip != 0 || (total & 15) != 0) {
+        const int last = total >> 4, g = lane < E ? 0 : last;
+        const int byte = 16 * g + (lane & (E - 1)) * (int)sizeof(T);
+        const bool whole = 16 * g >= skip && 16 * g + 16 <= total;
+        if (lane < 2 * E && (lane < E || last > 0) && !whole && byte >= skip && byte < total) {
+          const uint32_t from = at + 16u + (uint32_t)(byte - skip);
+          if (sizeof(T) == 4) {
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+            *reinterpret_cast<uint32_t*>(to + byte) = x;
+          } else {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
+            *reinterpret_cast<uint16_t*>(to + byte) = x;
           }
         }
+      }
     } else if (in) {
       if (n == CHUNK) {
         *reinterpret_cast<uint4*>(next) = *reinterpret_cast<const uint4*>(&r);
@@ -363,6 +369,24 @@ __device__ __forceinline__ Place place(const Tiling& t) {
   return p;
 }
 
+// The widest tile (256 chunks to 4, or to 32 where a warp takes a span of one
+// row) that leaves at most a sixteenth of its lanes past the rows' end, and
+// about ACT_CTAS CTAs.
+constexpr int64_t ACT_CTAS = 152 * 8;  // two waves of four CTAs per SM
+inline Tiling make_tiling(int64_t rows, int64_t cols, bool span, dim3* grid) {
+  Tiling t;
+  t.rows = rows, t.cols = (int32_t)cols, t.c8s = (int32_t)(act_ldc(cols) / CHUNK);
+  t.wide = 8;
+  while (t.wide > (span ? 5 : 2) && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
+  const int64_t across = ((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide, at_once = 256 >> t.wide;
+  int64_t slabs = (ACT_CTAS + across - 1) / across;
+  const int64_t most = (rows + at_once - 1) / at_once;
+  if (slabs > most) slabs = most;
+  if (slabs > 65535) slabs = 65535;
+  t.slab = ((rows + slabs - 1) / slabs + at_once - 1) / at_once * at_once;
+  *grid = dim3((unsigned)across, (unsigned)((rows + t.slab - 1) / t.slab));
+  return t;
+}
 }  // namespace gc
 
 // Runs a statement with T the element type of a valid dtype.

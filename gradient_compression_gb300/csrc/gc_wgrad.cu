@@ -10,7 +10,10 @@ namespace gc {
 // Mathematics and precision.  q's code has 7 bits and its step is a power of
 // two, so q is exact in bf16; a bf16 dy is too, an fp16 dy is the exact sum
 // of two bf16 terms (11 bits = 8 + 3) and an fp32 dy of three (24 = 8 + 8 +
-// 8).  Every product is therefore exact and only the fp32 sums round.
+// 8).  Every product is therefore exact and only the fp32 sums round.  The
+// terms, and a bf16 dy whose rows cannot be copied in bulk, are written to the
+// workspace first: 8192 x 1024 x 1024 in fp16 takes 43 us so, and took 52 with
+// dy split beside the MMAs by the unpacking warps.
 //
 // Tile.  A CTA computes 256 (n) x 256 (k) of dw: two accumulators of 128 x
 // 256 fp32, all 512 columns of the SM's tensor memory.  q has to be unpacked
@@ -50,7 +53,7 @@ constexpr int WG_SMEM = WG_RING + WG_OUT * 4096;  // + a 32 x 32 tile of the res
 constexpr int WG_CHAIN = 3200;             // rows of a chain
 
 struct WgArgs {
-  const void* dy;
+  const __nv_bfloat16* dy;      // the terms, one [rows, lddy] after another
   int64_t lddy, rows, n, k, ldc;
   const int8_t* codes;
   const uint8_t* steps;
@@ -88,13 +91,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -193,39 +195,33 @@ __device__ __forceinline__ uint32_t codes_bf16_any(uint32_t w, uint32_t step) {
 // The bytes of a word come out in the order 0, 2, 1, 3, so accumulator columns
 // 4 q + 1 and 4 q + 2 hold columns 4 q + 2 and 4 q + 1; the result undoes it.
 
-// 8 elements of dy from column c on, as they are; 0 outside [0, n).  Without
-// VEC the row may start anywhere: the 16-byte granules that hold an element of
-// the 8 are read as they lie, and the elements shifted out of them.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int64_t c, int64_t n) {
-  constexpr int W = CHUNK * (int)sizeof(T) / 4;
+// 8 elements of dy from column c on; 0 outside [0, n).  The row may start
+// anywhere: the 16-byte granules that hold an element of the 8 are read as
+// they lie, and the elements shifted out of them.
+__device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16* row, int64_t c, int64_t n) {
   const int in = (int)max((int64_t)0, min((int64_t)CHUNK, n - c));
-  Raw8<T> v;
-  uint4* out = reinterpret_cast<uint4*>(&v);
-  if (VEC && in == CHUNK) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) out[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
-    return v;
-  }
-  const int skip = (int)((uintptr_t)(row + c) & 15u), total = in > 0 ? skip + in * (int)sizeof(T) : 0;
+  const int skip = (int)((uintptr_t)(row + c) & 15u), total = in > 0 ? skip + 2 * in : 0;
   const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + c) - skip);
-  uint32_t w[W + 4];
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i <= W / 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint4 x = 16 * i < total ? __ldg(from + i) : make_uint4(0u, 0u, 0u, 0u);
     w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
   }
-  shift_words<W>(w, skip);
+  shift_words<4>(w, skip);
+  Raw8<__nv_bfloat16> v;
 #pragma unroll
-  for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(&v)[i] = w[i];
+  for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(&v)[i] = w[i];
   if (in < CHUNK) {
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i)
-      if (i >= in) v.e[i] = from_f32<T>(0.0f);
+      if (i >= in) v.e[i] = from_f32<__nv_bfloat16>(0.0f);
   }
   return v;
 }
 
+// TMA: the terms of dy come by bulk tensor copies; else a bf16 dy whose rows
+// do not start on 16-byte boundaries, by the unpacking warps' own loads.
 template <int PARTS, bool TMA>
 struct WgShape {
   static constexpr int M = PARTS == 1 ? 256 : 128;      // n of a tile
@@ -361,12 +357,9 @@ __device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map
   return ok;
 }
 
-// TMA: dy is bf16 and its rows start on 16-byte boundaries, so that its
-// tiles come by bulk tensor copies; else the unpacking warps load it too,
-// split into PARTS bf16 terms.  A CTA takes every gridDim.x-th item (a tile and
-// a split of the rows); all roles walk the same items, and `g` counts the
-// stages.
-template <typename T, int PARTS, bool TMA, bool VEC>
+// A CTA takes every gridDim.x-th item (a tile and a split of the rows); all
+// roles walk the same items, and `g` counts the stages.
+template <int PARTS, bool TMA>
 __global__ void __launch_bounds__(WG_THREADS, 1)
     k_weight_grad(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap out_map,
                   const __grid_constant__ WgArgs a) {
@@ -415,8 +408,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     const uint32_t off0 = PARTS * A_BYTES + (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + (uint32_t)(((lane & 7) ^ w) << 4);
     const uint32_t off1 =
         PARTS * A_BYTES + (uint32_t)(lane >> 3) * BLOCK + (uint32_t)w * 128u + 512u + (uint32_t)(((lane & 7) ^ (w + 4)) << 4);
-    // dy: a row takes AL lanes
-    constexpr int AL = S::M / 8, AR = 32 / AL, AN = ROWS / AR;  // lanes per row, rows at a time, times
     for (int i0 = blockIdx.x; ok && i0 < a.items; i0 += gridDim.x) {
       const WgItem m = item_at(i0);
       const int64_t kc = min(m.k0 + 8 * lane, a.ldc - 8), span = m.t1 - m.t0;
@@ -455,39 +446,19 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         if constexpr (TMA) {
           if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
         } else {
-          Raw8<T> d[AN];
+          // rows w, w + 4, ... of dy, 32 lanes each
+          Raw8<__nv_bfloat16> d[ROWS];
 #pragma unroll
-          for (int i = 0; i < AN; ++i) {
-            const int64_t t = m.t0 + (int64_t)it * KT + WG_TEAM * (AR * i + lane / AL) + w;
+          for (int i = 0; i < ROWS; ++i) {
+            const int64_t t = m.t0 + (int64_t)it * KT + WG_TEAM * i + w;
             const bool in = t < m.t1;  // rows past the split's end: zeros
-            d[i] = load8<T, VEC>(static_cast<const T*>(a.dy) + (in ? t : m.t0) * a.lddy, m.n0 + 8 * (lane % AL), in ? a.n : 0);
+            d[i] = load8(a.dy + (in ? t : m.t0) * a.lddy, m.n0 + 8 * lane, in ? a.n : 0);
           }
           if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
 #pragma unroll
-          for (int i = 0; i < AN; ++i) {
-            const int t = WG_TEAM * (AR * i + lane / AL) + w;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(d[i].e[j]);
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-              uint32_t x[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                // the upper halves: truncation to bf16, so that nothing overflows
-                x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
-                if (p + 1 < PARTS) {
-#pragma unroll
-                  for (int e = 2 * j; e < 2 * j + 2; ++e) {
-                    const float top = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
-                    v[e] = isinf(v[e]) ? 0.0f : __fsub_rn(v[e], top);
-                  }
-                }
-              }
-              st_shared16(st + p * A_BYTES + (uint32_t)(lane % AL / 8) * BLOCK + (uint32_t)t * 128u +
-                              (uint32_t)(((lane & 7) ^ (t & 7)) << 4),
-                          x[0], x[1], x[2], x[3]);
-            }
+          for (int i = 0; i < ROWS; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(&d[i]);
+            st_shared16(st + ((i & 1) ? off1 : off0) - A_BYTES + 1024u * (i >> 1), x.x, x.y, x.z, x.w);
           }
         }
         uint32_t odd = 0u;
@@ -527,10 +498,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         for (int it = 0; it < m.iters; ++it, ++g) {
           const int s = g % STAGES;
           if (!(ok = mbar_wait(empty(s), ((g / STAGES) & 1) ^ 1))) break;
-          mbar_expect(full_a(s), A_BYTES);
+          mbar_expect(full_a(s), PARTS * A_BYTES);
           const uint32_t st = base + (uint32_t)s * S::STAGE;
           const int y = (int)(m.t0 + (int64_t)it * KT);
-          for (int b = 0; b < S::M / 64; ++b) tma_load_2d(st + b * BLOCK, &dy_map, (int)m.n0 + 64 * b, y, full_a(s));
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+            for (int b = 0; b < S::M / 64; ++b)
+              tma_load_3d(st + p * A_BYTES + b * BLOCK, &dy_map, (int)m.n0 + 64 * b, y, p, full_a(s));
         }
       }
       // its copies in flight write this CTA's memory: see them land
@@ -624,19 +599,87 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// dw = (dw +) cscale * the splits' sums in their order.
-__global__ void __launch_bounds__(256) k_weight_grad_join(const float* part, int splits, int64_t n, int64_t k, int64_t ldp,
+// dw = (dw +) cscale * the splits' sums in their order, four columns per
+// thread and four sums' loads at a time.  vec: rows of dw on 16-byte
+// boundaries.
+__global__ void __launch_bounds__(256) k_weight_grad_join(const float4* part, int splits, int64_t n, int64_t k, int64_t fours,
                                                           const void* cscale, int ctype, float* dw, int64_t lddw,
-                                                          int accumulate) {
+                                                          int accumulate, bool vec) {
   chain_wait();
-  const int64_t total = n * k;
+  const int64_t total = n * fours;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / k, c = i - r * k;
-    float s = 0.0f;
-    for (int p = 0; p < splits; ++p) s = __fadd_rn(s, part[(p * n + r) * ldp + c]);
-    if (cscale) s = __fmul_rn(s, load_as_f32(cscale, ctype, c));
+    const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)i / (uint32_t)fours) : i / fours;
+    const int64_t c = (i - r * fours) * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < splits; p += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = p + q < splits ? __ldg(part + (p + q) * total + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s[0] = __fadd_rn(s[0], v[q].x), s[1] = __fadd_rn(s[1], v[q].y);
+        s[2] = __fadd_rn(s[2], v[q].z), s[3] = __fadd_rn(s[3], v[q].w);
+      }
+    }
     float* o = dw + r * lddw + c;
-    *o = accumulate ? __fadd_rn(*o, s) : s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + e >= k) break;
+      if (cscale) s[e] = __fmul_rn(s[e], load_as_f32(cscale, ctype, c + e));
+      if (accumulate) s[e] = __fadd_rn(o[e], s[e]);
+    }
+    if (vec && c + 4 <= k) {
+      *reinterpret_cast<float4*>(o) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < k) o[e] = s[e];
+    }
+  }
+}
+
+// The bf16 terms of dy, one [rows, ldt] after another: the upper halves of
+// what is left, by truncation, so that nothing overflows and the rest is exact.
+template <typename T, int PARTS, bool SPAN>
+__global__ void __launch_bounds__(256, 4) k_split(const T* dy, int64_t ld, Tiling t, __nv_bfloat16* terms, int64_t ldt) {
+  constexpr int AHEAD = 8 / (int)(sizeof(T) / 2);
+  __shared__ float4 shared[Rows<T, SPAN>::bytes(AHEAD, 256) / 16];
+  chain_wait();
+  const Place p = place(t);
+  Rows<T, SPAN> in(shared, 256, dy + p.r * ld, p.step * ld, p.c8, p.n, t.cols);
+  __nv_bfloat16* to = terms + p.r * ldt + (int64_t)p.c8 * CHUNK;
+  int64_t r = p.r, next = p.r;
+  auto copy = [&](int slot) {
+    in.copy(slot, next < p.end);
+    copy_group();
+    next += p.step;
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
+  int slot = 0;
+  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step, to += p.step * ldt) {
+    float v[CHUNK];
+    wait_groups<AHEAD - 2>();
+    in.landed();
+    in.take(slot, r < p.end ? p.n : 0, v);
+    in.done();
+    copy((slot + AHEAD - 1) % AHEAD);
+    slot = (slot + 1) % AHEAD;
+    const bool put = r < p.end && (int64_t)p.c8 * CHUNK < ldt;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+      if (q + 1 < PARTS) {
+#pragma unroll
+        for (int e = 0; e < CHUNK; ++e) {
+          const float top = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
+          v[e] = isinf(v[e]) ? 0.0f : __fsub_rn(v[e], top);
+        }
+      }
+      if (put) *reinterpret_cast<uint4*>(to + q * t.rows * ldt) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
   }
 }
 
@@ -671,12 +714,14 @@ static TensorMapEncode tensor_map_encode() {
   }();
   return encode;
 }
-// dy (bf16) as a 2-D tensor of 64 x 64 boxes under the 128-byte swizzle.
-static bool make_dy_map(CUtensorMap* m, const WgArgs& a) {
+// The terms of dy as a 3-D tensor (n, rows, term) of 64 x 64 boxes under the
+// 128-byte swizzle.
+static bool make_dy_map(CUtensorMap* m, const WgArgs& a, int parts) {
   const TensorMapEncode encode = tensor_map_encode();
-  const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.lddy * 2};
-  const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
-  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.dy), dims, strides, box, step,
+  const cuuint64_t dims[3] = {(cuuint64_t)a.n, (cuuint64_t)a.rows, (cuuint64_t)parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.lddy * 2, (cuuint64_t)a.lddy * 2 * (cuuint64_t)a.rows};
+  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(a.dy), dims, strides, box, step,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -691,9 +736,9 @@ static bool make_out_map(CUtensorMap* m, const WgArgs& a) {
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int PARTS, bool TMA, bool VEC>
+template <int PARTS, bool TMA>
 static bool launch_wg(const WgArgs& a, cudaStream_t s) {
-  auto kern = k_weight_grad<T, PARTS, TMA, VEC>;
+  auto kern = k_weight_grad<PARTS, TMA>;
   // the registers that the groups share out are those of the launch: with
   // fewer the kernel would wait for more
   static const bool ready = [=] {
@@ -702,9 +747,38 @@ static bool launch_wg(const WgArgs& a, cudaStream_t s) {
            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) == cudaSuccess;
   }();
   CUtensorMap dy_map = {}, out_map = {};
-  if (!ready || (TMA && !make_dy_map(&dy_map, a)) || (a.bulk && !make_out_map(&out_map, a))) return false;
+  if (!ready || (TMA && !make_dy_map(&dy_map, a, PARTS)) || (a.bulk && !make_out_map(&out_map, a))) return false;
   launch_chained(kern, (unsigned)(a.items < WG_SMS ? a.items : WG_SMS), WG_THREADS, WG_SMEM, s, dy_map, out_map, a);
   return true;
+}
+
+template <typename T, int PARTS>
+static void launch_split(const void* dy, int64_t lddy, int64_t rows, int64_t n, __nv_bfloat16* terms, int64_t ldt,
+                         cudaStream_t s) {
+  const bool span = sizeof(T) == 4 || !aligned16(dy) || lddy % 8 != 0;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, n, span, &grid);
+  // a bf16 dy comes here only as spans, fp32 always does
+  auto kern = span ? k_split<T, PARTS, true> : k_split<T, PARTS, PARTS != 2>;
+  launch_chained(kern, grid, 256, 0, s, static_cast<const T*>(dy), lddy, t, terms, ldt);
+}
+
+// Workspace: the diagnostic words, dy's terms (none for a bf16 dy whose n
+// elements per row can lie on 16-byte boundaries), the splits' sums.
+struct WgSpace {
+  int parts, splits;
+  int64_t ldt;  // row stride of the terms
+  size_t terms, sums, bytes;
+};
+static WgSpace wg_space(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
+  WgSpace w;
+  w.parts = dtype == GC_BF16 ? 1 : dtype == GC_F16 ? 2 : 3;
+  w.splits = wg_splits(rows, n, k, dtype);
+  w.ldt = (n + 7) / 8 * 8;
+  w.terms = DIAG_BYTES;
+  w.sums = w.terms + (dtype == GC_BF16 && n % 8 == 0 ? 0 : align_up((size_t)w.parts * rows * w.ldt * 2, 256));
+  w.bytes = w.sums + (w.splits > 1 ? (size_t)w.splits * n * wg_ldp(k) * sizeof(float) : 0);
+  return w;
 }
 
 }  // namespace gc
@@ -717,8 +791,7 @@ extern "C" gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, 
   if (st == GC_OK) st = validate_matrix(rows, k, dtype);
   if (st != GC_OK) return st;
   if (!bytes) return GC_ERR_INVALID_ARG;
-  const int splits = wg_splits(rows, n, k, dtype);
-  *bytes = DIAG_BYTES + (splits > 1 ? (size_t)splits * (size_t)n * (size_t)wg_ldp(k) * sizeof(float) : 0);
+  *bytes = wg_space(rows, n, k, dtype).bytes;
   return GC_OK;
 }
 
@@ -736,13 +809,15 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
   if (rows > 0 && ((st = check_matrix(dy, lddy, n, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK))
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int splits = wg_splits(rows, n, k, dtype), acc = (flags & GC_ACCUMULATE) ? 1 : 0;
+  const WgSpace w = wg_space(rows, n, k, dtype);
+  const int splits = w.splits, acc = (flags & GC_ACCUMULATE) ? 1 : 0;
   const int64_t tiles_n = (k + WG_N - 1) / WG_N, items = wg_tiles_m(n, dtype) * tiles_n * splits;
   if (items > INT64_C(1073741823)) return GC_ERR_LAYOUT;
-  float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + DIAG_BYTES);
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  float* part = reinterpret_cast<float*>(ws + w.sums);
   if (rows > 0) {
     WgArgs a;
-    a.dy = dy, a.lddy = lddy, a.rows = rows, a.n = n, a.k = k, a.ldc = act_ldc(k);
+    a.dy = static_cast<const __nv_bfloat16*>(dy), a.lddy = lddy, a.rows = rows, a.n = n, a.k = k, a.ldc = act_ldc(k);
     a.codes = codes, a.steps = steps;
     a.cscale = splits > 1 ? nullptr : col_scale, a.ctype = col_scale_dtype;
     a.accumulate = splits > 1 ? 0 : acc;
@@ -750,21 +825,28 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
     a.bulk = aligned16(a.out) && a.ldo % 4 == 0;
     a.splits = splits, a.tiles_n = (int)tiles_n, a.items = (int)items;
     a.span = wg_span(rows, splits);
-    a.diag = static_cast<uint32_t*>(workspace);
-    const bool vec = aligned16(dy) && lddy % 8 == 0;
-    bool ok;
-    if (dtype == GC_BF16)
-      ok = vec ? launch_wg<__nv_bfloat16, 1, true, true>(a, s) : launch_wg<__nv_bfloat16, 1, false, false>(a, s);
-    else if (dtype == GC_F16)
-      ok = vec ? launch_wg<__half, 2, false, true>(a, s) : launch_wg<__half, 2, false, false>(a, s);
-    else
-      ok = vec ? launch_wg<float, 3, false, true>(a, s) : launch_wg<float, 3, false, false>(a, s);
+    a.diag = reinterpret_cast<uint32_t*>(ws);
+    const bool bulk = dtype == GC_BF16 && aligned16(dy) && lddy % 8 == 0;  // dy as it is
+    if (!bulk && w.sums > w.terms) {
+      __nv_bfloat16* terms = reinterpret_cast<__nv_bfloat16*>(ws + w.terms);
+      if (dtype == GC_BF16)
+        launch_split<__nv_bfloat16, 1>(dy, lddy, rows, n, terms, w.ldt, s);
+      else if (dtype == GC_F16)
+        launch_split<__half, 2>(dy, lddy, rows, n, terms, w.ldt, s);
+      else
+        launch_split<float, 3>(dy, lddy, rows, n, terms, w.ldt, s);
+      a.dy = terms, a.lddy = w.ldt;
+    }
+    const bool ok = w.parts == 2   ? launch_wg<2, true>(a, s)
+                    : w.parts == 3 ? launch_wg<3, true>(a, s)
+                    : bulk || w.sums > w.terms ? launch_wg<1, true>(a, s) : launch_wg<1, false>(a, s);
     if (!ok) return GC_ERR_CUDA;
   }
   if (splits > 1 || rows == 0) {
-    const int64_t blocks = (n * k + 255) / 256;
-    launch_chained(k_weight_grad_join, (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, s, (const float*)part,
-                   rows == 0 ? 0 : splits, n, k, wg_ldp(k), col_scale, (int)col_scale_dtype, dw, lddw, acc);
+    const int64_t fours = wg_ldp(k) / 4, blocks = (n * fours + 255) / 256;
+    launch_chained(k_weight_grad_join, (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, s,
+                   reinterpret_cast<const float4*>(part), rows == 0 ? 0 : splits, n, k, fours, col_scale,
+                   (int)col_scale_dtype, dw, lddw, acc, aligned16(dw) && lddw % 4 == 0);
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
