@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(256, 4) k_split(const T* dy, int64_t ld, Tilin
 constexpr int WG_SMS = 152;  // of a GB300
 
 // Splits of the rows: as many as keep every SM busy when there are few
-// tiles, each of at least 256 rows.  A split has a multiple of 64 rows.
+// tiles, each of at least 128 rows.  A split has a multiple of 64 rows.
 static int64_t wg_span(int64_t rows, int64_t splits) { return ((rows + splits - 1) / splits + 63) / 64 * 64; }
 static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
   const int m = dtype == GC_BF16 ? WgShape<1, true>::M : WgShape<2, false>::M;
@@ -695,7 +695,7 @@ static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
 static int wg_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
   const int64_t tiles = wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N);
   int64_t s = WG_SMS / tiles;
-  if (s > rows / 256) s = rows / 256;
+  if (s > rows / 128) s = rows / 128;
   if (s < 2) return 1;
   const int64_t span = wg_span(rows, s);
   return (int)((rows + span - 1) / span);
