@@ -4,10 +4,19 @@
 
 namespace gc {
 
+// Every kernel here is one pass over its matrices, bound by memory; the times
+// below are for 32768 x 4096 (checkpoints) and 8192 x 14336 (gates), and the
+// share of the rate of a plain copy (6.67 TB/s) that their bytes reach.
+//
 // The loops keep AHEAD - 1 rows' loads in flight while they work on one, in
 // rings of shared memory.  Four CTAs per SM with 112 bytes per thread in
 // flight are 114 KB; the two dies' memories are about 1.5 us away under load,
-// and 6.7 TB/s is 44 KB per SM and us.
+// and 6.7 TB/s is 44 KB per SM and us.  Rows that are not on 16-byte
+// boundaries cost the shifting of their spans on top, and are bound by the
+// issue of instructions.
+
+// The step from the group's largest magnitude, over four lanes, then the
+// codes.  bf16 64 us (0.96), fp32 108 us (0.94), bf16 rows of 4095 86 us (0.71).
 template <typename T, bool SPAN>
 __global__ void __launch_bounds__(256, 4) k_act_compress(const T* x, int64_t ld, Tiling t, int8_t* codes, uint8_t* steps) {
   constexpr int AHEAD = 8 / (int)(sizeof(T) / 2);
@@ -45,11 +54,14 @@ __global__ void __launch_bounds__(256, 4) k_act_compress(const T* x, int64_t ld,
   }
 }
 
-// Codes and steps take three registers a row: four rows ahead stay there.
+// Codes and steps take three registers a row, so the rows ahead stay there:
+// eight of a 16-bit type, four of fp32 (four and eight: 66 and 112 us, and 92
+// for rows of 4095).  bf16 64 us (0.96), fp32 107 us (0.95), bf16 rows of 4095
+// 71 us (0.86).
 template <typename T, bool SPAN>
-__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
+__global__ void __launch_bounds__(256, SPAN && sizeof(T) == 2 ? 2 : 3)
     k_act_decompress(const int8_t* codes, const uint8_t* steps, Tiling t, T* out, int64_t ld) {
-  constexpr int ROWS = 4;
+  constexpr int ROWS = 16 / (int)sizeof(T);
   __shared__ float4 stage[SPAN ? 8 * RowsOut<T, SPAN>::STAGE : 1];
   chain_wait();
   const Place p = place(t);
@@ -78,6 +90,7 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
     if (lead + ROWS * p.step < p.end) fetch(r + ROWS * p.step);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i, r += p.step) {
+      if (lead + i * p.step >= p.end) break;
       float v[CHUNK];
       chunk_values(cn[i], bn[i], v);
       to.put(v, p.n, r < p.end, own);
@@ -91,55 +104,81 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
 // u |p| in p into a relative error of the result, |p| up to 87: the rounding
 // errors of g^2 and of the last product are carried along in `low` and
 // applied as exp(-(p + low)) = exp(-p) (1 - low).
-// Below -80, where 1 + exp(-p) is exp(-p) and soon overflows, the sigmoid is
-// exp(p).
-// PRECISE (fp32 results): correctly rounded division and CUDA's expf.  For
-// 16-bit results the hardware's exponential and reciprocal, a few 2^-23 off
-// (and |p| 2^-24 from the argument), are 2^-10 of the result's own rounding
-// and a third of the instructions, which bound these kernels next to memory.
-template <int KIND, bool PRECISE>
+constexpr float GELU_C = 1.5957691216057308f, GELU_CA = 0.0713548162726009f;  // 2 sqrt(2/pi), times 0.044715
+// Beyond +-30 GELU's sigmoid is 0 or 1 in fp32; the clamp keeps g^3 and p'
+// finite there, so that 0 * p' stays 0 (and lets a NaN through).
+constexpr float GELU_FAR = 30.0f;
+
+// For fp32 results: correctly rounded division and CUDA's expf.  Below -80,
+// where 1 + exp(-p) is exp(-p) and soon overflows, the sigmoid is exp(p).
+template <int KIND>
 __device__ __forceinline__ float gate_sigmoid(float g, float* dp) {
   float p = g, low = 0.0f;
   *dp = 1.0f;
   if (KIND == GC_GATE_GELU_TANH) {
-    constexpr float C = 1.5957691216057308f, CA = 0.0713548162726009f;  // 2 sqrt(2/pi), times 0.044715
-    // beyond +-30 the sigmoid is 0 or 1 in fp32; the clamp keeps g^3 and p'
-    // finite there, so that 0 * p' stays 0 (and lets a NaN through)
-    const float t = fabsf(g) > 30.0f ? copysignf(30.0f, g) : g;
-    const float t2 = __fmul_rn(t, t), w = __fmaf_rn(CA, t2, C);
+    const float t = fabsf(g) > GELU_FAR ? copysignf(GELU_FAR, g) : g;
+    const float t2 = __fmul_rn(t, t), w = __fmaf_rn(GELU_CA, t2, GELU_C);
     p = __fmul_rn(w, t);
-    low = __fmaf_rn(CA * __fmaf_rn(t, t, -t2), t, __fmaf_rn(w, t, -p));
-    *dp = __fmaf_rn(2.0f * CA, t2, w);
-  }
-  if (KIND == GC_GATE_SILU && !PRECISE) {
-    // far out on the left the exponential is infinite and the sigmoid 0,
-    // where it would be below 2^-126
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
-    return s;
+    low = __fmaf_rn(GELU_CA * __fmaf_rn(t, t, -t2), t, __fmaf_rn(w, t, -p));
+    *dp = __fmaf_rn(2.0f * GELU_CA, t2, w);
   }
   const bool far = p < -80.0f;
-  const float z = far ? p : -p;
-  float e;
-  if (PRECISE) {
-    e = expf(z);
-  } else {
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(z, 1.4426950408889634f)));
-  }
+  float e = expf(far ? p : -p);
   if (KIND == GC_GATE_GELU_TANH) e = __fmaf_rn(e, far ? low : -low, e);
-  const float one = __fadd_rn(1.0f, e);
-  float s;
-  if (PRECISE) {
-    s = __fdiv_rn(1.0f, one);
-  } else {
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(one));
-  }
-  return far ? e : s;
+  return far ? e : __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
 }
 
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// For 16-bit results, two at a time: the hardware's exponential and
+// reciprocal, a few 2^-23 off (and |p| 2^-24 from SiLU's argument), are 2^-10
+// of the result's own rounding and a third of the instructions.
+// SiLU: far out on the left the exponential is infinite and the sigmoid 0,
+// where it would be below 2^-126.
+// GELU: with h = 2^(-z/2), z = |p| log2(e), and f = h^2 the sigmoid is
+// 1 / (1 + f) on the right and f / (1 + f) on the left, where nothing
+// overflows and f reaches below 2^-126 (the exponential itself does not).
+template <int KIND>
+__device__ __forceinline__ F2 gate_sigmoid2(const float* g, F2* dp) {
+  constexpr float LOG2E = 1.4426950408889634f;
+  float x[2], r[2];
+  if (KIND == GC_GATE_SILU) {
+    put2(x, mul2(get2(g), f2(-LOG2E)));
+    put2(r, add2(f2(ex2_ftz(x[0]), ex2_ftz(x[1])), f2(1.0f)));
+    *dp = f2(1.0f);
+    return f2(rcp_ftz(r[0]), rcp_ftz(r[1]));
+  }
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x[0]) : "f"(fabsf(g[0])), "f"(GELU_FAR));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x[1]) : "f"(fabsf(g[1])), "f"(GELU_FAR));
+  const F2 t = get2(x), minus_t = mul2(t, f2(-1.0f)), minus_t2 = mul2(t, minus_t);
+  const F2 w = fma2(minus_t2, f2(-0.5f * LOG2E * GELU_CA), f2(0.5f * LOG2E * GELU_C)), minus_z = mul2(w, minus_t);
+  const F2 low = fma2(mul2(t, f2(0.5f * LOG2E * GELU_CA)), fma2(t, t, minus_t2), fma2(w, t, minus_z));
+  *dp = fma2(minus_t2, f2(-3.0f * GELU_CA), f2(GELU_C));
+  put2(x, minus_z);
+  F2 h = f2(ex2_ftz(x[0]), ex2_ftz(x[1]));
+  h = fma2(h, mul2(low, f2(-0.693147180559945f)), h);
+  const F2 f = mul2(h, h);
+  put2(x, add2(f, f2(1.0f)));
+  const F2 right = f2(rcp_ftz(x[0]), rcp_ftz(x[1]));
+  put2(r, right), put2(x, mul2(f, right));
+  return f2(g[0] < 0.0f ? x[0] : r[0], g[1] < 0.0f ? x[1] : r[1]);
+}
+
+// Registers for the packed arithmetic matter more than a fourth CTA per SM
+// (two for spans).  With both checkpoints: bf16 148 us for either kind (0.96;
+// GELU with scalar arithmetic 172), fp32 276 us (0.90) and 320 with GELU, bf16
+// rows of 14335 180 us (0.79) and 225.
 template <typename T, int KIND, bool SPAN>
-__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
+__global__ void __launch_bounds__(256, SPAN && sizeof(T) == 2 ? 2 : 3)
     k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, Tiling t, T* out, int64_t ldo, int8_t* gcodes,
             uint8_t* gsteps, int8_t* ucodes, uint8_t* usteps) {
   constexpr int AHEAD = 4 / (int)(sizeof(T) / 2);
@@ -182,17 +221,30 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
       }
       ac += dc, as += ds;
     }
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < CHUNK; ++e) {
-      float dp;
-      g[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp)), u[e]);
+      for (int e = 0; e < CHUNK; ++e) {
+        float dp;
+        g[e] = __fmul_rn(__fmul_rn(g[e], gate_sigmoid<KIND>(g[e], &dp)), u[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < CHUNK; e += 2) {
+        F2 dp;
+        put2(g + e, mul2(mul2(get2(g + e), gate_sigmoid2<KIND>(g + e, &dp)), get2(u + e)));
+      }
     }
     to.put(g, n, r < p.end, own);
   }
 }
 
+// dout and both codes come through rings, the step bytes through registers.
+// Three CTAs per SM (two for spans): the fourth would leave 64 registers and
+// spill (152 and 184 us).  bf16 145 us (0.98), GELU 160 us (0.89; 214 with
+// scalar arithmetic); with the activation's checkpoint 166 and 182 us; fp32
+// 308 us (0.80); bf16 rows of 14335 188 us (0.76).
 template <typename T, int KIND, bool SPAN>
-__global__ void __launch_bounds__(256, SPAN ? 3 : 4)
+__global__ void __launch_bounds__(256, SPAN ? 2 : 3)
     k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
                      const uint8_t* usteps, Tiling t, T* dgate, int64_t lddg, T* dup, int64_t lddu, int8_t* ocodes,
                      uint8_t* osteps) {
@@ -245,14 +297,26 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
       chunk_values(code.take(2 * i), ng[i], g);
       chunk_values(code.take(2 * i + 1), nu[i], u);
       copy((i + AHEAD - 1) % AHEAD);
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) {
-        float dp;
-        const float s = gate_sigmoid<KIND, sizeof(T) == 4>(g[e], &dp), act = __fmul_rn(g[e], s);
-        const float slope = __fmaf_rn(__fmul_rn(act, __fsub_rn(1.0f, s)), dp, s);
-        g[e] = __fmul_rn(__fmul_rn(d[e], u[e]), slope);  // dgate
-        a[e] = __fmul_rn(act, u[e]);
-        u[e] = __fmul_rn(d[e], act);  // dup
+        for (int e = 0; e < CHUNK; ++e) {
+          float dp;
+          const float s = gate_sigmoid<KIND>(g[e], &dp), act = __fmul_rn(g[e], s);
+          const float slope = __fmaf_rn(__fmul_rn(act, __fsub_rn(1.0f, s)), dp, s);
+          g[e] = __fmul_rn(__fmul_rn(d[e], u[e]), slope);  // dgate
+          a[e] = __fmul_rn(act, u[e]);
+          u[e] = __fmul_rn(d[e], act);  // dup
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < CHUNK; e += 2) {
+          F2 dp;
+          const F2 s = gate_sigmoid2<KIND>(g + e, &dp), act = mul2(get2(g + e), s), de = get2(d + e), ue = get2(u + e);
+          const F2 slope = fma2(mul2(act, fma2(s, f2(-1.0f), f2(1.0f))), dp, s);
+          put2(g + e, mul2(mul2(de, ue), slope));
+          put2(a + e, mul2(act, ue));
+          put2(u + e, mul2(de, act));
+        }
       }
       gto.put(g, n, r < p.end, own);
       uto.put(u, n, r < p.end, own);
@@ -271,7 +335,7 @@ __global__ void __launch_bounds__(256, SPAN ? 3 : 4)
 
 // The kernel for rows on 16-byte boundaries, or for any.  (fp32 takes spans
 // always: 8 fp32 per lane are 32 bytes, and copies of every other 16 bytes
-// reached 0.6 of the copy rate.)
+// reached 0.6 of the copy's rate.)
 template <typename K>
 static K row_kernel(bool span, K aligned, K any) {
   return span ? any : aligned;

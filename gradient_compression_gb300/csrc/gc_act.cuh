@@ -72,6 +72,42 @@ __device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[CHUNK]) {
   for (int i = 0; i < CHUNK; ++i) v[i] = to_f32(r.e[i]);
 }
 
+// Two fp32 operations in one instruction (each lane rounds as its scalar form
+// does).  The streaming kernels are bound by the issue of instructions next to
+// memory: with scalar arithmetic GELU's backward issued in 82% of the cycles at
+// 0.66 of a copy's rate, now 0.89.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ F2 get2(const float* v) { return f2(v[0], v[1]); }
+__device__ __forceinline__ void put2(float* v, F2 x) { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(x.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -79,9 +115,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 // The step byte of the group that this lane's 8 values belong to.
 __device__ __forceinline__ uint32_t chunk_step(const float (&v)[CHUNK]) {
-  float top = fabsf(v[0]);
+  float top = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-  for (int i = 1; i < CHUNK; ++i) top = max_nan(top, fabsf(v[i]));
+  for (int i = 2; i < CHUNK; i += 2) top = max_nan(top, fabsf(v[i]), fabsf(v[i + 1]));
   top = max_nan(top, __shfl_xor_sync(FULL, top, 1));
   top = max_nan(top, __shfl_xor_sync(FULL, top, 2));
   return act_step(__float_as_uint(top));
@@ -93,7 +129,11 @@ __device__ __forceinline__ uint2 chunk_codes(const float (&v)[CHUNK], uint32_t b
   const float inverse = act_inverse(b);
   uint32_t w[CHUNK];
 #pragma unroll
-  for (int i = 0; i < CHUNK; ++i) w[i] = __float_as_uint(__fmaf_rn(v[i], inverse, 12582912.0f));
+  for (int i = 0; i < CHUNK; i += 2) {
+    float x[2];
+    put2(x, fma2(get2(v + i), f2(inverse), f2(12582912.0f)));
+    w[i] = __float_as_uint(x[0]), w[i + 1] = __float_as_uint(x[1]);
+  }
   if (__builtin_expect(b >= 248u, 0)) {
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i)
@@ -106,12 +146,14 @@ __device__ __forceinline__ uint2 chunk_codes(const float (&v)[CHUNK], uint32_t b
 }
 // The values of 8 codes: code + 128 in the low byte of 2^23's significand.
 __device__ __forceinline__ void chunk_values(uint2 c, uint32_t b, float (&v)[CHUNK]) {
-  const float scale = act_scale(b);
+  const F2 scale = f2(act_scale(b)), bias = f2(-8388736.0f);
   const uint32_t x = c.x ^ 0x80808080u, y = c.y ^ 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440 + i)), 8388736.0f), scale);
-    v[4 + i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(y, 0x4B000000u, 0x7440 + i)), 8388736.0f), scale);
+  for (int i = 0; i < CHUNK; i += 2) {
+    const uint32_t w = i < 4 ? x : y;
+    const F2 raw = f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + (i & 3))),
+                      __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441 + (i & 3))));
+    put2(v + i, mul2(add2(raw, bias), scale));
   }
 }
 
