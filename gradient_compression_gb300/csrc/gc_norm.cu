@@ -80,10 +80,10 @@ struct RowChunks {
   __device__ __forceinline__ bool held(int j) const { return MODE == ROW_FULL || c8(j) < chunks; }  // in the checkpoint
 };
 
-// Rows ahead come through rings in shared memory: SLOTS - 1 rows are in flight
-// while one is worked on (none for the widest rows that are spans or fp32,
-// whose second slot does not fit).  Registers for the rows ahead cost the warps that hide the
-// latency: 0.5 of the copy rate; three or four slots measured no faster.
+// Rows ahead come through rings in shared memory: one row is in flight while
+// one is worked on (none for the widest rows that are spans or fp32, whose
+// second slot does not fit).  Registers for the rows ahead cost the warps that
+// hide the latency: 0.5 of a copy's rate; three or four slots measured no faster.
 template <typename T, int N, int MODE>
 struct RowShared {
   static constexpr bool SPAN = MODE == ROW_SPAN;
@@ -147,8 +147,14 @@ struct RowTo {
   __device__ __forceinline__ void done() { to.next += to.step; }
 };
 
+// One pass, bound by memory and by what a row's warps wait for each other:
+// 16384 x 4096 in bf16 with residual, h, rstd and checkpoint takes 103 us
+// (0.88 of a copy's rate), 16384 x 8192 213 us (0.85), fp32 203 us (0.85), rows
+// of 4095 158 us (0.57: spans, bound by instructions).  The bounds stand for
+// registers: 80 a thread, three CTAs of 256 per SM, or 128 and two for spans
+// (170 us, fp32 227 us, with three).
 template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
+__global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
               int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
               uint8_t* steps) {
@@ -180,8 +186,7 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
   int turn = 0, slot = 0;
   for (int64_t lead = (int64_t)blockIdx.x * at.per; lead < rows; lead += stride, r += stride) {
     const bool in = r < rows;
-    float v[N][CHUNK];
-    float ss = 0.0f;
+    float v[N][CHUNK], ss[2] = {0.0f, 0.0f};
     if (SLOTS == 1) copy(0);
     wait_groups<0>();
     xin.in.landed();
@@ -193,10 +198,10 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
         float t[CHUNK];
         rin.take(slot, j, n, t);
 #pragma unroll
-        for (int e = 0; e < CHUNK; ++e) v[j][e] = __fadd_rn(v[j][e], t[e]);
+        for (int e = 0; e < CHUNK; e += 2) put2(v[j] + e, add2(get2(v[j] + e), get2(t + e)));
       }
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) ss = __fmaf_rn(v[j][e], v[j][e], ss);
+      for (int e = 0; e < CHUNK; e += 2) put2(ss, fma2(get2(v[j] + e), get2(v[j] + e), get2(ss)));
     }
     xin.in.done();
     if (res) rin.in.done();
@@ -209,13 +214,13 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
       for (int j = 0; j < N; ++j) hto.put(j, v[j], at.n(j), in, own);
       hto.done();
     }
-    const float rs = rms_inverse(row_sum(ss, at.W, red, turn), share, eps);
+    const float rs = rms_inverse(row_sum(__fadd_rn(ss[0], ss[1]), at.W, red, turn), share, eps);
     if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) v[j][e] = __fmul_rn(v[j][e], rs);
+      for (int e = 0; e < CHUNK; e += 2) put2(v[j] + e, mul2(get2(v[j] + e), f2(rs)));
       if (codes) {
         // past the row's end the values are 0 * rstd, which a rstd that is
         // not finite would turn into NaN
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
         float t[CHUNK];
         load_weights(shared, at.chunks, at.c8(j), t);
 #pragma unroll
-        for (int e = 0; e < CHUNK; ++e) t[e] = __fmul_rn(v[j][e], t[e]);
+        for (int e = 0; e < CHUNK; e += 2) put2(t + e, mul2(get2(v[j] + e), get2(t + e)));
         yto.put(j, t, at.n(j), in, own);
       }
     }
@@ -246,14 +251,22 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 3 : 1)
 
 // Gradient: gw = dy * weight, dx = rstd (gw - q mean(gw q)) + dh, and each
 // thread's share of dw = sum dy q of its columns over the rows that its CTA
-// walks over, one partial sum per CTA and row at a time.
+// walks over, one partial sum per CTA.
+// Bound by memory and by the waits within a row, as above.  With four chunks
+// per lane (rows on 16-byte boundaries) fewer warps wait for a row; gw and q do
+// not fit into registers next to dw across that wait and are worked out AGAIN
+// from the rings.  16384 x 4096 in bf16 with dh and dw: 81 us (0.87 of a copy's
+// rate; two chunks 88, four without AGAIN 130), 8192 columns 158 us (0.89; 166),
+// 16384 columns 289 us (0.98).  Spans and fp32, bound by instructions, keep two
+// chunks: rows of 4095 134 us (0.53; four chunks 165), fp32 164 us (0.80; 230).
 template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
+__global__ void __launch_bounds__(512, 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
                        const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
                        int warps, T* dx, int64_t lddx, float* part) {
   using S = RowShared<T, N, MODE>;
   constexpr int SLOTS = S::SLOTS;
+  constexpr bool AGAIN = N == 4;
   __shared__ float red[2][16];
   extern __shared__ float4 shared[];
   chain_wait();
@@ -311,8 +324,7 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     din.in.landed();
     if (SLOTS == 2) copy(slot ^ 1);
     if (lead + stride < rows) fetch(r + stride);
-    float gw[N][CHUNK], q[N][CHUNK];
-    float s = 0.0f;
+    float gw[N][CHUNK], q[N][CHUNK], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
@@ -327,22 +339,31 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
           if (MODE == ROW_FULL || e >= n) q[j][e] = 0.0f;
       }
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) {
-        dw[j][e] = __fmaf_rn(gw[j][e], q[j][e], dw[j][e]);
-        gw[j][e] = __fmul_rn(gw[j][e], w[e]);
-        s = __fmaf_rn(gw[j][e], q[j][e], s);
+      for (int e = 0; e < CHUNK; e += 2) {
+        const F2 g = get2(gw[j] + e), qe = get2(q[j] + e), ge = mul2(g, get2(w + e));
+        put2(dw[j] + e, fma2(g, qe, get2(dw[j] + e)));
+        put2(gw[j] + e, ge);
+        put2(s, fma2(ge, qe, get2(s)));
       }
     }
-    const float mean = __fmul_rn(row_sum(s, at.W, red, turn), share);
+    const float minus_mean = __fmul_rn(row_sum(__fadd_rn(s[0], s[1]), at.W, red, turn), -share);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
       float t[CHUNK];
       if (dh) hin.take(slot, j, n, t);
+      if (AGAIN) {
+        float w[CHUNK];
+        din.take(slot, j, n, gw[j]);
+        load_weights(shared, at.chunks, at.c8(j), w);
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) {
-        const float v = __fmul_rn(inverse, __fmaf_rn(-q[j][e], mean, gw[j][e]));
-        gw[j][e] = dh ? __fadd_rn(v, t[e]) : v;
+        for (int e = 0; e < CHUNK; e += 2) put2(gw[j] + e, mul2(get2(gw[j] + e), get2(w + e)));
+      }
+      if (AGAIN || sizeof(T) == 4) chunk_values(code.take(slot * N + j), step[j], q[j]);
+#pragma unroll
+      for (int e = 0; e < CHUNK; e += 2) {
+        const F2 v = mul2(f2(inverse), fma2(get2(q[j] + e), f2(minus_mean), get2(gw[j] + e)));
+        put2(gw[j] + e, dh ? add2(v, get2(t + e)) : v);
       }
       to.put(j, gw[j], at.n(j), in, own);
     }
@@ -352,18 +373,43 @@ __global__ void __launch_bounds__(N == 2 ? 256 : 512, N == 2 ? 2 : 1)
     if (SLOTS == 2) slot ^= 1;
   }
   if (!part) return;
+  part += (int64_t)blockIdx.x * ldc;
+  if (at.per == 1) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float4* o = reinterpret_cast<float4*>(part + start + j * at.apart * CHUNK);
+      if (at.held(j)) {
+        o[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+        o[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+      }
+    }
+    return;
+  }
+  // the rows at a time of narrow matrices, added up in their order by way of
+  // the rings' memory
+  static_assert((N > 2 && MODE == ROW_SPAN) || 2 * N * sizeof(float4) <= 2 * N * sizeof(T) * CHUNK * SLOTS, "room for the sums");
+  float4* const sums = reinterpret_cast<float4*>(rings);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    float* o = part + ((int64_t)blockIdx.x * at.per + at.sub) * ldc + start + j * at.apart * CHUNK;  // rows of ldc floats
-    if (at.held(j)) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    sums[(2 * j) * blockDim.x + threadIdx.x] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+    sums[(2 * j + 1) * blockDim.x + threadIdx.x] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * N * at.apart; i += blockDim.x) {
+    const int half = i / at.apart, lane = i - half * at.apart, c8 = lane + (half >> 1) * at.apart;
+    float4 t = sums[half * blockDim.x + lane];
+    for (int p = 1; p < at.per; ++p) {
+      const float4 v = sums[half * blockDim.x + p * at.apart + lane];
+      t.x = __fadd_rn(t.x, v.x), t.y = __fadd_rn(t.y, v.y), t.z = __fadd_rn(t.z, v.z), t.w = __fadd_rn(t.w, v.w);
     }
+    if (c8 < at.chunks) reinterpret_cast<float4*>(part)[2 * c8 + (half & 1)] = t;
   }
 }
 
 // dw[c] = (dw[c] +) the partial sums in a fixed order: 32 columns per CTA, 32
-// warps each over every 32nd sum, its loads issued eight at a time.
+// warps each over every 32nd sum, its loads issued eight at a time: bound by
+// their latency.  1031 x 1001 in fp32 takes 7.6 us with its backward pass.
 __global__ void __launch_bounds__(1024) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, int64_t ldp, float* dw,
                                                           int accumulate) {
   __shared__ float sum[32][33];
@@ -389,6 +435,8 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_dw_join(const float* part, int
 }
 
 // ---------------------------------------------------------------- wide rows
+// The plain way for rows that no CTA's registers hold: read twice, the second
+// time mostly from L2, and dw by a pass of its own.
 // The sum over the CTA, the same bits in every thread.
 __device__ __forceinline__ float cta_sum(float v, float* red) {
   for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
@@ -488,12 +536,13 @@ __global__ void __launch_bounds__(NTHREADS)
 // ---------------------------------------------------------------- shapes
 constexpr int NORM_SMS = 152;  // of a GB300
 
-// Warps per row for two chunks per lane, four beyond 4096 columns.
-static int norm_chunks(int64_t cols) { return cols <= 4096 ? 2 : 4; }
-static RowShape norm_shape(int64_t cols) {
+// Chunks per lane: two up to 8192 columns, four beyond; but four in the
+// backward pass of 16-bit rows on 16-byte boundaries.
+static int norm_chunks(int64_t cols, bool four) { return cols <= 8192 && !four ? 2 : 4; }
+static RowShape norm_shape(int64_t cols, int chunks) {
   RowShape s;
   s.warps = 1;
-  while ((int64_t)s.warps * norm_chunks(cols) * 256 < cols) s.warps *= 2;
+  while ((int64_t)s.warps * chunks * 256 < cols) s.warps *= 2;
   s.threads = s.warps == 16 ? 512 : 256;
   return s;
 }
@@ -509,23 +558,24 @@ static bool allow_shared() {
   static const bool ok = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 232192) == cudaSuccess;
   return ok;
 }
-static int row_mode(int64_t cols, const RowShape& s, bool vec) {
+static int row_mode(int64_t cols, const RowShape& s, int chunks, bool vec) {
   if (!vec) return ROW_SPAN;
-  return cols == (int64_t)s.warps * norm_chunks(cols) * 256 ? ROW_FULL : ROW_CHUNKS;
+  return cols == (int64_t)s.warps * chunks * 256 ? ROW_FULL : ROW_CHUNKS;
 }
 template <int N>
 struct Chunks {
   static constexpr int value = N;
 };
-// CTAs of 256 threads per SM in a grid: two waves of three forward (110 us for
-// 16384 x 4096 in bf16; one wave 116), one of two backward, whose sums of dw
-// grow with the CTAs.
-constexpr int FORWARD_PER_SM = 6, BACKWARD_PER_SM = 2;
+// CTAs of 256 threads per SM in a grid: two waves forward (103 us for 16384 x
+// 4096 in bf16; one wave and four 108 and 107), one of two CTAs backward, whose
+// sums of dw grow with the CTAs.
+constexpr int FORWARD_PER_SM = 6, SPAN_PER_SM = 4, BACKWARD_PER_SM = 2;
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
   if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
-  const RowShape s = norm_shape(cols);
-  return norm_grid(rows, s, BACKWARD_PER_SM) * (s.threads / 32 / s.warps);
+  const int two = norm_grid(rows, norm_shape(cols, norm_chunks(cols, false)), BACKWARD_PER_SM);
+  const int four = norm_grid(rows, norm_shape(cols, 4), BACKWARD_PER_SM);
+  return two > four ? two : four;
 }
 
 }  // namespace gc
@@ -556,16 +606,17 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
                                          groups, static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps));
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
-  const RowShape shape = norm_shape(cols);
+  const int chunks = norm_chunks(cols, false);
+  const RowShape shape = norm_shape(cols, chunks);
   const bool vec = chunk_aligned(x, ldx, dtype) && (!residual || chunk_aligned(residual, ldr, dtype)) &&
                    (!y || chunk_aligned(y, ldy, dtype)) && (!h || chunk_aligned(h, ldh, dtype));
-  const int mode = row_mode(cols, shape, vec);
+  const int mode = row_mode(cols, shape, chunks, vec);
   GC_BY_DTYPE(dtype, T, {
-    auto go = [&](auto chunks) -> bool {
-      constexpr int N = decltype(chunks)::value;
+    auto go = [&](auto per_lane) -> bool {
+      constexpr int N = decltype(per_lane)::value;
       constexpr bool ANY = sizeof(T) == 4;  // fp32 rows are spans always
       auto run = [&](auto kern, size_t ring) -> bool {
-        launch_chained(kern, (unsigned)norm_grid(rows, shape, FORWARD_PER_SM), shape.threads,
+        launch_chained(kern, (unsigned)norm_grid(rows, shape, mode == ROW_SPAN ? SPAN_PER_SM : FORWARD_PER_SM), shape.threads,
                        (size_t)groups * ACT_GROUP * sizeof(float) + ring, s, static_cast<const T*>(x), ldx,
                        static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows, cols, groups, shape.warps,
                        static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
@@ -576,7 +627,7 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
       if (mode == ROW_CHUNKS) return allow_shared<k_rmsnorm<T, N, LANES>>() && run(k_rmsnorm<T, N, LANES>, RowShared<T, N, LANES>::forward(shape.threads));
       return allow_shared<k_rmsnorm<T, N, ROW_SPAN>>() && run(k_rmsnorm<T, N, ROW_SPAN>, RowShared<T, N, ROW_SPAN>::forward(shape.threads));
     };
-    if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
+    if (!(chunks == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
@@ -634,15 +685,17 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
     });
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
-  const RowShape shape = norm_shape(cols);
   const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
-  const int mode = row_mode(cols, shape, vec);
+  const int chunks = norm_chunks(cols, vec);
+  const RowShape shape = norm_shape(cols, chunks);
+  const int grid = norm_grid(rows, shape, BACKWARD_PER_SM);
+  const int mode = row_mode(cols, shape, chunks, vec);
   GC_BY_DTYPE(dtype, T, {
-    auto go = [&](auto chunks) -> bool {
-      constexpr int N = decltype(chunks)::value;
+    auto go = [&](auto per_lane) -> bool {
+      constexpr int N = decltype(per_lane)::value;
       constexpr bool ANY = sizeof(T) == 4;  // fp32 rows are spans always
       auto run = [&](auto kern, size_t ring) -> bool {
-        launch_chained(kern, (unsigned)norm_grid(rows, shape, BACKWARD_PER_SM), shape.threads,
+        launch_chained(kern, (unsigned)grid, shape.threads,
                        (size_t)groups * ACT_GROUP * sizeof(float) + ring, s, static_cast<const T*>(dy), lddy,
                        static_cast<const T*>(dh), lddh, codes, steps, rstd, weight, weight_dtype, rows, cols, groups,
                        shape.warps, static_cast<T*>(dx), lddx, part);
@@ -653,8 +706,8 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
       if (mode == ROW_CHUNKS) return allow_shared<k_rmsnorm_backward<T, N, LANES>>() && run(k_rmsnorm_backward<T, N, LANES>, RowShared<T, N, LANES>::backward(shape.threads));
       return allow_shared<k_rmsnorm_backward<T, N, ROW_SPAN>>() && run(k_rmsnorm_backward<T, N, ROW_SPAN>, RowShared<T, N, ROW_SPAN>::backward(shape.threads));
     };
-    if (!(norm_chunks(cols) == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
+    if (!(chunks == 2 ? go(Chunks<2>()) : go(Chunks<4>()))) return GC_ERR_CUDA;
   });
-  if (dw) join(parts);
+  if (dw) join(grid);
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
