@@ -152,7 +152,8 @@ typedef struct gc_diag {
 #define GC_DIAG_INDEX_ORDER 0x10u    /* decompress met a worker's indices not ascending within a
                                         tensor; see gc_sparse_decompress_accumulate */
 #define GC_DIAG_TIMEOUT 0x20u        /* a grid-wide wait of the one-launch path ran out (about a
-                                        second); that call's outputs are incomplete */
+                                        second), or a wait inside gc_act_weight_grad; that call's
+                                        outputs are incomplete */
 
 /* CUDA-graph capture.  gc_ef_topk_compress_dev_iter and
  * gc_quantize_stochastic_dev_iter are gc_ef_topk_compress and
@@ -557,7 +558,10 @@ gc_status gc_dense_decompress_accumulate(const gc_layout* dev, const gc_layout* 
  * Matrices.  A matrix m[rows, cols] of `dtype` is row-major: row r starts
  * `ld` elements after row r - 1 (ld >= cols), its columns are consecutive.
  * Any base address, ld and width of whole elements are accepted.  0 <= rows
- * and 1 <= cols, both < 2^31; offsets inside a matrix are 64-bit.
+ * and 1 <= cols, both < 2^31; offsets inside a matrix are 64-bit.  Reads may
+ * take in the whole of a 16-byte granule of memory that holds an element.
+ * GC_ERR_LAYOUT: rows, cols or ld outside these bounds; GC_ERR_ALIGNMENT: a
+ * base that is no multiple of its element, or codes off a 16-byte boundary.
  *
  * Checkpoint.  x[rows, cols] is held as int8 codes[rows, ldc], ldc = 32 *
  * ceil(cols / 32), pad codes 0, and uint8 steps[rows, ldc / 32], one step
@@ -644,7 +648,12 @@ gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, 
  * fp32 into the arena (added to dw with GC_ACCUMULATE), row r of dw at
  * r * lddw.  col_scale (ones) is the norm's weight where q is gc_rmsnorm's
  * checkpoint.  Products are exact (an fp16 or fp32 dy is split into two or
- * three bf16 terms) and summed in fp32.  Workspace 256-byte aligned. */
+ * three bf16 terms) and summed in fp32 by the tensor cores, which truncate, in
+ * chains of at most 3200 rows; the chains' sums are added in fp32 that rounds
+ * (and flushes to zero below 2^-126).  Workspace 256-byte aligned; it holds
+ * dy's terms (not for a bf16 dy with n a multiple of 8) and, with few tiles of
+ * dw, partial sums.  Its head is for gc_get_device_status: GC_DIAG_TIMEOUT if
+ * a wait inside the kernel ran out, dw then being incomplete. */
 gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t rows, int64_t n,
                              const int8_t* codes, const uint8_t* steps, int64_t k,
                              const void* col_scale, int32_t col_scale_dtype, float* dw,
