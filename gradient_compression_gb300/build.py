@@ -1,4 +1,5 @@
-"""Builds libgc.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libgc.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_marshal.so (the compiled argument marshalling of activations.py) with g++.
 
 Every translation unit is compiled in parallel, then linked into one shared
 library next to this file.  `-fmad=false` keeps each fp32 multiply and add a
@@ -10,11 +11,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgc.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["gc_api.cu", "gc_topk.cu", "gc_dense.cu", "gc_decompress.cu", "gc_noalloc.cu", "gc_powersgd.cu",
            "gc_act.cu", "gc_norm.cu", "gc_wgrad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,10 +39,28 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _build_marshal():
+    """Against the installed torch, whose tensors it takes."""
+    import torch
+    top = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(top, "include"), "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "gc_marshal.cpp"), "-o", tmp,
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed on gc_marshal.cpp:\n%s" % res.stderr)
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
@@ -60,8 +81,10 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,334 @@
+// Argument marshalling of activations.py: the checks of tensors and the calls
+// of libgc's activation entry points.  A call of one token takes the GPU 1 to 5
+// us; checked in Python and passed through ctypes, its host side took 7 (norm)
+// to 13 us (gated activation, with the slices of its projection).
+//
+// Functions return the entry point's status; what is wrong with a tensor
+// raises ValueError before anything is enqueued.
+#include <Python.h>
+
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/gc.h"
+
+namespace {
+
+// ---------------------------------------------------------------- entry points
+struct Entry {
+  decltype(&gc_act_compress) act_compress;
+  decltype(&gc_act_decompress) act_decompress;
+  decltype(&gc_rmsnorm) rmsnorm;
+  decltype(&gc_rmsnorm_backward) rmsnorm_backward;
+  decltype(&gc_gated_act) gated_act;
+  decltype(&gc_gated_act_backward) gated_act_backward;
+  decltype(&gc_act_weight_grad) act_weight_grad;
+} entry;
+
+// bind(addresses of the entry points in the order above), as loaded by the package
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  void** slots = reinterpret_cast<void**>(&entry);
+  if (n != (Py_ssize_t)(sizeof(entry) / sizeof(void*))) {
+    PyErr_SetString(PyExc_TypeError, "bind: wrong number of entry points");
+    return nullptr;
+  }
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    slots[i] = PyLong_AsVoidPtr(args[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  Py_RETURN_NONE;
+}
+
+// ---------------------------------------------------------------- checks
+struct Bad {};  // a Python exception is set
+
+[[noreturn]] void bad(const char* format, ...) {
+  va_list va;
+  va_start(va, format);
+  PyErr_FormatV(PyExc_ValueError, format, va);
+  va_end(va);
+  throw Bad{};
+}
+
+const char* type_name(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return "torch.float32";
+    case at::kBFloat16: return "torch.bfloat16";
+    case at::kHalf: return "torch.float16";
+    default: return c10::toString(t);
+  }
+}
+int type_code(const at::Tensor& t, const char* name) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return GC_F32;
+    case at::kBFloat16: return GC_BF16;
+    case at::kHalf: return GC_F16;
+    default: bad("%s: %s is not supported", name, c10::toString(t.scalar_type()));
+  }
+}
+
+const at::Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) bad("%s: a tensor is needed", name);
+  return THPVariable_Unpack(o);
+}
+
+struct Mat {
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+// A matrix argument after its checks; rows < 0 takes any shape.
+Mat matrix(const at::Tensor& t, const char* name, int64_t rows = -1, int64_t cols = -1) {
+  if (t.dim() != 2 || !t.is_cuda()) bad("%s: a 2-D CUDA tensor is needed", name);
+  const int64_t r = t.size(0), c = t.size(1);
+  if (rows >= 0 && (r != rows || c != cols))
+    bad("%s: shape (%lld, %lld) where (%lld, %lld) is needed", name, (long long)r, (long long)c, (long long)rows, (long long)cols);
+  if (t.stride(1) != 1 && c > 1) bad("%s: columns are not consecutive", name);
+  Mat m;
+  m.ld = t.stride(0);
+  if (m.ld < c) {
+    if (r > 1) bad("%s: rows overlap", name);
+    m.ld = c;
+  }
+  m.p = t.data_ptr();
+  return m;
+}
+// The same where an argument may be None, of the type of another.
+Mat matrix(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+  if (o == Py_None) return Mat();
+  const at::Tensor& t = tensor(o, name);
+  const Mat m = matrix(t, name, rows, cols);
+  if (t.scalar_type() != type) bad("%s: %s where %s is needed", name, type_name(t.scalar_type()), type_name(type));
+  return m;
+}
+Mat needed(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+  tensor(o, name);
+  return matrix(o, name, rows, cols, type);
+}
+
+// A contiguous vector argument, fp32 or (code given) of any of the types.
+void* vector(PyObject* o, const char* name, int64_t n, int* code) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  const at::ScalarType s = t.scalar_type();
+  const bool fits = s == at::kFloat || (code && (s == at::kBFloat16 || s == at::kHalf));
+  if (t.dim() != 1 || t.size(0) != n || !t.is_cuda() || !fits || !t.is_contiguous())
+    bad("%s: a contiguous CUDA vector of %lld elements of torch.float32%s is needed", name, (long long)n,
+        code ? " or torch.bfloat16 or torch.float16" : "");
+  if (code) *code = type_code(t, name);
+  return t.data_ptr();
+}
+
+struct Space {
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+Space workspace(PyObject* o) {
+  Space w;
+  if (o == Py_None) return w;
+  const at::Tensor& t = tensor(o, "workspace");
+  if (!t.is_cuda() || t.scalar_type() != at::kByte || !t.is_contiguous()) bad("workspace: a contiguous CUDA uint8 tensor is needed");
+  w.p = t.data_ptr(), w.bytes = (size_t)t.numel();
+  return w;
+}
+
+// An ActCheckpoint: its size and its arrays' addresses, which its constructor checked.
+PyObject *s_rows, *s_cols, *s_codes, *s_steps, *s_stream;
+int64_t number(PyObject* o, PyObject* field) {
+  PyObject* v = PyObject_GetAttr(o, field);
+  if (!v) throw Bad{};
+  const int64_t x = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  if (x == -1 && PyErr_Occurred()) throw Bad{};
+  return x;
+}
+struct Held {
+  int64_t rows = 0, cols = 0;
+  int8_t* codes = nullptr;
+  uint8_t* steps = nullptr;
+};
+Held held(PyObject* o) {
+  Held h;
+  h.rows = number(o, s_rows), h.cols = number(o, s_cols);
+  h.codes = reinterpret_cast<int8_t*>(number(o, s_codes)), h.steps = reinterpret_cast<uint8_t*>(number(o, s_steps));
+  return h;
+}
+Held held(PyObject* o, const char* name, int64_t rows, int64_t cols) {
+  if (o == Py_None) return Held();
+  const Held h = held(o);
+  if (h.rows != rows || h.cols != cols)
+    bad("%s: a checkpoint of (%lld, %lld) where (%lld, %lld) is needed", name, (long long)h.rows, (long long)h.cols,
+        (long long)rows, (long long)cols);
+  return h;
+}
+
+// A torch stream, a number, or None for the current stream of the tensor's device.
+void* stream_of(PyObject* o, const at::Tensor& t) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+  PyObject* v = PyObject_HasAttr(o, s_stream) ? PyObject_GetAttr(o, s_stream) : PyNumber_Long(o);
+  if (!v) throw Bad{};
+  void* s = PyLong_AsVoidPtr(v);
+  Py_DECREF(v);
+  if (!s && PyErr_Occurred()) throw Bad{};
+  return s;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Bad{};
+  return v != 0;
+}
+
+template <typename F, typename... A>
+PyObject* call(F f, A... a) {
+  gc_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = f(a...);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+// ---------------------------------------------------------------- calls
+using Args = PyObject* const*;
+
+PyObject* act_compress(Args a) {  // x, ckpt, stream
+  const at::Tensor& x = tensor(a[0], "x");
+  const Held h = held(a[1]);
+  const Mat m = matrix(x, "x", h.rows, h.cols);
+  return call(entry.act_compress, m.p, m.ld, type_code(x, "x"), h.rows, h.cols, h.codes, h.steps, stream_of(a[2], x));
+}
+
+PyObject* act_decompress(Args a) {  // ckpt, out, stream
+  const Held h = held(a[0]);
+  const at::Tensor& out = tensor(a[1], "out");
+  const Mat m = matrix(out, "out", h.rows, h.cols);
+  return call(entry.act_decompress, h.codes, h.steps, h.rows, h.cols, m.p, m.ld, type_code(out, "out"), stream_of(a[2], out));
+}
+
+PyObject* rmsnorm(Args a) {  // x, weight, eps, y, residual, h, rstd, ckpt, stream
+  const at::Tensor& x = tensor(a[0], "x");
+  const Mat mx = matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  const at::ScalarType type = x.scalar_type();
+  const int code = type_code(x, "x");
+  const Mat r = matrix(a[4], "residual", rows, cols, type), y = matrix(a[3], "y", rows, cols, type),
+            h = matrix(a[5], "h", rows, cols, type);
+  int wcode = 0;
+  void* const w = vector(a[1], "weight", cols, &wcode);
+  float* const rstd = static_cast<float*>(vector(a[6], "rstd", rows, nullptr));
+  const Held c = held(a[7], "ckpt", rows, cols);
+  const double eps = PyFloat_AsDouble(a[2]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Bad{};
+  return call(entry.rmsnorm, mx.p, mx.ld, r.p, r.ld, code, w, wcode, (float)eps, rows, cols, y.p, y.ld, h.p, h.ld, rstd,
+              c.codes, c.steps, stream_of(a[8], x));
+}
+
+PyObject* rmsnorm_backward(Args a) {  // dy, ckpt, rstd, weight, dx, dw, workspace, dh, accumulate, stream
+  const at::Tensor& dy = tensor(a[0], "dy");
+  const Held c = held(a[1]);
+  const Mat d = matrix(dy, "dy", c.rows, c.cols);
+  const at::ScalarType type = dy.scalar_type();
+  const int code = type_code(dy, "dy");
+  const Mat dx = needed(a[4], "dx", c.rows, c.cols, type), dh = matrix(a[7], "dh", c.rows, c.cols, type);
+  int wcode = 0;
+  void* const w = vector(a[3], "weight", c.cols, &wcode);
+  float* const dw = static_cast<float*>(vector(a[5], "dw", c.cols, nullptr));
+  const Space ws = dw ? workspace(a[6]) : Space();
+  if (a[2] == Py_None) bad("rstd is needed");
+  float* const rstd = static_cast<float*>(vector(a[2], "rstd", c.rows, nullptr));
+  return call(entry.rmsnorm_backward, d.p, d.ld, dh.p, dh.ld, code, c.codes, c.steps, rstd, w, wcode, c.rows, c.cols, dx.p,
+              dx.ld, dw, truth(a[8]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[9], dy));
+}
+
+int kind_of(PyObject* o) {
+  const long k = PyLong_AsLong(o);
+  if (k == -1 && PyErr_Occurred()) throw Bad{};
+  return (int)k;
+}
+
+PyObject* gated_act(Args a) {  // kind, gate, up, out, ckpt_gate, ckpt_up, stream
+  const at::Tensor& gate = tensor(a[1], "gate");
+  const Mat g = matrix(gate, "gate");
+  const int64_t rows = gate.size(0), cols = gate.size(1);
+  const at::ScalarType type = gate.scalar_type();
+  const int code = type_code(gate, "gate");
+  const Mat u = needed(a[2], "up", rows, cols, type), out = needed(a[3], "out", rows, cols, type);
+  const Held cg = held(a[4], "ckpt_gate", rows, cols), cu = held(a[5], "ckpt_up", rows, cols);
+  return call(entry.gated_act, kind_of(a[0]), g.p, g.ld, u.p, u.ld, code, rows, cols, out.p, out.ld, cg.codes, cg.steps,
+              cu.codes, cu.steps, stream_of(a[6], gate));
+}
+
+PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out, stream
+  const at::Tensor& dout = tensor(a[1], "dout");
+  const Held cg = held(a[2]);
+  const Mat d = matrix(dout, "dout", cg.rows, cg.cols);
+  const at::ScalarType type = dout.scalar_type();
+  const int code = type_code(dout, "dout");
+  const Mat dg = needed(a[4], "dgate", cg.rows, cg.cols, type), du = needed(a[5], "dup", cg.rows, cg.cols, type);
+  const Held cu = held(a[3], "ckpt_up", cg.rows, cg.cols), co = held(a[6], "ckpt_out", cg.rows, cg.cols);
+  return call(entry.gated_act_backward, kind_of(a[0]), d.p, d.ld, code, cg.codes, cg.steps, cu.codes, cu.steps, cg.rows,
+              cg.cols, dg.p, dg.ld, du.p, du.ld, co.codes, co.steps, stream_of(a[7], dout));
+}
+
+PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accumulate, stream
+  const at::Tensor& dy = tensor(a[0], "dy");
+  const Held c = held(a[1]);
+  const int64_t n = dy.dim() > 0 ? dy.size(-1) : 0;
+  const Mat d = matrix(dy, "dy", c.rows, n), dw = needed(a[2], "dw", n, c.cols, at::kFloat);
+  const int code = type_code(dy, "dy");
+  int scode = 0;
+  void* const scale = vector(a[4], "col_scale", c.cols, &scode);
+  const Space ws = workspace(a[3]);
+  return call(entry.act_weight_grad, d.p, d.ld, code, c.rows, n, c.codes, c.steps, c.cols, scale, scode,
+              static_cast<float*>(dw.p), dw.ld, truth(a[5]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[6], dy));
+}
+
+// checkpoint(codes, steps, rows, groups): the arrays of an ActCheckpoint, checked; their addresses
+PyObject* checkpoint(Args a) {
+  const int64_t rows = PyLong_AsLongLong(a[2]), groups = PyLong_AsLongLong(a[3]);
+  if (PyErr_Occurred()) throw Bad{};
+  const at::Tensor &codes = tensor(a[0], "codes"), &steps = tensor(a[1], "steps");
+  auto check = [&](const at::Tensor& t, const char* name, int64_t cols, at::ScalarType type, const char* what) {
+    if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !t.is_cuda())
+      bad("%s: a contiguous CUDA %s tensor of shape (%lld, %lld) is needed", name, what, (long long)rows, (long long)cols);
+  };
+  check(codes, "codes", 32 * groups, at::kChar, "int8");
+  check(steps, "steps", groups, at::kByte, "uint8");
+  return Py_BuildValue("NN", PyLong_FromVoidPtr(codes.data_ptr()), PyLong_FromVoidPtr(steps.data_ptr()));
+}
+
+template <PyObject* (*F)(Args), int N>
+PyObject* checked(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%d arguments are needed", N);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Bad&) {
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+#define GC_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&checked<f, n>)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&bind)), METH_FASTCALL, nullptr},
+                         GC_METHOD(checkpoint, 4),
+                         GC_METHOD(act_compress, 3),
+                         GC_METHOD(act_decompress, 3),
+                         GC_METHOD(rmsnorm, 9),
+                         GC_METHOD(rmsnorm_backward, 10),
+                         GC_METHOD(gated_act, 7),
+                         GC_METHOD(gated_act_backward, 8),
+                         GC_METHOD(act_weight_grad, 7),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__marshal() {
+  s_rows = PyUnicode_InternFromString("rows"), s_cols = PyUnicode_InternFromString("cols");
+  s_codes = PyUnicode_InternFromString("_codes"), s_steps = PyUnicode_InternFromString("_steps");
+  s_stream = PyUnicode_InternFromString("cuda_stream");
+  return PyModule_Create(&module);
+}
