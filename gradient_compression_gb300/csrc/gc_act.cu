@@ -167,7 +167,7 @@ __device__ __forceinline__ F2 gate_sigmoid2(const float* g, F2* dp) {
   F2 h = f2(ex2_ftz(x[0]), ex2_ftz(x[1]));
   h = fma2(h, mul2(low, f2(-0.693147180559945f)), h);
   const F2 f = mul2(h, h);
-  put2(x, add2(f, f2(1.0f)));
+  put2(x, fma2(h, h, f2(1.0f)));
   const F2 right = f2(rcp_ftz(x[0]), rcp_ftz(x[1]));
   put2(r, right), put2(x, mul2(f, right));
   return f2(g[0] < 0.0f ? x[0] : r[0], g[1] < 0.0f ? x[1] : r[1]);

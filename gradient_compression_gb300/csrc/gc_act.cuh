@@ -75,7 +75,9 @@ __device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[CHUNK]) {
 // Two fp32 operations in one instruction (each lane rounds as its scalar form
 // does).  The streaming kernels are bound by the issue of instructions next to
 // memory: with scalar arithmetic GELU's backward issued in 82% of the cycles at
-// 0.66 of a copy's rate, now 0.89.
+// 0.66 of a copy's rate, now 0.89.  A product that is only added to something
+// is written as fma2: the assembler fuses mul2 and add2 in some kernels and not
+// in others, and the bits are to be the same in all.
 struct F2 {
   uint64_t v;
 };

@@ -16,18 +16,26 @@ struct RowShape {
   int threads;  // of a CTA
 };
 
-// The sum over a row's warps of each thread's v, the same bits in all of its
-// threads.  `red` holds 2 x 16 floats and is used alternately: one barrier.
-__device__ __forceinline__ float row_sum(float v, int W, float (&red)[2][16], int& turn) {
+// The sum over a row's warps of each thread's V values, the same bits in all of
+// its threads.  `red` holds 2 x 32 floats and is used alternately: one barrier.
+// With V = 2 a warp stands for two, w and w + W, of the order with V = 1: a row
+// gives the same bits on twice the warps.
+template <int V>
+__device__ __forceinline__ float row_sum(float (&v)[V], int W, float (&red)[2][32], int& turn) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
-  if (W == 1) return v;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(FULL, v[i], o));
+  if (W == 1) return V == 1 ? v[0] : __fadd_rn(v[0], v[V - 1]);
+  const int warp = threadIdx.x >> 5, w = warp & (W - 1);
+  float* const of = &red[turn][(warp - w) * V];
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) of[i * W + w] = v[i];
+  }
   __syncthreads();
-  const float* of = &red[turn][warp & ~(W - 1)];
   float s = __fadd_rn(of[0], of[1]);
-  for (int i = 2; i < W; i += 2) s = __fadd_rn(s, __fadd_rn(of[i], of[i + 1]));
+  for (int i = 2; i < V * W; i += 2) s = __fadd_rn(s, __fadd_rn(of[i], of[i + 1]));
   turn ^= 1;
   return s;
 }
@@ -41,11 +49,32 @@ __device__ __forceinline__ float rms_inverse(float ss, float share, float eps) {
 // four of every chunk apart, so that a warp's 16-byte loads meet no bank
 // twice.  Ones without weights, zeros past the row's end.
 __device__ __forceinline__ void stage_weights(float4* ws, const void* weight, int wtype, int64_t cols, int chunks) {
-  float* f = reinterpret_cast<float*>(ws);
-  for (int c = threadIdx.x; c < chunks * CHUNK; c += blockDim.x)
-    f[((c >> 2) & 1) * 4 * chunks + (c >> 3) * 4 + (c & 3)] = c < cols ? (weight ? load_as_f32(weight, wtype, c) : 1.0f) : 0.0f;
+  const bool lanes = ((uintptr_t)weight & 15u) == 0;
+#pragma unroll 2
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    const int n = (int)min(cols - (int64_t)c * CHUNK, (int64_t)CHUNK);
+    float w[CHUNK];
+    if (weight && lanes && n == CHUNK) {
+      if (wtype == GC_F32) {
+        const float4* from = static_cast<const float4*>(weight) + 2 * c;
+        const float4 a = __ldg(from), b = __ldg(from + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else {
+        const uint4 a = __ldg(static_cast<const uint4*>(weight) + c);
+        if (wtype == GC_BF16)
+          unpack(*reinterpret_cast<const Raw8<__nv_bfloat16>*>(&a), w);
+        else
+          unpack(*reinterpret_cast<const Raw8<__half>*>(&a), w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) w[e] = e < n ? (weight ? load_as_f32(weight, wtype, (int64_t)c * CHUNK + e) : 1.0f) : 0.0f;
+    }
+    ws[c] = make_float4(w[0], w[1], w[2], w[3]), ws[chunks + c] = make_float4(w[4], w[5], w[6], w[7]);
+  }
   __syncthreads();
 }
+
 __device__ __forceinline__ void load_weights(const float4* ws, int chunks, int c8, float (&w)[CHUNK]) {
   const int c = min(c8, chunks - 1);  // a lane past the row's end weighs nothing
   const float4 a = ws[c], b = ws[chunks + c];
@@ -160,7 +189,7 @@ __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
               uint8_t* steps) {
   using S = RowShared<T, N, MODE>;
   constexpr int SLOTS = S::SLOTS;
-  __shared__ float red[2][16];
+  __shared__ float red[2][32];
   extern __shared__ float4 shared[];  // the weights, then the rings and the warps' staging
   chain_wait();
   const RowChunks<N, MODE> at(warps, cols, groups);
@@ -214,7 +243,8 @@ __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
       for (int j = 0; j < N; ++j) hto.put(j, v[j], at.n(j), in, own);
       hto.done();
     }
-    const float rs = rms_inverse(row_sum(__fadd_rn(ss[0], ss[1]), at.W, red, turn), share, eps);
+    float sum[1] = {__fadd_rn(ss[0], ss[1])};
+    const float rs = rms_inverse(row_sum(sum, at.W, red, turn), share, eps);
     if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -267,7 +297,8 @@ __global__ void __launch_bounds__(512, 1)
   using S = RowShared<T, N, MODE>;
   constexpr int SLOTS = S::SLOTS;
   constexpr bool AGAIN = N == 4;
-  __shared__ float red[2][16];
+  constexpr int V = N / 2;
+  __shared__ float red[2][32];
   extern __shared__ float4 shared[];
   chain_wait();
   const RowChunks<N, MODE> at(warps, cols, groups);
@@ -324,7 +355,7 @@ __global__ void __launch_bounds__(512, 1)
     din.in.landed();
     if (SLOTS == 2) copy(slot ^ 1);
     if (lead + stride < rows) fetch(r + stride);
-    float gw[N][CHUNK], q[N][CHUNK], s[2] = {0.0f, 0.0f};
+    float gw[N][CHUNK], q[N][CHUNK], s[V][2] = {};
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
@@ -343,10 +374,13 @@ __global__ void __launch_bounds__(512, 1)
         const F2 g = get2(gw[j] + e), qe = get2(q[j] + e), ge = mul2(g, get2(w + e));
         put2(dw[j] + e, fma2(g, qe, get2(dw[j] + e)));
         put2(gw[j] + e, ge);
-        put2(s, fma2(ge, qe, get2(s)));
+        put2(s[j % V], fma2(ge, qe, get2(s[j % V])));
       }
     }
-    const float minus_mean = __fmul_rn(row_sum(__fadd_rn(s[0], s[1]), at.W, red, turn), -share);
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = __fadd_rn(s[i][0], s[i][1]);
+    const float minus_mean = __fmul_rn(row_sum(sum, at.W, red, turn), -share);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
@@ -362,8 +396,8 @@ __global__ void __launch_bounds__(512, 1)
       if (AGAIN || sizeof(T) == 4) chunk_values(code.take(slot * N + j), step[j], q[j]);
 #pragma unroll
       for (int e = 0; e < CHUNK; e += 2) {
-        const F2 v = mul2(f2(inverse), fma2(get2(q[j] + e), f2(minus_mean), get2(gw[j] + e)));
-        put2(gw[j] + e, dh ? add2(v, get2(t + e)) : v);
+        const F2 v = fma2(get2(q[j] + e), f2(minus_mean), get2(gw[j] + e));
+        put2(gw[j] + e, dh ? fma2(f2(inverse), v, get2(t + e)) : mul2(f2(inverse), v));
       }
       to.put(j, gw[j], at.n(j), in, own);
     }
@@ -537,8 +571,9 @@ __global__ void __launch_bounds__(NTHREADS)
 constexpr int NORM_SMS = 152;  // of a GB300
 
 // Chunks per lane: two up to 8192 columns, four beyond; but four in the
-// backward pass of 16-bit rows on 16-byte boundaries.
-static int norm_chunks(int64_t cols, bool four) { return cols <= 8192 && !four ? 2 : 4; }
+// backward pass of 16-bit rows on 16-byte boundaries (up to 512 columns have
+// one warp either way).
+static int norm_chunks(int64_t cols, bool four) { return cols <= (four ? 512 : 8192) ? 2 : 4; }
 static RowShape norm_shape(int64_t cols, int chunks) {
   RowShape s;
   s.warps = 1;
@@ -574,7 +609,7 @@ static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
   if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
   const int two = norm_grid(rows, norm_shape(cols, norm_chunks(cols, false)), BACKWARD_PER_SM);
-  const int four = norm_grid(rows, norm_shape(cols, 4), BACKWARD_PER_SM);
+  const int four = norm_grid(rows, norm_shape(cols, norm_chunks(cols, true)), BACKWARD_PER_SM);
   return two > four ? two : four;
 }
 
