@@ -337,8 +337,13 @@ __global__ void __launch_bounds__(256, SPAN ? 2 : 3)
 // always: 8 fp32 per lane are 32 bytes, and copies of every other 16 bytes
 // reached 0.6 of the copy's rate.)
 template <typename K>
-static K row_kernel(bool span, K aligned, K any) {
-  return span ? any : aligned;
+struct RowKernel {
+  K kern;
+  int ctas;  // that an SM holds
+};
+template <auto ALIGNED, auto ANY>
+static RowKernel<decltype(ANY)> row_kernel(bool span) {
+  return span ? RowKernel<decltype(ANY)>{ANY, resident<ANY>()} : RowKernel<decltype(ANY)>{ALIGNED, resident<ALIGNED>()};
 }
 
 }  // namespace gc
@@ -353,11 +358,12 @@ extern "C" gc_status gc_act_compress(const void* x, int64_t ld, int32_t dtype, i
   if (rows == 0) return GC_OK;
   if ((st = check_matrix(x, ld, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK) return st;
   const bool span = !chunk_aligned(x, ld, dtype);
-  dim3 grid;
-  const Tiling t = make_tiling(rows, cols, span, &grid);
-  GC_BY_DTYPE(dtype, T, launch_chained(row_kernel(span, k_act_compress<T, sizeof(T) == 4>, k_act_compress<T, true>), grid, 256, 0,
-                                       static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, t, codes,
-                                       steps));
+  GC_BY_DTYPE(dtype, T, {
+    const auto k = row_kernel<&k_act_compress<T, sizeof(T) == 4>, &k_act_compress<T, true>>(span);
+    dim3 grid;
+    const Tiling t = make_tiling(rows, cols, span, k.ctas, &grid);
+    launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(x), ld, t, codes, steps);
+  });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -369,11 +375,12 @@ extern "C" gc_status gc_act_decompress(const int8_t* codes, const uint8_t* steps
   if (rows == 0) return GC_OK;
   if ((st = check_codes(codes, steps)) != GC_OK || (st = check_matrix(out, ldo, cols, dtype)) != GC_OK) return st;
   const bool span = !chunk_aligned(out, ldo, dtype);
-  dim3 grid;
-  const Tiling t = make_tiling(rows, cols, span, &grid);
-  GC_BY_DTYPE(dtype, T, launch_chained(row_kernel(span, k_act_decompress<T, sizeof(T) == 4>, k_act_decompress<T, true>), grid, 256, 0,
-                                       static_cast<cudaStream_t>(stream), codes, steps, t, static_cast<T*>(out),
-                                       ldo));
+  GC_BY_DTYPE(dtype, T, {
+    const auto k = row_kernel<&k_act_decompress<T, sizeof(T) == 4>, &k_act_decompress<T, true>>(span);
+    dim3 grid;
+    const Tiling t = make_tiling(rows, cols, span, k.ctas, &grid);
+    launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), codes, steps, t, static_cast<T*>(out), ldo);
+  });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -393,13 +400,13 @@ extern "C" gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, c
     if ((st = check_codes(gate_codes, gate_steps)) != GC_OK || (st = check_codes(up_codes, up_steps)) != GC_OK)
       return st;
   const bool span = !(chunk_aligned(gate, ldg, dtype) && chunk_aligned(up, ldu, dtype) && chunk_aligned(out, ldo, dtype));
-  dim3 grid;
-  const Tiling t = make_tiling(rows, cols, span, &grid);
   GC_BY_DTYPE(dtype, T, {
     constexpr bool S = sizeof(T) == 4;
-    auto kern = kind == GC_GATE_SILU ? row_kernel(span, k_gated<T, GC_GATE_SILU, S>, k_gated<T, GC_GATE_SILU, true>)
-                                     : row_kernel(span, k_gated<T, GC_GATE_GELU_TANH, S>, k_gated<T, GC_GATE_GELU_TANH, true>);
-    launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
+    const auto k = kind == GC_GATE_SILU ? row_kernel<&k_gated<T, GC_GATE_SILU, S>, &k_gated<T, GC_GATE_SILU, true>>(span)
+                                        : row_kernel<&k_gated<T, GC_GATE_GELU_TANH, S>, &k_gated<T, GC_GATE_GELU_TANH, true>>(span);
+    dim3 grid;
+    const Tiling t = make_tiling(rows, cols, span, k.ctas, &grid);
+    launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(gate), ldg,
                    static_cast<const T*>(up), ldu, t, static_cast<T*>(out), ldo, gate_codes, gate_steps, up_codes,
                    up_steps);
   });
@@ -423,14 +430,14 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
   const bool span = !(chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype));
-  dim3 grid;
-  const Tiling t = make_tiling(rows, cols, span, &grid);
   GC_BY_DTYPE(dtype, T, {
     constexpr bool S = sizeof(T) == 4;
-    auto kern = kind == GC_GATE_SILU
-                    ? row_kernel(span, k_gated_backward<T, GC_GATE_SILU, S>, k_gated_backward<T, GC_GATE_SILU, true>)
-                    : row_kernel(span, k_gated_backward<T, GC_GATE_GELU_TANH, S>, k_gated_backward<T, GC_GATE_GELU_TANH, true>);
-    launch_chained(kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
+    const auto k = kind == GC_GATE_SILU
+                       ? row_kernel<&k_gated_backward<T, GC_GATE_SILU, S>, &k_gated_backward<T, GC_GATE_SILU, true>>(span)
+                       : row_kernel<&k_gated_backward<T, GC_GATE_GELU_TANH, S>, &k_gated_backward<T, GC_GATE_GELU_TANH, true>>(span);
+    dim3 grid;
+    const Tiling t = make_tiling(rows, cols, span, k.ctas, &grid);
+    launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
                    gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
                    out_codes, out_steps);
   });

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   int g = 0;
 
   if (warp < WG_CONV) {
-    // ------------------------------------------------ unpack q (and split dy)
+    // ------------------------------------------------ unpack q
     if (S::REGS_CONV < WG_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_CONV));
     // Lanes past q's last column read the last columns again: what they put
     // into the tile reaches only columns of the accumulators that are not
@@ -756,11 +756,11 @@ template <typename T, int PARTS>
 static void launch_split(const void* dy, int64_t lddy, int64_t rows, int64_t n, __nv_bfloat16* terms, int64_t ldt,
                          cudaStream_t s) {
   const bool span = sizeof(T) == 4 || !aligned16(dy) || lddy % 8 != 0;
-  dim3 grid;
-  const Tiling t = make_tiling(rows, n, span, &grid);
   // a bf16 dy comes here only as spans, fp32 always does
-  auto kern = span ? k_split<T, PARTS, true> : k_split<T, PARTS, PARTS != 2>;
-  launch_chained(kern, grid, 256, 0, s, static_cast<const T*>(dy), lddy, t, terms, ldt);
+  constexpr auto ALIGNED = &k_split<T, PARTS, PARTS != 2>, ANY = &k_split<T, PARTS, true>;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, n, span, span ? resident<ANY>() : resident<ALIGNED>(), &grid);
+  launch_chained(span ? ANY : ALIGNED, grid, 256, 0, s, static_cast<const T*>(dy), lddy, t, terms, ldt);
 }
 
 // Workspace: the diagnostic words, dy's terms (none for a bf16 dy whose n
