@@ -47,7 +47,8 @@ __device__ __forceinline__ float rms_inverse(float ss, float share, float eps) {
 
 // The weights as fp32 in shared memory, once per CTA: the first and the last
 // four of every chunk apart, so that a warp's 16-byte loads meet no bank
-// twice.  Ones without weights, zeros past the row's end.
+// twice.  Ones without weights, zeros past the row's end.  Read 16 bytes a lane:
+// element by element this took every CTA's start 2.3 us longer.
 __device__ __forceinline__ void stage_weights(float4* ws, const void* weight, int wtype, int64_t cols, int chunks) {
   const bool lanes = ((uintptr_t)weight & 15u) == 0;
 #pragma unroll 2
@@ -177,11 +178,12 @@ struct RowTo {
 };
 
 // One pass, bound by memory and by what a row's warps wait for each other:
-// 16384 x 4096 in bf16 with residual, h, rstd and checkpoint takes 103 us
-// (0.88 of a copy's rate), 16384 x 8192 213 us (0.85), fp32 203 us (0.85), rows
-// of 4095 158 us (0.57: spans, bound by instructions).  The bounds stand for
-// registers: 80 a thread, three CTAs of 256 per SM, or 128 and two for spans
-// (170 us, fp32 227 us, with three).
+// 16384 x 4096 in bf16 with residual, h, rstd and checkpoint takes 94 us (0.97
+// of a copy's rate), 16384 x 8192 203 us (0.89), fp32 194 us (0.88), rows of 4095
+// 149 us (0.61: spans, bound by instructions); one row 2.7 us.  The bounds stand
+// for registers: 80 a thread, three CTAs of 256 per SM (four of 64: 104 us, two
+// 99), or 128 and two for spans (12 and 25 us more, rows of 4095 and fp32, with
+// three).
 template <typename T, int N, int MODE>
 __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
@@ -285,10 +287,11 @@ __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
 // Bound by memory and by the waits within a row, as above.  With four chunks
 // per lane (rows on 16-byte boundaries) fewer warps wait for a row; gw and q do
 // not fit into registers next to dw across that wait and are worked out AGAIN
-// from the rings.  16384 x 4096 in bf16 with dh and dw: 81 us (0.87 of a copy's
-// rate; two chunks 88, four without AGAIN 130), 8192 columns 158 us (0.89; 166),
-// 16384 columns 289 us (0.98).  Spans and fp32, bound by instructions, keep two
-// chunks: rows of 4095 134 us (0.53; four chunks 165), fp32 164 us (0.80; 230).
+// from the rings (88 us with two chunks where four took 81, and four without
+// AGAIN 130).  16384 x 4096 in bf16 with dh and dw: 76 us (0.93 of a copy's rate),
+// 8192 columns 148 us (0.96), 16384 columns 281 us (1.0).  Spans and fp32, bound by
+// instructions, keep two chunks: rows of 4095 126 us (0.56), fp32 157 us (0.83);
+// with four 30 and 60 us more.
 template <typename T, int N, int MODE>
 __global__ void __launch_bounds__(512, 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(512, 1)
 
 // dw[c] = (dw[c] +) the partial sums in a fixed order: 32 columns per CTA, 32
 // warps each over every 32nd sum, its loads issued eight at a time: bound by
-// their latency.  1031 x 1001 in fp32 takes 7.6 us with its backward pass.
+// their latency.  1031 x 1001 in fp32 takes 7.1 us with its backward pass.
 __global__ void __launch_bounds__(1024) k_rmsnorm_dw_join(const float* part, int parts, int64_t cols, int64_t ldp, float* dw,
                                                           int accumulate) {
   __shared__ float sum[32][33];
@@ -601,9 +604,9 @@ template <int N>
 struct Chunks {
   static constexpr int value = N;
 };
-// CTAs of 256 threads per SM in a grid: two waves forward (103 us for 16384 x
-// 4096 in bf16; one wave and four 108 and 107), one of two CTAs backward, whose
-// sums of dw grow with the CTAs.
+// CTAs of 256 threads per SM in a grid: two waves forward (94 us for 16384 x
+// 4096 in bf16; one wave 101, four 94, but 8192 columns 203, 250 and 208), one of
+// two CTAs backward, whose sums of dw grow with the CTAs.
 constexpr int FORWARD_PER_SM = 6, SPAN_PER_SM = 4, BACKWARD_PER_SM = 2;
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;

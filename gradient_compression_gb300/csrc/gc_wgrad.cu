@@ -2,6 +2,8 @@
 // tensor cores: dw[n, k] = sum_t dy[t, n] * q[t, k], q = code * step.
 #include <cuda.h>
 
+#include <cmath>
+
 #include "gc_act.cuh"
 #include "gc_host.h"
 
@@ -10,9 +12,9 @@ namespace gc {
 // Mathematics and precision.  q's code has 7 bits and its step is a power of
 // two, so q is exact in bf16; a bf16 dy is too, an fp16 dy is the exact sum
 // of two bf16 terms (11 bits = 8 + 3) and an fp32 dy of three (24 = 8 + 8 +
-// 8).  Every product is therefore exact and only the fp32 sums round.  The
-// terms, and a bf16 dy whose rows cannot be copied in bulk, are written to the
-// workspace first: 8192 x 1024 x 1024 in fp16 takes 43 us so, and took 52 with
+// 8, for numbers above 2^-109).  Every product is therefore exact and only the
+// fp32 sums round.  The terms, and a bf16 dy whose rows cannot be copied in bulk, are written to the
+// workspace first: 8192 x 1024 x 1024 in fp16 takes 40 us so, and took 52 with
 // dy split beside the MMAs by the unpacking warps.
 //
 // Tile.  A CTA computes 256 (n) x 256 (k) of dw: two accumulators of 128 x
@@ -33,6 +35,11 @@ namespace gc {
 // own.  The two accumulators' chains end half a chain apart, so that the
 // other one's MMAs go on with the stages at hand meanwhile; and CTAs end them
 // at different times, so that they do not all write at once.
+//
+// Measured: 16384 x 14336 x 4096 in bf16 1.23 ms, 1566 TFLOP/s (one chain 1.12 ms;
+// 1.35 ms in long runs under the power cap); 8192 x 4864 x 2048 110 us, where a
+// library's product of two bf16 matrices takes 92; 8192 x 1024 x 1024 25 us, in
+// fp16 40 us.
 //
 // Both operands have the summed index t as their slow dimension in memory,
 // so both are staged "MN-major": 128-byte rows of 64 consecutive n (or k) of
@@ -358,7 +365,9 @@ __device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map
 }
 
 // A CTA takes every gridDim.x-th item (a tile and a split of the rows); all
-// roles walk the same items, and `g` counts the stages.
+// roles walk the same items, and `g` counts the stages.  !TMA is reached by a
+// bf16 dy off 16-byte boundaries whose n is a multiple of 8, for which no
+// workspace is set aside.
 template <int PARTS, bool TMA>
 __global__ void __launch_bounds__(WG_THREADS, 1)
     k_weight_grad(const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap out_map,
@@ -600,8 +609,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 }
 
 // dw = (dw +) cscale * the splits' sums in their order, four columns per
-// thread and four sums' loads at a time.  vec: rows of dw on 16-byte
-// boundaries.
+// thread and eight sums' loads at a time.  vec: rows of dw on 16-byte
+// boundaries.  Bound by L2 and latency: four sums of 1024 x 1024 take 6 us.
 __global__ void __launch_bounds__(256) k_weight_grad_join(const float4* part, int splits, int64_t n, int64_t k, int64_t fours,
                                                           const void* cscale, int ctype, float* dw, int64_t lddw,
                                                           int accumulate, bool vec) {
@@ -611,12 +620,12 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const float4* part, in
     const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)i / (uint32_t)fours) : i / fours;
     const int64_t c = (i - r * fours) * 4;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = 0; p < splits; p += 4) {
-      float4 v[4];
+    for (int p = 0; p < splits; p += 8) {
+      float4 v[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = p + q < splits ? __ldg(part + (p + q) * total + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int q = 0; q < 8; ++q) v[q] = p + q < splits ? __ldg(part + (p + q) * total + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 8; ++q) {
         s[0] = __fadd_rn(s[0], v[q].x), s[1] = __fadd_rn(s[1], v[q].y);
         s[2] = __fadd_rn(s[2], v[q].z), s[3] = __fadd_rn(s[3], v[q].w);
       }
@@ -640,6 +649,7 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const float4* part, in
 
 // The bf16 terms of dy, one [rows, ldt] after another: the upper halves of
 // what is left, by truncation, so that nothing overflows and the rest is exact.
+// Bound by memory: 8192 x 1024 in fp16 takes 8 us.
 template <typename T, int PARTS, bool SPAN>
 __global__ void __launch_bounds__(256, 4) k_split(const T* dy, int64_t ld, Tiling t, __nv_bfloat16* terms, int64_t ldt) {
   constexpr int AHEAD = 8 / (int)(sizeof(T) / 2);
@@ -685,20 +695,25 @@ __global__ void __launch_bounds__(256, 4) k_split(const T* dy, int64_t ld, Tilin
 
 constexpr int WG_SMS = 152;  // of a GB300
 
-// Splits of the rows: as many as keep every SM busy when there are few
-// tiles, each of at least 128 rows.  A split has a multiple of 64 rows.
 static int64_t wg_span(int64_t rows, int64_t splits) { return ((rows + splits - 1) / splits + 63) / 64 * 64; }
 static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
   const int m = dtype == GC_BF16 ? WgShape<1, true>::M : WgShape<2, false>::M;
   return (n + m - 1) / m;
 }
+// Splits of the rows where there are fewer tiles than SMs.  In us: 64 rows take
+// STAGE, a split's sums take 8 bytes an element at 7 TB/s and 0.1 to write and
+// to join, the join's launch 2; with s splits STAGE * stages / s + each * s, least
+// for their root.  (500 x 4096 x 1024 in bf16 takes 13.6 us whole and 19.8 in
+// two; 1000 x 333 x 1001 in fp32 14.5 in six, 16.6 in three, 23.9 whole.)
 static int wg_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
-  const int64_t tiles = wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N);
-  int64_t s = WG_SMS / tiles;
-  if (s > rows / 128) s = rows / 128;
+  const int64_t most = WG_SMS / (wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N)), stages = (rows + 63) / 64;
+  const double stage = dtype == GC_F32 ? 1.0 : 0.67, each = (double)n * (double)k * 8.0 / 7e6 + 0.1;
+  int64_t s = (int64_t)std::sqrt((double)stages * stage / each);
+  if (s > most) s = most;
   if (s < 2) return 1;
   const int64_t span = wg_span(rows, s);
-  return (int)((rows + span - 1) / span);
+  s = (rows + span - 1) / span;
+  return (double)(span / 64) * stage + (double)s * each + 2.0 < (double)stages * stage ? (int)s : 1;
 }
 static int64_t wg_ldp(int64_t k) { return (k + 3) / 4 * 4; }  // row stride of the splits' sums
 
