@@ -576,7 +576,7 @@ gc_status gc_dense_decompress_accumulate(const gc_layout* dev, const gc_layout* 
  *
  * Arithmetic is fp32 whatever the dtype, each output rounded to its type
  * once; sums are fp32 with a fixed order, so results are bit-identical from
- * run to run.  Unless stated otherwise buffers must not overlap. */
+ * run to run (and, sums over rows apart, for every base address and ld).  Unless stated otherwise buffers must not overlap. */
 typedef enum gc_dtype { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
 
 #define GC_ACCUMULATE 0x1u /* flags: add to dw instead of writing it */
