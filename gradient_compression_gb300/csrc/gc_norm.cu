@@ -5,11 +5,12 @@
 namespace gc {
 
 // A row is held in registers by W warps, N chunks of 8 columns per lane (chunk
-// (j W + w) 32 + lane), so that it is read once; a CTA of 8 warps (16 for the
-// widest rows) works on 8 / W rows at a time and walks over the rows.  Rows
+// (j W + w) 32 + lane), so that it is read once; a CTA of up to 8 warps (W, if
+// that is more) works on 8 / W rows at a time and walks over the rows.  Rows
 // wider than 16384 are read twice (the _wide kernels).
 constexpr int NTHREADS = 256;
 constexpr int64_t NORM_WIDEST = 16384;
+constexpr int THREADS_80 = 768, THREADS_128 = 512;  // of an SM, 80 or 128 registers each
 
 struct RowShape {
   int warps;    // W
@@ -21,21 +22,21 @@ struct RowShape {
 // With V = 2 a warp stands for two, w and w + W, of the order with V = 1: a row
 // gives the same bits on twice the warps.
 template <int V>
-__device__ __forceinline__ float row_sum(float (&v)[V], int W, float (&red)[2][32], int& turn) {
+__device__ __forceinline__ float row_sum(float (&v)[V], int W, int w, float (&red)[2][32], int& turn) {
 #pragma unroll
   for (int o = 16; o; o >>= 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(FULL, v[i], o));
   if (W == 1) return V == 1 ? v[0] : __fadd_rn(v[0], v[V - 1]);
-  const int warp = threadIdx.x >> 5, w = warp & (W - 1);
-  float* const of = &red[turn][(warp - w) * V];
+  float* const of = &red[turn][((int)(threadIdx.x >> 5) - w) * V];  // w: this warp of the row's W
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) of[i * W + w] = v[i];
   }
   __syncthreads();
   float s = __fadd_rn(of[0], of[1]);
-  for (int i = 2; i < V * W; i += 2) s = __fadd_rn(s, __fadd_rn(of[i], of[i + 1]));
+  for (int i = 2; i + 1 < V * W; i += 2) s = __fadd_rn(s, __fadd_rn(of[i], of[i + 1]));
+  if (V == 1 && (W & 1)) s = __fadd_rn(s, of[W - 1]);
   turn ^= 1;
   return s;
 }
@@ -179,13 +180,13 @@ struct RowTo {
 
 // One pass, bound by memory and by what a row's warps wait for each other:
 // 16384 x 4096 in bf16 with residual, h, rstd and checkpoint takes 94 us (0.97
-// of a copy's rate), 16384 x 8192 203 us (0.89), fp32 194 us (0.88), rows of 4095
-// 149 us (0.61: spans, bound by instructions); one row 2.7 us.  The bounds stand
+// of a copy's rate), 5120 columns 118 us (0.97), 8192 202 us (0.90), fp32 195 us (0.88), rows of
+// 4095 150 us (0.60: spans, bound by instructions); one row 2.7 us.  The bounds stand
 // for registers: 80 a thread, three CTAs of 256 per SM (four of 64: 104 us, two
 // 99), or 128 and two for spans (12 and 25 us more, rows of 4095 and fp32, with
 // three).
 template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
+__global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? THREADS_80 : THREADS_128, 1)
     k_rmsnorm(const T* x, int64_t ldx, const T* res, int64_t ldr, const void* weight, int wtype, float eps, int64_t rows,
               int64_t cols, int64_t groups, int warps, T* y, int64_t ldy, T* h, int64_t ldh, float* rstd, int8_t* codes,
               uint8_t* steps) {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
       hto.done();
     }
     float sum[1] = {__fadd_rn(ss[0], ss[1])};
-    const float rs = rms_inverse(row_sum(sum, at.W, red, turn), share, eps);
+    const float rs = rms_inverse(row_sum(sum, at.W, at.first >> 5, red, turn), share, eps);
     if (rstd && in && threadIdx.x % (32 * at.W) == 0) rstd[r] = rs;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -290,10 +291,10 @@ __global__ void __launch_bounds__(N == 2 && MODE != ROW_SPAN ? 768 : 512, 1)
 // from the rings (88 us with two chunks where four took 81, and four without
 // AGAIN 130).  16384 x 4096 in bf16 with dh and dw: 76 us (0.93 of a copy's rate),
 // 8192 columns 148 us (0.96), 16384 columns 281 us (1.0).  Spans and fp32, bound by
-// instructions, keep two chunks: rows of 4095 126 us (0.56), fp32 157 us (0.83);
+// instructions, keep two chunks: rows of 4095 126 us (0.56), fp32 161 us (0.81);
 // with four 30 and 60 us more.
 template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(THREADS_128, 1)
     k_rmsnorm_backward(const T* dy, int64_t lddy, const T* dh, int64_t lddh, const int8_t* codes, const uint8_t* steps,
                        const float* rstd, const void* weight, int wtype, int64_t rows, int64_t cols, int64_t groups,
                        int warps, T* dx, int64_t lddx, float* part) {
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(512, 1)
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = __fadd_rn(s[i][0], s[i][1]);
-    const float minus_mean = __fmul_rn(row_sum(sum, at.W, red, turn), -share);
+    const float minus_mean = __fmul_rn(row_sum(sum, at.W, at.first >> 5, red, turn), -share);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int n = in ? at.n(j) : 0;
@@ -577,17 +578,20 @@ constexpr int NORM_SMS = 152;  // of a GB300
 // backward pass of 16-bit rows on 16-byte boundaries (up to 512 columns have
 // one warp either way).
 static int norm_chunks(int64_t cols, bool four) { return cols <= (four ? 512 : 8192) ? 2 : 4; }
+// Warps: an even number with two chunks, half of it with four, so that both add
+// up a row in the same order; as many as 1024 columns each take (5120 columns
+// on 16 warps of two chunks took 202 us for 16384 rows, on ten 118).
 static RowShape norm_shape(int64_t cols, int chunks) {
   RowShape s;
-  s.warps = 1;
-  while ((int64_t)s.warps * chunks * 256 < cols) s.warps *= 2;
-  s.threads = s.warps == 16 ? 512 : 256;
+  s.warps = cols <= 512 ? 1 : (int)((cols + 1023) / 1024) * (chunks == 2 ? 2 : 1);
+  s.threads = s.warps * (s.warps < 8 ? 8 / s.warps : 1) * 32;
   return s;
 }
-// CTAs: one per set of rows, at most `per_sm` per SM.
-static int norm_grid(int64_t rows, const RowShape& s, int per_sm) {
+// CTAs: one per set of rows, at most `waves` times as many as the SMs hold,
+// each SM `threads` threads.
+static int norm_grid(int64_t rows, const RowShape& s, int threads, int waves) {
   const int per = s.threads / 32 / s.warps;
-  const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * per_sm * 256 / s.threads;
+  const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * (threads / s.threads) * waves;
   return (int)(ctas < most ? ctas : most);
 }
 // Shared memory for the widest rows, asked for once per kernel.
@@ -604,15 +608,17 @@ template <int N>
 struct Chunks {
   static constexpr int value = N;
 };
-// CTAs of 256 threads per SM in a grid: two waves forward (94 us for 16384 x
-// 4096 in bf16; one wave 101, four 94, but 8192 columns 203, 250 and 208), one of
-// two CTAs backward, whose sums of dw grow with the CTAs.
-constexpr int FORWARD_PER_SM = 6, SPAN_PER_SM = 4, BACKWARD_PER_SM = 2;
+// What the SMs hold by the kernels' registers: two waves forward (94 us for 16384 x 4096 in bf16; one wave 101, four 94), one
+// backward, whose sums of dw grow with the CTAs.
+static int forward_grid(int64_t rows, const RowShape& s, int chunks, int mode) {
+  return norm_grid(rows, s, chunks == 2 && mode != ROW_SPAN ? THREADS_80 : THREADS_128, 2);
+}
+static int backward_grid(int64_t rows, const RowShape& s) { return norm_grid(rows, s, THREADS_128, 1); }
 static int dw_parts(int64_t rows, int64_t cols) {
   if (rows < 1) return 1;
   if (cols > NORM_WIDEST) return (int)(rows < 64 ? rows : 64);
-  const int two = norm_grid(rows, norm_shape(cols, norm_chunks(cols, false)), BACKWARD_PER_SM);
-  const int four = norm_grid(rows, norm_shape(cols, norm_chunks(cols, true)), BACKWARD_PER_SM);
+  const int two = backward_grid(rows, norm_shape(cols, norm_chunks(cols, false)));
+  const int four = backward_grid(rows, norm_shape(cols, norm_chunks(cols, true)));
   return two > four ? two : four;
 }
 
@@ -654,7 +660,7 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
       constexpr int N = decltype(per_lane)::value;
       constexpr bool ANY = sizeof(T) == 4;  // fp32 rows are spans always
       auto run = [&](auto kern, size_t ring) -> bool {
-        launch_chained(kern, (unsigned)norm_grid(rows, shape, mode == ROW_SPAN ? SPAN_PER_SM : FORWARD_PER_SM), shape.threads,
+        launch_chained(kern, (unsigned)forward_grid(rows, shape, chunks, mode), shape.threads,
                        (size_t)groups * ACT_GROUP * sizeof(float) + ring, s, static_cast<const T*>(x), ldx,
                        static_cast<const T*>(residual), ldr, weight, weight_dtype, eps, rows, cols, groups, shape.warps,
                        static_cast<T*>(y), ldy, static_cast<T*>(h), ldh, rstd, codes, steps);
@@ -726,7 +732,7 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
   const bool vec = chunk_aligned(dy, lddy, dtype) && (!dh || chunk_aligned(dh, lddh, dtype)) && chunk_aligned(dx, lddx, dtype);
   const int chunks = norm_chunks(cols, vec);
   const RowShape shape = norm_shape(cols, chunks);
-  const int grid = norm_grid(rows, shape, BACKWARD_PER_SM);
+  const int grid = backward_grid(rows, shape);
   const int mode = row_mode(cols, shape, chunks, vec);
   GC_BY_DTYPE(dtype, T, {
     auto go = [&](auto per_lane) -> bool {
