@@ -24,7 +24,7 @@ def off(x):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
-@pytest.mark.parametrize("cols", [1, 33, 500, 512, 513, 1000, 1024, 1030, 2048, 4095, 4096, 5000, 8192, 9000, 16384, 16400])
+@pytest.mark.parametrize("cols", [1, 33, 500, 512, 513, 1000, 1024, 1030, 2048, 4095, 4096, 5000, 8192, 9000, 16384, 16400, 1500, 2500, 3300, 5120, 12288])
 def test_norm(gc, cols, dtype):
     rows = 37
     gen = torch.Generator(device="cuda").manual_seed(cols)
@@ -58,3 +58,30 @@ def test_gated(gc, cols, dtype, kind):
         got.append((a, dg, du, back, ca.codes, ca.steps, cg.codes, cu.codes))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [300, 700, 1500, 2500, 3300, 5120, 6001, 9000, 12288])
+def test_norm_gradient_against_64_bits(gc, cols, dtype):
+    """Every number of warps per row and of rows per CTA.  With u = 2^-24: a sum
+    of n products, in any order, is within n u of the sum of their magnitudes;
+    dx has a handful of further roundings, and one to its type."""
+    rows, u = 700, 2.0 ** -24
+    own = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    ck = gc.ActCheckpoint(rows, cols)
+    gc.act_compress(torch.randn(rows, cols, generator=gen, device="cuda"), ck)
+    dy, dh = (torch.randn(rows, cols, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    w = torch.rand(cols, generator=gen, device="cuda").to(dtype)
+    rstd = 0.5 + torch.rand(rows, generator=gen, device="cuda")
+    dx, dw = torch.empty_like(dy), torch.empty(cols, device="cuda")
+    gc.rmsnorm_backward(dy, ck, rstd, w, dx, dw, gc.rmsnorm_backward_workspace(rows, cols), dh=dh)
+    q = torch.empty(rows, cols, device="cuda")
+    gc.act_decompress(ck, q)
+    q, d, gw, r = q.double(), dy.double(), dy.double() * w.double(), rstd.double()[:, None]
+    assert ((dw.double() - (d * q).sum(0)).abs() <= (rows + 2) * u * (d * q).abs().sum(0)).all()
+    want = r * (gw - q * (gw * q).mean(1, keepdim=True)) + dh.double()
+    size = r * (gw.abs() + q.abs() * (gw * q).abs().mean(1, keepdim=True)) + dh.double().abs()
+    room = (cols + 8) * u * r * q.abs() * (gw * q).abs().mean(1, keepdim=True) + 8 * u * size
+    # fp16 rounds results below 2^-14 to multiples of 2^-24
+    assert ((dx.double() - want).abs() <= room + own * (want.abs() + room) + (2.0 ** -25 if dtype == torch.float16 else 0)).all()
