@@ -428,10 +428,7 @@ static int resident() {
 // Large matrices: about ACT_CTAS CTAs (with six for every SM the gates' gradient of
 // 8192 x 14336 takes 154 us instead of 145).  Small ones, whose CTAs would have
 // a few rows each: one wave of the CTAs that fit (2048 x 4096: 11.4 us instead
-// of 12.2; 128 x 14336: 3.8 instead of 4.7; 777 x 4097: 8.5 instead of 9.8), but
-// three of the six that fit for an SM where a checkpoint of rows on 16-byte
-// boundaries is written (777 x 4096: 3.1 us instead of 3.7; spans of 4000 x
-// 3333, bound by instructions, take 17.2 us so instead of 11.9).
+// of 12.2; 128 x 14336: 3.8 instead of 4.7; 777 x 4097: 8.5 instead of 9.8).
 constexpr int64_t ACT_SMS = 152, ACT_CTAS = ACT_SMS * 8, ACT_FEW = 8;
 inline Tiling make_tiling(int64_t rows, int64_t cols, bool span, int ctas, dim3* grid) {
   Tiling t;
@@ -440,7 +437,7 @@ inline Tiling make_tiling(int64_t rows, int64_t cols, bool span, int ctas, dim3*
   while (t.wide > (span ? 5 : 2) && ((((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide) << t.wide) > t.c8s + t.c8s / 16) --t.wide;
   const int64_t across = ((int64_t)t.c8s + (1 << t.wide) - 1) >> t.wide, at_once = 256 >> t.wide;
   const int64_t most = (rows + at_once - 1) / at_once;
-  int64_t slabs = most * across < ACT_FEW * ACT_CTAS ? ACT_SMS * (ctas < 3 || span ? ctas : 3) / across : (ACT_CTAS + across - 1) / across;
+  int64_t slabs = most * across < ACT_FEW * ACT_CTAS ? ACT_SMS * ctas / across : (ACT_CTAS + across - 1) / across;
   if (slabs < 1) slabs = 1;
   if (slabs > most) slabs = most;
   if (slabs > 65535) slabs = 65535;

@@ -704,11 +704,11 @@ static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
 // STAGE, a split's sums take 8 bytes an element at 7 TB/s and 0.1 to write and
 // to join, the join's launch 2; with s splits STAGE * stages / s + each * s, least
 // for their root.  (500 x 4096 x 1024 in bf16 takes 13.6 us whole and 19.8 in
-// two; 1000 x 333 x 1001 in fp32 14.5 in six, 16.6 in three, 23.9 whole.)
+// two; 1000 x 333 x 1001 in fp32 15.0 in six, 15.6 in four, 23.9 whole.)
 static int wg_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
   const int64_t most = WG_SMS / (wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N)), stages = (rows + 63) / 64;
   const double stage = dtype == GC_F32 ? 1.0 : 0.67, each = (double)n * (double)k * 8.0 / 7e6 + 0.1;
-  int64_t s = (int64_t)std::sqrt((double)stages * stage / each);
+  int64_t s = (int64_t)(std::sqrt((double)stages * stage / each) + 0.5);
   if (s > most) s = most;
   if (s < 2) return 1;
   const int64_t span = wg_span(rows, s);
