@@ -140,10 +140,12 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 }
 
 // For 16-bit results, two at a time: the hardware's exponential and
-// reciprocal, a few 2^-23 off (and |p| 2^-24 from SiLU's argument), are 2^-10
+// reciprocal, a few 2^-23 off (and |p| 2^-23 from SiLU's argument), are at most 2^-8
 // of the result's own rounding and a third of the instructions.
-// SiLU: far out on the left the exponential is infinite and the sigmoid 0,
-// where it would be below 2^-126.
+// SiLU: with h = 2^(-g log2(e) / 2) the sigmoid is 1 / (1 + h^2), taken as
+// 2^-64 / (2^-64 + (2^-32 h)^2): neither the sum overflows nor the reciprocal
+// vanishes before the sigmoid is below all of fp32 (1 + e^-g itself is past
+// the reciprocal's 2^126 from g = -87.3 on, where the product is still 1e-36).
 // GELU: with h = 2^(-z/2), z = |p| log2(e), and f = h^2 the sigmoid is
 // 1 / (1 + f) on the right and f / (1 + f) on the left, where nothing
 // overflows and f reaches below 2^-126 (the exponential itself does not).
@@ -152,10 +154,12 @@ __device__ __forceinline__ F2 gate_sigmoid2(const float* g, F2* dp) {
   constexpr float LOG2E = 1.4426950408889634f;
   float x[2], r[2];
   if (KIND == GC_GATE_SILU) {
-    put2(x, mul2(get2(g), f2(-LOG2E)));
-    put2(r, add2(f2(ex2_ftz(x[0]), ex2_ftz(x[1])), f2(1.0f)));
+    constexpr float SMALL = 5.421010862427522e-20f, ROOT = 2.3283064365386963e-10f;  // 2^-64, 2^-32
+    put2(x, mul2(get2(g), f2(-0.5f * LOG2E)));
+    const F2 h = mul2(f2(ex2_ftz(x[0]), ex2_ftz(x[1])), f2(ROOT));
+    put2(r, fma2(h, h, f2(SMALL)));
     *dp = f2(1.0f);
-    return f2(rcp_ftz(r[0]), rcp_ftz(r[1]));
+    return mul2(f2(rcp_ftz(r[0]), rcp_ftz(r[1])), f2(SMALL));
   }
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(x[0]) : "f"(fabsf(g[0])), "f"(GELU_FAR));
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(x[1]) : "f"(fabsf(g[1])), "f"(GELU_FAR));
@@ -176,7 +180,7 @@ __device__ __forceinline__ F2 gate_sigmoid2(const float* g, F2* dp) {
 // Registers for the packed arithmetic matter more than a fourth CTA per SM
 // (two for spans).  With both checkpoints: bf16 148 us for either kind (0.96;
 // GELU with scalar arithmetic 172), fp32 276 us (0.90) and 320 with GELU, bf16
-// rows of 14335 180 us (0.79) and 225.
+// rows of 14335 181 us (0.78) and 225.
 template <typename T, int KIND, bool SPAN>
 __global__ void __launch_bounds__(256, SPAN && sizeof(T) == 2 ? 2 : 3)
     k_gated(const T* gate, int64_t ldg, const T* up, int64_t ldu, Tiling t, T* out, int64_t ldo, int8_t* gcodes,
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(256, SPAN && sizeof(T) == 2 ? 2 : 3)
 // dout and both codes come through rings, the step bytes through registers.
 // Three CTAs per SM (two for spans): the fourth would leave 64 registers and
 // spill (152 and 184 us).  bf16 145 us (0.98), GELU 160 us (0.89; 214 with
-// scalar arithmetic); with the activation's checkpoint 166 and 182 us; fp32
-// 308 us (0.80); bf16 rows of 14335 188 us (0.76).
+// scalar arithmetic); with the activation's checkpoint 168 and 182 us; fp32
+// 308 us (0.80); bf16 rows of 14335 193 us (0.74).
 template <typename T, int KIND, bool SPAN>
 __global__ void __launch_bounds__(256, SPAN ? 2 : 3)
     k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
