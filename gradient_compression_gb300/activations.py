@@ -51,9 +51,10 @@ class ActCheckpoint:
     """Codes and steps of an activation x[rows, cols] held in 8 bits.
 
     codes int8[rows, ldc] with ldc = 32 * ceil(cols / 32), steps uint8[rows,
-    ldc / 32]; allocated here unless given."""
+    ldc / 32]; allocated here unless given.  Every call takes the two tensors
+    as they are then, so they may be moved away and put back."""
 
-    __slots__ = ("rows", "cols", "codes", "steps", "_codes", "_steps")
+    __slots__ = ("rows", "cols", "codes", "steps")
 
     def __init__(self, rows, cols, device="cuda", codes=None, steps=None):
         self.rows, self.cols = int(rows), int(cols)
@@ -65,8 +66,8 @@ class ActCheckpoint:
             codes = torch.empty(shape, dtype=torch.int8, device=device)
         if steps is None:
             steps = torch.empty((self.rows, groups), dtype=torch.uint8, device=device)
+        (_calls or _marshal()).checkpoint(codes, steps, self.rows, self.cols)
         self.codes, self.steps = codes, steps
-        self._codes, self._steps = (_calls or _marshal()).checkpoint(codes, steps, self.rows, groups)
 
     @property
     def nbytes(self) -> int:

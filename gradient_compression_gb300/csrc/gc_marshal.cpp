@@ -131,30 +131,59 @@ Space workspace(PyObject* o) {
   return w;
 }
 
-// An ActCheckpoint: its size and its arrays' addresses, which its constructor checked.
+// An ActCheckpoint: its size and its arrays as they are at the call (they may
+// have been replaced, moved or resized since it was made), held on to until it returns.
 PyObject *s_rows, *s_cols, *s_codes, *s_steps, *s_stream;
-int64_t number(PyObject* o, PyObject* field) {
+PyObject* attribute(PyObject* o, PyObject* field, const char* name) {
   PyObject* v = PyObject_GetAttr(o, field);
-  if (!v) throw Bad{};
+  if (v) return v;
+  if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw Bad{};
+  PyErr_Clear();
+  bad("%s: an ActCheckpoint is needed", name);
+}
+int64_t number(PyObject* o, PyObject* field, const char* name) {
+  PyObject* v = attribute(o, field, name);
   const int64_t x = PyLong_AsLongLong(v);
   Py_DECREF(v);
   if (x == -1 && PyErr_Occurred()) throw Bad{};
   return x;
 }
+at::Tensor array(PyObject* o, PyObject* field, const char* name) {
+  PyObject* v = attribute(o, field, name);
+  at::Tensor t;
+  if (THPVariable_Check(v)) t = THPVariable_Unpack(v);
+  Py_DECREF(v);
+  if (!t.defined()) bad("%s: its %U is no tensor", name, field);
+  return t;
+}
+void check_array(const at::Tensor& t, const char* name, int64_t rows, int64_t cols, at::ScalarType type, const char* what) {
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !t.is_cuda())
+    bad("%s: a contiguous CUDA %s tensor of shape (%lld, %lld) is needed", name, what, (long long)rows, (long long)cols);
+}
+void check_arrays(const at::Tensor& codes, const at::Tensor& steps, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1 || cols > INT64_C(2147483647))
+    bad("a checkpoint of (%lld, %lld)", (long long)rows, (long long)cols);
+  const int64_t groups = (cols + 31) / 32;
+  check_array(codes, "codes", rows, 32 * groups, at::kChar, "int8");
+  check_array(steps, "steps", rows, groups, at::kByte, "uint8");
+}
 struct Held {
   int64_t rows = 0, cols = 0;
   int8_t* codes = nullptr;
   uint8_t* steps = nullptr;
+  at::Tensor arrays[2];
 };
-Held held(PyObject* o) {
+Held held(PyObject* o, const char* name) {
   Held h;
-  h.rows = number(o, s_rows), h.cols = number(o, s_cols);
-  h.codes = reinterpret_cast<int8_t*>(number(o, s_codes)), h.steps = reinterpret_cast<uint8_t*>(number(o, s_steps));
+  h.rows = number(o, s_rows, name), h.cols = number(o, s_cols, name);
+  h.arrays[0] = array(o, s_codes, name), h.arrays[1] = array(o, s_steps, name);
+  check_arrays(h.arrays[0], h.arrays[1], h.rows, h.cols);
+  h.codes = static_cast<int8_t*>(h.arrays[0].data_ptr()), h.steps = static_cast<uint8_t*>(h.arrays[1].data_ptr());
   return h;
 }
 Held held(PyObject* o, const char* name, int64_t rows, int64_t cols) {
   if (o == Py_None) return Held();
-  const Held h = held(o);
+  Held h = held(o, name);
   if (h.rows != rows || h.cols != cols)
     bad("%s: a checkpoint of (%lld, %lld) where (%lld, %lld) is needed", name, (long long)h.rows, (long long)h.cols,
         (long long)rows, (long long)cols);
@@ -192,14 +221,16 @@ using Args = PyObject* const*;
 
 PyObject* act_compress(Args a) {  // x, ckpt, stream
   const at::Tensor& x = tensor(a[0], "x");
-  const Held h = held(a[1]);
+  matrix(x, "x");
+  const Held h = held(a[1], "ckpt");
   const Mat m = matrix(x, "x", h.rows, h.cols);
   return call(entry.act_compress, m.p, m.ld, type_code(x, "x"), h.rows, h.cols, h.codes, h.steps, stream_of(a[2], x));
 }
 
 PyObject* act_decompress(Args a) {  // ckpt, out, stream
-  const Held h = held(a[0]);
   const at::Tensor& out = tensor(a[1], "out");
+  matrix(out, "out");
+  const Held h = held(a[0], "ckpt");
   const Mat m = matrix(out, "out", h.rows, h.cols);
   return call(entry.act_decompress, h.codes, h.steps, h.rows, h.cols, m.p, m.ld, type_code(out, "out"), stream_of(a[2], out));
 }
@@ -224,7 +255,8 @@ PyObject* rmsnorm(Args a) {  // x, weight, eps, y, residual, h, rstd, ckpt, stre
 
 PyObject* rmsnorm_backward(Args a) {  // dy, ckpt, rstd, weight, dx, dw, workspace, dh, accumulate, stream
   const at::Tensor& dy = tensor(a[0], "dy");
-  const Held c = held(a[1]);
+  matrix(dy, "dy");
+  const Held c = held(a[1], "ckpt");
   const Mat d = matrix(dy, "dy", c.rows, c.cols);
   const at::ScalarType type = dy.scalar_type();
   const int code = type_code(dy, "dy");
@@ -259,7 +291,8 @@ PyObject* gated_act(Args a) {  // kind, gate, up, out, ckpt_gate, ckpt_up, strea
 
 PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out, stream
   const at::Tensor& dout = tensor(a[1], "dout");
-  const Held cg = held(a[2]);
+  matrix(dout, "dout");
+  const Held cg = held(a[2], "ckpt_gate");
   const Mat d = matrix(dout, "dout", cg.rows, cg.cols);
   const at::ScalarType type = dout.scalar_type();
   const int code = type_code(dout, "dout");
@@ -271,8 +304,9 @@ PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate
 
 PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accumulate, stream
   const at::Tensor& dy = tensor(a[0], "dy");
-  const Held c = held(a[1]);
-  const int64_t n = dy.dim() > 0 ? dy.size(-1) : 0;
+  matrix(dy, "dy");
+  const Held c = held(a[1], "ckpt");
+  const int64_t n = dy.size(1);
   const Mat d = matrix(dy, "dy", c.rows, n), dw = needed(a[2], "dw", n, c.cols, at::kFloat);
   const int code = type_code(dy, "dy");
   int scode = 0;
@@ -282,18 +316,12 @@ PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accu
               static_cast<float*>(dw.p), dw.ld, truth(a[5]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[6], dy));
 }
 
-// checkpoint(codes, steps, rows, groups): the arrays of an ActCheckpoint, checked; their addresses
+// checkpoint(codes, steps, rows, cols): the checks of an ActCheckpoint's arrays
 PyObject* checkpoint(Args a) {
-  const int64_t rows = PyLong_AsLongLong(a[2]), groups = PyLong_AsLongLong(a[3]);
+  const int64_t rows = PyLong_AsLongLong(a[2]), cols = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred()) throw Bad{};
-  const at::Tensor &codes = tensor(a[0], "codes"), &steps = tensor(a[1], "steps");
-  auto check = [&](const at::Tensor& t, const char* name, int64_t cols, at::ScalarType type, const char* what) {
-    if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !t.is_cuda())
-      bad("%s: a contiguous CUDA %s tensor of shape (%lld, %lld) is needed", name, what, (long long)rows, (long long)cols);
-  };
-  check(codes, "codes", 32 * groups, at::kChar, "int8");
-  check(steps, "steps", groups, at::kByte, "uint8");
-  return Py_BuildValue("NN", PyLong_FromVoidPtr(codes.data_ptr()), PyLong_FromVoidPtr(steps.data_ptr()));
+  check_arrays(tensor(a[0], "codes"), tensor(a[1], "steps"), rows, cols);
+  Py_RETURN_NONE;
 }
 
 template <PyObject* (*F)(Args), int N>
@@ -328,7 +356,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 PyMODINIT_FUNC PyInit__marshal() {
   s_rows = PyUnicode_InternFromString("rows"), s_cols = PyUnicode_InternFromString("cols");
-  s_codes = PyUnicode_InternFromString("_codes"), s_steps = PyUnicode_InternFromString("_steps");
+  s_codes = PyUnicode_InternFromString("codes"), s_steps = PyUnicode_InternFromString("steps");
   s_stream = PyUnicode_InternFromString("cuda_stream");
   return PyModule_Create(&module);
 }

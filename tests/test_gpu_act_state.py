@@ -1,0 +1,61 @@
+"""A checkpoint is read and written where its arrays are at the call."""
+import copy
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gc(cuda_device):
+    from gradient_compression_gb300 import build
+    build.build()
+    import gradient_compression_gb300 as gcmod
+    gcmod.lib()
+    return gcmod
+
+
+def test_checkpoint_restored_from_the_host(gc):
+    """A checkpoint offloaded and brought back to other memory is read there."""
+    x = torch.randn(9, 100, device="cuda")
+    ck, want, out = gc.ActCheckpoint(9, 100), torch.empty_like(x), torch.empty_like(x)
+    gc.act_compress(x, ck)
+    gc.act_decompress(ck, want)
+    codes, steps = ck.codes, ck.steps                       # the first memory stays alive, and changes
+    away = codes.cpu(), steps.cpu()
+    ck.codes, ck.steps = away[0].cuda(), away[1].cuda()
+    codes.zero_()
+    gc.act_decompress(ck, out)
+    assert torch.equal(out, want)
+    gc.act_compress(2 * x, ck)                              # written there, too
+    assert bool((codes == 0).all()) and bool((ck.steps.int() == steps.int() + 1).all())
+
+
+def test_deep_copy_of_a_checkpoint(gc):
+    x = torch.randn(9, 100, device="cuda")
+    ck, want, out = gc.ActCheckpoint(9, 100), torch.empty_like(x), torch.empty_like(x)
+    gc.act_compress(x, ck)
+    gc.act_decompress(ck, want)
+    twin = copy.deepcopy(ck)
+    gc.act_compress(torch.zeros_like(x), ck)
+    gc.act_decompress(twin, out)
+    assert torch.equal(out, want)
+
+
+def test_storage_given_up_and_taken_again(gc):
+    """Its memory freed between forward and backward, as sharding and offloading
+    do: refused meanwhile, right after."""
+    x = torch.randn(9, 100, device="cuda")
+    ck, want, out = gc.ActCheckpoint(9, 100), torch.empty_like(x), torch.empty_like(x)
+    gc.act_compress(x, ck)
+    gc.act_decompress(ck, want)
+    away, size = ck.codes.cpu(), ck.codes.untyped_storage().nbytes()
+    ck.codes.untyped_storage().resize_(0)
+    with pytest.raises(gc.GCError):
+        gc.act_decompress(ck, out)
+    other = torch.full((size,), 3, dtype=torch.int8, device="cuda")      # somebody else's by now
+    ck.codes.untyped_storage().resize_(size)
+    ck.codes.copy_(away)
+    gc.act_decompress(ck, out)
+    assert torch.equal(out, want) and bool((other == 3).all())
