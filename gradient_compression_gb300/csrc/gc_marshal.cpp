@@ -7,6 +7,7 @@
 // raises ValueError before anything is enqueued.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -72,13 +73,25 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// The GPU of a call's tensors, the first one's: the others have to be there too.
+struct Gpu {
+  c10::DeviceIndex index = -1;
+  bool holds(const at::Tensor& t, const char* name) {
+    if (!t.is_cuda()) return false;
+    const c10::DeviceIndex i = t.device().index();
+    if (index < 0) index = i;
+    if (i != index) bad("%s: on cuda:%d where cuda:%d is needed", name, (int)i, (int)index);
+    return true;
+  }
+};
+
 struct Mat {
   void* p = nullptr;
   int64_t ld = 0;
 };
 // A matrix argument after its checks; rows < 0 takes any shape.
-Mat matrix(const at::Tensor& t, const char* name, int64_t rows = -1, int64_t cols = -1) {
-  if (t.dim() != 2 || !t.is_cuda()) bad("%s: a 2-D CUDA tensor is needed", name);
+Mat matrix(Gpu& on, const at::Tensor& t, const char* name, int64_t rows = -1, int64_t cols = -1) {
+  if (t.dim() != 2 || !on.holds(t, name)) bad("%s: a 2-D CUDA tensor is needed", name);
   const int64_t r = t.size(0), c = t.size(1);
   if (rows >= 0 && (r != rows || c != cols))
     bad("%s: shape (%lld, %lld) where (%lld, %lld) is needed", name, (long long)r, (long long)c, (long long)rows, (long long)cols);
@@ -93,25 +106,25 @@ Mat matrix(const at::Tensor& t, const char* name, int64_t rows = -1, int64_t col
   return m;
 }
 // The same where an argument may be None, of the type of another.
-Mat matrix(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+Mat matrix(Gpu& on, PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
   if (o == Py_None) return Mat();
   const at::Tensor& t = tensor(o, name);
-  const Mat m = matrix(t, name, rows, cols);
+  const Mat m = matrix(on, t, name, rows, cols);
   if (t.scalar_type() != type) bad("%s: %s where %s is needed", name, type_name(t.scalar_type()), type_name(type));
   return m;
 }
-Mat needed(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+Mat needed(Gpu& on, PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
   tensor(o, name);
-  return matrix(o, name, rows, cols, type);
+  return matrix(on, o, name, rows, cols, type);
 }
 
 // A contiguous vector argument, fp32 or (code given) of any of the types.
-void* vector(PyObject* o, const char* name, int64_t n, int* code) {
+void* vector(Gpu& on, PyObject* o, const char* name, int64_t n, int* code) {
   if (o == Py_None) return nullptr;
   const at::Tensor& t = tensor(o, name);
   const at::ScalarType s = t.scalar_type();
   const bool fits = s == at::kFloat || (code && (s == at::kBFloat16 || s == at::kHalf));
-  if (t.dim() != 1 || t.size(0) != n || !t.is_cuda() || !fits || !t.is_contiguous())
+  if (t.dim() != 1 || t.size(0) != n || !on.holds(t, name) || !fits || !t.is_contiguous())
     bad("%s: a contiguous CUDA vector of %lld elements of torch.float32%s is needed", name, (long long)n,
         code ? " or torch.bfloat16 or torch.float16" : "");
   if (code) *code = type_code(t, name);
@@ -122,11 +135,11 @@ struct Space {
   void* p = nullptr;
   size_t bytes = 0;
 };
-Space workspace(PyObject* o) {
+Space workspace(Gpu& on, PyObject* o) {
   Space w;
   if (o == Py_None) return w;
   const at::Tensor& t = tensor(o, "workspace");
-  if (!t.is_cuda() || t.scalar_type() != at::kByte || !t.is_contiguous()) bad("workspace: a contiguous CUDA uint8 tensor is needed");
+  if (!on.holds(t, "workspace") || t.scalar_type() != at::kByte || !t.is_contiguous()) bad("workspace: a contiguous CUDA uint8 tensor is needed");
   w.p = t.data_ptr(), w.bytes = (size_t)t.numel();
   return w;
 }
@@ -156,16 +169,16 @@ at::Tensor array(PyObject* o, PyObject* field, const char* name) {
   if (!t.defined()) bad("%s: its %U is no tensor", name, field);
   return t;
 }
-void check_array(const at::Tensor& t, const char* name, int64_t rows, int64_t cols, at::ScalarType type, const char* what) {
-  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !t.is_cuda())
+void check_array(Gpu& on, const at::Tensor& t, const char* name, int64_t rows, int64_t cols, at::ScalarType type, const char* what) {
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !on.holds(t, name))
     bad("%s: a contiguous CUDA %s tensor of shape (%lld, %lld) is needed", name, what, (long long)rows, (long long)cols);
 }
-void check_arrays(const at::Tensor& codes, const at::Tensor& steps, int64_t rows, int64_t cols) {
+void check_arrays(Gpu& on, const at::Tensor& codes, const at::Tensor& steps, int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1 || cols > INT64_C(2147483647))
     bad("a checkpoint of (%lld, %lld)", (long long)rows, (long long)cols);
   const int64_t groups = (cols + 31) / 32;
-  check_array(codes, "codes", rows, 32 * groups, at::kChar, "int8");
-  check_array(steps, "steps", rows, groups, at::kByte, "uint8");
+  check_array(on, codes, "codes", rows, 32 * groups, at::kChar, "int8");
+  check_array(on, steps, "steps", rows, groups, at::kByte, "uint8");
 }
 struct Held {
   int64_t rows = 0, cols = 0;
@@ -173,17 +186,17 @@ struct Held {
   uint8_t* steps = nullptr;
   at::Tensor arrays[2];
 };
-Held held(PyObject* o, const char* name) {
+Held held(Gpu& on, PyObject* o, const char* name) {
   Held h;
   h.rows = number(o, s_rows, name), h.cols = number(o, s_cols, name);
   h.arrays[0] = array(o, s_codes, name), h.arrays[1] = array(o, s_steps, name);
-  check_arrays(h.arrays[0], h.arrays[1], h.rows, h.cols);
+  check_arrays(on, h.arrays[0], h.arrays[1], h.rows, h.cols);
   h.codes = static_cast<int8_t*>(h.arrays[0].data_ptr()), h.steps = static_cast<uint8_t*>(h.arrays[1].data_ptr());
   return h;
 }
-Held held(PyObject* o, const char* name, int64_t rows, int64_t cols) {
+Held held(Gpu& on, PyObject* o, const char* name, int64_t rows, int64_t cols) {
   if (o == Py_None) return Held();
-  Held h = held(o, name);
+  Held h = held(on, o, name);
   if (h.rows != rows || h.cols != cols)
     bad("%s: a checkpoint of (%lld, %lld) where (%lld, %lld) is needed", name, (long long)h.rows, (long long)h.cols,
         (long long)rows, (long long)cols);
@@ -207,11 +220,16 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
+// The entry point, with the tensors' GPU the thread's current one (whose streams
+// and kernels the launches take), and the thread's own again after it.
 template <typename F, typename... A>
-PyObject* call(F f, A... a) {
+PyObject* call(const Gpu& on, F f, A... a) {
   gc_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = f(a...);
+  c10::DeviceIndex was = on.index;
+  const bool elsewhere = c10::cuda::GetDevice(&was) == cudaSuccess && was != on.index;
+  st = elsewhere && c10::cuda::SetDevice(on.index) != cudaSuccess ? GC_ERR_CUDA : f(a...);
+  if (elsewhere) (void)c10::cuda::SetDevice(was);
   Py_END_ALLOW_THREADS;
   return PyLong_FromLong(st);
 }
@@ -220,54 +238,58 @@ PyObject* call(F f, A... a) {
 using Args = PyObject* const*;
 
 PyObject* act_compress(Args a) {  // x, ckpt, stream
+  Gpu on;
   const at::Tensor& x = tensor(a[0], "x");
-  matrix(x, "x");
-  const Held h = held(a[1], "ckpt");
-  const Mat m = matrix(x, "x", h.rows, h.cols);
-  return call(entry.act_compress, m.p, m.ld, type_code(x, "x"), h.rows, h.cols, h.codes, h.steps, stream_of(a[2], x));
+  matrix(on, x, "x");
+  const Held h = held(on, a[1], "ckpt");
+  const Mat m = matrix(on, x, "x", h.rows, h.cols);
+  return call(on, entry.act_compress, m.p, m.ld, type_code(x, "x"), h.rows, h.cols, h.codes, h.steps, stream_of(a[2], x));
 }
 
 PyObject* act_decompress(Args a) {  // ckpt, out, stream
+  Gpu on;
   const at::Tensor& out = tensor(a[1], "out");
-  matrix(out, "out");
-  const Held h = held(a[0], "ckpt");
-  const Mat m = matrix(out, "out", h.rows, h.cols);
-  return call(entry.act_decompress, h.codes, h.steps, h.rows, h.cols, m.p, m.ld, type_code(out, "out"), stream_of(a[2], out));
+  matrix(on, out, "out");
+  const Held h = held(on, a[0], "ckpt");
+  const Mat m = matrix(on, out, "out", h.rows, h.cols);
+  return call(on, entry.act_decompress, h.codes, h.steps, h.rows, h.cols, m.p, m.ld, type_code(out, "out"), stream_of(a[2], out));
 }
 
 PyObject* rmsnorm(Args a) {  // x, weight, eps, y, residual, h, rstd, ckpt, stream
+  Gpu on;
   const at::Tensor& x = tensor(a[0], "x");
-  const Mat mx = matrix(x, "x");
+  const Mat mx = matrix(on, x, "x");
   const int64_t rows = x.size(0), cols = x.size(1);
   const at::ScalarType type = x.scalar_type();
   const int code = type_code(x, "x");
-  const Mat r = matrix(a[4], "residual", rows, cols, type), y = matrix(a[3], "y", rows, cols, type),
-            h = matrix(a[5], "h", rows, cols, type);
+  const Mat r = matrix(on, a[4], "residual", rows, cols, type), y = matrix(on, a[3], "y", rows, cols, type),
+            h = matrix(on, a[5], "h", rows, cols, type);
   int wcode = 0;
-  void* const w = vector(a[1], "weight", cols, &wcode);
-  float* const rstd = static_cast<float*>(vector(a[6], "rstd", rows, nullptr));
-  const Held c = held(a[7], "ckpt", rows, cols);
+  void* const w = vector(on, a[1], "weight", cols, &wcode);
+  float* const rstd = static_cast<float*>(vector(on, a[6], "rstd", rows, nullptr));
+  const Held c = held(on, a[7], "ckpt", rows, cols);
   const double eps = PyFloat_AsDouble(a[2]);
   if (eps == -1.0 && PyErr_Occurred()) throw Bad{};
-  return call(entry.rmsnorm, mx.p, mx.ld, r.p, r.ld, code, w, wcode, (float)eps, rows, cols, y.p, y.ld, h.p, h.ld, rstd,
+  return call(on, entry.rmsnorm, mx.p, mx.ld, r.p, r.ld, code, w, wcode, (float)eps, rows, cols, y.p, y.ld, h.p, h.ld, rstd,
               c.codes, c.steps, stream_of(a[8], x));
 }
 
 PyObject* rmsnorm_backward(Args a) {  // dy, ckpt, rstd, weight, dx, dw, workspace, dh, accumulate, stream
+  Gpu on;
   const at::Tensor& dy = tensor(a[0], "dy");
-  matrix(dy, "dy");
-  const Held c = held(a[1], "ckpt");
-  const Mat d = matrix(dy, "dy", c.rows, c.cols);
+  matrix(on, dy, "dy");
+  const Held c = held(on, a[1], "ckpt");
+  const Mat d = matrix(on, dy, "dy", c.rows, c.cols);
   const at::ScalarType type = dy.scalar_type();
   const int code = type_code(dy, "dy");
-  const Mat dx = needed(a[4], "dx", c.rows, c.cols, type), dh = matrix(a[7], "dh", c.rows, c.cols, type);
+  const Mat dx = needed(on, a[4], "dx", c.rows, c.cols, type), dh = matrix(on, a[7], "dh", c.rows, c.cols, type);
   int wcode = 0;
-  void* const w = vector(a[3], "weight", c.cols, &wcode);
-  float* const dw = static_cast<float*>(vector(a[5], "dw", c.cols, nullptr));
-  const Space ws = dw ? workspace(a[6]) : Space();
+  void* const w = vector(on, a[3], "weight", c.cols, &wcode);
+  float* const dw = static_cast<float*>(vector(on, a[5], "dw", c.cols, nullptr));
+  const Space ws = dw ? workspace(on, a[6]) : Space();
   if (a[2] == Py_None) bad("rstd is needed");
-  float* const rstd = static_cast<float*>(vector(a[2], "rstd", c.rows, nullptr));
-  return call(entry.rmsnorm_backward, d.p, d.ld, dh.p, dh.ld, code, c.codes, c.steps, rstd, w, wcode, c.rows, c.cols, dx.p,
+  float* const rstd = static_cast<float*>(vector(on, a[2], "rstd", c.rows, nullptr));
+  return call(on, entry.rmsnorm_backward, d.p, d.ld, dh.p, dh.ld, code, c.codes, c.steps, rstd, w, wcode, c.rows, c.cols, dx.p,
               dx.ld, dw, truth(a[8]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[9], dy));
 }
 
@@ -278,49 +300,53 @@ int kind_of(PyObject* o) {
 }
 
 PyObject* gated_act(Args a) {  // kind, gate, up, out, ckpt_gate, ckpt_up, stream
+  Gpu on;
   const at::Tensor& gate = tensor(a[1], "gate");
-  const Mat g = matrix(gate, "gate");
+  const Mat g = matrix(on, gate, "gate");
   const int64_t rows = gate.size(0), cols = gate.size(1);
   const at::ScalarType type = gate.scalar_type();
   const int code = type_code(gate, "gate");
-  const Mat u = needed(a[2], "up", rows, cols, type), out = needed(a[3], "out", rows, cols, type);
-  const Held cg = held(a[4], "ckpt_gate", rows, cols), cu = held(a[5], "ckpt_up", rows, cols);
-  return call(entry.gated_act, kind_of(a[0]), g.p, g.ld, u.p, u.ld, code, rows, cols, out.p, out.ld, cg.codes, cg.steps,
+  const Mat u = needed(on, a[2], "up", rows, cols, type), out = needed(on, a[3], "out", rows, cols, type);
+  const Held cg = held(on, a[4], "ckpt_gate", rows, cols), cu = held(on, a[5], "ckpt_up", rows, cols);
+  return call(on, entry.gated_act, kind_of(a[0]), g.p, g.ld, u.p, u.ld, code, rows, cols, out.p, out.ld, cg.codes, cg.steps,
               cu.codes, cu.steps, stream_of(a[6], gate));
 }
 
 PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out, stream
+  Gpu on;
   const at::Tensor& dout = tensor(a[1], "dout");
-  matrix(dout, "dout");
-  const Held cg = held(a[2], "ckpt_gate");
-  const Mat d = matrix(dout, "dout", cg.rows, cg.cols);
+  matrix(on, dout, "dout");
+  const Held cg = held(on, a[2], "ckpt_gate");
+  const Mat d = matrix(on, dout, "dout", cg.rows, cg.cols);
   const at::ScalarType type = dout.scalar_type();
   const int code = type_code(dout, "dout");
-  const Mat dg = needed(a[4], "dgate", cg.rows, cg.cols, type), du = needed(a[5], "dup", cg.rows, cg.cols, type);
-  const Held cu = held(a[3], "ckpt_up", cg.rows, cg.cols), co = held(a[6], "ckpt_out", cg.rows, cg.cols);
-  return call(entry.gated_act_backward, kind_of(a[0]), d.p, d.ld, code, cg.codes, cg.steps, cu.codes, cu.steps, cg.rows,
+  const Mat dg = needed(on, a[4], "dgate", cg.rows, cg.cols, type), du = needed(on, a[5], "dup", cg.rows, cg.cols, type);
+  const Held cu = held(on, a[3], "ckpt_up", cg.rows, cg.cols), co = held(on, a[6], "ckpt_out", cg.rows, cg.cols);
+  return call(on, entry.gated_act_backward, kind_of(a[0]), d.p, d.ld, code, cg.codes, cg.steps, cu.codes, cu.steps, cg.rows,
               cg.cols, dg.p, dg.ld, du.p, du.ld, co.codes, co.steps, stream_of(a[7], dout));
 }
 
 PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accumulate, stream
+  Gpu on;
   const at::Tensor& dy = tensor(a[0], "dy");
-  matrix(dy, "dy");
-  const Held c = held(a[1], "ckpt");
+  matrix(on, dy, "dy");
+  const Held c = held(on, a[1], "ckpt");
   const int64_t n = dy.size(1);
-  const Mat d = matrix(dy, "dy", c.rows, n), dw = needed(a[2], "dw", n, c.cols, at::kFloat);
+  const Mat d = matrix(on, dy, "dy", c.rows, n), dw = needed(on, a[2], "dw", n, c.cols, at::kFloat);
   const int code = type_code(dy, "dy");
   int scode = 0;
-  void* const scale = vector(a[4], "col_scale", c.cols, &scode);
-  const Space ws = workspace(a[3]);
-  return call(entry.act_weight_grad, d.p, d.ld, code, c.rows, n, c.codes, c.steps, c.cols, scale, scode,
+  void* const scale = vector(on, a[4], "col_scale", c.cols, &scode);
+  const Space ws = workspace(on, a[3]);
+  return call(on, entry.act_weight_grad, d.p, d.ld, code, c.rows, n, c.codes, c.steps, c.cols, scale, scode,
               static_cast<float*>(dw.p), dw.ld, truth(a[5]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[6], dy));
 }
 
 // checkpoint(codes, steps, rows, cols): the checks of an ActCheckpoint's arrays
 PyObject* checkpoint(Args a) {
+  Gpu on;
   const int64_t rows = PyLong_AsLongLong(a[2]), cols = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred()) throw Bad{};
-  check_arrays(tensor(a[0], "codes"), tensor(a[1], "steps"), rows, cols);
+  check_arrays(on, tensor(a[0], "codes"), tensor(a[1], "steps"), rows, cols);
   Py_RETURN_NONE;
 }
 
