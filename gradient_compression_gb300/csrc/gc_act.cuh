@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "gc_common.cuh"
+#include "gc_host.h"
 
 namespace gc {
 
@@ -413,14 +414,32 @@ __device__ __forceinline__ Place place(const Tiling& t) {
   return p;
 }
 
-// The CTAs of 256 threads that an SM holds of a kernel.
+// The GPU that launches go to, -1 without one.
+static int current_device() {
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) (void)cudaGetLastError(), device = -1;
+  return device;
+}
+
+// The CTAs of 256 threads that an SM holds of a kernel; 1 where that cannot be had.
 template <auto KERN>
 static int resident() {
-  static const int ctas = [] {
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERN, 256, 0) == cudaSuccess && n > 0 ? n : 1;
-  }();
-  return ctas;
+  static PerDevice ctas;
+  const int n = ctas.get(current_device(), [] {
+    int held = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, KERN, 256, 0) == cudaSuccess) return held;
+    (void)cudaGetLastError();
+    return 0;
+  });
+  return n > 0 ? n : 1;
+}
+
+// Grants a kernel `bytes` of dynamic shared memory.
+template <typename K>
+static bool grant_shared(K kern, int bytes) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  return false;
 }
 
 // The widest tile (256 chunks to 4, or to 32 where a warp takes a span of one

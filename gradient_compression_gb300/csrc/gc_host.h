@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gc.h"
 
 namespace gc {
@@ -17,6 +19,24 @@ struct NvtxRange {
   ~NvtxRange() { nvtxRangePop(); }
   NvtxRange(const NvtxRange&) = delete;
   NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+// A positive number that a kernel's launches need of the GPU that they go to,
+// found out once on each: that one was asked says nothing about another, and a
+// failure (0) is not remembered.  Zero-initialised statics only.
+class PerDevice {
+ public:
+  template <typename F>
+  int get(int device, F&& find) {
+    if (device < 0 || device >= DEVICES) return find();
+    int n = known_[device].load(std::memory_order_acquire);
+    if (n == 0 && (n = find()) != 0) known_[device].store(n, std::memory_order_release);
+    return n;
+  }
+
+ private:
+  static constexpr int DEVICES = 64;
+  std::atomic<int> known_[DEVICES];
 };
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

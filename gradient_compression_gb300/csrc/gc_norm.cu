@@ -594,11 +594,11 @@ static int norm_grid(int64_t rows, const RowShape& s, int threads, int waves) {
   const int64_t ctas = (rows + per - 1) / per, most = (int64_t)NORM_SMS * (threads / s.threads) * waves;
   return (int)(ctas < most ? ctas : most);
 }
-// Shared memory for the widest rows, asked for once per kernel.
+// Shared memory for the widest rows, asked for once per kernel and GPU.
 template <auto KERN>
 static bool allow_shared() {
-  static const bool ok = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 232192) == cudaSuccess;
-  return ok;
+  static PerDevice granted;
+  return granted.get(current_device(), [] { return grant_shared(KERN, 232192) ? 1 : 0; }) != 0;
 }
 static int row_mode(int64_t cols, const RowShape& s, int chunks, bool vec) {
   if (!vec) return ROW_SPAN;

@@ -719,15 +719,17 @@ static int64_t wg_ldp(int64_t k) { return (k + 3) / 4 * 4; }  // row stride of t
 
 using TensorMapEncode = decltype(&cuTensorMapEncodeTiled);
 static TensorMapEncode tensor_map_encode() {
-  static const TensorMapEncode encode = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<TensorMapEncode>(f);
-  }();
-  return encode;
+  static std::atomic<void*> encode;
+  void* f = encode.load(std::memory_order_acquire);
+  if (f) return reinterpret_cast<TensorMapEncode>(f);
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    (void)cudaGetLastError();
+    return nullptr;  // asked again by the next call
+  }
+  encode.store(f, std::memory_order_release);
+  return reinterpret_cast<TensorMapEncode>(f);
 }
 // The terms of dy as a 3-D tensor (n, rows, term) of 64 x 64 boxes under the
 // 128-byte swizzle.
@@ -756,13 +758,14 @@ static bool launch_wg(const WgArgs& a, cudaStream_t s) {
   auto kern = k_weight_grad<PARTS, TMA>;
   // the registers that the groups share out are those of the launch: with
   // fewer the kernel would wait for more
-  static const bool ready = [=] {
+  static PerDevice ready;
+  const auto prepare = [=] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs == WG_REGS &&
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) == cudaSuccess;
-  }();
+    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return (void)cudaGetLastError(), 0;
+    return at.numRegs == WG_REGS && grant_shared(kern, WG_SMEM) ? 1 : 0;
+  };
   CUtensorMap dy_map = {}, out_map = {};
-  if (!ready || (TMA && !make_dy_map(&dy_map, a, PARTS)) || (a.bulk && !make_out_map(&out_map, a))) return false;
+  if (!ready.get(current_device(), prepare) || (TMA && !make_dy_map(&dy_map, a, PARTS)) || (a.bulk && !make_out_map(&out_map, a))) return false;
   launch_chained(kern, (unsigned)(a.items < WG_SMS ? a.items : WG_SMS), WG_THREADS, WG_SMEM, s, dy_map, out_map, a);
   return true;
 }
