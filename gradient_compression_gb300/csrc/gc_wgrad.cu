@@ -705,15 +705,28 @@ static int64_t wg_tiles_m(int64_t n, int32_t dtype) {
 // to join, the join's launch 2; with s splits STAGE * stages / s + each * s, least
 // for their root.  (500 x 4096 x 1024 in bf16 takes 13.6 us whole and 19.8 in
 // two; 1000 x 333 x 1001 in fp32 15.0 in six, 15.6 in four, 23.9 whole.)
+struct WgSplit {
+  int64_t stages;
+  double stage, each;
+};
+static WgSplit wg_split(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
+  return {(rows + 63) / 64, dtype == GC_F32 ? 1.0 : 0.67, (double)n * (double)k * 8.0 / 7e6 + 0.1};
+}
+// The most that so many rows, or fewer, are split into: it never falls as rows
+// grow, where the splits themselves do, by how the rows divide into stages.
+static int wg_most_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
+  const WgSplit w = wg_split(rows, n, k, dtype);
+  const int64_t most = WG_SMS / (wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N));
+  const int64_t s = (int64_t)(std::sqrt((double)w.stages * w.stage / w.each) + 0.5);
+  return (int)(s < most ? s : most);
+}
 static int wg_splits(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
-  const int64_t most = WG_SMS / (wg_tiles_m(n, dtype) * ((k + WG_N - 1) / WG_N)), stages = (rows + 63) / 64;
-  const double stage = dtype == GC_F32 ? 1.0 : 0.67, each = (double)n * (double)k * 8.0 / 7e6 + 0.1;
-  int64_t s = (int64_t)(std::sqrt((double)stages * stage / each) + 0.5);
-  if (s > most) s = most;
+  const WgSplit w = wg_split(rows, n, k, dtype);
+  int64_t s = wg_most_splits(rows, n, k, dtype);
   if (s < 2) return 1;
   const int64_t span = wg_span(rows, s);
   s = (rows + span - 1) / span;
-  return (double)(span / 64) * stage + (double)s * each + 2.0 < (double)stages * stage ? (int)s : 1;
+  return (double)(span / 64) * w.stage + (double)s * w.each + 2.0 < (double)w.stages * w.stage ? (int)s : 1;
 }
 static int64_t wg_ldp(int64_t k) { return (k + 3) / 4 * 4; }  // row stride of the splits' sums
 
@@ -782,7 +795,9 @@ static void launch_split(const void* dy, int64_t lddy, int64_t rows, int64_t n, 
 }
 
 // Workspace: the diagnostic words, dy's terms (none for a bf16 dy whose n
-// elements per row can lie on 16-byte boundaries), the splits' sums.
+// elements per row can lie on 16-byte boundaries), room for the sums of the most
+// splits, so that what holds many rows holds fewer (at most 40 MB: there are
+// splits only where all their tiles fit the SMs).
 struct WgSpace {
   int parts, splits;
   int64_t ldt;  // row stride of the terms
@@ -795,7 +810,8 @@ static WgSpace wg_space(int64_t rows, int64_t n, int64_t k, int32_t dtype) {
   w.ldt = (n + 7) / 8 * 8;
   w.terms = DIAG_BYTES;
   w.sums = w.terms + (dtype == GC_BF16 && n % 8 == 0 ? 0 : align_up((size_t)w.parts * rows * w.ldt * 2, 256));
-  w.bytes = w.sums + (w.splits > 1 ? (size_t)w.splits * n * wg_ldp(k) * sizeof(float) : 0);
+  const int most = wg_most_splits(rows, n, k, dtype);
+  w.bytes = w.sums + (most > 1 ? (size_t)most * n * wg_ldp(k) * sizeof(float) : 0);
   return w;
 }
 

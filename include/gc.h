@@ -605,7 +605,7 @@ gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t l
                      int64_t cols, void* y, int64_t ldy, void* h, int64_t ldh, float* rstd,
                      int8_t* codes, uint8_t* steps, void* stream);
 
-/* Bytes of workspace of gc_rmsnorm_backward with dw. */
+/* Bytes of workspace of gc_rmsnorm_backward with dw; they do for fewer rows, too. */
 gc_status gc_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
 
 /* Gradient of gc_rmsnorm at the checkpoint's values q of xh:
@@ -639,7 +639,7 @@ gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, in
                                 int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu,
                                 int8_t* out_codes, uint8_t* out_steps, void* stream);
 
-/* Bytes of workspace of gc_act_weight_grad. */
+/* Bytes of workspace of gc_act_weight_grad; they do for fewer rows, too. */
 gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dtype,
                                             size_t* bytes);
 

@@ -1,4 +1,5 @@
-"""A checkpoint is read and written where its arrays are at the call."""
+"""What the activation calls find at the call: a checkpoint where its arrays are
+then, a workspace that was set aside for another batch."""
 import copy
 
 import pytest
@@ -59,3 +60,15 @@ def test_storage_given_up_and_taken_again(gc):
     ck.codes.copy_(away)
     gc.act_decompress(ck, out)
     assert torch.equal(out, want) and bool((other == 3).all())
+
+
+def test_weight_grad_of_a_shorter_batch(gc):
+    """In the workspace of the full one, which is split into fewer parts."""
+    n = k = 512
+    ws = gc.act_weight_grad_workspace(16384, n, k, torch.bfloat16)
+    for rows in (16384, 16128, 4000, 1):
+        ck, dy = gc.ActCheckpoint(rows, k), torch.ones(rows, n, device="cuda", dtype=torch.bfloat16)
+        gc.act_compress(torch.ones(rows, k, device="cuda"), ck)
+        dw = torch.empty(n, k, device="cuda")
+        gc.act_weight_grad(dy, ck, dw, ws)
+        assert bool((dw == rows).all())
