@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   chain_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.diag = 0u;
+  if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) a.diag[threadIdx.x] = 0u;  // all that the status call reads
 
   auto item_at = [&](int i) { return wg_item<S>(a, i); };
   bool ok = true;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     }
     }
   }
-  if (!ok) atomicOr(a.diag, GC_DIAG_TIMEOUT);
+  if (!ok) atomicOr(a.diag + DIAG_ERR, GC_DIAG_TIMEOUT);
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -875,6 +875,8 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
                     : w.parts == 3 ? launch_wg<3, true>(a, s)
                     : bulk || w.sums > w.terms ? launch_wg<1, true>(a, s) : launch_wg<1, false>(a, s);
     if (!ok) return GC_ERR_CUDA;
+  } else if (!zero_chained(ws, DIAG_BYTES, s)) {
+    return GC_ERR_CUDA;
   }
   if (splits > 1 || rows == 0) {
     const int64_t fours = wg_ldp(k) / 4, blocks = (n * fours + 255) / 256;

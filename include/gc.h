@@ -652,8 +652,9 @@ gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, 
  * chains of at most 3200 rows; the chains' sums are added in fp32 that rounds
  * (and flushes to zero below 2^-126).  Workspace 256-byte aligned; it holds
  * dy's terms (not for a bf16 dy with n a multiple of 8) and, with few tiles of
- * dw, partial sums.  Its head is for gc_get_device_status: GC_DIAG_TIMEOUT if
- * a wait inside the kernel ran out, dw then being incomplete. */
+ * dw, partial sums.  Its head is for gc_get_device_status (after every call, all
+ * fields): GC_DIAG_TIMEOUT if a wait inside the kernel ran out, dw then being
+ * incomplete. */
 gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t rows, int64_t n,
                              const int8_t* codes, const uint8_t* steps, int64_t k,
                              const void* col_scale, int32_t col_scale_dtype, float* dw,

@@ -1,5 +1,6 @@
 """What the activation calls find at the call: a checkpoint where its arrays are
-then, a workspace that was set aside for another batch."""
+then, a workspace that was set aside for another batch; and what a weight
+gradient leaves there for the status call."""
 import copy
 
 import pytest
@@ -72,3 +73,18 @@ def test_weight_grad_of_a_shorter_batch(gc):
         dw = torch.empty(n, k, device="cuda")
         gc.act_weight_grad(dy, ck, dw, ws)
         assert bool((dw == rows).all())
+
+
+@pytest.mark.parametrize("rows", [0, 40, 9000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_status_of_a_weight_gradient(gc, dtype, rows):
+    """Every field, whatever the workspace held."""
+    ck, dy = gc.ActCheckpoint(rows, 72), torch.ones(rows, 40, device="cuda", dtype=dtype)
+    gc.act_compress(torch.ones(rows, 72, device="cuda"), ck)
+    ws = gc.act_weight_grad_workspace(rows, 40, 72, dtype)
+    ws.fill_(0xA5)
+    dw = torch.empty(40, 72, device="cuda")
+    gc.act_weight_grad(dy, ck, dw, ws)
+    d = gc.get_device_status(ws)
+    assert (d.error_bits, d.exact_tensors, d.overflow_tensors, d.one_launch) == (0, 0, 0, 0)
+    assert bool((dw == rows).all())
