@@ -76,6 +76,10 @@ inline gc_status check_matrix(const void* p, int64_t ld, int64_t cols, int32_t d
   if (ld < cols) return GC_ERR_LAYOUT;
   return ((uintptr_t)p & (dtype_bytes(dtype) - 1)) ? GC_ERR_ALIGNMENT : GC_OK;
 }
+// A vector that may be missing.
+inline gc_status check_vector(const void* p, int32_t dtype) {
+  return ((uintptr_t)p & (dtype_bytes(dtype) - 1)) ? GC_ERR_ALIGNMENT : GC_OK;
+}
 // 16-bit rows that start on 16-byte boundaries.
 inline bool chunk_aligned(const void* p, int64_t ld, int32_t dtype) {
   return dtype != GC_F32 && aligned16(p) && ld % 8 == 0;

@@ -639,7 +639,8 @@ extern "C" gc_status gc_rmsnorm(const void* x, int64_t ldx, const void* residual
       (residual && (st = check_matrix(residual, ldr, cols, dtype)) != GC_OK) ||
       (y && (st = check_matrix(y, ldy, cols, dtype)) != GC_OK) ||
       (h && (st = check_matrix(h, ldh, cols, dtype)) != GC_OK) ||
-      ((codes || steps) && (st = check_codes(codes, steps)) != GC_OK))
+      ((codes || steps) && (st = check_codes(codes, steps)) != GC_OK) ||
+      (st = check_vector(weight, weight_dtype)) != GC_OK || (st = check_vector(rstd, GC_F32)) != GC_OK)
     return st;
   const int64_t groups = act_ldc(cols) / 32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -697,7 +698,7 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
     size_t need = 0;
     gc_rmsnorm_backward_workspace_size(rows, cols, &need);
     if ((st = check_workspace(workspace, ws_bytes, need)) != GC_OK) return st;
-    if ((uintptr_t)dw & 3u) return GC_ERR_ALIGNMENT;
+    if ((st = check_vector(dw, GC_F32)) != GC_OK) return st;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t groups = act_ldc(cols) / 32;
@@ -711,7 +712,8 @@ extern "C" gc_status gc_rmsnorm_backward(const void* dy, int64_t lddy, const voi
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
   if ((st = check_matrix(dy, lddy, cols, dtype)) != GC_OK || (dh && (st = check_matrix(dh, lddh, cols, dtype)) != GC_OK) ||
-      (st = check_matrix(dx, lddx, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK)
+      (st = check_matrix(dx, lddx, cols, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK ||
+      (st = check_vector(weight, weight_dtype)) != GC_OK || (st = check_vector(rstd, GC_F32)) != GC_OK)
     return st;
   if (!rstd) return GC_ERR_INVALID_ARG;
   const int parts = dw_parts(rows, cols);

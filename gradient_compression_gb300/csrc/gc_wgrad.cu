@@ -838,7 +838,8 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
   gc_status st = gc_act_weight_grad_workspace_size(rows, n, k, dtype, &need);
   if (st != GC_OK) return st;
   if ((col_scale && !valid_dtype(col_scale_dtype)) || (flags & ~GC_ACCUMULATE)) return GC_ERR_INVALID_ARG;
-  if ((st = check_workspace(workspace, ws_bytes, need)) != GC_OK || (st = check_matrix(dw, lddw, k, GC_F32)) != GC_OK)
+  if ((st = check_workspace(workspace, ws_bytes, need)) != GC_OK || (st = check_matrix(dw, lddw, k, GC_F32)) != GC_OK ||
+      (st = check_vector(col_scale, col_scale_dtype)) != GC_OK)
     return st;
   if (rows > 0 && ((st = check_matrix(dy, lddy, n, dtype)) != GC_OK || (st = check_codes(codes, steps)) != GC_OK))
     return st;

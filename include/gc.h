@@ -561,7 +561,8 @@ gc_status gc_dense_decompress_accumulate(const gc_layout* dev, const gc_layout* 
  * and 1 <= cols, both < 2^31; offsets inside a matrix are 64-bit.  Reads may
  * take in the whole of a 16-byte granule of memory that holds an element.
  * GC_ERR_LAYOUT: rows, cols or ld outside these bounds; GC_ERR_ALIGNMENT: a
- * base that is no multiple of its element, or codes off a 16-byte boundary.
+ * base (of a matrix or a vector) that is no multiple of its element, or codes
+ * off a 16-byte boundary.
  *
  * Checkpoint.  x[rows, cols] is held as int8 codes[rows, ldc], ldc = 32 *
  * ceil(cols / 32), pad codes 0, and uint8 steps[rows, ldc / 32], one step
