@@ -84,18 +84,28 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 constexpr int WG_POLLS = 1 << 22;  // limit of every wait
-// Waits for the phase of the given parity to complete, a bounded number of
-// polls (each suspended by the hardware for at most about a microsecond).
+// Whether the phase of the given parity is complete; the hardware suspends the
+// thread until it is, for at most about a microsecond.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0u;
+}
+// Waits for it, a bounded number of polls: a thread of its own, or all lanes of
+// a warp, which go on or give up together (lanes that gave up by themselves
+// would leave the others waiting for them at the next vote).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < WG_POLLS; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.b32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+  for (int i = 0; i < WG_POLLS; ++i)
+    if (mbar_poll(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < WG_POLLS; ++i)
+    if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
   return false;
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -289,7 +299,7 @@ __device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map
       const int end1 = pos1 < m.iters ? wg_chain_end<S>(m.iters, 1, pos1) : m.iters + 1;
       const int h = end1 < end0 ? 1 : 0;
       const bool later = (h ? pos1 : pos0) > 0, add = later || a.accumulate;
-      ok = __all_sync(FULL, mbar_wait(full + 8u * h, (h ? used1 : used0) & 1));
+      ok = mbar_wait_warp(full + 8u * h, (h ? used1 : used0) & 1);
       if (!ok) break;
       if (h)
         ++used1, pos1 = end1;
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         const int slot = (g + it) % STAGES;
         const uint32_t st = base + (uint32_t)slot * S::STAGE;
         if constexpr (TMA) {
-          if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
+          if (!(ok = mbar_wait_warp(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
         } else {
           // rows w, w + 4, ... of dy, 32 lanes each
           Raw8<__nv_bfloat16> d[ROWS];
@@ -463,7 +473,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             const bool in = t < m.t1;  // rows past the split's end: zeros
             d[i] = load8(a.dy + (in ? t : m.t0) * a.lddy, m.n0 + 8 * lane, in ? a.n : 0);
           }
-          if (!(ok = mbar_wait(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
+          if (!(ok = mbar_wait_warp(empty(slot), (((g + it) / STAGES) & 1) ^ 1))) break;
 #pragma unroll
           for (int i = 0; i < ROWS; ++i) {
             const uint4 x = *reinterpret_cast<const uint4*>(&d[i]);
