@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   constexpr int KT = S::KT, BLOCK = S::BLOCK, A_BYTES = S::A_BYTES, STAGES = S::STAGES, CHAIN = S::CHAIN;
   constexpr int ROWS = KT / WG_TEAM;                    // t per unpacking warp and stage
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[3 * 8 + 4];
+  __shared__ __align__(8) uint64_t bars[3 * 8 + 5];
   __shared__ uint32_t tmem_base;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
@@ -395,10 +395,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   auto empty = [&](int s) { return bar0 + 128u + 8u * s; };
   auto acc_full = [&](int h) { return bar0 + 192u + 8u * h; };   // a chain's MMAs are done
   auto acc_empty = [&](int h) { return bar0 + 208u + 8u * h; };  // its sums have been read out
+  const uint32_t drained = bar0 + 224u;                          // all MMAs are done, after a wait that ran out
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(full_a(s), 1), mbar_init(full_b(s), WG_TEAM), mbar_init(empty(s), 1);
     for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), WG_OUT);
+    mbar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WG_MMA) {
@@ -603,9 +605,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         g += m.iters;
       }
       if (!ok) {
-        // MMAs in flight read this CTA's memory: see them end
-        mma_commit(acc_full(0));
-        mbar_wait(acc_full(0), (used0 - 1) & 1);
+        // MMAs in flight read this CTA's memory: see them end (by a barrier of
+        // their own: either accumulator's chain may be done while the other's runs)
+        mma_commit(drained);
+        mbar_wait(drained, 0);
       }
     }
     }
