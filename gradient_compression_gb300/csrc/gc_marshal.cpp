@@ -11,6 +11,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <utility>
+
 #include "../../include/gc.h"
 
 namespace {
@@ -89,15 +91,19 @@ struct Mat {
   void* p = nullptr;
   int64_t ld = 0;
 };
+void check_matrix(Gpu& on, const at::Tensor& t, const char* name) {
+  if (t.dim() != 2 || !on.holds(t, name)) bad("%s: a 2-D CUDA tensor is needed", name);
+}
 // A matrix argument after its checks; rows < 0 takes any shape.
 Mat matrix(Gpu& on, const at::Tensor& t, const char* name, int64_t rows = -1, int64_t cols = -1) {
-  if (t.dim() != 2 || !on.holds(t, name)) bad("%s: a 2-D CUDA tensor is needed", name);
-  const int64_t r = t.size(0), c = t.size(1);
+  check_matrix(on, t, name);
+  const at::IntArrayRef size = t.sizes(), stride = t.strides();
+  const int64_t r = size[0], c = size[1];
   if (rows >= 0 && (r != rows || c != cols))
     bad("%s: shape (%lld, %lld) where (%lld, %lld) is needed", name, (long long)r, (long long)c, (long long)rows, (long long)cols);
-  if (t.stride(1) != 1 && c > 1) bad("%s: columns are not consecutive", name);
+  if (stride[1] != 1 && c > 1) bad("%s: columns are not consecutive", name);
   Mat m;
-  m.ld = t.stride(0);
+  m.ld = stride[0];
   if (m.ld < c) {
     if (r > 1) bad("%s: rows overlap", name);
     m.ld = c;
@@ -161,16 +167,26 @@ int64_t number(PyObject* o, PyObject* field, const char* name) {
   if (x == -1 && PyErr_Occurred()) throw Bad{};
   return x;
 }
-at::Tensor array(PyObject* o, PyObject* field, const char* name) {
-  PyObject* v = attribute(o, field, name);
-  at::Tensor t;
-  if (THPVariable_Check(v)) t = THPVariable_Unpack(v);
-  Py_DECREF(v);
-  if (!t.defined()) bad("%s: its %U is no tensor", name, field);
-  return t;
-}
+// A tensor attribute, held on to.
+struct Array {
+  PyObject* of = nullptr;
+  Array() = default;
+  Array(PyObject* o, PyObject* field, const char* name) : of(attribute(o, field, name)) {
+    if (THPVariable_Check(of)) return;
+    Py_DECREF(of);
+    bad("%s: its %U is no tensor", name, field);
+  }
+  Array(Array&& a) noexcept : of(a.of) { a.of = nullptr; }
+  Array& operator=(Array&& a) noexcept {
+    std::swap(of, a.of);
+    return *this;
+  }
+  ~Array() { Py_XDECREF(of); }
+  const at::Tensor& tensor() const { return THPVariable_Unpack(of); }
+};
 void check_array(Gpu& on, const at::Tensor& t, const char* name, int64_t rows, int64_t cols, at::ScalarType type, const char* what) {
-  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() || !on.holds(t, name))
+  const at::IntArrayRef size = t.sizes();
+  if (size.size() != 2 || size[0] != rows || size[1] != cols || t.scalar_type() != type || !t.is_contiguous() || !on.holds(t, name))
     bad("%s: a contiguous CUDA %s tensor of shape (%lld, %lld) is needed", name, what, (long long)rows, (long long)cols);
 }
 void check_arrays(Gpu& on, const at::Tensor& codes, const at::Tensor& steps, int64_t rows, int64_t cols) {
@@ -184,14 +200,15 @@ struct Held {
   int64_t rows = 0, cols = 0;
   int8_t* codes = nullptr;
   uint8_t* steps = nullptr;
-  at::Tensor arrays[2];
+  Array arrays[2];
 };
 Held held(Gpu& on, PyObject* o, const char* name) {
   Held h;
   h.rows = number(o, s_rows, name), h.cols = number(o, s_cols, name);
-  h.arrays[0] = array(o, s_codes, name), h.arrays[1] = array(o, s_steps, name);
-  check_arrays(on, h.arrays[0], h.arrays[1], h.rows, h.cols);
-  h.codes = static_cast<int8_t*>(h.arrays[0].data_ptr()), h.steps = static_cast<uint8_t*>(h.arrays[1].data_ptr());
+  h.arrays[0] = Array(o, s_codes, name), h.arrays[1] = Array(o, s_steps, name);
+  const at::Tensor &codes = h.arrays[0].tensor(), &steps = h.arrays[1].tensor();
+  check_arrays(on, codes, steps, h.rows, h.cols);
+  h.codes = static_cast<int8_t*>(codes.data_ptr()), h.steps = static_cast<uint8_t*>(steps.data_ptr());
   return h;
 }
 Held held(Gpu& on, PyObject* o, const char* name, int64_t rows, int64_t cols) {
@@ -240,7 +257,7 @@ using Args = PyObject* const*;
 PyObject* act_compress(Args a) {  // x, ckpt, stream
   Gpu on;
   const at::Tensor& x = tensor(a[0], "x");
-  matrix(on, x, "x");
+  check_matrix(on, x, "x");
   const Held h = held(on, a[1], "ckpt");
   const Mat m = matrix(on, x, "x", h.rows, h.cols);
   return call(on, entry.act_compress, m.p, m.ld, type_code(x, "x"), h.rows, h.cols, h.codes, h.steps, stream_of(a[2], x));
@@ -249,7 +266,7 @@ PyObject* act_compress(Args a) {  // x, ckpt, stream
 PyObject* act_decompress(Args a) {  // ckpt, out, stream
   Gpu on;
   const at::Tensor& out = tensor(a[1], "out");
-  matrix(on, out, "out");
+  check_matrix(on, out, "out");
   const Held h = held(on, a[0], "ckpt");
   const Mat m = matrix(on, out, "out", h.rows, h.cols);
   return call(on, entry.act_decompress, h.codes, h.steps, h.rows, h.cols, m.p, m.ld, type_code(out, "out"), stream_of(a[2], out));
@@ -277,7 +294,7 @@ PyObject* rmsnorm(Args a) {  // x, weight, eps, y, residual, h, rstd, ckpt, stre
 PyObject* rmsnorm_backward(Args a) {  // dy, ckpt, rstd, weight, dx, dw, workspace, dh, accumulate, stream
   Gpu on;
   const at::Tensor& dy = tensor(a[0], "dy");
-  matrix(on, dy, "dy");
+  check_matrix(on, dy, "dy");
   const Held c = held(on, a[1], "ckpt");
   const Mat d = matrix(on, dy, "dy", c.rows, c.cols);
   const at::ScalarType type = dy.scalar_type();
@@ -315,7 +332,7 @@ PyObject* gated_act(Args a) {  // kind, gate, up, out, ckpt_gate, ckpt_up, strea
 PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out, stream
   Gpu on;
   const at::Tensor& dout = tensor(a[1], "dout");
-  matrix(on, dout, "dout");
+  check_matrix(on, dout, "dout");
   const Held cg = held(on, a[2], "ckpt_gate");
   const Mat d = matrix(on, dout, "dout", cg.rows, cg.cols);
   const at::ScalarType type = dout.scalar_type();
@@ -329,7 +346,7 @@ PyObject* gated_act_backward(Args a) {  // kind, dout, ckpt_gate, ckpt_up, dgate
 PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accumulate, stream
   Gpu on;
   const at::Tensor& dy = tensor(a[0], "dy");
-  matrix(on, dy, "dy");
+  check_matrix(on, dy, "dy");
   const Held c = held(on, a[1], "ckpt");
   const int64_t n = dy.size(1);
   const Mat d = matrix(on, dy, "dy", c.rows, n), dw = needed(on, a[2], "dw", n, c.cols, at::kFloat);
