@@ -36,8 +36,8 @@ namespace gc {
 // other one's MMAs go on with the stages at hand meanwhile; and CTAs end them
 // at different times, so that they do not all write at once.
 //
-// Measured: 16384 x 14336 x 4096 in bf16 1.23 ms, 1566 TFLOP/s (one chain 1.12 ms;
-// 1.35 ms in long runs under the power cap); 8192 x 4864 x 2048 110 us, where a
+// Measured: 16384 x 14336 x 4096 in bf16 1.36 ms, 1415 TFLOP/s, back to back under
+// the power cap (a call on its own 1.22 ms, one chain 1.12 ms); 8192 x 4864 x 2048 110 us, where a
 // library's product of two bf16 matrices takes 92; 8192 x 1024 x 1024 25 us, in
 // fp16 40 us.
 //
@@ -248,7 +248,8 @@ struct WgShape {
   static constexpr int STAGES = WG_RING / STAGE < 6 ? WG_RING / STAGE : 6;
   static constexpr int CHAIN = WG_CHAIN / KT;           // stages of a chain
   // Registers per thread as the roles share out those of the launch, so that
-  // none keeps its variables in memory: unpacking, writing, the rest.
+  // none keeps its variables in memory (without TMA 24 bytes are): unpacking,
+  // writing, the rest.
   static constexpr int REGS_CONV = TMA ? 80 : 96, REGS_OUT = TMA ? 120 : 112, REGS_REST = TMA ? 80 : 64;
   static_assert(WG_CONV * REGS_CONV + WG_OUT * REGS_OUT + 4 * REGS_REST <= WG_THREADS / 32 * WG_REGS, "registers");
 };
@@ -783,7 +784,8 @@ template <int PARTS, bool TMA>
 static bool launch_wg(const WgArgs& a, cudaStream_t s) {
   auto kern = k_weight_grad<PARTS, TMA>;
   // the registers that the groups share out are those of the launch: with
-  // fewer the kernel would wait for more
+  // fewer the kernel would wait for more, so it is not launched (a compiler
+  // that gives it other than 96 asks for other shares above)
   static PerDevice ready;
   const auto prepare = [=] {
     cudaFuncAttributes at;

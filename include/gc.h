@@ -573,11 +573,16 @@ gc_status gc_dense_decompress_accumulate(const gc_layout* dev, const gc_layout* 
  * magnitudes from 2^128 (1 - 2^-8) on need the clamp); value = code * step.
  * A group of zeros has b = 1.  A group holding a NaN or an infinity has
  * b = 255 and codes 0 and reads back as NaN.  Every finite value is exact
- * in bf16 and in fp32.  codes: 16-byte aligned.
+ * in bf16 and in fp32; fp16's range ends at 65504, and in a group whose m is
+ * 65280 or more magnitudes from 65024 on are held as 65536 or more, which read
+ * back into fp16 as infinities.  codes: 16-byte aligned.
  *
- * Arithmetic is fp32 whatever the dtype, each output rounded to its type
- * once; sums are fp32 with a fixed order, so results are bit-identical from
- * run to run (and, sums over rows apart, for every base address and ld).  Unless stated otherwise buffers must not overlap. */
+ * Arithmetic is fp32 whatever the dtype (the sigmoids of 16-bit gates by the
+ * hardware's exponential and reciprocal, relative error below 2^-16), each
+ * output rounded to its type once; sums are fp32 with a fixed order, so
+ * results are bit-identical from run to run (and, sums over rows apart, for
+ * every base address and ld).  Unless stated otherwise buffers must not
+ * overlap. */
 typedef enum gc_dtype { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
 
 #define GC_ACCUMULATE 0x1u /* flags: add to dw instead of writing it */
@@ -655,7 +660,8 @@ gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, 
  * dy's terms (not for a bf16 dy with n a multiple of 8) and, with few tiles of
  * dw, partial sums.  Its head is for gc_get_device_status (after every call, all
  * fields): GC_DIAG_TIMEOUT if a wait inside the kernel ran out, dw then being
- * incomplete. */
+ * incomplete.  GC_ERR_CUDA also where the library was built by a compiler
+ * that gives the kernel another number of registers than its roles share out. */
 gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t rows, int64_t n,
                              const int8_t* codes, const uint8_t* steps, int64_t k,
                              const void* col_scale, int32_t col_scale_dtype, float* dw,
