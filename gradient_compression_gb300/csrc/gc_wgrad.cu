@@ -59,13 +59,19 @@ constexpr int WG_RING = 192 * 1024;        // shared memory of the stages
 constexpr int WG_SMEM = WG_RING + WG_OUT * 4096;  // + a 32 x 32 tile of the result per writing warp
 constexpr int WG_CHAIN = 3200;             // rows of a chain
 
+// A bulk copy or reduction ends on a 16-byte boundary of a row, not at its last
+// element: it takes rows of the result that start on one, and the tile that a row
+// ends in only where it ends on one too, or where what follows is not the caller's.
+constexpr int WG_NONE = 0, WG_WHOLE = 1, WG_ALL = 2;
+
 struct WgArgs {
   const __nv_bfloat16* dy;      // the terms, one [rows, lddy] after another
   int64_t lddy, rows, n, k, ldc;
   const int8_t* codes;
   const uint8_t* steps;
   const void* cscale;           // of the result; NULL where it is a split's sums
-  int ctype, accumulate, bulk;  // bulk: rows of the result start on 16-byte boundaries
+  int ctype, accumulate;
+  int bulk;                     // tiles of the result that are written in bulk: WG_NONE, WG_WHOLE, WG_ALL
   float* out;                   // dw, or the splits' sums one [n, ldo] after another
   int64_t ldo;
   int splits, tiles_n, items;   // tiles along k; tiles * splits
@@ -321,6 +327,7 @@ __device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map
       auto put = [&](int c, float* x) {
         const int64_t c0 = k0 + 32 * c;
         if (rows == 0 || c0 >= a.k) return;  // uniform in the warp
+        const bool bulk = a.bulk == WG_ALL || (a.bulk == WG_WHOLE && c0 + 32 <= a.k);
         if (a.bulk && lane == 0) tma_put_read();
         if (a.cscale) {
           const float cs = c0 + lane < a.k ? load_as_f32(a.cscale, a.ctype, c0 + lane) : 0.0f;
@@ -333,7 +340,7 @@ __device__ __forceinline__ bool wg_write(const WgArgs& a, const CUtensorMap* map
         for (int q = 0; q < 8; ++q)
           st_shared16(tile + (uint32_t)lane * 128u + (uint32_t)((q ^ (lane & 7)) << 4), __float_as_uint(x[4 * q]),
                       __float_as_uint(x[4 * q + 2]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 3]));
-        if (a.bulk) {
+        if (bulk) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) tma_put(map, (int)c0, (int)r0, m.split, tile, add);
@@ -872,7 +879,7 @@ extern "C" gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dt
     a.cscale = splits > 1 ? nullptr : col_scale, a.ctype = col_scale_dtype;
     a.accumulate = splits > 1 ? 0 : acc;
     a.out = splits > 1 ? part : dw, a.ldo = splits > 1 ? wg_ldp(k) : lddw;
-    a.bulk = aligned16(a.out) && a.ldo % 4 == 0;
+    a.bulk = !(aligned16(a.out) && a.ldo % 4 == 0) ? WG_NONE : splits > 1 || k % 4 == 0 ? WG_ALL : WG_WHOLE;
     a.splits = splits, a.tiles_n = (int)tiles_n, a.items = (int)items;
     a.span = wg_span(rows, splits);
     a.diag = reinterpret_cast<uint32_t*>(ws);

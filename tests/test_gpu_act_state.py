@@ -88,3 +88,27 @@ def test_status_of_a_weight_gradient(gc, dtype, rows):
     d = gc.get_device_status(ws)
     assert (d.error_bits, d.exact_tensors, d.overflow_tensors, d.one_launch) == (0, 0, 0, 0)
     assert bool((dw == rows).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows, n, k", [(40, 8, 1), (40, 40, 7), (70, 130, 39), (500, 300, 254), (20, 24, 1459), (7000, 2600, 2598)])
+def test_weight_grad_beside_other_columns(gc, rows, n, k, dtype):
+    """Rows of dw on 16-byte boundaries that do not end on one: what lies between
+    them is somebody else's, whatever the last columns hold."""
+    x, dy = torch.ones(rows, k, device="cuda"), torch.ones(rows, n, device="cuda", dtype=dtype)
+    ws = gc.act_weight_grad_workspace(rows, n, k, dtype)
+    for spoiled in (False, True):
+        ck, ld = gc.ActCheckpoint(rows, k), (k + 7) // 4 * 4
+        if spoiled:
+            x[rows // 2, k - 1] = float("nan")
+        gc.act_compress(x, ck)
+        for accumulate in (False, True):
+            buf = torch.full((n, ld), 5.0, device="cuda")
+            flat = buf.view(-1)
+            # the last row ends with its columns, and with the matrix
+            dw = flat[:(n - 1) * ld + k].as_strided((n, k), (ld, 1))
+            gc.act_weight_grad(dy, ck, dw, ws, accumulate=accumulate)
+            assert bool((buf[:, k:] == 5.0).all())
+            last = (k - 1) // 32 * 32
+            assert bool((dw[:, :last] == rows + 5.0 * accumulate).all())
+            assert bool(torch.isnan(dw[:, last:]).all() if spoiled else (dw == rows + 5.0 * accumulate).all())
