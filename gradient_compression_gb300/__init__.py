@@ -36,6 +36,10 @@ class gc_matrix_layout(C.Structure):
     _fields_ = [("num_tensors", C.c_int32), ("start", C.c_void_p), ("rows", C.c_void_p), ("cols", C.c_void_p)]
 
 
+class gc_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("numel", C.c_int64), ("dtype", C.c_int32)]
+
+
 class gc_diag(C.Structure):
     _fields_ = [("error_bits", C.c_uint32), ("exact_tensors", C.c_uint32),
                 ("overflow_tensors", C.c_uint32), ("one_launch", C.c_uint32)]
@@ -101,6 +105,15 @@ def lib() -> C.CDLL:
         L.gc_gated_act_backward.argtypes = [I32, P, I64, I32, P, P, P, P, I64, I64, P, I64, P, I64, P, P, P]
         L.gc_act_weight_grad_workspace_size.argtypes = [I64, I64, I64, I32, C.POINTER(SZ)]
         L.gc_act_weight_grad.argtypes = [P, I64, I32, I64, I64, P, P, I64, P, I32, P, I64, U32, P, SZ, P]
+        L.gc_gated_proj_workspace_size.argtypes = [I64, I64, I64, U32, C.POINTER(SZ)]
+        L.gc_gated_proj.argtypes = [I32, P, I64, P, I64, P, I64, I32, I64, I64, I64, P, I64, P, P, P, P, P, SZ, P]
+        L.gc_gated_proj_backward_workspace_size.argtypes = [I64, I64, I64, U32, C.POINTER(SZ)]
+        L.gc_gated_proj_backward.argtypes = [I32, P, I64, I32, P, P, P, P, P, I64, P, I64, I64, I64, I64, P, I64, P, I64,
+                                             P, I64, P, P, P, SZ, P]
+        L.gc_grad_norm_workspace_size.argtypes = [I32, C.POINTER(SZ)]
+        TP = C.POINTER(gc_tensor)
+        L.gc_grad_norm.argtypes = [TP, I32, P, P, SZ, P]
+        L.gc_grad_clip.argtypes = [TP, TP, I32, P, F, P]
         L.gc_status_string.argtypes = [I32]
         L.gc_status_string.restype = C.c_char_p
         L.gc_version.restype = I32
@@ -119,7 +132,9 @@ def lib() -> C.CDLL:
                      "gc_ef_topk_compress_dev_iter", "gc_quantize_stochastic_dev_iter",
                      "gc_act_compress", "gc_act_decompress", "gc_rmsnorm", "gc_rmsnorm_backward_workspace_size",
                      "gc_rmsnorm_backward", "gc_gated_act", "gc_gated_act_backward",
-                     "gc_act_weight_grad_workspace_size", "gc_act_weight_grad"):
+                     "gc_act_weight_grad_workspace_size", "gc_act_weight_grad",
+                     "gc_gated_proj_workspace_size", "gc_gated_proj", "gc_gated_proj_backward_workspace_size",
+                     "gc_gated_proj_backward", "gc_grad_norm_workspace_size", "gc_grad_norm", "gc_grad_clip"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -524,7 +539,12 @@ class TopkCompressor:
 
 # ---------------------------------------------------------------------------- activation checkpoints
 
-from .activations import (ACT_GROUP, GC_ACCUMULATE, GC_BF16, GC_F16, GC_F32, GC_GATE_GELU_TANH,  # noqa: E402,F401
-                          GC_GATE_SILU, ActCheckpoint, act_compress, act_decompress, act_weight_grad,
-                          act_weight_grad_workspace, gated_act, gated_act_backward, rmsnorm, rmsnorm_backward,
-                          rmsnorm_backward_workspace)
+from .activations import (ACT_GROUP, GC_ACCUMULATE, GC_BF16, GC_COPY_ROWS, GC_COPY_WEIGHTS, GC_F16,  # noqa: E402,F401
+                          GC_F32, GC_GATE_GELU_TANH, GC_GATE_SILU, ActCheckpoint, act_compress, act_decompress,
+                          act_weight_grad, act_weight_grad_workspace, gated_act, gated_act_backward, gated_proj,
+                          gated_proj_backward, gated_proj_backward_workspace, gated_proj_workspace, rmsnorm,
+                          rmsnorm_backward, rmsnorm_backward_workspace)
+
+# ---------------------------------------------------------------------------- global gradient norm
+
+from .gradients import grad_clip, grad_norm, grad_norm_workspace  # noqa: E402,F401

@@ -18,6 +18,7 @@ from . import GC_OK, GCError, lib
 
 GC_F32, GC_BF16, GC_F16 = 0, 1, 2
 GC_ACCUMULATE = 0x1
+GC_COPY_ROWS, GC_COPY_WEIGHTS = 0x1, 0x2
 GC_GATE_SILU, GC_GATE_GELU_TANH = 0, 1
 ACT_GROUP = 32
 
@@ -32,7 +33,7 @@ def _marshal():
     L = lib()
     from . import _marshal as m
     names = ("act_compress", "act_decompress", "rmsnorm", "rmsnorm_backward", "gated_act", "gated_act_backward",
-             "act_weight_grad")
+             "act_weight_grad", "gated_proj", "gated_proj_backward", "grad_norm", "grad_clip")
     m.bind(*(C.cast(getattr(L, "gc_" + n), C.c_void_p).value for n in names))
     _calls = m
     return m
@@ -130,6 +131,51 @@ def gated_act_backward(kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out=None
     st = (_calls or _marshal()).gated_act_backward(kind, dout, ckpt_gate, ckpt_up, dgate, dup, ckpt_out, stream)
     if st:
         _check(st, "gc_gated_act_backward")
+
+
+def _unaligned(*mats):
+    """Whether one of the matrices does not start its rows on 16-byte boundaries."""
+    return any(t.data_ptr() % 16 or max(t.stride(0), t.size(1)) * t.element_size() % 16 for t in mats)
+
+
+def _gated_proj_workspace(entry, rows, w_gate, w_up):
+    for t in (*rows, w_gate, w_up):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            _bad("2-D tensors are needed")
+    out = C.c_size_t(0)
+    copied = (GC_COPY_ROWS if _unaligned(*rows) else 0) | (GC_COPY_WEIGHTS if _unaligned(w_gate, w_up) else 0)
+    _check(getattr(lib(), entry)(rows[0].size(0), w_gate.size(0), w_gate.size(1), copied, C.byref(out)), entry)
+    return _workspace(out, w_gate.device)
+
+
+def gated_proj_workspace(x, w_gate, w_up) -> torch.Tensor:
+    """For gated_proj of these, or of others of the same sizes, or fewer rows,
+    that need as few copies (those whose rows do not start on 16-byte boundaries)."""
+    return _gated_proj_workspace("gc_gated_proj_workspace_size", (x,), w_gate, w_up)
+
+
+def gated_proj(kind, x, w_gate, w_up, out, workspace, ckpt_gate=None, ckpt_up=None, stream=None):
+    """out[rows, n] = act(x @ w_gate.T) * (x @ w_up.T), and the checkpoints of the
+    two products where given; x[rows, k], weights [n, k], bf16 or fp16."""
+    st = (_calls or _marshal()).gated_proj(kind, x, w_gate, w_up, out, workspace, ckpt_gate, ckpt_up, stream)
+    if st:
+        _check(st, "gc_gated_proj")
+
+
+def gated_proj_backward_workspace(dgate, dup, w_gate, w_up) -> torch.Tensor:
+    """For gated_proj_backward, as gated_proj_workspace is for gated_proj."""
+    return _gated_proj_workspace("gc_gated_proj_backward_workspace_size", (dgate, dup), w_gate, w_up)
+
+
+def gated_proj_backward(kind, dout, ckpt_gate, ckpt_up, w_gate, w_up, dgate, dup, dx, workspace, ckpt_out=None,
+                        stream=None):
+    """Gradients of gated_proj from its checkpoints: dgate and dup (and the
+    checkpoint of act(gate) * up again) as gated_act_backward gives them, and
+    dx = dgate @ w_gate + dup @ w_up.  The weights' come from act_weight_grad."""
+    st = (_calls or _marshal()).gated_proj_backward(kind, dout, ckpt_gate, ckpt_up, w_gate, w_up, dgate, dup, dx,
+                                                    workspace, ckpt_out, stream)
+    if st:
+        _check(st, "gc_gated_proj_backward")
 
 
 def act_weight_grad_workspace(rows, n, k, dtype, device="cuda") -> torch.Tensor:

@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgc.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["gc_api.cu", "gc_topk.cu", "gc_dense.cu", "gc_decompress.cu", "gc_noalloc.cu", "gc_powersgd.cu",
-           "gc_act.cu", "gc_norm.cu", "gc_wgrad.cu"]
+           "gc_act.cu", "gc_norm.cu", "gc_wgrad.cu", "gc_proj.cu", "gc_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

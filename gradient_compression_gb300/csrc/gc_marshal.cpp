@@ -1,5 +1,5 @@
-// Argument marshalling of activations.py: the checks of tensors and the calls
-// of libgc's activation entry points.  A call of one token takes the GPU 1 to 5
+// Argument marshalling of activations.py and gradients.py: the checks of tensors
+// and the calls of libgc's entry points.  A call of one token takes the GPU 1 to 5
 // us; checked in Python and passed through ctypes, its host side took 7 (norm)
 // to 13 us (gated activation, with the slices of its projection).
 //
@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <utility>
+#include <vector>
 
 #include "../../include/gc.h"
 
@@ -26,6 +27,10 @@ struct Entry {
   decltype(&gc_gated_act) gated_act;
   decltype(&gc_gated_act_backward) gated_act_backward;
   decltype(&gc_act_weight_grad) act_weight_grad;
+  decltype(&gc_gated_proj) gated_proj;
+  decltype(&gc_gated_proj_backward) gated_proj_backward;
+  decltype(&gc_grad_norm) grad_norm;
+  decltype(&gc_grad_clip) grad_clip;
 } entry;
 
 // bind(addresses of the entry points in the order above), as loaded by the package
@@ -358,6 +363,107 @@ PyObject* act_weight_grad(Args a) {  // dy, ckpt, dw, workspace, col_scale, accu
               static_cast<float*>(dw.p), dw.ld, truth(a[5]) ? GC_ACCUMULATE : 0u, ws.p, ws.bytes, stream_of(a[6], dy));
 }
 
+PyObject* gated_proj(Args a) {  // kind, x, w_gate, w_up, out, workspace, ckpt_gate, ckpt_up, stream
+  Gpu on;
+  const at::Tensor &x = tensor(a[1], "x"), &w = tensor(a[2], "w_gate");
+  const Mat mx = matrix(on, x, "x");
+  check_matrix(on, w, "w_gate");
+  const int64_t rows = x.size(0), k = x.size(1), n = w.size(0);
+  const at::ScalarType type = x.scalar_type();
+  const int code = type_code(x, "x");
+  const Mat wg = needed(on, a[2], "w_gate", n, k, type), wu = needed(on, a[3], "w_up", n, k, type),
+            out = needed(on, a[4], "out", rows, n, type);
+  const Space ws = workspace(on, a[5]);
+  const Held cg = held(on, a[6], "ckpt_gate", rows, n), cu = held(on, a[7], "ckpt_up", rows, n);
+  return call(on, entry.gated_proj, kind_of(a[0]), mx.p, mx.ld, wg.p, wg.ld, wu.p, wu.ld, code, rows, n, k, out.p, out.ld, cg.codes,
+              cg.steps, cu.codes, cu.steps, ws.p, ws.bytes, stream_of(a[8], x));
+}
+
+// kind, dout, ckpt_gate, ckpt_up, w_gate, w_up, dgate, dup, dx, workspace, ckpt_out, stream
+PyObject* gated_proj_backward(Args a) {
+  Gpu on;
+  const at::Tensor &dout = tensor(a[1], "dout"), &w = tensor(a[4], "w_gate");
+  check_matrix(on, dout, "dout");
+  check_matrix(on, w, "w_gate");
+  const Held cg = held(on, a[2], "ckpt_gate");
+  const int64_t rows = cg.rows, n = cg.cols, k = w.size(1);
+  const Mat d = matrix(on, dout, "dout", rows, n);
+  const at::ScalarType type = dout.scalar_type();
+  const int code = type_code(dout, "dout");
+  const Mat wg = needed(on, a[4], "w_gate", n, k, type), wu = needed(on, a[5], "w_up", n, k, type);
+  const Mat dg = needed(on, a[6], "dgate", rows, n, type), du = needed(on, a[7], "dup", rows, n, type),
+            dx = needed(on, a[8], "dx", rows, k, type);
+  const Space ws = workspace(on, a[9]);
+  const Held cu = held(on, a[3], "ckpt_up", rows, n), co = held(on, a[10], "ckpt_out", rows, n);
+  return call(on, entry.gated_proj_backward, kind_of(a[0]), d.p, d.ld, code, cg.codes, cg.steps, cu.codes, cu.steps, wg.p, wg.ld,
+              wu.p, wu.ld, rows, n, k, dg.p, dg.ld, du.p, du.ld, dx.p, dx.ld, co.codes, co.steps, ws.p, ws.bytes,
+              stream_of(a[11], dout));
+}
+
+// ---------------------------------------------------------------- lists of tensors
+// A list or tuple, held on to until the call returns.
+struct List {
+  PyObject* of;
+  Py_ssize_t n;
+  List(PyObject* o, const char* name) : of(PySequence_Fast(o, "")) {
+    if (!of) {
+      PyErr_Clear();
+      bad("%s: a list of tensors is needed", name);
+    }
+    n = PySequence_Fast_GET_SIZE(of);
+    if (n > INT32_MAX) {
+      Py_DECREF(of);
+      bad("%s: too many tensors", name);
+    }
+  }
+  List(const List&) = delete;
+  ~List() { Py_DECREF(of); }
+  const at::Tensor& operator[](Py_ssize_t i) const { return tensor(PySequence_Fast_GET_ITEM(of, i), "a tensor of the list"); }
+};
+// One that fills its memory, in whatever order of its dimensions.
+gc_tensor dense(Gpu& on, const at::Tensor& t, const char* name) {
+  if (t.layout() != at::kStrided || !on.holds(t, name)) bad("%s: dense CUDA tensors are needed", name);
+  if (!t.is_contiguous() && !t.is_non_overlapping_and_dense()) bad("%s: a tensor with gaps or overlaps", name);
+  gc_tensor g;
+  g.dtype = type_code(t, name), g.numel = t.numel(), g.data = g.numel ? t.data_ptr() : nullptr;
+  return g;
+}
+bool same_order(const at::Tensor& a, const at::Tensor& b) {
+  return a.numel() == b.numel() && ((a.is_contiguous() && b.is_contiguous()) || (a.sizes() == b.sizes() && a.strides() == b.strides()));
+}
+
+PyObject* grad_norm(Args a) {  // tensors, norm, workspace, stream
+  Gpu on;
+  const at::Tensor& norm = tensor(a[1], "norm");
+  float* const to = static_cast<float*>(vector(on, a[1], "norm", 1, nullptr));
+  if (!to) bad("norm is needed");
+  const List l(a[0], "tensors");
+  std::vector<gc_tensor> t((size_t)l.n);
+  for (Py_ssize_t i = 0; i < l.n; ++i) t[i] = dense(on, l[i], "tensors");
+  const Space ws = workspace(on, a[2]);
+  return call(on, entry.grad_norm, t.data(), (int32_t)l.n, to, ws.p, ws.bytes, stream_of(a[3], norm));
+}
+
+PyObject* grad_clip(Args a) {  // tensors, norm, max_norm, out, stream
+  Gpu on;
+  const at::Tensor& norm = tensor(a[1], "norm");
+  const float* const from = static_cast<float*>(vector(on, a[1], "norm", 1, nullptr));
+  if (!from) bad("norm is needed");
+  const double most = PyFloat_AsDouble(a[2]);
+  if (most == -1.0 && PyErr_Occurred()) throw Bad{};
+  const List in(a[0], "tensors"), out(a[3] == Py_None ? a[0] : a[3], "out");
+  if (in.n != out.n) bad("out: %zd tensors where %zd are needed", out.n, in.n);
+  std::vector<gc_tensor> t((size_t)in.n), o;
+  if (a[3] != Py_None) o.resize((size_t)in.n);
+  for (Py_ssize_t i = 0; i < in.n; ++i) {
+    t[i] = dense(on, in[i], "tensors");
+    if (o.empty()) continue;
+    o[i] = dense(on, out[i], "out");
+    if (!same_order(in[i], out[i])) bad("out: tensor %zd has another shape or order", i);
+  }
+  return call(on, entry.grad_clip, t.data(), o.empty() ? t.data() : o.data(), (int32_t)in.n, from, (float)most, stream_of(a[4], norm));
+}
+
 // checkpoint(codes, steps, rows, cols): the checks of an ActCheckpoint's arrays
 PyObject* checkpoint(Args a) {
   Gpu on;
@@ -392,6 +498,10 @@ PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast
                          GC_METHOD(gated_act, 7),
                          GC_METHOD(gated_act_backward, 8),
                          GC_METHOD(act_weight_grad, 7),
+                         GC_METHOD(gated_proj, 9),
+                         GC_METHOD(gated_proj_backward, 12),
+                         GC_METHOD(grad_norm, 4),
+                         GC_METHOD(grad_clip, 5),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

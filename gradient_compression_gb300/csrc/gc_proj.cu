@@ -1,0 +1,542 @@
+// Gated projection on the fifth-generation tensor cores, out = act(x Wg^T) *
+// (x Wu^T), and its input's gradient dx = dgate Wg + dup Wu.
+#include "gc_act.cuh"
+#include "gc_gate.cuh"
+#include "gc_host.h"
+#include "gc_mma.cuh"
+
+namespace gc {
+
+// Mathematics and precision.  The operands are of 16 bits, so every product is
+// exact in the tensor cores' fp32; their sums truncate, a relative error of
+// about 1e-9 per term of the sum's length, far below the outputs' own rounding (2^-9 or
+// 2^-12).  G and U stay in fp32 from tensor memory to the activation, and the
+// checkpoints are taken of that.
+//
+// Tile.  128 rows of x by `bn` columns of out, one MMA of N = 2 bn for both
+// projections: the rows of Wg and of Wu lie one after another in shared memory, so
+// G is in the first bn columns of the accumulator and U in the next, and a
+// thread that reads out a row has both.  The gradient's tile is 128 rows by bn
+// columns of dx, its sum the concatenation of (dgate, Wg) and (dup, Wu).  Two
+// accumulators of up to 256 columns: one is read out while the next is summed.
+//
+// x, dgate and dup are "K-major" (the summed index is consecutive), and so are
+// the weights of the projection; the gradient sums over the weights' rows, which makes
+// them "MN-major".  Everything comes by bulk tensor copies under the 128-byte
+// swizzle, with zeros for what is outside a matrix.
+constexpr int GP_M = 128, GP_K = 64;         // rows of a tile, summed index of a stage
+constexpr int GP_A = GP_M * GP_K * 2;        // bytes of a stage's rows
+constexpr int GP_RING = 4 * (GP_A + 256 * GP_K * 2), GP_SLOTS = 8;
+constexpr int GP_OUT = 8, GP_FIRST = 4;      // warps that read out, the first of them
+constexpr int GP_THREADS = (GP_FIRST + GP_OUT) * 32;
+constexpr int GP_SMS = 152;                  // of a GB300
+constexpr int GP_POLLS = 1 << 22;            // limit of every wait
+
+__device__ __forceinline__ bool gp_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < GP_POLLS; ++i)
+    if (mbar_poll(bar, parity)) return true;
+  return false;
+}
+// All lanes of a warp, which go on or give up together.
+__device__ __forceinline__ bool gp_wait_warp(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < GP_POLLS; ++i)
+    if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
+  return false;
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// Shared-memory operand descriptor of a K-major tile under the 128-byte
+// swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t k_desc(uint32_t addr) { return mn_desc(addr, 16); }
+
+struct GpMaps {
+  CUtensorMap a0, a1, b0, b1;  // x, -, Wg, Wu; or dgate, dup, Wg, Wu
+};
+struct GpArgs {
+  int64_t rows, cols;          // of the result
+  int half, steps;             // stages of the first pair of operands, of both
+  int bn, slots, stage;        // columns of a tile, stages in the ring, bytes of one
+  int tiles_m, tiles_n, splits, items, span;  // span: stages of a split
+  int band;                    // tiles of a band of rows, which goes along all columns before the next one
+  void* out;
+  int64_t ldo;
+  bool vec;                    // rows of `out` start on 16-byte boundaries
+  int8_t *gcodes, *ucodes;
+  uint8_t *gsteps, *usteps;
+  float* part;                 // the splits' sums, one [rows, ldp] after another
+  int64_t ldp;
+  uint32_t* diag;
+};
+struct GpItem {
+  int m, n, split, s0, s1;
+};
+__device__ __forceinline__ GpItem gp_item(const GpArgs& a, int i) {
+  GpItem t;
+  t.split = i % a.splits;
+  const int tile = i / a.splits, band = tile / (a.band * a.tiles_n), r = tile % (a.band * a.tiles_n);
+  const int high = min(a.band, a.tiles_m - band * a.band);
+  t.m = band * a.band + r % high, t.n = r / high;
+  t.s0 = t.split * a.span, t.s1 = min(t.s0 + a.span, a.steps);
+  return t;
+}
+
+// Codes and step of the 32 values of a group that one thread holds.
+__device__ __forceinline__ void gp_hold(const float (&v)[32], int8_t* codes, uint8_t* step) {
+  float top = max_nan(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+  for (int i = 2; i < 32; i += 2) top = max_nan(top, fabsf(v[i]), fabsf(v[i + 1]));
+  const uint32_t b = act_step(__float_as_uint(top));
+  uint2 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[CHUNK];
+#pragma unroll
+    for (int e = 0; e < CHUNK; ++e) x[e] = v[8 * i + e];
+    q[i] = chunk_codes(x, b);
+  }
+  reinterpret_cast<uint4*>(codes)[0] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+  reinterpret_cast<uint4*>(codes)[1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
+  *step = (uint8_t)b;
+}
+// n of the 32 values of a row.
+template <typename T>
+__device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, bool vec) {
+  if (vec && n == 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Raw8<T> r;
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e) r.e[e] = from_f32<T>(v[8 * i + e]);
+      reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<const uint4*>(&r);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n) to[e] = from_f32<T>(v[e]);
+  }
+}
+
+// KIND: the activation; GP_BACK: the gradient.
+constexpr int GP_BACK = -1;
+template <typename T, int KIND>
+__global__ void __launch_bounds__(GP_THREADS, 1)
+    k_gated_proj(const __grid_constant__ GpMaps maps, const __grid_constant__ GpArgs a) {
+  constexpr bool BACK = KIND == GP_BACK;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[2 * GP_SLOTS + 5];
+  __shared__ uint32_t tmem_base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (GP_SLOTS + s); };
+  auto acc_full = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + h); };       // an accumulator's MMAs are done
+  auto acc_empty = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + 2 + h); };  // it has been read out
+  const uint32_t drained = bar0 + 8u * (2 * GP_SLOTS + 4);                     // all MMAs are done, after a wait that ran out
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < GP_SLOTS; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), GP_OUT);
+    mbar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) a.diag[threadIdx.x] = 0u;  // all that the status call reads
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------ operands
+    if (lane == 0) {
+      const uint32_t bytes = (uint32_t)(BACK ? GP_A + (a.bn + 63) / 64 * 64 * GP_K * 2 : GP_A + 2 * a.bn * GP_K * 2);
+      int slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
+      uint32_t turn = 0u;
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+        const GpItem t = gp_item(a, i);
+        for (int s = t.s0; s < t.s1; ++s) {
+          if (!(ok = gp_wait(empty(slot), (turn & 1u) ^ 1u))) break;
+          mbar_expect(full(slot), bytes);
+          const uint32_t st = base + (uint32_t)(slot * a.stage);
+          if (BACK) {
+            const bool second = s >= a.half;
+            const int x = (second ? s - a.half : s) * GP_K;
+            tma_load_2d(st, second ? &maps.a1 : &maps.a0, x, t.m * GP_M, full(slot));
+            for (int b = 0; b < a.bn; b += 64)
+              tma_load_2d(st + GP_A + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + b, x, full(slot));
+          } else {
+            tma_load_2d(st, &maps.a0, s * GP_K, t.m * GP_M, full(slot));
+            tma_load_2d(st + GP_A, &maps.b0, s * GP_K, t.n * a.bn, full(slot));
+            tma_load_2d(st + GP_A + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, full(slot));
+          }
+          if (++slot == a.slots) slot = 0, ++turn;
+          used = min(used + 1, a.slots);
+        }
+      }
+      // its copies in flight write this CTA's memory: see them land
+      if (!ok)
+        for (int j = 0; j < used; ++j) {
+          if (--slot < 0) slot = a.slots - 1, --turn;
+          gp_wait(full(slot), turn & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA
+    if (lane == 0) {
+      // fp32 accumulator, the operands' type, N, M = 128
+      constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (BACK ? 1u << 16 : 0u) |
+                             ((uint32_t)((BACK ? a.bn : 2 * a.bn) >> 3) << 17) | (8u << 24);
+      int slot = 0;
+      uint32_t turn = 0u, count = 0u;
+      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x, ++count) {
+        const GpItem t = gp_item(a, i);
+        const uint32_t acc = count & 1u;
+        if (!(ok = gp_wait(acc_empty(acc), ((count >> 1) & 1u) ^ 1u))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int s = t.s0; s < t.s1; ++s) {
+          if (!(ok = gp_wait(full(slot), turn & 1u))) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t st = base + (uint32_t)(slot * a.stage);
+#pragma unroll
+          for (int j = 0; j < GP_K / 16; ++j)
+            mma_f16(tmem + 256u * acc, k_desc(st + 32u * j),
+                    BACK ? mn_desc(st + GP_A + 2048u * j, GP_K * 128) : k_desc(st + GP_A + 32u * j), idesc, s > t.s0 || j > 0);
+          mma_commit(empty(slot));
+          if (++slot == a.slots) slot = 0, ++turn;
+        }
+        if (ok) mma_commit(acc_full(acc));
+      }
+      if (!ok) {
+        // MMAs in flight read this CTA's memory: see them end
+        mma_commit(drained);
+        gp_wait(drained, 0);
+      }
+    }
+  } else if (warp >= GP_FIRST) {
+    // ------------------------------------------------ result
+    const int quad = warp & 3, side = (warp - GP_FIRST) >> 2;
+    const int64_t ldc = act_ldc(a.cols);
+    uint32_t count = 0u;
+    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x, ++count) {
+      const GpItem t = gp_item(a, i);
+      const uint32_t acc = count & 1u;
+      if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
+      const int64_t row = (int64_t)t.m * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
+      for (int c = 32 * side; c < a.bn && c0 + c < a.cols; c += 64) {
+        const int64_t col = c0 + c;
+        const int n = (int)min((int64_t)32, a.cols - col);
+        float g[32];
+        tmem_load32(g, from + c);
+        if constexpr (BACK) {
+          if (row < a.rows) {
+            if (a.part)
+              gp_put(g, a.part + ((int64_t)t.split * a.rows + row) * a.ldp + col, n, true);
+            else
+              gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
+          }
+        } else {
+          float u[32];
+          tmem_load32(u, from + a.bn + c);
+          if (n < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e >= n) g[e] = u[e] = 0.0f;
+          }
+          if (row < a.rows) {
+            if (a.gcodes) {
+              gp_hold(g, a.gcodes + row * ldc + col, a.gsteps + row * (ldc >> 5) + (col >> 5));
+              gp_hold(u, a.ucodes + row * ldc + col, a.usteps + row * (ldc >> 5) + (col >> 5));
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              F2 dp;
+              put2(g + e, mul2(mul2(get2(g + e), gate_sigmoid2<KIND>(g + e, &dp)), get2(u + e)));
+            }
+            gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
+          }
+        }
+        __syncwarp();
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(acc));
+    }
+  }
+  if (!ok) atomicOr(a.diag + DIAG_ERR, GC_DIAG_TIMEOUT);
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+// fp32 rows are never written by a vector of T's size.
+template <>
+__device__ __forceinline__ void gp_put<float>(const float (&v)[32], float* to, int n, bool) {
+  if (n == 32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<float4*>(to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n) to[e] = v[e];
+  }
+}
+
+// dx = the splits' sums in their order, four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) k_gated_proj_join(const float4* part, int splits, int64_t rows, int64_t cols,
+                                                         int64_t fours, T* out, int64_t ldo) {
+  chain_wait();
+  const int64_t total = rows * fours;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / fours, c = (i - r * fours) * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < splits; ++p) {
+      const float4 v = __ldg(part + p * total + i);
+      s[0] = __fadd_rn(s[0], v.x), s[1] = __fadd_rn(s[1], v.y), s[2] = __fadd_rn(s[2], v.z), s[3] = __fadd_rn(s[3], v.w);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < cols) out[r * ldo + c + e] = from_f32<T>(s[e]);
+  }
+}
+
+// A copy whose rows start on 16-byte boundaries, of 16-bit elements.
+__global__ void __launch_bounds__(256) k_align_rows(const uint16_t* x, int64_t ld, int64_t rows, int64_t cols, uint16_t* to,
+                                                    int64_t ldt) {
+  chain_wait();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ldt + c] = x[r * ld + c];
+}
+
+// ---------------------------------------------------------------- host
+static bool make_map(CUtensorMap* m, int32_t dtype, const void* p, int64_t ld, int64_t rows, int64_t cols, int box_rows) {
+  const TensorMapEncode encode = tensor_map_encode();
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return encode && encode(m, dtype == GC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                          const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call is cut: the tile's width, and for the gradient the splits of its sum
+// where there are fewer tiles than SMs.
+struct GpPlan {
+  int bn, tiles_m, tiles_n, splits, span;
+};
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// The time of a stage goes by its bytes; a tile's fixed part is that of about six stages.
+static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t steps, bool back) {
+  GpPlan best = {};
+  double least = 0.0;
+  const int widest = back ? 256 : 128;
+  const int64_t tm = ceil_div(rows, GP_M);
+  for (int bn = widest; bn >= 32; bn -= 32) {
+    const int64_t tn = ceil_div(cols, bn), tiles = tm * tn;
+    const double stage = (16.0 + (back ? bn / 8.0 : bn / 4.0)) * 0.0084;  // us
+    const int most = back && tiles < GP_SMS ? (int)(GP_SMS / tiles < 16 ? GP_SMS / tiles : 16) : 1;
+    for (int s = 1; s <= most; ++s) {
+      const int64_t span = ceil_div(steps, s);
+      if (s > 1 && (span < 4 || ceil_div(steps, span) != s)) continue;
+      double us = (double)ceil_div(tiles * s, GP_SMS) * ((double)span + 6.0) * stage;
+      if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 8.0 / 7e6;
+      if (best.bn == 0 || us < least) best = {bn, (int)tm, (int)tn, s, (int)span}, least = us;
+    }
+  }
+  return best;
+}
+static int64_t gp_ldp(int64_t cols) { return (cols + 3) / 4 * 4; }
+static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+// Workspace: the diagnostic words, the aligned copies, the splits' sums (there are
+// splits only where all their tiles fit the SMs: at most 16, and 20 MB).
+struct GpSpace {
+  size_t rows[2], weights[2], sums, bytes;
+};
+static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, bool back) {
+  GpSpace w = {};
+  size_t at = DIAG_BYTES;
+  const auto room = [&](int64_t r, int64_t c) {
+    const size_t here = at;
+    at += align_up((size_t)r * gp_ld(c) * 2, 256);
+    return here;
+  };
+  if (copied & GC_COPY_WEIGHTS) w.weights[0] = room(n, k), w.weights[1] = room(n, k);
+  if (copied & GC_COPY_ROWS) {
+    w.rows[0] = room(rows, back ? n : k);
+    if (back) w.rows[1] = room(rows, n);
+  }
+  w.sums = at;
+  if (back) {
+    const double sums = 16.0 * (double)rows * (double)gp_ldp(k) * 4.0, most = (double)GP_SMS * GP_M * 256 * 4;
+    at += align_up((size_t)(sums < most ? sums : most), 256);
+  }
+  w.bytes = at;
+  return w;
+}
+static bool bulk_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
+
+static const void* align_rows(const void* x, int64_t* ld, int64_t rows, int64_t cols, unsigned char* to, cudaStream_t s) {
+  const int64_t ldt = gp_ld(cols);
+  launch_chained(k_align_rows, (unsigned)(rows < GP_SMS * 8 ? rows : GP_SMS * 8), 256, 0, s, static_cast<const uint16_t*>(x), *ld,
+                 rows, cols, reinterpret_cast<uint16_t*>(to), ldt);
+  *ld = ldt;
+  return to;
+}
+
+template <typename T, int KIND>
+static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
+  auto kern = k_gated_proj<T, KIND>;
+  static PerDevice ready;
+  if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_RING) ? 1 : 0; })) return false;
+  launch_chained(kern, (unsigned)(a.items < GP_SMS ? a.items : GP_SMS), GP_THREADS, GP_RING, s, maps, a);
+  return true;
+}
+static void set_plan(GpArgs* a, const GpPlan& p, bool back) {
+  a->bn = p.bn, a->tiles_m = p.tiles_m, a->tiles_n = p.tiles_n, a->splits = p.splits, a->span = p.span;
+  a->items = p.tiles_m * p.tiles_n * p.splits;
+  a->band = 16;
+  a->stage = GP_A + (back ? (p.bn + 63) / 64 * 64 : 2 * p.bn) * GP_K * 2;
+  a->slots = GP_RING / a->stage < GP_SLOTS ? GP_RING / a->stage : GP_SLOTS;
+}
+static gc_status check_sizes(int64_t rows, int64_t n, int64_t k) {
+  gc_status st = validate_matrix(rows, n, GC_BF16);
+  if (st == GC_OK) st = validate_matrix(rows, k, GC_BF16);
+  // tiles are counted in 32 bits
+  return st != GC_OK ? st : ceil_div(rows, GP_M) * ceil_div(n > k ? n : k, 32) > INT64_C(1073741823) ? GC_ERR_LAYOUT : GC_OK;
+}
+static bool valid_kind(int32_t kind) { return kind == GC_GATE_SILU || kind == GC_GATE_GELU_TANH; }
+
+}  // namespace gc
+
+using namespace gc;
+
+extern "C" gc_status gc_gated_proj_workspace_size(int64_t rows, int64_t n, int64_t k, uint32_t copied, size_t* bytes) {
+  const gc_status st = check_sizes(rows, n, k);
+  if (st != GC_OK) return st;
+  if (!bytes || (copied & ~(GC_COPY_ROWS | GC_COPY_WEIGHTS))) return GC_ERR_INVALID_ARG;
+  *bytes = gp_space(rows, n, k, copied, false).bytes;
+  return GC_OK;
+}
+extern "C" gc_status gc_gated_proj_backward_workspace_size(int64_t rows, int64_t n, int64_t k, uint32_t copied, size_t* bytes) {
+  const gc_status st = check_sizes(rows, n, k);
+  if (st != GC_OK) return st;
+  if (!bytes || (copied & ~(GC_COPY_ROWS | GC_COPY_WEIGHTS))) return GC_ERR_INVALID_ARG;
+  *bytes = gp_space(rows, n, k, copied, true).bytes;
+  return GC_OK;
+}
+
+extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, const void* w_gate, int64_t ldwg,
+                                   const void* w_up, int64_t ldwu, int32_t dtype, int64_t rows, int64_t n, int64_t k,
+                                   void* out, int64_t ldo, int8_t* gate_codes, uint8_t* gate_steps, int8_t* up_codes,
+                                   uint8_t* up_steps, void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("gc_gated_proj");
+  gc_status st = check_sizes(rows, n, k);
+  if (st != GC_OK) return st;
+  if (!valid_kind(kind) || !(dtype == GC_BF16 || dtype == GC_F16)) return GC_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if ((st = check_matrix(x, ldx, k, dtype)) != GC_OK || (st = check_matrix(w_gate, ldwg, k, dtype)) != GC_OK ||
+        (st = check_matrix(w_up, ldwu, k, dtype)) != GC_OK || (st = check_matrix(out, ldo, n, dtype)) != GC_OK)
+      return st;
+    if (gate_codes || gate_steps || up_codes || up_steps)
+      if ((st = check_codes(gate_codes, gate_steps)) != GC_OK || (st = check_codes(up_codes, up_steps)) != GC_OK) return st;
+  }
+  const uint32_t copied = rows == 0 ? 0u
+                                    : (bulk_rows(x, ldx) ? 0u : GC_COPY_ROWS) |
+                                          (bulk_rows(w_gate, ldwg) && bulk_rows(w_up, ldwu) ? 0u : GC_COPY_WEIGHTS);
+  const GpSpace w = gp_space(rows, n, k, copied, false);
+  if ((st = check_workspace(workspace, ws_bytes, w.bytes)) != GC_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
+  if (copied & GC_COPY_ROWS) x = align_rows(x, &ldx, rows, k, ws + w.rows[0], s);
+  if (!bulk_rows(w_gate, ldwg)) w_gate = align_rows(w_gate, &ldwg, n, k, ws + w.weights[0], s);
+  if (!bulk_rows(w_up, ldwu)) w_up = align_rows(w_up, &ldwu, n, k, ws + w.weights[1], s);
+  GpArgs a = {};
+  a.rows = rows, a.cols = n, a.steps = a.half = (int)ceil_div(k, GP_K);
+  set_plan(&a, gp_plan(rows, n, a.steps, false), false);
+  a.out = out, a.ldo = ldo, a.vec = bulk_rows(out, ldo);
+  a.gcodes = gate_codes, a.ucodes = up_codes, a.gsteps = gate_steps, a.usteps = up_steps;
+  a.diag = reinterpret_cast<uint32_t*>(ws);
+  GpMaps maps;
+  if (!make_map(&maps.a0, dtype, x, ldx, rows, k, GP_M) || !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, a.bn) ||
+      !make_map(&maps.b1, dtype, w_up, ldwu, n, k, a.bn))
+    return GC_ERR_CUDA;
+  maps.a1 = maps.a0;
+  const bool silu = kind == GC_GATE_SILU;
+  const bool ok = dtype == GC_BF16 ? (silu ? launch_gp<__nv_bfloat16, GC_GATE_SILU>(maps, a, s)
+                                           : launch_gp<__nv_bfloat16, GC_GATE_GELU_TANH>(maps, a, s))
+                                   : (silu ? launch_gp<__half, GC_GATE_SILU>(maps, a, s)
+                                           : launch_gp<__half, GC_GATE_GELU_TANH>(maps, a, s));
+  return ok && cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+
+extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
+                                            const int8_t* gate_codes, const uint8_t* gate_steps, const int8_t* up_codes,
+                                            const uint8_t* up_steps, const void* w_gate, int64_t ldwg, const void* w_up,
+                                            int64_t ldwu, int64_t rows, int64_t n, int64_t k, void* dgate, int64_t lddg,
+                                            void* dup, int64_t lddu, void* dx, int64_t lddx, int8_t* out_codes,
+                                            uint8_t* out_steps, void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("gc_gated_proj_backward");
+  gc_status st = check_sizes(rows, n, k);
+  if (st != GC_OK) return st;
+  if (!valid_kind(kind) || !(dtype == GC_BF16 || dtype == GC_F16)) return GC_ERR_INVALID_ARG;
+  if (rows > 0 &&
+      ((st = check_matrix(w_gate, ldwg, k, dtype)) != GC_OK || (st = check_matrix(w_up, ldwu, k, dtype)) != GC_OK ||
+       (st = check_matrix(dgate, lddg, n, dtype)) != GC_OK || (st = check_matrix(dup, lddu, n, dtype)) != GC_OK ||
+       (st = check_matrix(dx, lddx, k, dtype)) != GC_OK))
+    return st;
+  const uint32_t copied = rows == 0 ? 0u
+                                    : (bulk_rows(dgate, lddg) && bulk_rows(dup, lddu) ? 0u : GC_COPY_ROWS) |
+                                          (bulk_rows(w_gate, ldwg) && bulk_rows(w_up, ldwu) ? 0u : GC_COPY_WEIGHTS);
+  const GpSpace w = gp_space(rows, n, k, copied, true);
+  if ((st = check_workspace(workspace, ws_bytes, w.bytes)) != GC_OK) return st;
+  // checks the rest before anything is enqueued
+  st = gc_gated_act_backward(kind, dout, lddo, dtype, gate_codes, gate_steps, up_codes, up_steps, rows, n, dgate, lddg, dup,
+                             lddu, out_codes, out_steps, stream);
+  if (st != GC_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
+  const void *dg = dgate, *du = dup;
+  if (!bulk_rows(dg, lddg)) dg = align_rows(dg, &lddg, rows, n, ws + w.rows[0], s);
+  if (!bulk_rows(du, lddu)) du = align_rows(du, &lddu, rows, n, ws + w.rows[1], s);
+  if (!bulk_rows(w_gate, ldwg)) w_gate = align_rows(w_gate, &ldwg, n, k, ws + w.weights[0], s);
+  if (!bulk_rows(w_up, ldwu)) w_up = align_rows(w_up, &ldwu, n, k, ws + w.weights[1], s);
+  GpArgs a = {};
+  a.rows = rows, a.cols = k, a.half = (int)ceil_div(n, GP_K), a.steps = 2 * a.half;
+  const GpPlan p = gp_plan(rows, k, a.steps, true);
+  set_plan(&a, p, true);
+  a.out = dx, a.ldo = lddx, a.vec = bulk_rows(dx, lddx);
+  a.part = p.splits > 1 ? reinterpret_cast<float*>(ws + w.sums) : nullptr, a.ldp = gp_ldp(k);
+  a.diag = reinterpret_cast<uint32_t*>(ws);
+  GpMaps maps;
+  if (!make_map(&maps.a0, dtype, dg, lddg, rows, n, GP_M) || !make_map(&maps.a1, dtype, du, lddu, rows, n, GP_M) ||
+      !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, GP_K) || !make_map(&maps.b1, dtype, w_up, ldwu, n, k, GP_K))
+    return GC_ERR_CUDA;
+  if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, s) : launch_gp<__half, GP_BACK>(maps, a, s)))
+    return GC_ERR_CUDA;
+  if (a.part) {
+    const int64_t fours = a.ldp / 4, blocks = ceil_div(rows * fours, 256);
+    const unsigned grid = (unsigned)(blocks < GP_SMS * 8 ? blocks : GP_SMS * 8);
+    const float4* part = reinterpret_cast<const float4*>(a.part);
+    if (dtype == GC_BF16)
+      launch_chained(&k_gated_proj_join<__nv_bfloat16>, grid, 256, 0, s, part, p.splits, rows, k, fours,
+                     static_cast<__nv_bfloat16*>(dx), lddx);
+    else
+      launch_chained(&k_gated_proj_join<__half>, grid, 256, 0, s, part, p.splits, rows, k, fours, static_cast<__half*>(dx), lddx);
+  }
+  return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}

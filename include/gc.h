@@ -645,6 +645,50 @@ gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, in
                                 int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu,
                                 int8_t* out_codes, uint8_t* out_steps, void* stream);
 
+/* Gated projection: both projections of x[rows, k], the activation and the
+ * product in one,
+ *   G = x w_gate^T, U = x w_up^T, out = act(G) * U,
+ * and the checkpoints of G and U (all four arrays or none).  w_gate and w_up are
+ * [n, k] (halves of one matrix, say), out is [rows, n]; all of `dtype`, GC_BF16 or
+ * GC_F16 (GC_ERR_INVALID_ARG for GC_F32).  G and U are never rounded to it: the
+ * tensor cores' fp32 sums of exact products (which truncate: a relative error of about
+ * 1e-9 k of the terms' absolute sum) go into the activation and the checkpoints.
+ * Products read by bulk copies need x, w_gate and w_up to start on 16-byte
+ * boundaries, with row strides that are multiples of 16 bytes; those of them
+ * that do not are copied into the workspace first.  n and k < 2^31, k >= 1.
+ * gc_gated_proj_workspace_size: `copied` says which need room for that.  The
+ * workspace (256-byte aligned) does for fewer rows, too, and starts with what
+ * gc_get_device_status reads: GC_DIAG_TIMEOUT if a wait inside the kernel ran out,
+ * the outputs then being incomplete. */
+#define GC_COPY_ROWS 0x1u    /* copied: x (gc_gated_proj); dgate and dup (gc_gated_proj_backward) */
+#define GC_COPY_WEIGHTS 0x2u /* copied: w_gate and w_up */
+gc_status gc_gated_proj_workspace_size(int64_t rows, int64_t n, int64_t k, uint32_t copied,
+                                       size_t* bytes);
+gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, const void* w_gate, int64_t ldwg,
+                        const void* w_up, int64_t ldwu, int32_t dtype, int64_t rows, int64_t n,
+                        int64_t k, void* out, int64_t ldo, int8_t* gate_codes, uint8_t* gate_steps,
+                        int8_t* up_codes, uint8_t* up_steps, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/* Gradient of gc_gated_proj from dout[rows, n] at the checkpoints' values G and
+ * U: dgate, dup and the checkpoint of act(G) * U as gc_gated_act_backward gives
+ * them, and
+ *   dx[rows, k] = dgate w_gate + dup w_up
+ * from dgate and dup as they are rounded to `dtype`.  (The weights' gradients come from
+ * gc_act_weight_grad, of dgate and dup and the checkpoint of x.)  dgate or
+ * dup may be dout itself.  Types, alignment and workspace as for gc_gated_proj
+ * (GC_COPY_ROWS for dgate and dup); with few tiles of dx the workspace holds
+ * partial sums, which are added in a fixed order. */
+gc_status gc_gated_proj_backward_workspace_size(int64_t rows, int64_t n, int64_t k, uint32_t copied,
+                                                size_t* bytes);
+gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
+                                 const int8_t* gate_codes, const uint8_t* gate_steps,
+                                 const int8_t* up_codes, const uint8_t* up_steps,
+                                 const void* w_gate, int64_t ldwg, const void* w_up, int64_t ldwu,
+                                 int64_t rows, int64_t n, int64_t k, void* dgate, int64_t lddg,
+                                 void* dup, int64_t lddu, void* dx, int64_t lddx, int8_t* out_codes,
+                                 uint8_t* out_steps, void* workspace, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace of gc_act_weight_grad; they do for fewer rows, too. */
 gc_status gc_act_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dtype,
                                             size_t* bytes);
@@ -667,6 +711,47 @@ gc_status gc_act_weight_grad(const void* dy, int64_t lddy, int32_t dtype, int64_
                              const void* col_scale, int32_t col_scale_dtype, float* dw,
                              int64_t lddw, uint32_t flags, void* workspace, size_t ws_bytes,
                              void* stream);
+
+/* ------------------------------------------------------- global gradient norm
+ * The L2 norm of all gradients of a model, and clipping by it, before they are
+ * compressed: gc_ef_topk_compress_clipped bounds every tensor of an arena by
+ * itself, these bound the whole model's gradient, whose tensors may lie
+ * anywhere and be of different types. */
+
+/* A dense tensor: numel >= 0 consecutive elements of `dtype` (a gc_dtype) at a
+ * device address that is a multiple of the element; NULL without elements. */
+typedef struct gc_tensor {
+  void* data;
+  int64_t numel;
+  int32_t dtype;
+} gc_tensor;
+
+/* Bytes of workspace of gc_grad_norm for `count` tensors; they do for fewer, too. */
+gc_status gc_grad_norm_workspace_size(int32_t count, size_t* bytes);
+
+/* norm[0] (device fp32) = sqrt(sum of the squares of all elements of all
+ * tensors); 0 without any, a NaN where there is one, infinity where there is one
+ * or the norm passes fp32's range.  `tensors` is a host array, done with when the
+ * call returns.  Squares are summed in fp32 over at most 32 elements and in 64 bits
+ * beyond (in 64 bits throughout where fp32 would overflow or lose small ones), in
+ * an order set by the sizes: the same bits from run to run.  Any number of tensors
+ * (GC_ERR_LAYOUT: over 2^42 elements in all); reads may take in the whole of a
+ * 16-byte granule that holds an element.  Workspace 256-byte aligned. */
+gc_status gc_grad_norm(const gc_tensor* tensors, int32_t count, float* norm, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* out_t = c * in_t for every tensor, with N = norm[0] (device fp32, of
+ * gc_grad_norm; the caller may combine several workers' in between) and
+ * c = max_norm / N where N > max_norm, else 1 (so too where N is a NaN).
+ * c and the product are fp32, rounded to out_t's type once more.  in and out are
+ * host arrays of `count` tensors of pairwise equal numel, done with when the call
+ * returns; out_t may be in_t itself (the same address and type, left alone where
+ * c = 1), e.g. with in = out, or a tensor of another type, such as the arena's.
+ * max_norm >= 0, infinity for none.  GC_ERR_INVALID_ARG also where two of the
+ * written tensors overlap (the same one given twice, too), or one of them and
+ * another one that is read, or the norm. */
+gc_status gc_grad_clip(const gc_tensor* in, const gc_tensor* out, int32_t count, const float* norm,
+                       float max_norm, void* stream);
 
 /* Waits for `stream`, then reads the diagnostics that the last call using
  * `workspace` left there.  Returns GC_ERR_DEVICE if an error bit is set. */
