@@ -43,11 +43,50 @@ __device__ __forceinline__ bool gp_wait_warp(uint32_t bar, uint32_t parity) {
     if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
   return false;
 }
+// (The barrier may be the other CTA's of a pair.)
+template <bool PAIR>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// MMAs, and arrivals when the ones before are done, of a CTA or of a pair (there
+// on the barriers of both).
+template <bool PAIR>
+__device__ __forceinline__ void gp_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if (PAIR)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    mma_f16(d, a, b, idesc, add);
+}
+template <bool PAIR>
+__device__ __forceinline__ void gp_commit(uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+__device__ __forceinline__ uint32_t of_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Shared-memory operand descriptor of a K-major tile under the 128-byte
 // swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
@@ -59,7 +98,7 @@ struct GpMaps {
 struct GpArgs {
   int64_t rows, cols;          // of the result
   int half, steps;             // stages of the first pair of operands, of both
-  int bn, slots, stage;        // columns of a tile, stages in the ring, bytes of one
+  int bn, slots, stage, bytes; // columns of a tile, stages in the ring, room of one in a CTA, bytes that arrive in it
   int tiles_m, tiles_n, splits, items, span;  // span: stages of a split
   int band;                    // tiles of a band of rows, which goes along all columns before the next one
   void* out;
@@ -120,35 +159,46 @@ __device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, bool 
   }
 }
 
-// KIND: the activation; GP_BACK: the gradient.
+// KIND: the activation; GP_BACK: the gradient.  PAIR: a cluster of two CTAs
+// computes a tile of 256 rows, half of them each; the first one's thread issues
+// the MMAs of both, which read each CTA's rows and half of the columns' operand out
+// of its own memory.
 constexpr int GP_BACK = -1;
-template <typename T, int KIND>
-__global__ void __launch_bounds__(GP_THREADS, 1)
+template <typename T, int KIND, bool PAIR>
+__global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREADS, 1)
     k_gated_proj(const __grid_constant__ GpMaps maps, const __grid_constant__ GpArgs a) {
   constexpr bool BACK = KIND == GP_BACK;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[2 * GP_SLOTS + 5];
   __shared__ uint32_t tmem_base;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;
+  const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
-  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto full = [&](int s) { return bar0 + 8u * s; };                            // of the first CTA: both CTAs' copies are there
   auto empty = [&](int s) { return bar0 + 8u * (GP_SLOTS + s); };
   auto acc_full = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + h); };       // an accumulator's MMAs are done
-  auto acc_empty = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + 2 + h); };  // it has been read out
+  auto acc_empty = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + 2 + h); };  // of the first CTA: it has been read out
   const uint32_t drained = bar0 + 8u * (2 * GP_SLOTS + 4);                     // all MMAs are done, after a wait that ran out
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < GP_SLOTS; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), GP_OUT);
+    for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), PAIR ? 2 * GP_OUT : GP_OUT);
     mbar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (PAIR) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   chain_wait();
@@ -158,47 +208,56 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------ operands
     if (lane == 0) {
-      const uint32_t bytes = (uint32_t)(BACK ? GP_A + (a.bn + 63) / 64 * 64 * GP_K * 2 : GP_A + 2 * a.bn * GP_K * 2);
       int slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
       uint32_t turn = 0u;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+      for (int i = first; ok && i < a.items; i += stride) {
         const GpItem t = gp_item(a, i);
+        const int row = t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M, cols = PAIR ? a.bn / 2 : a.bn;
         for (int s = t.s0; s < t.s1; ++s) {
           if (!(ok = gp_wait(empty(slot), (turn & 1u) ^ 1u))) break;
-          mbar_expect(full(slot), bytes);
-          const uint32_t st = base + (uint32_t)(slot * a.stage);
+          if (rank == 0) mbar_expect(full(slot), (uint32_t)(PAIR ? 2 * a.bytes : a.bytes));
+          const uint32_t st = base + (uint32_t)(slot * a.stage), bar = PAIR ? of_leader(full(slot)) : full(slot);
           if (BACK) {
             const bool second = s >= a.half;
             const int x = (second ? s - a.half : s) * GP_K;
-            tma_load_2d(st, second ? &maps.a1 : &maps.a0, x, t.m * GP_M, full(slot));
-            for (int b = 0; b < a.bn; b += 64)
-              tma_load_2d(st + GP_A + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + b, x, full(slot));
+            tma_load_2d<PAIR>(st, second ? &maps.a1 : &maps.a0, x, row, bar);
+            for (int b = 0; b < cols; b += 64)
+              tma_load_2d<PAIR>(st + GP_A + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + rank * cols + b, x, bar);
           } else {
-            tma_load_2d(st, &maps.a0, s * GP_K, t.m * GP_M, full(slot));
-            tma_load_2d(st + GP_A, &maps.b0, s * GP_K, t.n * a.bn, full(slot));
-            tma_load_2d(st + GP_A + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, full(slot));
+            tma_load_2d<PAIR>(st, &maps.a0, s * GP_K, row, bar);
+            if (PAIR) {  // the first CTA has Wg's rows, the second Wu's
+              tma_load_2d<PAIR>(st + GP_A, rank ? &maps.b1 : &maps.b0, s * GP_K, t.n * a.bn, bar);
+            } else {
+              tma_load_2d<PAIR>(st + GP_A, &maps.b0, s * GP_K, t.n * a.bn, bar);
+              tma_load_2d<PAIR>(st + GP_A + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, bar);
+            }
           }
           if (++slot == a.slots) slot = 0, ++turn;
           used = min(used + 1, a.slots);
         }
       }
-      // its copies in flight write this CTA's memory: see them land
-      if (!ok)
-        for (int j = 0; j < used; ++j) {
-          if (--slot < 0) slot = a.slots - 1, --turn;
+      // Before this CTA may end: the last stages have been multiplied, and said so
+      // on its barriers; or, after a wait that ran out, its copies in flight have landed.
+      for (int j = 0; j < used; ++j) {
+        if (--slot < 0) slot = a.slots - 1, --turn;
+        if (ok)
+          ok = gp_wait(empty(slot), turn & 1u);
+        else if (rank == 0)
           gp_wait(full(slot), turn & 1u);
-        }
+        else
+          __nanosleep(100000);  // they arrive on the other CTA's barrier
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
-    if (lane == 0) {
-      // fp32 accumulator, the operands' type, N, M = 128
+    if (lane == 0 && rank == 0) {
+      // fp32 accumulator, the operands' type, N, M = 128 or 256
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (BACK ? 1u << 16 : 0u) |
-                             ((uint32_t)((BACK ? a.bn : 2 * a.bn) >> 3) << 17) | (8u << 24);
+                             ((uint32_t)((BACK ? a.bn : 2 * a.bn) >> 3) << 17) | (PAIR ? 16u << 24 : 8u << 24);
       int slot = 0;
       uint32_t turn = 0u, count = 0u;
-      for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x, ++count) {
+      for (int i = first; ok && i < a.items; i += stride, ++count) {
         const GpItem t = gp_item(a, i);
         const uint32_t acc = count & 1u;
         if (!(ok = gp_wait(acc_empty(acc), ((count >> 1) & 1u) ^ 1u))) break;
@@ -209,16 +268,16 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           const uint32_t st = base + (uint32_t)(slot * a.stage);
 #pragma unroll
           for (int j = 0; j < GP_K / 16; ++j)
-            mma_f16(tmem + 256u * acc, k_desc(st + 32u * j),
-                    BACK ? mn_desc(st + GP_A + 2048u * j, GP_K * 128) : k_desc(st + GP_A + 32u * j), idesc, s > t.s0 || j > 0);
-          mma_commit(empty(slot));
+            gp_mma<PAIR>(tmem + 256u * acc, k_desc(st + 32u * j),
+                         BACK ? mn_desc(st + GP_A + 2048u * j, GP_K * 128) : k_desc(st + GP_A + 32u * j), idesc, s > t.s0 || j > 0);
+          gp_commit<PAIR>(empty(slot));
           if (++slot == a.slots) slot = 0, ++turn;
         }
-        if (ok) mma_commit(acc_full(acc));
+        if (ok) gp_commit<PAIR>(acc_full(acc));
       }
       if (!ok) {
-        // MMAs in flight read this CTA's memory: see them end
-        mma_commit(drained);
+        // MMAs in flight read the CTAs' memory: see them end
+        gp_commit<PAIR>(drained);
         gp_wait(drained, 0);
       }
     }
@@ -227,13 +286,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     const int quad = warp & 3, side = (warp - GP_FIRST) >> 2;
     const int64_t ldc = act_ldc(a.cols);
     uint32_t count = 0u;
-    for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x, ++count) {
+    for (int i = first; ok && i < a.items; i += stride, ++count) {
       const GpItem t = gp_item(a, i);
       const uint32_t acc = count & 1u;
       if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
-      const int64_t row = (int64_t)t.m * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
+      const int64_t row = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
       for (int c = 32 * side; c < a.bn && c0 + c < a.cols; c += 64) {
         const int64_t col = c0 + c;
         const int n = (int)min((int64_t)32, a.cols - col);
@@ -271,14 +330,25 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty(acc));
+      if (lane == 0) {
+        if (PAIR)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_leader(acc_empty(acc))) : "memory");
+        else
+          mbar_arrive(acc_empty(acc));
+      }
     }
   }
   if (!ok) atomicOr(a.diag + DIAG_ERR, GC_DIAG_TIMEOUT);
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (PAIR) cluster_sync();  // neither ends, or gives its tensor memory back, while the other may reach it
+  if (warp == 1) {
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
 }
 // fp32 rows are never written by a vector of T's size.
 template <>
@@ -331,28 +401,33 @@ static bool make_map(CUtensorMap* m, int32_t dtype, const void* p, int64_t ld, i
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call is cut: the tile's width, and for the gradient the splits of its sum
-// where there are fewer tiles than SMs.
+// How a call is cut: pairs of CTAs or single ones, the tile's width, and for the
+// gradient the splits of its sum where there are fewer tiles than SMs.
 struct GpPlan {
+  bool pair;
   int bn, tiles_m, tiles_n, splits, span;
 };
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// The time of a stage goes by its bytes; a tile's fixed part is that of about six stages.
+// A stage takes the SMs 2 N clocks to multiply, and its bytes once in and once
+// out of shared memory at 128 a clock; a tile's fixed part is that of about six stages.
 static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t steps, bool back) {
   GpPlan best = {};
   double least = 0.0;
-  const int widest = back ? 256 : 128;
-  const int64_t tm = ceil_div(rows, GP_M);
-  for (int bn = widest; bn >= 32; bn -= 32) {
-    const int64_t tn = ceil_div(cols, bn), tiles = tm * tn;
-    const double stage = (16.0 + (back ? bn / 8.0 : bn / 4.0)) * 0.0084;  // us
-    const int most = back && tiles < GP_SMS ? (int)(GP_SMS / tiles < 16 ? GP_SMS / tiles : 16) : 1;
-    for (int s = 1; s <= most; ++s) {
-      const int64_t span = ceil_div(steps, s);
-      if (s > 1 && (span < 4 || ceil_div(steps, span) != s)) continue;
-      double us = (double)ceil_div(tiles * s, GP_SMS) * ((double)span + 6.0) * stage;
-      if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 8.0 / 7e6;
-      if (best.bn == 0 || us < least) best = {bn, (int)tm, (int)tn, s, (int)span}, least = us;
+  for (int pair = 0; pair < (rows > GP_M ? 2 : 1); ++pair) {
+    const int64_t tm = ceil_div(rows, pair ? 2 * GP_M : GP_M), workers = pair ? GP_SMS / 2 : GP_SMS;
+    for (int bn = back ? 256 : 128; bn >= 32; bn -= 32) {
+      if (pair && back && bn % 64 != 0) continue;
+      const int64_t tn = ceil_div(cols, bn), tiles = tm * tn;
+      const int wide = back ? bn : 2 * bn, mine = pair ? wide / 2 : wide;
+      const double bytes = 2.0 * (16384.0 + 128.0 * mine) / 128.0, mma = 2.0 * wide, stage = (bytes > mma ? bytes : mma) / 1900.0;  // us
+      const int most = back && tiles < workers ? (int)(workers / tiles < 16 ? workers / tiles : 16) : 1;
+      for (int s = 1; s <= most; ++s) {
+        const int64_t span = ceil_div(steps, s);
+        if (s > 1 && (span < 4 || ceil_div(steps, span) != s)) continue;
+        double us = (double)ceil_div(tiles * s, workers) * ((double)span + 6.0) * stage;
+        if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 8.0 / 7e6;
+        if (best.bn == 0 || us < least) best = {pair != 0, bn, (int)tm, (int)tn, s, (int)span}, least = us;
+      }
     }
   }
   return best;
@@ -396,19 +471,31 @@ static const void* align_rows(const void* x, int64_t* ld, int64_t rows, int64_t 
   return to;
 }
 
-template <typename T, int KIND>
+template <typename T, int KIND, bool PAIR>
 static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
-  auto kern = k_gated_proj<T, KIND>;
+  auto kern = k_gated_proj<T, KIND, PAIR>;
   static PerDevice ready;
   if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_RING) ? 1 : 0; })) return false;
-  launch_chained(kern, (unsigned)(a.items < GP_SMS ? a.items : GP_SMS), GP_THREADS, GP_RING, s, maps, a);
+  constexpr int WORKERS = PAIR ? GP_SMS / 2 : GP_SMS;
+  const unsigned workers = (unsigned)(a.items < WORKERS ? a.items : WORKERS);
+  launch_chained(kern, PAIR ? 2 * workers : workers, GP_THREADS, GP_RING, s, maps, a);
   return true;
 }
+template <typename T, int KIND>
+static bool launch_gp(const GpMaps& maps, const GpArgs& a, bool pair, cudaStream_t s) {
+  return pair ? launch_gp<T, KIND, true>(maps, a, s) : launch_gp<T, KIND, false>(maps, a, s);
+}
+// Rows of the copies of x, dgate and dup: no more than there are (copies of rows
+// that are not there cost as much as others).
+static int gp_box(int64_t rows) { return rows < GP_M ? (int)rows : GP_M; }
 static void set_plan(GpArgs* a, const GpPlan& p, bool back) {
   a->bn = p.bn, a->tiles_m = p.tiles_m, a->tiles_n = p.tiles_n, a->splits = p.splits, a->span = p.span;
   a->items = p.tiles_m * p.tiles_n * p.splits;
-  a->band = 16;
-  a->stage = GP_A + (back ? (p.bn + 63) / 64 * 64 : 2 * p.bn) * GP_K * 2;
+  a->band = p.pair ? 8 : 16;
+  const int wide = back ? p.bn : 2 * p.bn, mine = p.pair ? wide / 2 : wide;
+  const int columns = (back ? (mine + 63) / 64 * 64 : mine) * GP_K * 2;
+  a->bytes = gp_box(a->rows) * GP_K * 2 + columns;
+  a->stage = GP_A + columns;
   a->slots = GP_RING / a->stage < GP_SLOTS ? GP_RING / a->stage : GP_SLOTS;
 }
 static gc_status check_sizes(int64_t rows, int64_t n, int64_t k) {
@@ -466,20 +553,21 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
   if (!bulk_rows(w_up, ldwu)) w_up = align_rows(w_up, &ldwu, n, k, ws + w.weights[1], s);
   GpArgs a = {};
   a.rows = rows, a.cols = n, a.steps = a.half = (int)ceil_div(k, GP_K);
-  set_plan(&a, gp_plan(rows, n, a.steps, false), false);
+  const GpPlan p = gp_plan(rows, n, a.steps, false);
+  set_plan(&a, p, false);
   a.out = out, a.ldo = ldo, a.vec = bulk_rows(out, ldo);
   a.gcodes = gate_codes, a.ucodes = up_codes, a.gsteps = gate_steps, a.usteps = up_steps;
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;
-  if (!make_map(&maps.a0, dtype, x, ldx, rows, k, GP_M) || !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, a.bn) ||
+  if (!make_map(&maps.a0, dtype, x, ldx, rows, k, gp_box(rows)) || !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, a.bn) ||
       !make_map(&maps.b1, dtype, w_up, ldwu, n, k, a.bn))
     return GC_ERR_CUDA;
   maps.a1 = maps.a0;
   const bool silu = kind == GC_GATE_SILU;
-  const bool ok = dtype == GC_BF16 ? (silu ? launch_gp<__nv_bfloat16, GC_GATE_SILU>(maps, a, s)
-                                           : launch_gp<__nv_bfloat16, GC_GATE_GELU_TANH>(maps, a, s))
-                                   : (silu ? launch_gp<__half, GC_GATE_SILU>(maps, a, s)
-                                           : launch_gp<__half, GC_GATE_GELU_TANH>(maps, a, s));
+  const bool ok = dtype == GC_BF16 ? (silu ? launch_gp<__nv_bfloat16, GC_GATE_SILU>(maps, a, p.pair, s)
+                                           : launch_gp<__nv_bfloat16, GC_GATE_GELU_TANH>(maps, a, p.pair, s))
+                                   : (silu ? launch_gp<__half, GC_GATE_SILU>(maps, a, p.pair, s)
+                                           : launch_gp<__half, GC_GATE_GELU_TANH>(maps, a, p.pair, s));
   return ok && cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
@@ -523,10 +611,10 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   a.part = p.splits > 1 ? reinterpret_cast<float*>(ws + w.sums) : nullptr, a.ldp = gp_ldp(k);
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;
-  if (!make_map(&maps.a0, dtype, dg, lddg, rows, n, GP_M) || !make_map(&maps.a1, dtype, du, lddu, rows, n, GP_M) ||
+  if (!make_map(&maps.a0, dtype, dg, lddg, rows, n, gp_box(rows)) || !make_map(&maps.a1, dtype, du, lddu, rows, n, gp_box(rows)) ||
       !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, GP_K) || !make_map(&maps.b1, dtype, w_up, ldwu, n, k, GP_K))
     return GC_ERR_CUDA;
-  if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, s) : launch_gp<__half, GP_BACK>(maps, a, s)))
+  if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, p.pair, s) : launch_gp<__half, GP_BACK>(maps, a, p.pair, s)))
     return GC_ERR_CUDA;
   if (a.part) {
     const int64_t fours = a.ldp / 4, blocks = ceil_div(rows * fours, 256);
