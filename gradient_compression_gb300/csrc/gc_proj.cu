@@ -26,7 +26,7 @@ namespace gc {
 // swizzle, with zeros for what is outside a matrix.
 constexpr int GP_M = 128, GP_K = 64;         // rows of a tile, summed index of a stage
 constexpr int GP_A = GP_M * GP_K * 2;        // bytes of a stage's rows
-constexpr int GP_RING = 4 * (GP_A + 256 * GP_K * 2), GP_SLOTS = 8;
+constexpr int GP_RING = 4 * (GP_A + 256 * GP_K * 2), GP_SLOTS = 12;
 constexpr int GP_OUT = 8, GP_FIRST = 4;      // warps that read out, the first of them
 constexpr int GP_THREADS = (GP_FIRST + GP_OUT) * 32;
 constexpr int GP_SMS = 152;                  // of a GB300
@@ -98,12 +98,14 @@ struct GpMaps {
 struct GpArgs {
   int64_t rows, cols;          // of the result
   int half, steps;             // stages of the first pair of operands, of both
-  int bn, slots, stage, bytes; // columns of a tile, stages in the ring, room of one in a CTA, bytes that arrive in it
+  int bn, slots;               // columns of a tile, stages in the ring
+  int stage, room, bytes;      // room of a stage, of its rows (a multiple of 1024), bytes that arrive
   int tiles_m, tiles_n, splits, items, span;  // span: stages of a split
   int band;                    // tiles of a band of rows, which goes along all columns before the next one
   void* out;
   int64_t ldo;
-  bool vec;                    // rows of `out` start on 16-byte boundaries
+  int vec;                     // what rows of `out` start on, as gp_put takes it
+  bool whole, even;            // codes start on a 32-byte boundary; rows of steps on even addresses
   int8_t *gcodes, *ucodes;
   uint8_t *gsteps, *usteps;
   float* part;                 // the splits' sums, one [rows, ldp] after another
@@ -123,39 +125,72 @@ __device__ __forceinline__ GpItem gp_item(const GpArgs& a, int i) {
   return t;
 }
 
-// Codes and step of the 32 values of a group that one thread holds.
-__device__ __forceinline__ void gp_hold(const float (&v)[32], int8_t* codes, uint8_t* step) {
+// 32 bytes, which a thread has of its row, in as few stores as their address
+// allows: every thread's store is a request of its own to L2, which takes the SM 1.5
+// clocks whatever its size.
+__device__ __forceinline__ void gp_put32(void* to, const uint32_t (&w)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// The codes of the 32 values of a group that one thread holds; returns their step.
+__device__ __forceinline__ uint32_t gp_hold(const float (&v)[32], int8_t* codes, bool whole) {
   float top = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
   for (int i = 2; i < 32; i += 2) top = max_nan(top, fabsf(v[i]), fabsf(v[i + 1]));
   const uint32_t b = act_step(__float_as_uint(top));
-  uint2 q[4];
+  uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float x[CHUNK];
 #pragma unroll
     for (int e = 0; e < CHUNK; ++e) x[e] = v[8 * i + e];
-    q[i] = chunk_codes(x, b);
+    const uint2 q = chunk_codes(x, b);
+    w[2 * i] = q.x, w[2 * i + 1] = q.y;
   }
-  reinterpret_cast<uint4*>(codes)[0] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
-  reinterpret_cast<uint4*>(codes)[1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
-  *step = (uint8_t)b;
+  gp_put32(codes, w, whole);
+  return b;
 }
-// n of the 32 values of a row.
+// n of the 32 values of a row.  vec: 0 where rows start anywhere, 1 on 16-byte
+// boundaries, 2 on 32-byte ones.
 template <typename T>
-__device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, bool vec) {
+__device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, int vec) {
   if (vec && n == 32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Raw8<T> r;
+    for (int i = 0; i < 2; ++i) {
+      alignas(16) T r[16];
 #pragma unroll
-      for (int e = 0; e < CHUNK; ++e) r.e[e] = from_f32<T>(v[8 * i + e]);
-      reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<const uint4*>(&r);
+      for (int e = 0; e < 16; ++e) r[e] = from_f32<T>(v[16 * i + e]);
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint32_t*>(r)[e];
+      gp_put32(to + 16 * i, w, vec == 2);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (e < n) to[e] = from_f32<T>(v[e]);
+  }
+}
+// Sums of a split: rows on 32-byte boundaries.
+__device__ __forceinline__ void gp_put_sums(const float (&v)[32], float* to, int n) {
+  if (n == 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * i + e]);
+      gp_put32(to + 8 * i, w, true);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n) to[e] = v[e];
   }
 }
 
@@ -222,14 +257,14 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
             const int x = (second ? s - a.half : s) * GP_K;
             tma_load_2d<PAIR>(st, second ? &maps.a1 : &maps.a0, x, row, bar);
             for (int b = 0; b < cols; b += 64)
-              tma_load_2d<PAIR>(st + GP_A + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + rank * cols + b, x, bar);
+              tma_load_2d<PAIR>(st + a.room + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + rank * cols + b, x, bar);
           } else {
             tma_load_2d<PAIR>(st, &maps.a0, s * GP_K, row, bar);
             if (PAIR) {  // the first CTA has Wg's rows, the second Wu's
-              tma_load_2d<PAIR>(st + GP_A, rank ? &maps.b1 : &maps.b0, s * GP_K, t.n * a.bn, bar);
+              tma_load_2d<PAIR>(st + a.room, rank ? &maps.b1 : &maps.b0, s * GP_K, t.n * a.bn, bar);
             } else {
-              tma_load_2d<PAIR>(st + GP_A, &maps.b0, s * GP_K, t.n * a.bn, bar);
-              tma_load_2d<PAIR>(st + GP_A + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, bar);
+              tma_load_2d<PAIR>(st + a.room, &maps.b0, s * GP_K, t.n * a.bn, bar);
+              tma_load_2d<PAIR>(st + a.room + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, bar);
             }
           }
           if (++slot == a.slots) slot = 0, ++turn;
@@ -269,7 +304,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
 #pragma unroll
           for (int j = 0; j < GP_K / 16; ++j)
             gp_mma<PAIR>(tmem + 256u * acc, k_desc(st + 32u * j),
-                         BACK ? mn_desc(st + GP_A + 2048u * j, GP_K * 128) : k_desc(st + GP_A + 32u * j), idesc, s > t.s0 || j > 0);
+                         BACK ? mn_desc(st + a.room + 2048u * j, GP_K * 128) : k_desc(st + a.room + 32u * j), idesc, s > t.s0 || j > 0);
           gp_commit<PAIR>(empty(slot));
           if (++slot == a.slots) slot = 0, ++turn;
         }
@@ -293,21 +328,38 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
       const int64_t row = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
-      for (int c = 32 * side; c < a.bn && c0 + c < a.cols; c += 64) {
-        const int64_t col = c0 + c;
+      // the groups of 32 columns of this warp, next to each other
+      const int groups = (int)min((int64_t)(a.bn / 32), (a.cols - c0 + 31) / 32), half = (groups + 1) / 2;
+      const int begin = side ? half : 0, end = side ? groups : half;
+      uint32_t held = 0u;  // the steps of the group before
+      auto read_out = [&] {  // the accumulator may be written again
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_leader(acc_empty(acc))) : "memory");
+          else
+            mbar_arrive(acc_empty(acc));
+        }
+      };
+      if (begin == end) read_out();
+      for (int q = begin; q < end; ++q) {
+        const int64_t col = c0 + 32 * q;
         const int n = (int)min((int64_t)32, a.cols - col);
         float g[32];
-        tmem_load32(g, from + c);
+        tmem_load32(g, from + 32 * q);
         if constexpr (BACK) {
+          if (q + 1 == end) read_out();
           if (row < a.rows) {
             if (a.part)
-              gp_put(g, a.part + ((int64_t)t.split * a.rows + row) * a.ldp + col, n, true);
+              gp_put_sums(g, a.part + ((int64_t)t.split * a.rows + row) * a.ldp + col, n);
             else
               gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
           }
         } else {
           float u[32];
-          tmem_load32(u, from + a.bn + c);
+          tmem_load32(u, from + a.bn + 32 * q);
+          if (q + 1 == end) read_out();
           if (n < 32) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -315,8 +367,17 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
           }
           if (row < a.rows) {
             if (a.gcodes) {
-              gp_hold(g, a.gcodes + row * ldc + col, a.gsteps + row * (ldc >> 5) + (col >> 5));
-              gp_hold(u, a.ucodes + row * ldc + col, a.usteps + row * (ldc >> 5) + (col >> 5));
+              const int64_t at = row * (ldc >> 5) + (col >> 5);  // the group
+              const uint32_t bg = gp_hold(g, a.gcodes + 32 * at, a.whole), bu = gp_hold(u, a.ucodes + 32 * at, a.whole);
+              // two groups' steps at a time where they lie so
+              if (a.even && ((col >> 5) & 1) == 0 && q + 1 < end) {
+                held = bg | bu << 16;
+              } else if (a.even && ((col >> 5) & 1) != 0 && q > begin) {
+                *reinterpret_cast<uint16_t*>(a.gsteps + at - 1) = (uint16_t)((held & 255u) | bg << 8);
+                *reinterpret_cast<uint16_t*>(a.usteps + at - 1) = (uint16_t)(held >> 16 | bu << 8);
+              } else {
+                a.gsteps[at] = (uint8_t)bg, a.usteps[at] = (uint8_t)bu;
+              }
             }
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -327,14 +388,6 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
           }
         }
         __syncwarp();
-      }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_leader(acc_empty(acc))) : "memory");
-        else
-          mbar_arrive(acc_empty(acc));
       }
     }
   }
@@ -350,19 +403,6 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
-// fp32 rows are never written by a vector of T's size.
-template <>
-__device__ __forceinline__ void gp_put<float>(const float (&v)[32], float* to, int n, bool) {
-  if (n == 32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) reinterpret_cast<float4*>(to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < n) to[e] = v[e];
-  }
-}
-
 // dx = the splits' sums in their order, four columns per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) k_gated_proj_join(const float4* part, int splits, int64_t rows, int64_t cols,
@@ -382,12 +422,134 @@ __global__ void __launch_bounds__(256) k_gated_proj_join(const float4* part, int
   }
 }
 
-// A copy whose rows start on 16-byte boundaries, of 16-bit elements.
-__global__ void __launch_bounds__(256) k_align_rows(const uint16_t* x, int64_t ld, int64_t rows, int64_t cols, uint16_t* to,
-                                                    int64_t ldt) {
+// Copies whose rows start on 16-byte boundaries, of up to three matrices of
+// 16-bit elements with as many columns each, one after another along the grid's z.
+struct GpAlign {
+  const void* from[3];
+  void* to[3];
+  int64_t ld[3], rows[3];
+  int count;
+};
+__global__ void __launch_bounds__(256, 4) k_align_rows(const GpAlign a, Tiling t, int64_t ldt) {
+  using B = __nv_bfloat16;  // any 16 bits: they go through fp32's upper half and back
+  constexpr int AHEAD = 8;
+  __shared__ float4 shared[Rows<B, true>::bytes(AHEAD, 256) / 16];
   chain_wait();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ldt + c] = x[r * ld + c];
+  const int z = blockIdx.z;
+  t.rows = a.rows[z];
+  const Place p = place(t);
+  const int64_t ld = a.ld[z];
+  Rows<B, true> in(shared, 256, static_cast<const B*>(a.from[z]) + p.r * ld, p.step * ld, p.c8, p.n, t.cols);
+  B* to = static_cast<B*>(a.to[z]) + p.r * ldt + (int64_t)p.c8 * CHUNK;
+  int64_t r = p.r, next = p.r;
+  auto copy = [&](int slot) {
+    in.copy(slot, next < p.end);
+    copy_group();
+    next += p.step;
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
+  int slot = 0;
+  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step, to += p.step * ldt) {
+    float v[CHUNK];
+    wait_groups<AHEAD - 2>();
+    in.landed();
+    in.take(slot, r < p.end ? p.n : 0, v);
+    in.done();
+    copy((slot + AHEAD - 1) % AHEAD);
+    slot = (slot + 1) % AHEAD;
+    uint32_t x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+    if (r < p.end && (int64_t)p.c8 * CHUNK < ldt) *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// ---------------------------------------------------------------- one row
+// The projection of one row reads its weights once and does little else: a warp
+// per two columns of out streams their four rows of weights, 8 elements a lane,
+// through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
+// then over the lanes.  14336 x 4096 in bf16 takes 35.5 us (6.6 TB/s) and 4096 x 1024
+// 4.8; the tensor cores' kernel, whose copies take longer to get going, 39.0 and 8.4.
+// (Two rows take 40.4 us this way, for the registers of their sums, and 39.0 there.)
+// SPAN: rows of weights or of x that do not start on 16-byte boundaries.
+template <typename T, bool SPAN>
+struct Eight {  // 8 elements of a row from column c on, zeros past its end
+  static constexpr int N = SPAN ? 2 : 1;
+  uint4 w[N];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t k, bool stream) {
+    const T* const at = row + c;
+    const int skip = SPAN ? (int)((uintptr_t)at & 15u) : 0;
+    const int64_t bytes = skip + 2 * min((int64_t)CHUNK, k - c);  // of granules, from the first one on
+    const uint4* const from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(at) - skip);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (k - c > 0 && bytes > 16 * i) w[i] = stream ? __ldcs(from + i) : __ldg(from + i);
+    }
+  }
+  __device__ __forceinline__ void take(const T* row, int64_t c, int64_t k, float (&v)[CHUNK]) const {
+    uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[N - 1].x, w[N - 1].y, w[N - 1].z, w[N - 1].w};
+    if (SPAN) shift_words<4>(x, (int)((uintptr_t)(row + c) & 15u));
+    Raw8<T> r;
+    *reinterpret_cast<uint4*>(&r) = make_uint4(x[0], x[1], x[2], x[3]);
+    unpack(r, v);
+    if (k - c < CHUNK) {
+#pragma unroll
+      for (int e = 0; e < CHUNK; ++e)
+        if (e >= k - c) v[e] = 0.0f;
+    }
+  }
+};
+template <typename T, int KIND, bool SPAN>
+__global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu, int64_t n,
+                                                           int64_t k, T* out, uint32_t* diag) {
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
+  const int lane = threadIdx.x & 31;
+  const int64_t j = 2 * ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5));
+  if (j >= n) return;
+  const int64_t j1 = min(j + 1, n - 1);
+  const T* const w[4] = {wg + j * ldwg, wg + j1 * ldwg, wu + j * ldwu, wu + j1 * ldwu};
+  F2 sum[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
+  constexpr int STEPS = SPAN ? 1 : 2;  // steps whose loads are in flight together
+  for (int64_t c0 = 8 * lane; c0 < k; c0 += 256 * STEPS) {
+    Eight<T, SPAN> ws[STEPS][4], xs[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ws[s][i].load(w[i], c0 + 256 * s, k, true);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) xs[s].load(x, c0 + 256 * s, k, false);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int64_t c = c0 + 256 * s;
+      float xv[CHUNK];
+      xs[s].take(x, c, k, xv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float wv[CHUNK];
+        ws[s][i].take(w[i], c, k, wv);
+#pragma unroll
+        for (int e = 0; e < CHUNK; e += 2) sum[i] = fma2(get2(wv + e), get2(xv + e), sum[i]);
+      }
+    }
+  }
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float two[2];
+    put2(two, sum[i]);
+    v[i] = __fadd_rn(two[0], two[1]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v[i] = __fadd_rn(v[i], __shfl_xor_sync(FULL, v[i], d));
+  }
+  if (lane == 0) {
+    F2 dp;
+    put2(v, mul2(mul2(get2(v), gate_sigmoid2<KIND>(v, &dp)), get2(v + 2)));
+    out[j] = from_f32<T>(v[0]);
+    if (j + 1 < n) out[j + 1] = from_f32<T>(v[1]);
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -432,7 +594,7 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t steps, bool back) {
   }
   return best;
 }
-static int64_t gp_ldp(int64_t cols) { return (cols + 3) / 4 * 4; }
+static int64_t gp_ldp(int64_t cols) { return (cols + 7) / 8 * 8; }
 static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 // Workspace: the diagnostic words, the aligned copies, the splits' sums (there are
@@ -461,14 +623,32 @@ static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, boo
   w.bytes = at;
   return w;
 }
+static int put_width(const void* p, int64_t ld) {
+  return !(aligned16(p) && ld % 8 == 0) ? 0 : ((uintptr_t)p & 31u) == 0u && ld % 16 == 0 ? 2 : 1;
+}
 static bool bulk_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
 
-static const void* align_rows(const void* x, int64_t* ld, int64_t rows, int64_t cols, unsigned char* to, cudaStream_t s) {
-  const int64_t ldt = gp_ld(cols);
-  launch_chained(k_align_rows, (unsigned)(rows < GP_SMS * 8 ? rows : GP_SMS * 8), 256, 0, s, static_cast<const uint16_t*>(x), *ld,
-                 rows, cols, reinterpret_cast<uint16_t*>(to), ldt);
-  *ld = ldt;
-  return to;
+// Adds a matrix to those that are copied, and takes its copy in its place.
+static void add_copy(GpAlign* l, const void** x, int64_t* ld, int64_t rows, int64_t cols, unsigned char* to) {
+  l->from[l->count] = *x, l->to[l->count] = to, l->ld[l->count] = *ld, l->rows[l->count] = rows, ++l->count;
+  *x = to, *ld = gp_ld(cols);
+}
+static void align_rows(const GpAlign& l, int64_t cols, cudaStream_t s) {
+  if (l.count == 0) return;
+  int64_t rows = 0;
+  for (int i = 0; i < l.count; ++i) rows = l.rows[i] > rows ? l.rows[i] : rows;
+  dim3 grid;
+  const Tiling t = make_tiling(rows, cols, true, resident<&k_align_rows>(), &grid);
+  grid.z = (unsigned)l.count;
+  launch_chained(k_align_rows, grid, 256, 0, s, l, t, gp_ld(cols));
+}
+
+template <typename T, int KIND>
+static void launch_row(const void* x, const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int64_t n, int64_t k, void* out,
+                       bool span, uint32_t* diag, cudaStream_t s) {
+  launch_chained(span ? &k_gated_proj_row<T, KIND, true> : &k_gated_proj_row<T, KIND, false>, (unsigned)ceil_div(n, 16), 256, 0, s,
+                 static_cast<const T*>(x), static_cast<const T*>(wg), ldwg, static_cast<const T*>(wu), ldwu, n, k,
+                 static_cast<T*>(out), diag);
 }
 
 template <typename T, int KIND, bool PAIR>
@@ -495,7 +675,8 @@ static void set_plan(GpArgs* a, const GpPlan& p, bool back) {
   const int wide = back ? p.bn : 2 * p.bn, mine = p.pair ? wide / 2 : wide;
   const int columns = (back ? (mine + 63) / 64 * 64 : mine) * GP_K * 2;
   a->bytes = gp_box(a->rows) * GP_K * 2 + columns;
-  a->stage = GP_A + columns;
+    a->room = (gp_box(a->rows) * GP_K * 2 + 1023) / 1024 * 1024;
+  a->stage = a->room + columns;
   a->slots = GP_RING / a->stage < GP_SLOTS ? GP_RING / a->stage : GP_SLOTS;
 }
 static gc_status check_sizes(int64_t rows, int64_t n, int64_t k) {
@@ -548,22 +729,32 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* const ws = static_cast<unsigned char*>(workspace);
   if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
-  if (copied & GC_COPY_ROWS) x = align_rows(x, &ldx, rows, k, ws + w.rows[0], s);
-  if (!bulk_rows(w_gate, ldwg)) w_gate = align_rows(w_gate, &ldwg, n, k, ws + w.weights[0], s);
-  if (!bulk_rows(w_up, ldwu)) w_up = align_rows(w_up, &ldwu, n, k, ws + w.weights[1], s);
+  const bool silu = kind == GC_GATE_SILU;
+  if (rows == 1 && !gate_codes) {
+    const auto launch = dtype == GC_BF16 ? (silu ? &launch_row<__nv_bfloat16, GC_GATE_SILU> : &launch_row<__nv_bfloat16, GC_GATE_GELU_TANH>)
+                                         : (silu ? &launch_row<__half, GC_GATE_SILU> : &launch_row<__half, GC_GATE_GELU_TANH>);
+    launch(x, w_gate, ldwg, w_up, ldwu, n, k, out, copied != 0, reinterpret_cast<uint32_t*>(ws), s);
+    return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+  }
+  GpAlign copies = {};
+  if (copied & GC_COPY_ROWS) add_copy(&copies, &x, &ldx, rows, k, ws + w.rows[0]);
+  if (!bulk_rows(w_gate, ldwg)) add_copy(&copies, &w_gate, &ldwg, n, k, ws + w.weights[0]);
+  if (!bulk_rows(w_up, ldwu)) add_copy(&copies, &w_up, &ldwu, n, k, ws + w.weights[1]);
+  align_rows(copies, k, s);
   GpArgs a = {};
   a.rows = rows, a.cols = n, a.steps = a.half = (int)ceil_div(k, GP_K);
   const GpPlan p = gp_plan(rows, n, a.steps, false);
   set_plan(&a, p, false);
-  a.out = out, a.ldo = ldo, a.vec = bulk_rows(out, ldo);
+  a.out = out, a.ldo = ldo, a.vec = put_width(out, ldo);
   a.gcodes = gate_codes, a.ucodes = up_codes, a.gsteps = gate_steps, a.usteps = up_steps;
+  a.whole = (((uintptr_t)gate_codes | (uintptr_t)up_codes) & 31u) == 0u;
+  a.even = (((uintptr_t)gate_steps | (uintptr_t)up_steps | (uintptr_t)(act_ldc(n) >> 5)) & 1u) == 0u;
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;
   if (!make_map(&maps.a0, dtype, x, ldx, rows, k, gp_box(rows)) || !make_map(&maps.b0, dtype, w_gate, ldwg, n, k, a.bn) ||
       !make_map(&maps.b1, dtype, w_up, ldwu, n, k, a.bn))
     return GC_ERR_CUDA;
   maps.a1 = maps.a0;
-  const bool silu = kind == GC_GATE_SILU;
   const bool ok = dtype == GC_BF16 ? (silu ? launch_gp<__nv_bfloat16, GC_GATE_SILU>(maps, a, p.pair, s)
                                            : launch_gp<__nv_bfloat16, GC_GATE_GELU_TANH>(maps, a, p.pair, s))
                                    : (silu ? launch_gp<__half, GC_GATE_SILU>(maps, a, p.pair, s)
@@ -599,15 +790,18 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   unsigned char* const ws = static_cast<unsigned char*>(workspace);
   if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
   const void *dg = dgate, *du = dup;
-  if (!bulk_rows(dg, lddg)) dg = align_rows(dg, &lddg, rows, n, ws + w.rows[0], s);
-  if (!bulk_rows(du, lddu)) du = align_rows(du, &lddu, rows, n, ws + w.rows[1], s);
-  if (!bulk_rows(w_gate, ldwg)) w_gate = align_rows(w_gate, &ldwg, n, k, ws + w.weights[0], s);
-  if (!bulk_rows(w_up, ldwu)) w_up = align_rows(w_up, &ldwu, n, k, ws + w.weights[1], s);
+  GpAlign rows_copies = {}, weights_copies = {};
+  if (!bulk_rows(dg, lddg)) add_copy(&rows_copies, &dg, &lddg, rows, n, ws + w.rows[0]);
+  if (!bulk_rows(du, lddu)) add_copy(&rows_copies, &du, &lddu, rows, n, ws + w.rows[1]);
+  if (!bulk_rows(w_gate, ldwg)) add_copy(&weights_copies, &w_gate, &ldwg, n, k, ws + w.weights[0]);
+  if (!bulk_rows(w_up, ldwu)) add_copy(&weights_copies, &w_up, &ldwu, n, k, ws + w.weights[1]);
+  align_rows(rows_copies, n, s);
+  align_rows(weights_copies, k, s);
   GpArgs a = {};
   a.rows = rows, a.cols = k, a.half = (int)ceil_div(n, GP_K), a.steps = 2 * a.half;
   const GpPlan p = gp_plan(rows, k, a.steps, true);
   set_plan(&a, p, true);
-  a.out = dx, a.ldo = lddx, a.vec = bulk_rows(dx, lddx);
+  a.out = dx, a.ldo = lddx, a.vec = put_width(dx, lddx);
   a.part = p.splits > 1 ? reinterpret_cast<float*>(ws + w.sums) : nullptr, a.ldp = gp_ldp(k);
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;

@@ -98,7 +98,7 @@ def check_held(ck, value, error):
 
 # (rows, n, k): one token to several tiles, one stage to several rings, widths around every tile's
 SHAPES = [(1, 1, 1), (1, 32, 64), (2, 33, 65), (5, 31, 7), (77, 333, 1001), (128, 128, 128), (129, 257, 320), (1, 4096, 1024),
-          (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136)]
+          (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
