@@ -32,16 +32,29 @@ constexpr int GP_THREADS = (GP_FIRST + GP_OUT) * 32;
 constexpr int GP_SMS = 152;                  // of a GB300
 constexpr int GP_POLLS = 1 << 22;            // limit of every wait
 
-__device__ __forceinline__ bool gp_wait(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < GP_POLLS; ++i)
-    if (mbar_poll(bar, parity)) return true;
-  return false;
+// All lanes of a warp, which go on or give up together.  (Without a time to be
+// suspended for, which costs 40 clocks where the phase is complete already.)
+__device__ __forceinline__ bool gp_poll(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0u;
 }
-// All lanes of a warp, which go on or give up together.
 __device__ __forceinline__ bool gp_wait_warp(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < GP_POLLS; ++i)
-    if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
+    if (__all_sync(FULL, gp_poll(bar, parity))) return true;
   return false;
+}
+// One lane of a warp that is all there, always the same.  What a whole warp goes
+// through, and one lane of it issues, is issued from uniform registers: with a
+// branch for lane 0 a stage's four MMAs took 561 clocks to issue, now 380.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(p)::"memory");
+  return p != 0u;
 }
 // (The barrier may be the other CTA's of a pair.)
 template <bool PAIR>
@@ -71,19 +84,25 @@ __device__ __forceinline__ void gp_mma(uint32_t d, uint64_t a, uint64_t b, uint3
     mma_f16(d, a, b, idesc, add);
 }
 template <bool PAIR>
-__device__ __forceinline__ void gp_commit(uint32_t bar) {
+__device__ __forceinline__ void gp_commit(uint32_t bar, int leader) {
   if (PAIR)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3 << leader))
         : "memory");
   else
     mma_commit(bar);
 }
-__device__ __forceinline__ uint32_t of_leader(uint32_t addr) {
+// The same shared memory of another CTA of the cluster.
+__device__ __forceinline__ uint32_t of_cta(uint32_t addr, int cta) {
   uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
   return r;
+}
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -108,8 +127,6 @@ struct GpArgs {
   bool whole, even;            // codes start on a 32-byte boundary; rows of steps on even addresses
   int8_t *gcodes, *ucodes;
   uint8_t *gsteps, *usteps;
-  float* part;                 // the splits' sums, one [rows, ldp] after another
-  int64_t ldp;
   uint32_t* diag;
 };
 struct GpItem {
@@ -177,37 +194,60 @@ __device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, int v
       if (e < n) to[e] = from_f32<T>(v[e]);
   }
 }
-// Sums of a split: rows on 32-byte boundaries.
-__device__ __forceinline__ void gp_put_sums(const float (&v)[32], float* to, int n) {
-  if (n == 32) {
+// The groups of 32 columns of a tile that are there.
+__device__ __forceinline__ int gp_groups(const GpArgs& a, int n) {
+  return (int)min((int64_t)(a.bn / 32), (a.cols - (int64_t)n * a.bn + 31) / 32);
+}
+constexpr int GP_BACK = -1;
+// What a thread does with the sums of 32 columns, from `col` on, of its row: the gradient's as
+// they are; the projections' through the checkpoints and the activation.  held: the steps of the
+// group before, where this warp had that one (after) and two groups' steps are
+// written at a time; next: it has the next one, too.
+template <typename T, int KIND, int U>
+__device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row, int64_t col, float (&g)[32], float (&u)[U], uint32_t* held,
+                                          bool after, bool next) {
+  const int n = (int)min((int64_t)32, a.cols - col);
+  if constexpr (KIND != GP_BACK) {
+    if (n < 32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * i + e]);
-      gp_put32(to + 8 * i, w, true);
+      for (int e = 0; e < 32; ++e)
+        if (e >= n) g[e] = u[e] = 0.0f;
     }
-  } else {
+    if (a.gcodes) {
+      const int64_t at = row * (act_ldc(a.cols) >> 5) + (col >> 5);  // the group
+      const bool odd = ((col >> 5) & 1) != 0;
+      const uint32_t bg = gp_hold(g, a.gcodes + 32 * at, a.whole), bu = gp_hold(u, a.ucodes + 32 * at, a.whole);
+      if (a.even && !odd && next) {
+        *held = bg | bu << 16;
+      } else if (a.even && odd && after) {
+        *reinterpret_cast<uint16_t*>(a.gsteps + at - 1) = (uint16_t)((*held & 255u) | bg << 8);
+        *reinterpret_cast<uint16_t*>(a.usteps + at - 1) = (uint16_t)(*held >> 16 | bu << 8);
+      } else {
+        a.gsteps[at] = (uint8_t)bg, a.usteps[at] = (uint8_t)bu;
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < n) to[e] = v[e];
+    for (int e = 0; e < 32; e += 2) {
+      F2 dp;
+      put2(g + e, mul2(mul2(get2(g + e), gate_sigmoid2<KIND>(g + e, &dp)), get2(u + e)));
+    }
   }
+  gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
 }
 
 // KIND: the activation; GP_BACK: the gradient.  PAIR: a cluster of two CTAs
 // computes a tile of 256 rows, half of them each; the first one's thread issues
 // the MMAs of both, which read each CTA's rows and half of the columns' operand out
 // of its own memory.
-constexpr int GP_BACK = -1;
 template <typename T, int KIND, bool PAIR>
-__global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREADS, 1)
+__global__ void __launch_bounds__(GP_THREADS, 1)
     k_gated_proj(const __grid_constant__ GpMaps maps, const __grid_constant__ GpArgs a) {
   constexpr bool BACK = KIND == GP_BACK;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * GP_SLOTS + 5];
+  __shared__ __align__(8) uint64_t bars[2 * GP_SLOTS + 6];
   __shared__ uint32_t tmem_base;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;
+  const int warp = __shfl_sync(FULL, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (a uniform register)
+  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0, leader = PAIR ? cluster_rank() & ~1 : 0;
   const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };                            // of the first CTA: both CTAs' copies are there
@@ -215,11 +255,15 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
   auto acc_full = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + h); };       // an accumulator's MMAs are done
   auto acc_empty = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + 2 + h); };  // of the first CTA: it has been read out
   const uint32_t drained = bar0 + 8u * (2 * GP_SLOTS + 4);                     // all MMAs are done, after a wait that ran out
+  const uint32_t joined = drained + 8u;                                        // the other splits' sums are here
 
+  if (warp == 2 && elected()) {
+    for (const CUtensorMap* m : {&maps.a0, &maps.a1, &maps.b0, &maps.b1}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < GP_SLOTS; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
     for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), PAIR ? 2 * GP_OUT : GP_OUT);
-    mbar_init(drained, 1);
+    mbar_init(drained, 1), mbar_init(joined, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -233,25 +277,25 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (PAIR) cluster_sync();
+  if (PAIR || a.splits > 1) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = __shfl_sync(FULL, tmem_base, 0);
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) a.diag[threadIdx.x] = 0u;  // all that the status call reads
 
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------ operands
-    if (lane == 0) {
-      int slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
-      uint32_t turn = 0u;
-      for (int i = first; ok && i < a.items; i += stride) {
-        const GpItem t = gp_item(a, i);
-        const int row = t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M, cols = PAIR ? a.bn / 2 : a.bn;
-        for (int s = t.s0; s < t.s1; ++s) {
-          if (!(ok = gp_wait(empty(slot), (turn & 1u) ^ 1u))) break;
+    int slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
+    uint32_t turn = 0u;
+    for (int i = first; ok && i < a.items; i += stride) {
+      const GpItem t = gp_item(a, i);
+      const int row = t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M, cols = PAIR ? a.bn / 2 : a.bn;
+      for (int s = t.s0; s < t.s1; ++s) {
+        if (!(ok = gp_wait_warp(empty(slot), (turn & 1u) ^ 1u))) break;
+        const uint32_t st = base + (uint32_t)(slot * a.stage), bar = PAIR ? of_cta(full(slot), leader) : full(slot);
+        if (elected()) {
           if (rank == 0) mbar_expect(full(slot), (uint32_t)(PAIR ? 2 * a.bytes : a.bytes));
-          const uint32_t st = base + (uint32_t)(slot * a.stage), bar = PAIR ? of_leader(full(slot)) : full(slot);
           if (BACK) {
             const bool second = s >= a.half;
             const int x = (second ? s - a.half : s) * GP_K;
@@ -267,25 +311,26 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
               tma_load_2d<PAIR>(st + a.room + a.bn * (GP_K * 2), &maps.b1, s * GP_K, t.n * a.bn, bar);
             }
           }
-          if (++slot == a.slots) slot = 0, ++turn;
-          used = min(used + 1, a.slots);
         }
+        __syncwarp();
+        if (++slot == a.slots) slot = 0, ++turn;
+        used = min(used + 1, a.slots);
       }
-      // Before this CTA may end: the last stages have been multiplied, and said so
-      // on its barriers; or, after a wait that ran out, its copies in flight have landed.
-      for (int j = 0; j < used; ++j) {
-        if (--slot < 0) slot = a.slots - 1, --turn;
-        if (ok)
-          ok = gp_wait(empty(slot), turn & 1u);
-        else if (rank == 0)
-          gp_wait(full(slot), turn & 1u);
-        else
-          __nanosleep(100000);  // they arrive on the other CTA's barrier
-      }
+    }
+    // Before this CTA may end: the last stages have been multiplied, and said so
+    // on its barriers; or, after a wait that ran out, its copies in flight have landed.
+    for (int j = 0; j < used; ++j) {
+      if (--slot < 0) slot = a.slots - 1, --turn;
+      if (ok)
+        ok = gp_wait_warp(empty(slot), turn & 1u);
+      else if (rank == 0)
+        gp_wait_warp(full(slot), turn & 1u);
+      else
+        __nanosleep(100000);  // they arrive on the other CTA's barrier
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // fp32 accumulator, the operands' type, N, M = 128 or 256
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (BACK ? 1u << 16 : 0u) |
@@ -295,31 +340,33 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
       for (int i = first; ok && i < a.items; i += stride, ++count) {
         const GpItem t = gp_item(a, i);
         const uint32_t acc = count & 1u;
-        if (!(ok = gp_wait(acc_empty(acc), ((count >> 1) & 1u) ^ 1u))) break;
+        if (!(ok = gp_wait_warp(acc_empty(acc), ((count >> 1) & 1u) ^ 1u))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int s = t.s0; s < t.s1; ++s) {
-          if (!(ok = gp_wait(full(slot), turn & 1u))) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t st = base + (uint32_t)(slot * a.stage);
+          // (what was copied is ordered by the barrier alone)
+          if (!(ok = gp_wait_warp(full(slot), turn & 1u))) break;
+          const uint32_t st = base + (uint32_t)(slot * a.stage), d = tmem + 256u * acc;
+          const uint64_t da = k_desc(st), db = BACK ? mn_desc(st + a.room, GP_K * 128) : k_desc(st + a.room);
+          if (elected()) {
+            gp_mma<PAIR>(d, da, db, idesc, s > t.s0);
 #pragma unroll
-          for (int j = 0; j < GP_K / 16; ++j)
-            gp_mma<PAIR>(tmem + 256u * acc, k_desc(st + 32u * j),
-                         BACK ? mn_desc(st + a.room + 2048u * j, GP_K * 128) : k_desc(st + a.room + 32u * j), idesc, s > t.s0 || j > 0);
-          gp_commit<PAIR>(empty(slot));
+            for (int j = 1; j < GP_K / 16; ++j) gp_mma<PAIR>(d, da + 2u * j, db + (BACK ? 128u : 2u) * j, idesc, true);
+            gp_commit<PAIR>(empty(slot), leader);
+            if (s + 1 == t.s1) gp_commit<PAIR>(acc_full(acc), leader);
+          }
+          __syncwarp();
           if (++slot == a.slots) slot = 0, ++turn;
         }
-        if (ok) gp_commit<PAIR>(acc_full(acc));
       }
       if (!ok) {
         // MMAs in flight read the CTAs' memory: see them end
-        gp_commit<PAIR>(drained);
-        gp_wait(drained, 0);
+        if (elected()) gp_commit<PAIR>(drained, leader);
+        gp_wait_warp(drained, 0);
       }
     }
   } else if (warp >= GP_FIRST) {
     // ------------------------------------------------ result
     const int quad = warp & 3, side = (warp - GP_FIRST) >> 2;
-    const int64_t ldc = act_ldc(a.cols);
     uint32_t count = 0u;
     for (int i = first; ok && i < a.items; i += stride, ++count) {
       const GpItem t = gp_item(a, i);
@@ -327,66 +374,112 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
       if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
+      if (a.splits > 1) break;  // the tile's only one: below
       const int64_t row = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
       // the groups of 32 columns of this warp, next to each other
-      const int groups = (int)min((int64_t)(a.bn / 32), (a.cols - c0 + 31) / 32), half = (groups + 1) / 2;
+      const int groups = gp_groups(a, t.n), half = (groups + 1) / 2;
       const int begin = side ? half : 0, end = side ? groups : half;
       uint32_t held = 0u;  // the steps of the group before
       auto read_out = [&] {  // the accumulator may be written again
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
+          // (at the scope of the CTA: what is to be ordered is in tensor memory, by the
+          // fence above; a release to the cluster waits 2000 clocks for this thread's stores)
           if (PAIR)
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_leader(acc_empty(acc))) : "memory");
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_cta(acc_empty(acc), leader)) : "memory");
           else
             mbar_arrive(acc_empty(acc));
         }
       };
       if (begin == end) read_out();
       for (int q = begin; q < end; ++q) {
-        const int64_t col = c0 + 32 * q;
-        const int n = (int)min((int64_t)32, a.cols - col);
-        float g[32];
+        float g[32], u[BACK ? 1 : 32];
         tmem_load32(g, from + 32 * q);
-        if constexpr (BACK) {
-          if (q + 1 == end) read_out();
-          if (row < a.rows) {
-            if (a.part)
-              gp_put_sums(g, a.part + ((int64_t)t.split * a.rows + row) * a.ldp + col, n);
-            else
-              gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
-          }
-        } else {
-          float u[32];
-          tmem_load32(u, from + a.bn + 32 * q);
-          if (q + 1 == end) read_out();
-          if (n < 32) {
+        if constexpr (!BACK) tmem_load32(u, from + a.bn + 32 * q);
+        if (q + 1 == end) read_out();
+        if (row < a.rows) gp_finish<T, KIND>(a, row, c0 + 32 * q, g, u, &held, q > begin, q + 1 < end);
+        __syncwarp();
+      }
+    }
+  }
+  if (a.splits > 1) {
+    // The cluster's CTAs (pairs) have summed a part of the tile each, and end together
+    // here.  Group q of its columns is finished by split q % splits: the others
+    // send it their sums, and it adds them in the splits' order.  They go by bulk
+    // copies from ring to ring, which nothing else reads or writes any more when all are
+    // here: what arrives first, what leaves behind it, 4 KB (32 rows) of a block by
+    // each warp.  (Stored by the threads themselves, a row each, 64 KB took 9500 clocks.)
+    const GpItem t = gp_item(a, first);
+    const int quad = warp & 3, side = (warp - GP_FIRST) >> 2, groups = gp_groups(a, t.n), most = (groups + a.splits - 1) / a.splits;
+    constexpr uint32_t BLOCK = GP_M * 128;  // 32 columns of a CTA's rows
+    constexpr int BLOCKS = BACK ? 1 : 2;
+    const uint32_t here = (uint32_t)(32 * quad) * 128u;  // of a warp's part of a block
+    const uint32_t row128 = here + (uint32_t)lane * 128u;
+    if (threadIdx.x == 0)
+      mbar_expect(joined, (uint32_t)((groups - t.split + a.splits - 1) / a.splits * (a.splits - 1)) * (BLOCKS * BLOCK));
+    __syncwarp();
+    cluster_sync();
+    const bool mine = warp >= GP_FIRST && ok;
+    const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
+    // where split `of` puts its sums of the owner's group q
+    auto block = [&](int q, int owner, int of) { return (uint32_t)((q / a.splits) * (a.splits - 1) + of - (of > owner)) * (BLOCKS * BLOCK); };
+    if (mine) {
+      for (int q = side; q < groups; q += 2) {
+        const int owner = q % a.splits, cta = PAIR ? 2 * owner + rank : owner;
+        if (owner == t.split) continue;
+        const int sent = q - (q + a.splits - 1 - t.split) / a.splits;  // of the groups of others
+        const uint32_t src = base + (uint32_t)(most * (a.splits - 1) + sent) * (BLOCKS * BLOCK), dst = base + block(q, owner, t.split);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e >= n) g[e] = u[e] = 0.0f;
-          }
-          if (row < a.rows) {
-            if (a.gcodes) {
-              const int64_t at = row * (ldc >> 5) + (col >> 5);  // the group
-              const uint32_t bg = gp_hold(g, a.gcodes + 32 * at, a.whole), bu = gp_hold(u, a.ucodes + 32 * at, a.whole);
-              // two groups' steps at a time where they lie so
-              if (a.even && ((col >> 5) & 1) == 0 && q + 1 < end) {
-                held = bg | bu << 16;
-              } else if (a.even && ((col >> 5) & 1) != 0 && q > begin) {
-                *reinterpret_cast<uint16_t*>(a.gsteps + at - 1) = (uint16_t)((held & 255u) | bg << 8);
-                *reinterpret_cast<uint16_t*>(a.usteps + at - 1) = (uint16_t)(held >> 16 | bu << 8);
-              } else {
-                a.gsteps[at] = (uint8_t)bg, a.usteps[at] = (uint8_t)bu;
+        for (int b = 0; b < BLOCKS; ++b) {
+          float v[32];
+          tmem_load32(v, from + 32 * q + (b ? a.bn : 0));
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared16(src + b * BLOCK + row128 + (uint32_t)((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                        __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (elected())
+            asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 4096, [%2];" ::"r"(
+                             of_cta(dst + b * BLOCK + here, cta)),
+                         "r"(src + b * BLOCK + here), "r"(of_cta(joined, cta))
+                         : "memory");
+          __syncwarp();
+        }
+      }
+      ok = gp_wait_warp(joined, 0u);
+    }
+    if (mine && ok) {
+      const uint32_t at = base + row128;
+      const int64_t row = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad + lane;
+      for (int q = t.split + side * a.splits; q < groups; q += 2 * a.splits) {
+        float sum[BLOCKS][32];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+          float own[32];
+          tmem_load32(own, from + 32 * q + (b ? a.bn : 0));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sum[b][e] = t.split == 0 ? own[e] : 0.0f;
+          for (int p = 0; p < a.splits; ++p) {
+            if (p == t.split) {
+              if (p > 0) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sum[b][e] = __fadd_rn(sum[b][e], own[e]);
               }
+              continue;
             }
+            const uint32_t src = at + block(q, t.split, p) + b * BLOCK;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              F2 dp;
-              put2(g + e, mul2(mul2(get2(g + e), gate_sigmoid2<KIND>(g + e, &dp)), get2(u + e)));
+            for (int c = 0; c < 8; ++c) {
+              const uint4 x = shared16(src + (uint32_t)((c ^ (lane & 7)) << 4));
+              sum[b][4 * c] = __fadd_rn(sum[b][4 * c], __uint_as_float(x.x)), sum[b][4 * c + 1] = __fadd_rn(sum[b][4 * c + 1], __uint_as_float(x.y));
+              sum[b][4 * c + 2] = __fadd_rn(sum[b][4 * c + 2], __uint_as_float(x.z)), sum[b][4 * c + 3] = __fadd_rn(sum[b][4 * c + 3], __uint_as_float(x.w));
             }
-            gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
           }
         }
+        uint32_t held = 0u;
+        if (row < a.rows) gp_finish<T, KIND>(a, row, (int64_t)t.n * a.bn + 32 * q, sum[0], sum[BLOCKS - 1], &held, false, false);
         __syncwarp();
       }
     }
@@ -395,7 +488,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (PAIR) cluster_sync();  // neither ends, or gives its tensor memory back, while the other may reach it
+  if (PAIR || a.splits > 1) cluster_sync();  // none ends, or gives its tensor memory back, while another may reach it
   if (warp == 1) {
     if (PAIR)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -403,25 +496,6 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(GP_THREAD
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
-// dx = the splits' sums in their order, four columns per thread.
-template <typename T>
-__global__ void __launch_bounds__(256) k_gated_proj_join(const float4* part, int splits, int64_t rows, int64_t cols,
-                                                         int64_t fours, T* out, int64_t ldo) {
-  chain_wait();
-  const int64_t total = rows * fours;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / fours, c = (i - r * fours) * 4;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = 0; p < splits; ++p) {
-      const float4 v = __ldg(part + p * total + i);
-      s[0] = __fadd_rn(s[0], v.x), s[1] = __fadd_rn(s[1], v.y), s[2] = __fadd_rn(s[2], v.z), s[3] = __fadd_rn(s[3], v.w);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < cols) out[r * ldo + c + e] = from_f32<T>(s[e]);
-  }
-}
-
 // Copies whose rows start on 16-byte boundaries, of up to three matrices of
 // 16-bit elements with as many columns each, one after another along the grid's z.
 struct GpAlign {
@@ -430,7 +504,7 @@ struct GpAlign {
   int64_t ld[3], rows[3];
   int count;
 };
-__global__ void __launch_bounds__(256, 4) k_align_rows(const GpAlign a, Tiling t, int64_t ldt) {
+__global__ void __launch_bounds__(256, 4) k_align_rows(const __grid_constant__ GpAlign a, Tiling t, int64_t ldt) {
   using B = __nv_bfloat16;  // any 16 bits: they go through fp32's upper half and back
   constexpr int AHEAD = 8;
   __shared__ float4 shared[Rows<B, true>::bytes(AHEAD, 256) / 16];
@@ -563,44 +637,60 @@ static bool make_map(CUtensorMap* m, int32_t dtype, const void* p, int64_t ld, i
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call is cut: pairs of CTAs or single ones, the tile's width, and for the
-// gradient the splits of its sum where there are fewer tiles than SMs.
+// How a call is cut: pairs of CTAs or single ones, the tile's width, and the
+// splits of its sum, the CTAs of a cluster, where there are fewer tiles than SMs.
 struct GpPlan {
   bool pair;
   int bn, tiles_m, tiles_n, splits, span;
 };
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int GP_CLUSTER = 8;
+// Clusters of so many CTAs (of any of the kernels, which take an SM each) that the GPU holds.
+static int gp_clusters(int device, int ctas) {
+  static PerDevice held[GP_CLUSTER + 1];
+  return held[ctas].get(device, [=] {
+    const auto kern = &k_gated_proj<__nv_bfloat16, GP_BACK, false>;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas), cfg.blockDim = dim3(GP_THREADS), cfg.dynamicSmemBytes = GP_RING, cfg.attrs = &at, cfg.numAttrs = 1;
+    int n = 0;
+    if (grant_shared(kern, GP_RING) && cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess) return n;
+    (void)cudaGetLastError();
+    return 0;
+  });
+}
 // A stage takes the SMs 2 N clocks to multiply, and its bytes once in and once
-// out of shared memory at 128 a clock; a tile's fixed part is that of about six stages.
-static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t steps, bool back) {
+// out of shared memory at 128 a clock, and not less than 400 to issue; a tile's
+// fixed part is that of about six stages, and joining splits 3 us.
+static GpPlan gp_plan(int64_t rows, int64_t cols, int steps, bool back) {
   GpPlan best = {};
   double least = 0.0;
+  const int device = current_device();
   for (int pair = 0; pair < (rows > GP_M ? 2 : 1); ++pair) {
-    const int64_t tm = ceil_div(rows, pair ? 2 * GP_M : GP_M), workers = pair ? GP_SMS / 2 : GP_SMS;
+    const int tm = (int)ceil_div(rows, pair ? 2 * GP_M : GP_M), workers = pair ? GP_SMS / 2 : GP_SMS, of = pair ? 2 : 1;
     for (int bn = back ? 256 : 128; bn >= 32; bn -= 32) {
-      if (pair && back && bn % 64 != 0) continue;
-      const int64_t tn = ceil_div(cols, bn), tiles = tm * tn;
-      const int wide = back ? bn : 2 * bn, mine = pair ? wide / 2 : wide;
-      const double bytes = 2.0 * (16384.0 + 128.0 * mine) / 128.0, mma = 2.0 * wide, stage = (bytes > mma ? bytes : mma) / 1900.0;  // us
-      const int most = back && tiles < workers ? (int)(workers / tiles < 16 ? workers / tiles : 16) : 1;
-      for (int s = 1; s <= most; ++s) {
-        const int64_t span = ceil_div(steps, s);
-        if (s > 1 && (span < 4 || ceil_div(steps, span) != s)) continue;
-        double us = (double)ceil_div(tiles * s, workers) * ((double)span + 6.0) * stage;
-        if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 8.0 / 7e6;
-        if (best.bn == 0 || us < least) best = {pair != 0, bn, (int)tm, (int)tn, s, (int)span}, least = us;
+      const int tn = (int)ceil_div(cols, bn), tiles = tm * tn, groups = bn / 32, wide = back ? bn : 2 * bn, mine = wide / of;
+      const int bytes = 2 * (16384 + 128 * mine) / 128, clocks = bytes > 2 * wide ? bytes : 2 * wide;
+      const double stage = (clocks > 400 ? clocks : 400) / 1900.0;  // us
+      for (int s = 1; s * of <= GP_CLUSTER && (s == 1 || tiles * s <= workers); ++s) {
+        const int span = (steps + s - 1) / s;
+        if (s > 1 && (span < 4 || (steps + span - 1) / span != s ||
+                      ((groups + s - 1) / s * (s - 1) + groups - groups / s) * (back ? 1 : 2) * GP_M * 128 > GP_RING || tiles > gp_clusters(device, s * of)))
+          continue;
+        const double us = (tiles * s + workers - 1) / workers * (span + 6.0) * stage + (s > 1 ? 3.0 : 0.0);
+        if (best.bn == 0 || us < least) best = {pair != 0, bn, tm, tn, s, span}, least = us;
       }
     }
   }
   return best;
 }
-static int64_t gp_ldp(int64_t cols) { return (cols + 7) / 8 * 8; }
 static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
-// Workspace: the diagnostic words, the aligned copies, the splits' sums (there are
-// splits only where all their tiles fit the SMs: at most 16, and 20 MB).
+// Workspace: the diagnostic words and the aligned copies.
 struct GpSpace {
-  size_t rows[2], weights[2], sums, bytes;
+  size_t rows[2], weights[2], bytes;
 };
 static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, bool back) {
   GpSpace w = {};
@@ -614,11 +704,6 @@ static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, boo
   if (copied & GC_COPY_ROWS) {
     w.rows[0] = room(rows, back ? n : k);
     if (back) w.rows[1] = room(rows, n);
-  }
-  w.sums = at;
-  if (back) {
-    const double sums = 16.0 * (double)rows * (double)gp_ldp(k) * 4.0, most = (double)GP_SMS * GP_M * 256 * 4;
-    at += align_up((size_t)(sums < most ? sums : most), 256);
   }
   w.bytes = at;
   return w;
@@ -657,9 +742,19 @@ static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
   static PerDevice ready;
   if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_RING) ? 1 : 0; })) return false;
   constexpr int WORKERS = PAIR ? GP_SMS / 2 : GP_SMS;
-  const unsigned workers = (unsigned)(a.items < WORKERS ? a.items : WORKERS);
-  launch_chained(kern, PAIR ? 2 * workers : workers, GP_THREADS, GP_RING, s, maps, a);
-  return true;
+  const unsigned workers = (unsigned)(a.splits > 1 || a.items < WORKERS ? a.items : WORKERS);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)((PAIR ? 2 : 1) * a.splits), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((PAIR ? 2 : 1) * workers), cfg.blockDim = dim3(GP_THREADS), cfg.dynamicSmemBytes = GP_RING, cfg.stream = s;
+  cfg.attrs = at, cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  cfg.numAttrs = 1;  // not as a dependent launch, then
+  return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess;
 }
 template <typename T, int KIND>
 static bool launch_gp(const GpMaps& maps, const GpArgs& a, bool pair, cudaStream_t s) {
@@ -802,7 +897,6 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   const GpPlan p = gp_plan(rows, k, a.steps, true);
   set_plan(&a, p, true);
   a.out = dx, a.ldo = lddx, a.vec = put_width(dx, lddx);
-  a.part = p.splits > 1 ? reinterpret_cast<float*>(ws + w.sums) : nullptr, a.ldp = gp_ldp(k);
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;
   if (!make_map(&maps.a0, dtype, dg, lddg, rows, n, gp_box(rows)) || !make_map(&maps.a1, dtype, du, lddu, rows, n, gp_box(rows)) ||
@@ -810,15 +904,5 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
     return GC_ERR_CUDA;
   if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, p.pair, s) : launch_gp<__half, GP_BACK>(maps, a, p.pair, s)))
     return GC_ERR_CUDA;
-  if (a.part) {
-    const int64_t fours = a.ldp / 4, blocks = ceil_div(rows * fours, 256);
-    const unsigned grid = (unsigned)(blocks < GP_SMS * 8 ? blocks : GP_SMS * 8);
-    const float4* part = reinterpret_cast<const float4*>(a.part);
-    if (dtype == GC_BF16)
-      launch_chained(&k_gated_proj_join<__nv_bfloat16>, grid, 256, 0, s, part, p.splits, rows, k, fours,
-                     static_cast<__nv_bfloat16*>(dx), lddx);
-    else
-      launch_chained(&k_gated_proj_join<__half>, grid, 256, 0, s, part, p.splits, rows, k, fours, static_cast<__half*>(dx), lddx);
-  }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
