@@ -169,11 +169,13 @@ __global__ void __launch_bounds__(256, SPAN && sizeof(T) == 2 ? 2 : 3)
 // spill (152 and 184 us).  bf16 145 us (0.98), GELU 160 us (0.89; 214 with
 // scalar arithmetic); with the activation's checkpoint 168 and 182 us; fp32
 // 308 us (0.80); bf16 rows of 14335 193 us (0.74).
-template <typename T, int KIND, bool SPAN>
+// COPY (of spans): dgate and dup once more, as matrices whose rows start on
+// 16-byte boundaries, for bulk copies.
+template <typename T, int KIND, bool SPAN, bool COPY = false>
 __global__ void __launch_bounds__(256, SPAN ? 2 : 3)
     k_gated_backward(const T* dout, int64_t lddo, const int8_t* gcodes, const uint8_t* gsteps, const int8_t* ucodes,
                      const uint8_t* usteps, Tiling t, T* dgate, int64_t lddg, T* dup, int64_t lddu, int8_t* ocodes,
-                     uint8_t* osteps) {
+                     uint8_t* osteps, T* gcopy, T* ucopy, int64_t ldcopy) {
   constexpr int AHEAD = sizeof(T) == 2 ? 4 : 2;
   constexpr size_t RING = Rows<T, SPAN>::bytes(AHEAD, 256) / 16;
   __shared__ float4 shared[RING + (SPAN ? 8 * RowsOut<T, SPAN>::STAGE : 0)];
@@ -246,6 +248,16 @@ __global__ void __launch_bounds__(256, SPAN ? 2 : 3)
       }
       gto.put(g, n, r < p.end, own);
       uto.put(u, n, r < p.end, own);
+      if constexpr (COPY) {
+        const int64_t at = (int64_t)p.c8 * CHUNK;
+        if (r < p.end && at < ldcopy) {
+          Raw8<T> x, y;
+#pragma unroll
+          for (int e = 0; e < CHUNK; ++e) x.e[e] = from_f32<T>(g[e]), y.e[e] = from_f32<T>(u[e]);
+          *reinterpret_cast<uint4*>(gcopy + r * ldcopy + at) = *reinterpret_cast<const uint4*>(&x);
+          *reinterpret_cast<uint4*>(ucopy + r * ldcopy + at) = *reinterpret_cast<const uint4*>(&y);
+        }
+      }
       if (ocodes) {
         const uint32_t b = chunk_step(a);
         const uint2 q = chunk_codes(a, b);
@@ -341,12 +353,13 @@ extern "C" gc_status gc_gated_act(int32_t kind, const void* gate, int64_t ldg, c
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
-extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
-                                           const int8_t* gate_codes, const uint8_t* gate_steps,
-                                           const int8_t* up_codes, const uint8_t* up_steps, int64_t rows,
-                                           int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu,
-                                           int8_t* out_codes, uint8_t* out_steps, void* stream) {
-  NvtxRange nvtx_range("gc_gated_act_backward");
+namespace gc {
+// gc_gated_act_backward; with `copies`, also dgate and dup of a 16-bit type, one
+// [rows, ldcopy] after another, ldcopy the next multiple of 8.
+gc_status gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype, const int8_t* gate_codes,
+                             const uint8_t* gate_steps, const int8_t* up_codes, const uint8_t* up_steps, int64_t rows,
+                             int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu, int8_t* out_codes,
+                             uint8_t* out_steps, void* copies, void* stream) {
   gc_status st = validate_matrix(rows, cols, dtype);
   if (st != GC_OK) return st;
   if (kind != GC_GATE_SILU && kind != GC_GATE_GELU_TANH) return GC_ERR_INVALID_ARG;
@@ -358,8 +371,23 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
   const bool span = !(chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype));
+  const int64_t ldcopy = (cols + 7) / 8 * 8;
   GC_BY_DTYPE(dtype, T, {
     constexpr bool S = sizeof(T) == 4;
+    T* const gcopy = static_cast<T*>(copies);
+    T* const ucopy = copies ? gcopy + rows * ldcopy : nullptr;
+    if constexpr (!S) {
+      if (copies) {
+        const auto k = kind == GC_GATE_SILU ? row_kernel<&k_gated_backward<T, GC_GATE_SILU, true, true>, &k_gated_backward<T, GC_GATE_SILU, true, true>>(true)
+                                            : row_kernel<&k_gated_backward<T, GC_GATE_GELU_TANH, true, true>, &k_gated_backward<T, GC_GATE_GELU_TANH, true, true>>(true);
+        dim3 grid;
+        const Tiling t = make_tiling(rows, cols, true, k.ctas, &grid);
+        launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
+                       gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
+                       out_codes, out_steps, gcopy, ucopy, ldcopy);
+        return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+      }
+    }
     const auto k = kind == GC_GATE_SILU
                        ? row_kernel<&k_gated_backward<T, GC_GATE_SILU, S>, &k_gated_backward<T, GC_GATE_SILU, true>>(span)
                        : row_kernel<&k_gated_backward<T, GC_GATE_GELU_TANH, S>, &k_gated_backward<T, GC_GATE_GELU_TANH, true>>(span);
@@ -367,7 +395,18 @@ extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64
     const Tiling t = make_tiling(rows, cols, span, k.ctas, &grid);
     launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
                    gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
-                   out_codes, out_steps);
+                   out_codes, out_steps, static_cast<T*>(nullptr), static_cast<T*>(nullptr), (int64_t)0);
   });
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+}  // namespace gc
+
+extern "C" gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
+                                           const int8_t* gate_codes, const uint8_t* gate_steps,
+                                           const int8_t* up_codes, const uint8_t* up_steps, int64_t rows,
+                                           int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu,
+                                           int8_t* out_codes, uint8_t* out_steps, void* stream) {
+  NvtxRange nvtx_range("gc_gated_act_backward");
+  return gated_act_backward(kind, dout, lddo, dtype, gate_codes, gate_steps, up_codes, up_steps, rows, cols, dgate, lddg, dup,
+                            lddu, out_codes, out_steps, nullptr, stream);
 }

@@ -93,6 +93,10 @@ inline gc_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 // Defined by the operation files.
+gc_status gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype, const int8_t* gate_codes,
+                             const uint8_t* gate_steps, const int8_t* up_codes, const uint8_t* up_steps, int64_t rows,
+                             int64_t cols, void* dgate, int64_t lddg, void* dup, int64_t lddu, int8_t* out_codes,
+                             uint8_t* out_steps, void* copies, void* stream);
 size_t topk_workspace_bytes(const gc_layout* h, bool sampled);
 size_t dense_workspace_bytes(const gc_layout* h);
 size_t sparse_decompress_workspace_bytes(const gc_layout* h);

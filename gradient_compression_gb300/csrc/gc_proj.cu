@@ -690,7 +690,7 @@ static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 // Workspace: the diagnostic words and the aligned copies.
 struct GpSpace {
-  size_t rows[2], weights[2], bytes;
+  size_t rows, weights[2], bytes;
 };
 static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, bool back) {
   GpSpace w = {};
@@ -702,8 +702,7 @@ static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, boo
   };
   if (copied & GC_COPY_WEIGHTS) w.weights[0] = room(n, k), w.weights[1] = room(n, k);
   if (copied & GC_COPY_ROWS) {
-    w.rows[0] = room(rows, back ? n : k);
-    if (back) w.rows[1] = room(rows, n);
+    w.rows = room(back ? 2 * rows : rows, back ? n : k);
   }
   w.bytes = at;
   return w;
@@ -832,7 +831,7 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
   GpAlign copies = {};
-  if (copied & GC_COPY_ROWS) add_copy(&copies, &x, &ldx, rows, k, ws + w.rows[0]);
+  if (copied & GC_COPY_ROWS) add_copy(&copies, &x, &ldx, rows, k, ws + w.rows);
   if (!bulk_rows(w_gate, ldwg)) add_copy(&copies, &w_gate, &ldwg, n, k, ws + w.weights[0]);
   if (!bulk_rows(w_up, ldwu)) add_copy(&copies, &w_up, &ldwu, n, k, ws + w.weights[1]);
   align_rows(copies, k, s);
@@ -878,20 +877,19 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   const GpSpace w = gp_space(rows, n, k, copied, true);
   if ((st = check_workspace(workspace, ws_bytes, w.bytes)) != GC_OK) return st;
   // checks the rest before anything is enqueued
-  st = gc_gated_act_backward(kind, dout, lddo, dtype, gate_codes, gate_steps, up_codes, up_steps, rows, n, dgate, lddg, dup,
-                             lddu, out_codes, out_steps, stream);
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  unsigned char* const copies = (copied & GC_COPY_ROWS) ? ws + w.rows : nullptr;  // of dgate and dup
+  st = gated_act_backward(kind, dout, lddo, dtype, gate_codes, gate_steps, up_codes, up_steps, rows, n, dgate, lddg, dup, lddu,
+                          out_codes, out_steps, copies, stream);
   if (st != GC_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  unsigned char* const ws = static_cast<unsigned char*>(workspace);
   if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
   const void *dg = dgate, *du = dup;
-  GpAlign rows_copies = {}, weights_copies = {};
-  if (!bulk_rows(dg, lddg)) add_copy(&rows_copies, &dg, &lddg, rows, n, ws + w.rows[0]);
-  if (!bulk_rows(du, lddu)) add_copy(&rows_copies, &du, &lddu, rows, n, ws + w.rows[1]);
-  if (!bulk_rows(w_gate, ldwg)) add_copy(&weights_copies, &w_gate, &ldwg, n, k, ws + w.weights[0]);
-  if (!bulk_rows(w_up, ldwu)) add_copy(&weights_copies, &w_up, &ldwu, n, k, ws + w.weights[1]);
-  align_rows(rows_copies, n, s);
-  align_rows(weights_copies, k, s);
+  if (copies) lddg = lddu = gp_ld(n), dg = copies, du = copies + (size_t)rows * lddg * 2;
+  GpAlign weights = {};
+  if (!bulk_rows(w_gate, ldwg)) add_copy(&weights, &w_gate, &ldwg, n, k, ws + w.weights[0]);
+  if (!bulk_rows(w_up, ldwu)) add_copy(&weights, &w_up, &ldwu, n, k, ws + w.weights[1]);
+  align_rows(weights, k, s);
   GpArgs a = {};
   a.rows = rows, a.cols = k, a.half = (int)ceil_div(n, GP_K), a.steps = 2 * a.half;
   const GpPlan p = gp_plan(rows, k, a.steps, true);
