@@ -405,16 +405,11 @@ PyObject* gated_proj_backward(Args a) {
 struct List {
   PyObject* of;
   Py_ssize_t n;
-  List(PyObject* o, const char* name) : of(PySequence_Fast(o, "")) {
-    if (!of) {
-      PyErr_Clear();
-      bad("%s: a list of tensors is needed", name);
-    }
-    n = PySequence_Fast_GET_SIZE(of);
-    if (n > INT32_MAX) {
-      Py_DECREF(of);
-      bad("%s: too many tensors", name);
-    }
+  List(PyObject* o, const char* name) : of(o) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) bad("%s: a list of tensors is needed", name);
+    n = PySequence_Fast_GET_SIZE(o);
+    if (n > INT32_MAX) bad("%s: too many tensors", name);
+    Py_INCREF(of);
   }
   List(const List&) = delete;
   ~List() { Py_DECREF(of); }

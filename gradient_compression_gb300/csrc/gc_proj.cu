@@ -35,20 +35,18 @@ constexpr int GP_THREADS = (GP_FIRST + GP_OUT) * 32;
 constexpr int GP_SMS = 152;                  // of a GB300
 constexpr int GP_POLLS = 1 << 22;            // limit of every wait
 
-// All lanes of a warp, which go on or give up together.  (Without a time to be
-// suspended for, which costs 40 clocks where the phase is complete already.)
-__device__ __forceinline__ bool gp_poll(uint32_t bar, uint32_t parity) {
+// All lanes of a warp, which go on or give up together.  (Asked first without
+// being suspended, which costs 40 clocks where the phase is complete already.)
+__device__ __forceinline__ bool gp_wait_warp(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}\n"
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}\n"
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  return done != 0u;
-}
-__device__ __forceinline__ bool gp_wait_warp(uint32_t bar, uint32_t parity) {
+  if (__all_sync(FULL, done != 0u)) return true;
   for (int i = 0; i < GP_POLLS; ++i)
-    if (__all_sync(FULL, gp_poll(bar, parity))) return true;
+    if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
   return false;
 }
 // One lane of a warp that is all there, always the same.  What a whole warp goes
@@ -438,12 +436,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       mbar_expect(joined, (uint32_t)((groups - t.split + a.splits - 1) / a.splits * (a.splits - 1) * BLOCKS * quads) * 4096u);
     __syncwarp();
     cluster_sync();
-    const bool mine = warp >= GP_FIRST && quad < quads && ok;
+    const bool mine = warp >= GP_FIRST && quad < quads;
     const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
     // where split `of` puts its sums of the owner's group q
     auto block = [&](int q, int owner, int of) { return (uint32_t)((q / a.splits) * (a.splits - 1) + of - (of > owner)) * (BLOCKS * BLOCK); };
     if (mine) {
-      for (int q = side; q < groups; q += 2) {
+      for (int q = side; ok && q < groups; q += 2) {
         const int owner = q % a.splits, cta = PAIR ? 2 * owner + rank : owner;
         if (owner == t.split) continue;
         const int sent = q - (q + a.splits - 1 - t.split) / a.splits;  // of the groups of others
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           __syncwarp();
         }
       }
-      ok = gp_wait_warp(joined, 0u);
+      ok = gp_wait_warp(joined, 0u) && ok;  // in any case: what is on its way here lands before this CTA ends
     }
     if (mine && ok) {
       const uint32_t at = base + row128;
@@ -704,7 +702,7 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
       const int steps = (back ? 2 : 1) * ((blocks + parts - 1) / parts);
       const int bytes = 2 * (gp_room(rows) + 128 * wide / of) / 128, work = bytes > 2 * wide ? bytes : 2 * wide, issue = parts == 2 ? 250 : 400;
       const double stage = parts * (work > issue ? work : issue);  // clocks
-      for (int s = 1; s * of <= GP_CLUSTER && (s == 1 || tiles * s <= workers); ++s) {
+      for (int s = 1; s * of <= GP_CLUSTER && (s == 1 || tiles <= workers / s); ++s) {
         const int span = (steps + s - 1) / s;
         if (s > 1 && (span < 2 || (steps + span - 1) / span != s ||
                       ((groups + s - 1) / s * (s - 1) + groups - groups / s) * (back ? 1 : 2) * GP_M * 128 > GP_RING ||

@@ -98,7 +98,8 @@ def check_held(ck, value, error):
 
 # (rows, n, k): one token to several tiles, one stage to several rings, widths around every tile's
 SHAPES = [(1, 1, 1), (1, 32, 64), (2, 33, 65), (5, 31, 7), (77, 333, 1001), (128, 128, 128), (129, 257, 320), (1, 4096, 1024),
-          (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264)]
+          (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264),
+          (30, 1200, 1096), (100, 64, 2000)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -169,7 +170,7 @@ def test_a_row_that_is_not_finite_spoils_no_other(gc, bad):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("shape", SHAPES + [(128, 9000, 64), (40, 14336, 1024)])
+@pytest.mark.parametrize("shape", SHAPES + [(128, 9000, 64), (40, 14336, 1024), (31, 2100, 96), (600, 8200, 300), (257, 4500, 1001)])
 def test_backward(gc, shape, dtype, kind):
     rows, n, k = shape
     dt = DT[dtype]
@@ -372,3 +373,106 @@ def test_against_the_calls_it_stands_for(gc):
         assert torch.equal(out, ref)
         for a, b in ((0, 2), (1, 3)):
             assert torch.equal(cks[a].codes, cks[b].codes) and torch.equal(cks[a].steps, cks[b].steps)
+
+
+def test_two_calls_at_once(gc):
+    """On two streams, each with a workspace and outputs of its own."""
+    gen = torch.Generator().manual_seed(12)
+    rows, n, k = 520, 1500, 700
+    x = [torch.randn(rows, k, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    w = (torch.randn(2 * n, k, generator=gen) / 27).to(torch.bfloat16).cuda()
+    d = torch.randn(rows, n, generator=gen).to(torch.bfloat16).cuda()
+
+    def buffers(i):
+        b = dict(out=torch.empty(rows, n, dtype=torch.bfloat16, device="cuda"), c=[gc.ActCheckpoint(rows, n) for _ in range(2)],
+                 d=torch.empty(rows, 2 * n, dtype=torch.bfloat16, device="cuda"), dx=torch.empty_like(x[i]))
+        b["ws"] = gc.gated_proj_workspace(x[i], w[:n], w[n:])
+        b["wb"] = gc.gated_proj_backward_workspace(b["d"][:, :n], b["d"][:, n:], w[:n], w[n:])
+        return b
+
+    def step(i, b, s=None):
+        gc.gated_proj(0, x[i], w[:n], w[n:], b["out"], b["ws"], *b["c"], stream=s)
+        gc.gated_proj_backward(0, d, *b["c"], w[:n], w[n:], b["d"][:, :n], b["d"][:, n:], b["dx"], b["wb"], stream=s)
+
+    apart = [buffers(i) for i in range(2)]
+    for i in range(2):
+        step(i, apart[i])
+    together, streams = [buffers(i) for i in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            step(i, together[i], streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(apart, together):
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["dx"], b["dx"]) and torch.equal(a["d"], b["d"])
+        assert gc.get_device_status(b["ws"]).error_bits == 0 and gc.get_device_status(b["wb"]).error_bits == 0
+
+
+def test_a_workspace_does_for_fewer_rows_and_again(gc):
+    """Kept from a large call for smaller ones, and used by call after call."""
+    gen = torch.Generator().manual_seed(13)
+    n, k = 333, 201
+    w = (torch.randn(2 * n, k, generator=gen) / 14).to(torch.float16).cuda()
+    big = torch.randn(700, k, generator=gen).to(torch.float16).cuda()
+    ws = gc.gated_proj_workspace(big, w[:n], w[n:])
+    for rows in (700, 1, 64, 129, 3, 700):
+        out, ref = (torch.empty(rows, n, dtype=torch.float16, device="cuda") for _ in range(2))
+        x = big[:rows]
+        gc.gated_proj(1, x, w[:n], w[n:], out, ws)
+        gc.gated_proj(1, x, w[:n], w[n:], ref, gc.gated_proj_workspace(x, w[:n], w[n:]))
+        assert torch.equal(out, ref) and gc.get_device_status(ws).error_bits == 0
+
+
+def test_strides_of_one_row(gc):
+    """A single row of any stride, also of none."""
+    gen = torch.Generator().manual_seed(14)
+    k, n = 328, 100
+    w = (torch.randn(2 * n, k, generator=gen) / 18).to(torch.bfloat16).cuda()
+    x = torch.randn(1, k, generator=gen).to(torch.bfloat16).cuda()
+    ref = torch.empty(1, n, dtype=torch.bfloat16, device="cuda")
+    gc.gated_proj(0, x, w[:n], w[n:], ref, gc.gated_proj_workspace(x, w[:n], w[n:]))
+    for y in (x.as_strided((1, k), (0, 1)), x.as_strided((1, k), (5, 1)), x.as_strided((1, k), (k + 3, 1)), x[0].unsqueeze(0)):
+        out = torch.empty(1, n, dtype=torch.bfloat16, device="cuda")
+        gc.gated_proj(0, y, w[:n], w[n:], out, gc.gated_proj_workspace(y, w[:n], w[n:]))
+        assert torch.equal(out, ref)
+        ck = [gc.ActCheckpoint(1, n), gc.ActCheckpoint(1, n)]
+        gc.gated_proj(0, y, w[:n], w[n:], out, gc.gated_proj_workspace(y, w[:n], w[n:]), *ck)
+        assert float((out.float() - ref.float()).abs().max()) <= 2.0 ** -7 * float(ref.abs().max())
+    with pytest.raises(ValueError):
+        gc.gated_proj(0, x.expand(3, k), w[:n], w[n:], torch.empty(3, n, dtype=torch.bfloat16, device="cuda"),
+                      torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+
+
+def test_every_cut_of_a_call(gc):
+    """Sizes that the rule for tiles, pairs and splits cuts in different ways,
+    inputs of small integers, so that every sum is exact and so is every output."""
+    gen = torch.Generator().manual_seed(15)
+    for rows, n, k in ((1, 8192, 64), (17, 8192, 96), (33, 14336, 32), (64, 4096, 512), (100, 14336, 128), (128, 2048, 256),
+                       (130, 4096, 64), (200, 14336, 256), (256, 1000, 1024), (300, 9000, 64), (512, 14336, 128), (700, 2000, 520),
+                       (1031, 4100, 1000), (2048, 1024, 1024), (5000, 100, 64), (9000, 64, 40)):
+        dt = torch.bfloat16
+        dg = torch.randint(-1, 2, (rows, n), generator=gen, dtype=torch.int8).cuda()
+        w = torch.randint(-1, 2, (2 * n, k), generator=gen, dtype=torch.int8).cuda()
+        # checkpoints for which dgate = 0 and dup = dout / 2 exactly: act(G) = 1/2 is not
+        # exact, so the gradient's product is checked on dup alone, with U = 0
+        cg, cu = gc.ActCheckpoint(rows, n), gc.ActCheckpoint(rows, n)
+        gc.act_compress(torch.full((rows, n), 64.0, dtype=dt, device="cuda"), cg)      # act(64) = 64 in silu
+        gc.act_compress(torch.zeros(rows, n, dtype=dt, device="cuda"), cu)
+        dout, wd = dg.to(dt), w.to(dt)
+        a, b, dx = (torch.empty(rows, c, dtype=dt, device="cuda") for c in (n, n, k))
+        wb = gc.gated_proj_backward_workspace(a, b, wd[:n], wd[n:])
+        gc.gated_proj_backward(gc.GC_GATE_SILU, dout, cg, cu, wd[:n], wd[n:], a, b, dx, wb)
+        assert gc.get_device_status(wb).error_bits == 0
+        assert int((a != 0).sum()) == 0 and torch.equal(b, 64 * dout)
+        want = (64.0 * (dg.double() @ w[n:].double())).to(dt)
+        assert torch.equal(dx, want), (rows, n, k)
+        # the projections: G = 0 wherever x's columns are, U from small integers
+        x = torch.randint(-1, 2, (rows, k), generator=gen, dtype=torch.int8).cuda()
+        out = torch.empty(rows, n, dtype=dt, device="cuda")
+        cks = [gc.ActCheckpoint(rows, n) for _ in range(2)]
+        gc.gated_proj(gc.GC_GATE_SILU, x.to(dt), wd[:n], wd[n:], out, gc.gated_proj_workspace(x.to(dt), wd[:n], wd[n:]), *cks)
+        for ck, part in zip(cks, (w[:n], w[n:])):
+            full = x.double() @ part.double().T
+            ref = gc.ActCheckpoint(rows, n)
+            gc.act_compress(full.float(), ref)
+            assert torch.equal(ck.codes, ref.codes) and torch.equal(ck.steps, ref.steps), (rows, n, k)

@@ -145,7 +145,8 @@ def test_binding_refusals(gc):
                  lambda: gc.grad_norm([host], torch.zeros(1), ws), lambda: gc.grad_norm(3, torch.zeros(1), ws),
                  lambda: gc.grad_norm([host], None, ws), lambda: gc.grad_norm([None], torch.zeros(1), ws),
                  lambda: gc.grad_clip([host], torch.zeros(1), 1.0), lambda: gc.grad_clip([host], None, 1.0),
-                 lambda: gc.grad_clip(host, 1.0, 1.0)):
+                 lambda: gc.grad_clip(host, 1.0, 1.0), lambda: gc.grad_norm(host, torch.zeros(1), ws),
+                 lambda: gc.grad_norm((t for t in [host]), torch.zeros(1), ws)):
         with pytest.raises(ValueError):
             call()
     assert gc.grad_norm_workspace([host, host], device="cpu").numel() >= 8
