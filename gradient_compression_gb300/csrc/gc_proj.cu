@@ -28,7 +28,8 @@ constexpr int GP_M = 128, GP_K = 64;         // rows of a tile, summed index of 
 constexpr int GP_RING = 192 * 1024, GP_SLOTS = 12;
 // An MMA reads 128 rows also where there are fewer, whose room is smaller: past
 // the last one's there has to be shared memory, too (whatever it holds, it only
-// reaches rows of the accumulator that are not there).
+// reaches rows of the accumulator that are not there: it is the warps' stages for
+// what they write).
 constexpr int GP_SHARED = GP_RING + GP_M * GP_K * 2;
 constexpr int GP_OUT = 8, GP_FIRST = 4;      // warps that read out, the first of them
 constexpr int GP_THREADS = (GP_FIRST + GP_OUT) * 32;
@@ -129,6 +130,8 @@ struct GpArgs {
   bool whole, even;            // codes start on a 32-byte boundary; rows of steps on even addresses
   int8_t *gcodes, *ucodes;
   uint8_t *gsteps, *usteps;
+  float* sums;                 // of splits that a kernel of its own joins, one [rows, lds] after another
+  int64_t lds;
   uint32_t* diag;
 };
 struct GpItem {
@@ -175,25 +178,58 @@ __device__ __forceinline__ uint32_t gp_hold(const float (&v)[32], int8_t* codes,
   gp_put32(codes, w, whole);
   return b;
 }
-// n of the 32 values of a row.  vec: 0 where rows start anywhere, 1 on 16-byte
-// boundaries, 2 on 32-byte ones.
+// n of the 32 values of each lane's row, a warp's rows one after another from the
+// one at `to` on; there: this lane's row is.  vec: 0 where rows start anywhere, 1 on
+// 16-byte boundaries, 2 on 32-byte ones.  Rows that start anywhere, and the last
+// columns, go through `stage` (the warp's own 2 KB) and a lane per column: stored by
+// the lanes of their rows 138 x 7785 took 23 us instead of 8.
 template <typename T>
-__device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int n, int vec) {
+__device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int64_t ld, bool there, int n, int vec, uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[2][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    alignas(16) T r[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r[e] = from_f32<T>(v[16 * i + e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[i][e] = reinterpret_cast<const uint32_t*>(r)[e];
+  }
   if (vec && n == 32) {
+    T* const row = to + lane * ld;
+    if (there) gp_put32(row, w[0], vec == 2), gp_put32(row + 16, w[1], vec == 2);
+    return;
+  }
+  // 16-byte chunk c of row r at chunk c ^ (r / 2 & 3)
+  const int rows = __popc(__ballot_sync(FULL, there));
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      alignas(16) T r[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) r[e] = from_f32<T>(v[16 * i + e]);
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint32_t*>(r)[e];
-      gp_put32(to + 16 * i, w, vec == 2);
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t* const x = &w[c >> 1][4 * (c & 1)];
+    st_shared16(stage + (uint32_t)lane * 64u + (uint32_t)((c ^ ((lane >> 1) & 3)) << 4), x[0], x[1], x[2], x[3]);
+  }
+  __syncwarp();
+  if (lane < n) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(to + lane);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, o += ld) {
+      uint16_t x;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(x)
+                   : "r"(stage + (uint32_t)r * 64u + (uint32_t)(((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (uint32_t)(lane & 7) * 2u)
+                   : "memory");
+      *o = x;
     }
-  } else {
+  }
+}
+// fp32 sums of a split: rows on 32-byte boundaries.
+__device__ __forceinline__ void gp_put_sums(const float (&v)[32], float* to, int n) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < n) to[e] = from_f32<T>(v[e]);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * i + e]);
+    if (8 * i < n) gp_put32(to + 8 * i, w, true);  // rows have room for whole eights
   }
 }
 // The groups of 32 columns of a tile that are there.
@@ -201,21 +237,23 @@ __device__ __forceinline__ int gp_groups(const GpArgs& a, int n) {
   return (int)min((int64_t)(a.bn / 32), (a.cols - (int64_t)n * a.bn + 31) / 32);
 }
 constexpr int GP_BACK = -1;
-// What a thread does with the sums of 32 columns, from `col` on, of its row: the gradient's as
-// they are; the projections' through the checkpoints and the activation.  held: the steps of the
-// group before, where this warp had that one (after) and two groups' steps are
-// written at a time; next: it has the next one, too.
+// What a warp does with the sums of 32 columns, from `col` on, of its rows, row0 + lane: the
+// gradient's as they are; the projections' through the checkpoints and the activation.  held: the
+// steps of the group before, where this warp had that one (after) and two groups' steps
+// are written at a time; next: it has the next one, too.
 template <typename T, int KIND, int U>
-__device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row, int64_t col, float (&g)[32], float (&u)[U], uint32_t* held,
-                                          bool after, bool next) {
+__device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row0, int64_t col, float (&g)[32], float (&u)[U], uint32_t* held,
+                                          bool after, bool next, uint32_t stage) {
   const int n = (int)min((int64_t)32, a.cols - col);
+  const int64_t row = row0 + (threadIdx.x & 31);
+  const bool there = row < a.rows;
   if constexpr (KIND != GP_BACK) {
     if (n < 32) {
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         if (e >= n) g[e] = u[e] = 0.0f;
     }
-    if (a.gcodes) {
+    if (a.gcodes && there) {
       const int64_t at = row * (act_ldc(a.cols) >> 5) + (col >> 5);  // the group
       const bool odd = ((col >> 5) & 1) != 0;
       const uint32_t bg = gp_hold(g, a.gcodes + 32 * at, a.whole), bu = gp_hold(u, a.ucodes + 32 * at, a.whole);
@@ -234,7 +272,7 @@ __device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row, int64_t 
       put2(g + e, mul2(mul2(get2(g + e), gate_sigmoid2<KIND>(g + e, &dp)), get2(u + e)));
     }
   }
-  gp_put(g, static_cast<T*>(a.out) + row * a.ldo + col, n, a.vec);
+  gp_put(g, static_cast<T*>(a.out) + row0 * a.ldo + col, a.ldo, there, n, a.vec, stage);
 }
 
 // KIND: the activation; GP_BACK: the gradient.  PAIR: a cluster of two CTAs
@@ -279,7 +317,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (PAIR || a.splits > 1) cluster_sync();
+  const bool joint = a.splits > 1 && !a.sums;  // a cluster's splits
+  if (PAIR || joint) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = __shfl_sync(FULL, tmem_base, 0);
   chain_wait();
@@ -388,8 +427,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
-      if (a.splits > 1) break;  // the tile's only one: below
-      const int64_t row = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad + lane, c0 = (int64_t)t.n * a.bn;
+      if (joint) break;  // the tile's only one: below
+      const int64_t row0 = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad, c0 = (int64_t)t.n * a.bn;
+      const uint32_t stage = base + GP_RING + (uint32_t)(warp - GP_FIRST) * 2048u;
       // the groups of 32 columns of this warp, next to each other
       const int groups = gp_groups(a, t.n), half = (groups + 1) / 2;
       const int begin = side ? half : 0, end = side ? groups : half;
@@ -412,12 +452,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         tmem_load32(g, from + 32 * q);
         if constexpr (!BACK) tmem_load32(u, from + a.bn + 32 * q);
         if (q + 1 == end) read_out();
-        if (row < a.rows) gp_finish<T, KIND>(a, row, c0 + 32 * q, g, u, &held, q > begin, q + 1 < end);
+        if (row0 < a.rows) {
+          if (BACK && a.sums) {
+            if (row0 + lane < a.rows)
+              gp_put_sums(g, a.sums + ((int64_t)t.split * a.rows + row0 + lane) * a.lds + c0 + 32 * q,
+                          (int)min((int64_t)32, a.cols - c0 - 32 * q));
+          } else {
+            gp_finish<T, KIND>(a, row0, c0 + 32 * q, g, u, &held, q > begin, q + 1 < end, stage);
+          }
+        }
         __syncwarp();
       }
     }
   }
-  if (a.splits > 1) {
+  if (joint) {
     // The cluster's CTAs (pairs) have summed a part of the tile each, and end together
     // here.  Group q of its columns is finished by split q % splits: the others
     // send it their sums, and it adds them in the splits' order.  They go by bulk
@@ -468,7 +516,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     }
     if (mine && ok) {
       const uint32_t at = base + row128;
-      const int64_t row = row0 + 32 * quad + lane;
+      const uint32_t stage = base + GP_RING + (uint32_t)(warp - GP_FIRST) * 2048u;
       for (int q = t.split + side * a.splits; q < groups; q += 2 * a.splits) {
         float sum[BLOCKS][32];
 #pragma unroll
@@ -495,7 +543,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           }
         }
         uint32_t held = 0u;
-        if (row < a.rows) gp_finish<T, KIND>(a, row, (int64_t)t.n * a.bn + 32 * q, sum[0], sum[BLOCKS - 1], &held, false, false);
+        gp_finish<T, KIND>(a, row0 + 32 * quad, (int64_t)t.n * a.bn + 32 * q, sum[0], sum[BLOCKS - 1], &held, false, false, stage);
         __syncwarp();
       }
     }
@@ -504,7 +552,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (PAIR || a.splits > 1) cluster_sync();  // none ends, or gives its tensor memory back, while another may reach it
+  if (PAIR || joint) cluster_sync();  // none ends, or gives its tensor memory back, while another may reach it
   if (warp == 1) {
     if (PAIR)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -512,59 +560,31 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
-// Copies whose rows start on 16-byte boundaries, of up to three matrices of
-// 16-bit elements with as many columns each, one after another along the grid's z.
-struct GpAlign {
-  const void* from[3];
-  void* to[3];
-  int64_t ld[3], rows[3];
-  int count;
-};
-__global__ void __launch_bounds__(256, 4) k_align_rows(const __grid_constant__ GpAlign a, Tiling t, int64_t ldt) {
-  using B = __nv_bfloat16;  // any 16 bits: they go through fp32's upper half and back
-  constexpr int AHEAD = 8;
-  __shared__ float4 shared[Rows<B, true>::bytes(AHEAD, 256) / 16];
+// dx = the splits' sums in their order, a column per thread and eight sums' loads
+// at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) k_gated_proj_join(const float* sums, int splits, int64_t rows, int cols, int64_t lds, T* out,
+                                                         int64_t ldo) {
   chain_wait();
-  const int z = blockIdx.z;
-  t.rows = a.rows[z];
-  const Place p = place(t);
-  const int64_t ld = a.ld[z];
-  Rows<B, true> in(shared, 256, static_cast<const B*>(a.from[z]) + p.r * ld, p.step * ld, p.c8, p.n, t.cols);
-  B* to = static_cast<B*>(a.to[z]) + p.r * ldt + (int64_t)p.c8 * CHUNK;
-  int64_t r = p.r, next = p.r;
-  auto copy = [&](int slot) {
-    in.copy(slot, next < p.end);
-    copy_group();
-    next += p.step;
-  };
+  const int64_t r = blockIdx.y, plane = rows * lds;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  const float* const from = sums + r * lds + c;
+  float sum = 0.0f;
+  for (int p = 0; p < splits; p += 8) {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < AHEAD - 1; ++i) copy(i);
-  int slot = 0;
-  for (int64_t lead = (int64_t)blockIdx.y * t.slab; lead < p.end; lead += p.step, r += p.step, to += p.step * ldt) {
-    float v[CHUNK];
-    wait_groups<AHEAD - 2>();
-    in.landed();
-    in.take(slot, r < p.end ? p.n : 0, v);
-    in.done();
-    copy((slot + AHEAD - 1) % AHEAD);
-    slot = (slot + 1) % AHEAD;
-    uint32_t x[4];
+    for (int q = 0; q < 8; ++q) v[q] = p + q < splits ? __ldg(from + (p + q) * plane) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
-    if (r < p.end && (int64_t)p.c8 * CHUNK < ldt) *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+    for (int q = 0; q < 8; ++q) sum = __fadd_rn(sum, v[q]);
   }
+  out[r * ldo + c] = from_f32<T>(sum);
 }
 
-// ---------------------------------------------------------------- one row
-// The projection of one row reads its weights once and does little else: a warp
-// per two columns of out streams their four rows of weights, 8 elements a lane,
-// through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
-// then over the lanes.  14336 x 4096 in bf16 takes 35.5 us (6.6 TB/s) and 4096 x 1024
-// 4.8; the tensor cores' kernel, whose copies take longer to get going, 39.0 and 8.4.
-// (Two rows take 40.4 us this way, for the registers of their sums, and 39.0 there.)
-// SPAN: rows of weights or of x that do not start on 16-byte boundaries.
+// 8 elements of a row from column c on, wherever it starts; zeros past its end k.
+// The granules of memory that hold them are read whole and the elements shifted out.
 template <typename T, bool SPAN>
-struct Eight {  // 8 elements of a row from column c on, zeros past its end
+struct Eight {
   static constexpr int N = SPAN ? 2 : 1;
   uint4 w[N];
   __device__ __forceinline__ void load(const T* row, int64_t c, int64_t k, bool stream) {
@@ -578,11 +598,14 @@ struct Eight {  // 8 elements of a row from column c on, zeros past its end
       if (k - c > 0 && bytes > 16 * i) w[i] = stream ? __ldcs(from + i) : __ldg(from + i);
     }
   }
-  __device__ __forceinline__ void take(const T* row, int64_t c, int64_t k, float (&v)[CHUNK]) const {
+  __device__ __forceinline__ uint4 words(const T* row, int64_t c) const {
     uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[N - 1].x, w[N - 1].y, w[N - 1].z, w[N - 1].w};
     if (SPAN) shift_words<4>(x, (int)((uintptr_t)(row + c) & 15u));
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  __device__ __forceinline__ void take(const T* row, int64_t c, int64_t k, float (&v)[CHUNK]) const {
     Raw8<T> r;
-    *reinterpret_cast<uint4*>(&r) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(&r) = words(row, c);
     unpack(r, v);
     if (k - c < CHUNK) {
 #pragma unroll
@@ -591,6 +614,50 @@ struct Eight {  // 8 elements of a row from column c on, zeros past its end
     }
   }
 };
+
+// Copies whose rows start on 16-byte boundaries, of up to three matrices of
+// 16-bit elements with as many columns each, one after another along the grid's z.
+// A thread has every gridDim.x * 256-th 8 elements, four at a time; the elements
+// past a row's end are whatever follows it (what reads the copies does not).
+struct GpAlign {
+  const void* from[3];
+  void* to[3];
+  int64_t ld[3], rows[3];
+  int count;
+};
+__global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAlign a, int64_t cols, uint32_t chunks) {
+  using B = __nv_bfloat16;  // any 16 bits
+  chain_wait();
+  const int z = blockIdx.z;
+  const B* const x = static_cast<const B*>(a.from[z]);
+  uint4* const to = static_cast<uint4*>(a.to[z]);
+  const int64_t ld = a.ld[z], total = a.rows[z] * chunks, stride = (int64_t)gridDim.x * 256;
+  for (int64_t q0 = (int64_t)blockIdx.x * 256 + threadIdx.x; q0 < total; q0 += 4 * stride) {
+    Eight<B, true> v[4];
+    const B* row[4];
+    int64_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t q = q0 + i * stride;
+      if (q >= total) break;
+      const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)q / chunks) : q / chunks;
+      row[i] = x + r * ld, c[i] = (q - r * chunks) * CHUNK;
+      v[i].load(row[i], c[i], cols, false);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (q0 + i * stride < total) to[q0 + i * stride] = v[i].words(row[i], c[i]);
+  }
+}
+
+// ---------------------------------------------------------------- one row
+// The projection of one row reads its weights once and does little else: a warp
+// per two columns of out streams their four rows of weights, 8 elements a lane,
+// through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
+// then over the lanes.  14336 x 4096 in bf16 takes 35.5 us (6.6 TB/s) and 4096 x 1024
+// 4.8; the tensor cores' kernel, whose copies take longer to get going, 39.0 and 8.4.
+// (Two rows take 40.4 us this way, for the registers of their sums, and 39.0 there.)
+// SPAN: rows of weights or of x that do not start on 16-byte boundaries.
 template <typename T, int KIND, bool SPAN>
 __global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu, int64_t n,
                                                            int64_t k, T* out, uint32_t* diag) {
@@ -656,7 +723,7 @@ static bool make_map(CUtensorMap* m, int32_t dtype, const void* p, int64_t ld, i
 // How a call is cut: pairs of CTAs or single ones, the tile's width, and the
 // splits of its sum, the CTAs of a cluster, where there are fewer tiles than SMs.
 struct GpPlan {
-  bool pair;
+  bool pair, apart;  // apart: the splits are CTAs of their own, joined by another kernel
   int bn, parts, tiles_m, tiles_n, splits, span;
 };
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -689,6 +756,8 @@ static int gp_columns(int bn, bool pair, bool back) {
 // A part takes the SMs 2 N clocks to multiply, its bytes once in and once out of
 // shared memory at 128 a clock, and not less than 400 to issue (250 of two); a
 // tile's fixed part is 3000 clocks, and joining splits takes 11000, or less for few rows.
+// The gradient of few rows, whose sum may be long and whose tiles few, is also cut
+// into more splits than a cluster has CTAs, whose sums go through the workspace.
 static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
   GpPlan best = {};
   double least = 0.0;
@@ -709,7 +778,14 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
                       tiles > gp_clusters(device, s * of)))
           continue;
         const double clocks = (tiles * s + workers - 1) / workers * (span * stage + 3000.0) + (s > 1 ? join : 0.0);
-        if (best.bn == 0 || clocks < least) best = {pair != 0, bn, parts, tm, tn, s, span}, least = clocks;
+        if (best.bn == 0 || clocks < least) best = {pair != 0, false, bn, parts, tm, tn, s, span}, least = clocks;
+      }
+      if (!back || rows > GP_M || tiles > workers / 2) continue;
+      for (int span = 2; span < steps; span = span < 8 ? span + 1 : span * 5 / 4) {
+        const int s = (steps + span - 1) / span;
+        if (s < 2 || s > workers / tiles) continue;
+        const double clocks = span * stage + 3000.0 + 5500.0 + s * (30.0 + (double)rows * (double)cols * 0.0015);
+        if (clocks < least) best = {false, true, bn, parts, tm, tn, s, span}, least = clocks;
       }
     }
   }
@@ -717,10 +793,12 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
 }
 static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
-// Workspace: the diagnostic words and the aligned copies.
+// Workspace: the diagnostic words, the aligned copies, the sums of the splits that go
+// through it (those of at most 128 rows, whose tiles and splits fit the SMs: 20 MB at most).
 struct GpSpace {
-  size_t rows, weights[2], bytes;
+  size_t rows, weights[2], sums, bytes;
 };
+static int64_t gp_lds(int64_t cols) { return (cols + 7) / 8 * 8; }
 static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, bool back) {
   GpSpace w = {};
   size_t at = DIAG_BYTES;
@@ -732,6 +810,12 @@ static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, boo
   if (copied & GC_COPY_WEIGHTS) w.weights[0] = room(n, k), w.weights[1] = room(n, k);
   if (copied & GC_COPY_ROWS) {
     w.rows = room(back ? 2 * rows : rows, back ? n : k);
+  }
+  w.sums = at;
+  if (back) {
+    const double sums = (double)GP_SMS * (double)(rows < GP_M ? rows : GP_M) * (double)gp_lds(k) * 4.0;
+    constexpr double MOST = (double)GP_SMS * GP_M * 256 * 4;
+    at += align_up((size_t)(sums < MOST ? sums : MOST), 256);
   }
   w.bytes = at;
   return w;
@@ -750,10 +834,9 @@ static void align_rows(const GpAlign& l, int64_t cols, cudaStream_t s) {
   if (l.count == 0) return;
   int64_t rows = 0;
   for (int i = 0; i < l.count; ++i) rows = l.rows[i] > rows ? l.rows[i] : rows;
-  dim3 grid;
-  const Tiling t = make_tiling(rows, cols, true, resident<&k_align_rows>(), &grid);
-  grid.z = (unsigned)l.count;
-  launch_chained(k_align_rows, grid, 256, 0, s, l, t, gp_ld(cols));
+  const int64_t chunks = gp_ld(cols) / CHUNK, blocks = ceil_div(rows * chunks, 256);
+  launch_chained(k_align_rows, dim3((unsigned)(blocks < GP_SMS * 16 ? blocks : GP_SMS * 16), 1, (unsigned)l.count), 256, 0, s, l, cols,
+                 (uint32_t)chunks);
 }
 
 template <typename T, int KIND>
@@ -770,10 +853,11 @@ static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
   static PerDevice ready;
   if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_SHARED) ? 1 : 0; })) return false;
   constexpr int WORKERS = PAIR ? GP_SMS / 2 : GP_SMS;
-  const unsigned workers = (unsigned)(a.splits > 1 || a.items < WORKERS ? a.items : WORKERS);
+  const bool joint = a.splits > 1 && !a.sums;
+  const unsigned workers = (unsigned)(joint || a.items < WORKERS ? a.items : WORKERS);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)((PAIR ? 2 : 1) * a.splits), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = (unsigned)((PAIR ? 2 : 1) * (joint ? a.splits : 1)), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -928,6 +1012,7 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   const GpPlan p = gp_plan(rows, k, n, true);
   set_plan(&a, p, n, true);
   a.out = dx, a.ldo = lddx, a.vec = put_width(dx, lddx);
+  if (p.apart) a.sums = reinterpret_cast<float*>(ws + w.sums), a.lds = gp_lds(k);
   a.diag = reinterpret_cast<uint32_t*>(ws);
   GpMaps maps;
   if (!make_map(&maps.a0, dtype, dg, lddg, rows, n, gp_box(rows)) || !make_map(&maps.a1, dtype, du, lddu, rows, n, gp_box(rows)) ||
@@ -935,5 +1020,13 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
     return GC_ERR_CUDA;
   if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, p, s) : launch_gp<__half, GP_BACK>(maps, a, p, s)))
     return GC_ERR_CUDA;
+  if (p.apart) {
+    const dim3 grid((unsigned)ceil_div(k, 256), (unsigned)rows);  // of at most 128
+    if (dtype == GC_BF16)
+      launch_chained(&k_gated_proj_join<__nv_bfloat16>, grid, 256, 0, s, a.sums, p.splits, rows, (int)k, a.lds,
+                     static_cast<__nv_bfloat16*>(dx), lddx);
+    else
+      launch_chained(&k_gated_proj_join<__half>, grid, 256, 0, s, a.sums, p.splits, rows, (int)k, a.lds, static_cast<__half*>(dx), lddx);
+  }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }

@@ -677,7 +677,8 @@ gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, const void* w_
  * from dgate and dup as they are rounded to `dtype`.  (The weights' gradients come from
  * gc_act_weight_grad, of dgate and dup and the checkpoint of x.)  dgate or
  * dup may be dout itself.  Types, alignment and workspace as for gc_gated_proj
- * (GC_COPY_ROWS for dgate and dup). */
+ * (GC_COPY_ROWS for dgate and dup); for few rows the workspace holds partial
+ * sums, which are added in a fixed order. */
 gc_status gc_gated_proj_backward_workspace_size(int64_t rows, int64_t n, int64_t k, uint32_t copied,
                                                 size_t* bytes);
 gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int64_t lddo, int32_t dtype,
