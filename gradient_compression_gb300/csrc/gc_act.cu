@@ -371,23 +371,27 @@ gc_status gated_act_backward(int32_t kind, const void* dout, int64_t lddo, int32
   if (out_codes || out_steps)
     if ((st = check_codes(out_codes, out_steps)) != GC_OK) return st;
   const bool span = !(chunk_aligned(dout, lddo, dtype) && chunk_aligned(dgate, lddg, dtype) && chunk_aligned(dup, lddu, dtype));
-  const int64_t ldcopy = (cols + 7) / 8 * 8;
+  if (copies) {
+    const auto launch = [&](auto* gcopy) {
+      using T = std::remove_pointer_t<decltype(gcopy)>;
+      constexpr auto SILU = &k_gated_backward<T, GC_GATE_SILU, true, true>, GELU = &k_gated_backward<T, GC_GATE_GELU_TANH, true, true>;
+      dim3 grid;
+      const Tiling t = make_tiling(rows, cols, true, kind == GC_GATE_SILU ? resident<SILU>() : resident<GELU>(), &grid);
+      const int64_t ldcopy = (cols + 7) / 8 * 8;
+      launch_chained(kind == GC_GATE_SILU ? SILU : GELU, grid, 256, 0, static_cast<cudaStream_t>(stream),
+                     static_cast<const T*>(dout), lddo, gate_codes, gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg,
+                     static_cast<T*>(dup), lddu, out_codes, out_steps, gcopy, gcopy + rows * ldcopy, ldcopy);
+    };
+    if (dtype == GC_BF16)
+      launch(static_cast<__nv_bfloat16*>(copies));
+    else if (dtype == GC_F16)
+      launch(static_cast<__half*>(copies));
+    else
+      return GC_ERR_INVALID_ARG;
+    return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+  }
   GC_BY_DTYPE(dtype, T, {
     constexpr bool S = sizeof(T) == 4;
-    T* const gcopy = static_cast<T*>(copies);
-    T* const ucopy = copies ? gcopy + rows * ldcopy : nullptr;
-    if constexpr (!S) {
-      if (copies) {
-        const auto k = kind == GC_GATE_SILU ? row_kernel<&k_gated_backward<T, GC_GATE_SILU, true, true>, &k_gated_backward<T, GC_GATE_SILU, true, true>>(true)
-                                            : row_kernel<&k_gated_backward<T, GC_GATE_GELU_TANH, true, true>, &k_gated_backward<T, GC_GATE_GELU_TANH, true, true>>(true);
-        dim3 grid;
-        const Tiling t = make_tiling(rows, cols, true, k.ctas, &grid);
-        launch_chained(k.kern, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(dout), lddo, gate_codes,
-                       gate_steps, up_codes, up_steps, t, static_cast<T*>(dgate), lddg, static_cast<T*>(dup), lddu,
-                       out_codes, out_steps, gcopy, ucopy, ldcopy);
-        return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
-      }
-    }
     const auto k = kind == GC_GATE_SILU
                        ? row_kernel<&k_gated_backward<T, GC_GATE_SILU, S>, &k_gated_backward<T, GC_GATE_SILU, true>>(span)
                        : row_kernel<&k_gated_backward<T, GC_GATE_GELU_TANH, S>, &k_gated_backward<T, GC_GATE_GELU_TANH, true>>(span);

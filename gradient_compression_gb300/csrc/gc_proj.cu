@@ -1,5 +1,8 @@
 // Gated projection on the fifth-generation tensor cores, out = act(x Wg^T) *
 // (x Wu^T), and its input's gradient dx = dgate Wg + dup Wu.
+#include <algorithm>
+#include <type_traits>
+
 #include "gc_act.cuh"
 #include "gc_gate.cuh"
 #include "gc_host.h"
@@ -753,15 +756,23 @@ static int gp_columns(int bn, bool pair, bool back) {
   const int wide = back ? bn : 2 * bn, mine = pair ? wide / 2 : wide;
   return (back ? (mine + 63) / 64 * 64 : mine) * GP_K * 2;
 }
+// Whether what a cluster's splits send and receive of a tile's groups fits the ring.
+static bool gp_fits(int groups, int s, bool back) {
+  return ((groups + s - 1) / s * (s - 1) + groups - groups / s) * (back ? 1 : 2) * GP_M * 128 <= GP_RING;
+}
 // A part takes the SMs 2 N clocks to multiply, its bytes once in and once out of
 // shared memory at 128 a clock, and not less than 400 to issue (250 of two); a
-// tile's fixed part is 3000 clocks, and joining splits takes 11000, or less for few rows.
-// The gradient of few rows, whose sum may be long and whose tiles few, is also cut
-// into more splits than a cluster has CTAs, whose sums go through the workspace.
+// tile's fixed part is 3000 clocks.  Joining splits takes a cluster 10400 (of two) to
+// 14600 (of eight), or less for few rows; the gradient, whose sum may be long and
+// whose tiles few, may also be cut into more splits, whose sums go through the
+// workspace and cost another kernel.  Operands that half of L2 does not hold come
+// from memory, at 27 bytes a clock and SM that takes part and 3500 in all.
 static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
   GpPlan best = {};
   double least = 0.0;
-  const double join = 5000.0 + 1500.0 * (rows < GP_M ? (double)ceil_div(rows, 32) : 4.0);
+  const double bytes_in = (4.0 * (double)cols + (back ? 4.0 : 2.0) * (double)rows) * (double)summed;
+  const double memory = bytes_in > 64e6 ? bytes_in / 27.0 : 0.0, all = 3500.0 / 27.0;  // clocks of one SM; the SMs that take all there is
+  const double quads = rows < GP_M ? (double)ceil_div(rows, 32) : 4.0;
   const int device = current_device(), blocks = (int)ceil_div(summed, GP_K);
   for (int pair = 0; pair < (rows > GP_M ? 2 : 1); ++pair) {
     const int tm = (int)ceil_div(rows, pair ? 2 * GP_M : GP_M), workers = pair ? GP_SMS / 2 : GP_SMS, of = pair ? 2 : 1;
@@ -773,19 +784,20 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
       const double stage = parts * (work > issue ? work : issue);  // clocks
       for (int s = 1; s * of <= GP_CLUSTER && (s == 1 || tiles <= workers / s); ++s) {
         const int span = (steps + s - 1) / s;
-        if (s > 1 && (span < 2 || (steps + span - 1) / span != s ||
-                      ((groups + s - 1) / s * (s - 1) + groups - groups / s) * (back ? 1 : 2) * GP_M * 128 > GP_RING ||
-                      tiles > gp_clusters(device, s * of)))
+        if (s > 1 && (span < 2 || (steps + span - 1) / span != s || !gp_fits(groups, s, back) || tiles > gp_clusters(device, s * of)))
           continue;
-        const double clocks = (tiles * s + workers - 1) / workers * (span * stage + 3000.0) + (s > 1 ? join : 0.0);
+        const int rounds = (tiles * s + workers - 1) / workers;
+        const double product = rounds * span * stage, fed = memory / std::min((double)(std::min(tiles * s, workers) * of), all);
+        const double clocks = (product > fed ? product : fed) + rounds * 3000.0 + (s > 1 ? 3500.0 + (1400.0 + 175.0 * s) * quads : 0.0);
         if (best.bn == 0 || clocks < least) best = {pair != 0, false, bn, parts, tm, tn, s, span}, least = clocks;
       }
-      if (!back || rows > GP_M || tiles > workers / 2) continue;
+      if (!back || tiles > workers / 2) continue;
       for (int span = 2; span < steps; span = span < 8 ? span + 1 : span * 5 / 4) {
         const int s = (steps + span - 1) / span;
         if (s < 2 || s > workers / tiles) continue;
-        const double clocks = span * stage + 3000.0 + 5500.0 + s * (30.0 + (double)rows * (double)cols * 0.0015);
-        if (clocks < least) best = {false, true, bn, parts, tm, tn, s, span}, least = clocks;
+        const double product = span * stage, fed = memory / std::min((double)(tiles * s * of), all);
+        const double clocks = (product > fed ? product : fed) + 3000.0 + 8000.0 + s * (30.0 + (double)rows * (double)cols * 0.0023);
+        if (clocks < least) best = {pair != 0, true, bn, parts, tm, tn, s, span}, least = clocks;
       }
     }
   }
@@ -794,7 +806,7 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
 static int64_t gp_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 // Workspace: the diagnostic words, the aligned copies, the sums of the splits that go
-// through it (those of at most 128 rows, whose tiles and splits fit the SMs: 20 MB at most).
+// through it (whose tiles all fit the SMs: 20 MB at most).
 struct GpSpace {
   size_t rows, weights[2], sums, bytes;
 };
@@ -813,7 +825,7 @@ static GpSpace gp_space(int64_t rows, int64_t n, int64_t k, uint32_t copied, boo
   }
   w.sums = at;
   if (back) {
-    const double sums = (double)GP_SMS * (double)(rows < GP_M ? rows : GP_M) * (double)gp_lds(k) * 4.0;
+    const double sums = (double)GP_SMS * (double)rows * (double)gp_lds(k) * 4.0;
     constexpr double MOST = (double)GP_SMS * GP_M * 256 * 4;
     at += align_up((size_t)(sums < MOST ? sums : MOST), 256);
   }
@@ -854,6 +866,7 @@ static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
   if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_SHARED) ? 1 : 0; })) return false;
   constexpr int WORKERS = PAIR ? GP_SMS / 2 : GP_SMS;
   const bool joint = a.splits > 1 && !a.sums;
+  if (joint && !gp_fits(a.bn / 32, a.splits, KIND == GP_BACK)) return false;
   const unsigned workers = (unsigned)(joint || a.items < WORKERS ? a.items : WORKERS);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1021,7 +1034,7 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   if (!(dtype == GC_BF16 ? launch_gp<__nv_bfloat16, GP_BACK>(maps, a, p, s) : launch_gp<__half, GP_BACK>(maps, a, p, s)))
     return GC_ERR_CUDA;
   if (p.apart) {
-    const dim3 grid((unsigned)ceil_div(k, 256), (unsigned)rows);  // of at most 128
+    const dim3 grid((unsigned)ceil_div(k, 256), (unsigned)rows);  // at most 128 of each SM
     if (dtype == GC_BF16)
       launch_chained(&k_gated_proj_join<__nv_bfloat16>, grid, 256, 0, s, a.sums, p.splits, rows, (int)k, a.lds,
                      static_cast<__nv_bfloat16*>(dx), lddx);
