@@ -169,7 +169,13 @@ __global__ void __launch_bounds__(256) k_grad_norm_join(const double* part, int 
   __shared__ double warps[8];
   chain_wait();
   double sum = 0.0;
-  for (int i = threadIdx.x; i < count; i += 256) sum += part[i];
+  for (int i = threadIdx.x; i < count; i += 4 * 256) {  // four loads at a time: a wave's sums at once
+    double v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = i + 256 * j < count ? part[i + 256 * j] : 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += v[j];
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;

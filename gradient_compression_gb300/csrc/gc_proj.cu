@@ -27,6 +27,19 @@ namespace gc {
 // the weights of the projection; the gradient sums over the weights' rows, which makes
 // them "MN-major".  Everything comes by bulk tensor copies under the 128-byte
 // swizzle, with zeros for what is outside a matrix.
+//
+// Pairs.  Of more than 128 rows two CTAs share a tile of 256: each stages its own
+// rows and half of the columns' operand, 32 KB a stage instead of 48 for the same
+// MMAs, which shared memory would bound otherwise (8192 x 14336 x 4096: 1071 us
+// instead of 1218).  A stage of 64 takes 525 clocks where the MMAs alone take 512.
+//
+// Measured in bf16, back to back: 8192 x 14336 x 4096 1.04-1.11 ms (1.73-1.85
+// PFLOP/s under the power cap; a library's product of the same size, without the
+// activation, 1.06-1.11), with checkpoints 1.08-1.13, its gradient 1.09-1.14 behind
+// dgate and dup (a library's product 1.08-1.13); on its own 2048 x 14336 x 4096's
+// gradient takes 249 us, tensor pipe active 93%.  2048 x 4096 x 1024: 23 and, with
+// checkpoints, 25 us, the gradient 27: four rounds of tiles where 3.4 would do, and
+// the splits' join.  48 x 14336 x 4096: 39 us, 6.0 TB/s of weights.
 constexpr int GP_M = 128, GP_K = 64;         // rows of a tile, summed index of a part of a stage
 constexpr int GP_RING = 192 * 1024, GP_SLOTS = 12;
 // An MMA reads 128 rows also where there are fewer, whose room is smaller: past

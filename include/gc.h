@@ -152,8 +152,9 @@ typedef struct gc_diag {
 #define GC_DIAG_INDEX_ORDER 0x10u    /* decompress met a worker's indices not ascending within a
                                         tensor; see gc_sparse_decompress_accumulate */
 #define GC_DIAG_TIMEOUT 0x20u        /* a grid-wide wait of the one-launch path ran out (about a
-                                        second), or a wait inside gc_act_weight_grad; that call's
-                                        outputs are incomplete */
+                                        second), or a wait inside gc_act_weight_grad or
+                                        gc_gated_proj(_backward); that call's outputs are
+                                        incomplete */
 
 /* CUDA-graph capture.  gc_ef_topk_compress_dev_iter and
  * gc_quantize_stochastic_dev_iter are gc_ef_topk_compress and
