@@ -892,7 +892,9 @@ static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
   if (cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess) return true;
   (void)cudaGetLastError();
   cfg.numAttrs = 1;  // not as a dependent launch, then
-  return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess) return true;
+  (void)cudaGetLastError();  // this call's, not the next one's
+  return false;
 }
 template <typename T, int KIND>
 static bool launch_gp(const GpMaps& maps, const GpArgs& a, const GpPlan& p, cudaStream_t s) {

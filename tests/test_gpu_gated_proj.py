@@ -476,3 +476,98 @@ def test_every_cut_of_a_call(gc):
             ref = gc.ActCheckpoint(rows, n)
             gc.act_compress(full.float(), ref)
             assert torch.equal(ck.codes, ref.codes) and torch.equal(ck.steps, ref.steps), (rows, n, k)
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_gradients_over_dout(gc, off):
+    """dgate, or dup, may be dout itself, on 16-byte boundaries and off them."""
+    rows, n, k = 150, 424, 328
+    gen = torch.Generator().manual_seed(16)
+    cks = [gc.ActCheckpoint(rows, n), gc.ActCheckpoint(rows, n)]
+    for c in cks:
+        gc.act_compress(torch.randn(rows, n, generator=gen).cuda(), c)
+    w = (torch.randn(2 * n, k, generator=gen) / 20).to(torch.bfloat16).cuda()
+    d = torch.randn(rows, n, generator=gen).to(torch.bfloat16).cuda()
+
+    def buffer():
+        return torch.zeros(rows, n + 8, dtype=torch.bfloat16, device="cuda")[:, off:off + n]
+
+    def call(dout, dg, du):
+        dx = torch.empty(rows, k, dtype=torch.bfloat16, device="cuda")
+        gc.gated_proj_backward(0, dout, *cks, w[:n], w[n:], dg, du, dx, gc.gated_proj_backward_workspace(dg, du, w[:n], w[n:]))
+        return dg.clone(), du.clone(), dx
+
+    want = call(d, buffer(), buffer())
+    for which in (0, 1):
+        own, other = buffer(), buffer()
+        own.copy_(d)
+        got = call(own, own, other) if which == 0 else call(own, other, own)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_matrix_for_both_projections(gc):
+    gen = torch.Generator().manual_seed(17)
+    for rows in (1, 50, 300):
+        x = torch.randn(rows, 96, generator=gen).to(torch.float16).cuda()
+        w = (torch.randn(70, 96, generator=gen) / 10).to(torch.float16).cuda()
+        out, ref = (torch.empty(rows, 70, dtype=torch.float16, device="cuda") for _ in range(2))
+        gc.gated_proj(0, x, w, w, out, gc.gated_proj_workspace(x, w, w))
+        both = torch.cat((w, w))
+        gc.gated_proj(0, x, both[:70], both[70:], ref, gc.gated_proj_workspace(x, both[:70], both[70:]))
+        assert torch.equal(out, ref)
+
+
+def test_weights_aligned_apart(gc):
+    """One of the weights, or one of the gradients, on 16-byte boundaries and the other off them."""
+    gen = torch.Generator().manual_seed(18)
+    rows, n, k = 200, 104, 136
+    x = torch.randn(rows, k, generator=gen).to(torch.bfloat16).cuda()
+    wg, wu = ((torch.randn(n, k, generator=gen) / 12).to(torch.bfloat16).cuda() for _ in range(2))
+    d = torch.randn(rows, n, generator=gen).to(torch.bfloat16).cuda()
+    cks = [gc.ActCheckpoint(rows, n), gc.ActCheckpoint(rows, n)]
+
+    def moved(t, by):
+        m = torch.zeros(t.shape[0], t.shape[1] + 8, dtype=t.dtype, device="cuda")[:, by:by + t.shape[1]]
+        m.copy_(t)
+        return m
+
+    def call(a, b, c, e):
+        wg_, wu_ = moved(wg, a), moved(wu, b)
+        out, dx = torch.empty_like(d), torch.empty_like(x)
+        gc.gated_proj(1, x, wg_, wu_, out, gc.gated_proj_workspace(x, wg_, wu_), *cks)
+        dg, du = moved(d, c), moved(d, e)
+        gc.gated_proj_backward(1, d, *cks, wg_, wu_, dg, du, dx, gc.gated_proj_backward_workspace(dg, du, wg_, wu_))
+        return out, dg.clone(), du.clone(), dx
+
+    want = call(0, 0, 0, 0)
+    for cut in ((0, 1, 0, 0), (3, 0, 0, 0), (0, 0, 0, 5), (0, 0, 7, 0), (1, 2, 3, 4)):
+        assert all(torch.equal(a, b) for a, b in zip(call(*cut), want)), cut
+
+
+def test_codes_past_2_31(gc):
+    """A checkpoint and an output of more than 2^31 elements, exact sums: the last rows' are right."""
+    rows, n, k = 150_016, 14_336, 64
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    x = torch.randint(-1, 2, (rows, k), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    w = torch.randint(-1, 2, (2 * n, k), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    out, cks = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda"), [gc.ActCheckpoint(rows, n) for _ in range(2)]
+    gc.gated_proj(0, x, w[:n], w[n:], out, gc.gated_proj_workspace(x, w[:n], w[n:]), *cks)
+    for rows_ in (slice(0, 130), slice(149_760, 150_016)):
+        part = x[rows_]
+        ref, few = torch.empty(part.shape[0], n, dtype=torch.bfloat16, device="cuda"), [gc.ActCheckpoint(part.shape[0], n) for _ in range(2)]
+        gc.gated_proj(0, part, w[:n], w[n:], ref, gc.gated_proj_workspace(part, w[:n], w[n:]), *few)
+        assert torch.equal(out[rows_], ref)
+        for a, b in zip(cks, few):
+            assert torch.equal(a.codes[rows_], b.codes) and torch.equal(a.steps[rows_], b.steps)
+    # and its gradient, over the outputs
+    d, dx = out, torch.empty_like(x)
+    dg = torch.empty_like(out)
+    gc.gated_proj_backward(0, d, *cks, w[:n], w[n:], dg, d, dx, gc.gated_proj_backward_workspace(dg, d, w[:n], w[n:]))
+    last = slice(149_760, 150_016)
+    ck = [gc.ActCheckpoint(256, n, codes=c.codes[last].clone(), steps=c.steps[last].clone()) for c in cks]
+    g2, u2, x2 = torch.empty_like(ref), torch.empty_like(ref), torch.empty(256, k, dtype=torch.bfloat16, device="cuda")
+    gc.gated_proj_backward(0, ref, *ck, w[:n], w[n:], g2, u2, x2, gc.gated_proj_backward_workspace(g2, u2, w[:n], w[n:]))
+    assert torch.equal(dg[last], g2) and torch.equal(d[last], u2)
+    want, error = sums64(torch.cat((g2, u2), 1), w.T)
+    for got in (dx[last], x2):
+        assert bool(((got.double().cpu() - want).abs() <= rounded(want, error, torch.bfloat16)).all())

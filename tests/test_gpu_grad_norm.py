@@ -233,3 +233,38 @@ def test_a_step_before_compression(gc):
     e.zero_()
     idx, val, _, _ = comp(by_hand, e, seed=1, it=0)
     assert torch.equal(got[0], idx) and torch.equal(got[1], val)
+
+
+def test_some_in_place_and_some_not(gc):
+    gen = torch.Generator().manual_seed(21)
+    tensors = some([5000, 77, 300, 9001], ["f32", "bf16"], gen)
+    before = [t.clone() for t in tensors]
+    outs = [tensors[0], torch.empty(77, device="cuda"), tensors[2], torch.empty(9001, dtype=torch.float16, device="cuda")]
+    norm = torch.tensor([8.0], device="cuda")
+    for most in (4.0, 16.0):
+        for t, b in zip(tensors, before):
+            t.copy_(b)
+        gc.grad_clip(tensors, norm, most, out=outs)
+        for o, b in zip(outs, before):
+            assert torch.equal(o, (b.float() * min(1.0, most / 8.0)).to(o.dtype))
+        assert torch.equal(tensors[1], before[1]) and torch.equal(tensors[3], before[3])
+    with pytest.raises(gc.GCError):                    # an output that is another one's input
+        gc.grad_clip(tensors, norm, 4.0, out=[tensors[0], tensors[2][:77], tensors[2], outs[3]])
+
+
+def test_two_norms_at_once(gc):
+    """On two streams, each with a workspace of its own; then one workspace by call after call."""
+    gen = torch.Generator().manual_seed(22)
+    lists = [some([300_000, 5, 70_000], ["f32"], gen), some([100_000] * 20, ["bf16"], gen)]
+    want = [norm_of(gc, t) for t in lists]
+    norms, spaces = [torch.zeros(1, device="cuda") for _ in lists], [gc.grad_norm_workspace(t) for t in lists]
+    streams = [torch.cuda.Stream() for _ in lists]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for t, n, w, s in zip(lists, norms, spaces, streams):
+            gc.grad_norm(t, n, w, stream=s)
+    torch.cuda.synchronize()
+    assert [float(n) for n in norms] == want
+    ws = gc.grad_norm_workspace(lists[1])
+    for t, n in zip(lists + lists[::-1], want + want[::-1]):
+        assert norm_of(gc, t, ws) == n
