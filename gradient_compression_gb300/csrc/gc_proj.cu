@@ -666,21 +666,26 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
   }
 }
 
-// ---------------------------------------------------------------- one row
+// ---------------------------------------------------------------- few rows
 // The projection of one row reads its weights once and does little else: a warp
 // per two columns of out streams their four rows of weights, 8 elements a lane,
 // through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
-// then over the lanes.  14336 x 4096 in bf16 takes 35.5 us (6.6 TB/s) and 4096 x 1024
-// 4.8; the tensor cores' kernel, whose copies take longer to get going, 39.0 and 8.4.
-// (Two rows take 40.4 us this way, for the registers of their sums, and 39.0 there.)
-// SPAN: rows of weights or of x that do not start on 16-byte boundaries.
+// then over the lanes.  14336 x 4096 in bf16 takes 34.6 us (6.8 TB/s) and 4096 x 1024
+// 4.0; the tensor cores' kernel, whose copies take longer to get going, 38.4 and 5.8.
+// A few rows, each by warps of its own, read the weights again from L2, 5 TB/s: two
+// rows of 4096 x 1024 take 5.4 us and three 7.1, there 6.1; eight of 1024 x 512 5.0,
+// there 5.7; two of 5888 x 780, which would be copied first, 11.2, there 17.0, and
+// four 20.4 and 16.9.  SPAN: rows of weights or of x off 16-byte boundaries.
+constexpr int GP_FEW = 8;
+constexpr double GP_FEW_BYTES = 36e6;  // of weights, each row's
 template <typename T, int KIND, bool SPAN>
-__global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu, int64_t n,
-                                                           int64_t k, T* out, uint32_t* diag) {
+__global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu,
+                                                           int64_t n, int64_t k, T* out, int64_t ldo, unsigned rows, uint32_t* diag) {
   chain_wait();
-  if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
+  x += blockIdx.x % rows * ldx, out += blockIdx.x % rows * ldo;
   const int lane = threadIdx.x & 31;
-  const int64_t j = 2 * ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5));
+  const int64_t j = 2 * ((int64_t)(blockIdx.x / rows) * 8 + (threadIdx.x >> 5));
   if (j >= n) return;
   const int64_t j1 = min(j + 1, n - 1);
   const T* const w[4] = {wg + j * ldwg, wg + j1 * ldwg, wu + j * ldwu, wu + j1 * ldwu};
@@ -865,11 +870,11 @@ static void align_rows(const GpAlign& l, int64_t cols, cudaStream_t s) {
 }
 
 template <typename T, int KIND>
-static void launch_row(const void* x, const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int64_t n, int64_t k, void* out,
-                       bool span, uint32_t* diag, cudaStream_t s) {
-  launch_chained(span ? &k_gated_proj_row<T, KIND, true> : &k_gated_proj_row<T, KIND, false>, (unsigned)ceil_div(n, 16), 256, 0, s,
-                 static_cast<const T*>(x), static_cast<const T*>(wg), ldwg, static_cast<const T*>(wu), ldwu, n, k,
-                 static_cast<T*>(out), diag);
+static void launch_row(const void* x, int64_t ldx, int64_t rows, const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int64_t n,
+                       int64_t k, void* out, int64_t ldo, bool span, uint32_t* diag, cudaStream_t s) {
+  launch_chained(span ? &k_gated_proj_row<T, KIND, true> : &k_gated_proj_row<T, KIND, false>, (unsigned)(rows * ceil_div(n, 16)), 256, 0, s,
+                 static_cast<const T*>(x), ldx, static_cast<const T*>(wg), ldwg, static_cast<const T*>(wu), ldwu, n, k,
+                 static_cast<T*>(out), ldo, (unsigned)rows, diag);
 }
 
 template <typename T, int KIND, bool PAIR, int PARTS>
@@ -969,10 +974,10 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
   unsigned char* const ws = static_cast<unsigned char*>(workspace);
   if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
   const bool silu = kind == GC_GATE_SILU;
-  if (rows == 1 && !gate_codes) {
+  if (!gate_codes && (rows == 1 || (rows <= GP_FEW && 4.0 * (double)rows * (double)n * (double)k <= GP_FEW_BYTES))) {
     const auto launch = dtype == GC_BF16 ? (silu ? &launch_row<__nv_bfloat16, GC_GATE_SILU> : &launch_row<__nv_bfloat16, GC_GATE_GELU_TANH>)
                                          : (silu ? &launch_row<__half, GC_GATE_SILU> : &launch_row<__half, GC_GATE_GELU_TANH>);
-    launch(x, w_gate, ldwg, w_up, ldwu, n, k, out, copied != 0, reinterpret_cast<uint32_t*>(ws), s);
+    launch(x, ldx, rows, w_gate, ldwg, w_up, ldwu, n, k, out, ldo, copied != 0, reinterpret_cast<uint32_t*>(ws), s);
     return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
   }
   GpAlign copies = {};

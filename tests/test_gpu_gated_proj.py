@@ -99,7 +99,8 @@ def check_held(ck, value, error):
 # (rows, n, k): one token to several tiles, one stage to several rings, widths around every tile's
 SHAPES = [(1, 1, 1), (1, 32, 64), (2, 33, 65), (5, 31, 7), (77, 333, 1001), (128, 128, 128), (129, 257, 320), (1, 4096, 1024),
           (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264),
-          (30, 1200, 1096), (100, 64, 2000)]
+          (30, 1200, 1096), (100, 64, 2000),
+          (8, 500, 300), (2, 301, 130), (6, 2000, 1500)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
