@@ -211,9 +211,10 @@ __device__ __forceinline__ void gp_put(const float (&v)[32], T* to, int64_t ld, 
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[i][e] = reinterpret_cast<const uint32_t*>(r)[e];
   }
-  if (vec && n == 32) {
+  if (vec && (n & 15) == 0) {
     T* const row = to + lane * ld;
-    if (there) gp_put32(row, w[0], vec == 2), gp_put32(row + 16, w[1], vec == 2);
+    if (there) gp_put32(row, w[0], vec == 2);
+    if (there && n == 32) gp_put32(row + 16, w[1], vec == 2);
     return;
   }
   // 16-byte chunk c of row r at chunk c ^ (r / 2 & 3)
@@ -248,19 +249,17 @@ __device__ __forceinline__ void gp_put_sums(const float (&v)[32], float* to, int
     if (8 * i < n) gp_put32(to + 8 * i, w, true);  // rows have room for whole eights
   }
 }
-// The groups of 32 columns of a tile that are there.
-__device__ __forceinline__ int gp_groups(const GpArgs& a, int n) {
-  return (int)min((int64_t)(a.bn / 32), (a.cols - (int64_t)n * a.bn + 31) / 32);
-}
+// The columns of a tile that are there; its groups of 32 of them.
+__device__ __forceinline__ int gp_width(const GpArgs& a, int n) { return (int)min((int64_t)a.bn, a.cols - (int64_t)n * a.bn); }
+__device__ __forceinline__ int gp_groups(const GpArgs& a, int n) { return (gp_width(a, n) + 31) / 32; }
 constexpr int GP_BACK = -1;
-// What a warp does with the sums of 32 columns, from `col` on, of its rows, row0 + lane: the
+// What a warp does with the sums of n of 32 columns, from `col` on, of its rows, row0 + lane: the
 // gradient's as they are; the projections' through the checkpoints and the activation.  held: the
 // steps of the group before, where this warp had that one (after) and two groups' steps
 // are written at a time; next: it has the next one, too.
 template <typename T, int KIND, int U>
-__device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row0, int64_t col, float (&g)[32], float (&u)[U], uint32_t* held,
-                                          bool after, bool next, uint32_t stage) {
-  const int n = (int)min((int64_t)32, a.cols - col);
+__device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row0, int64_t col, int n, float (&g)[32], float (&u)[U],
+                                          uint32_t* held, bool after, bool next, uint32_t stage) {
   const int64_t row = row0 + (threadIdx.x & 31);
   const bool there = row < a.rows;
   if constexpr (KIND != GP_BACK) {
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       const int64_t row0 = (int64_t)t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M + 32 * quad, c0 = (int64_t)t.n * a.bn;
       const uint32_t stage = base + GP_RING + (uint32_t)(warp - GP_FIRST) * 2048u;
       // the groups of 32 columns of this warp, next to each other
-      const int groups = gp_groups(a, t.n), half = (groups + 1) / 2;
+      const int width = gp_width(a, t.n), groups = gp_groups(a, t.n), half = (groups + 1) / 2;
       const int begin = side ? half : 0, end = side ? groups : half;
       uint32_t held = 0u;  // the steps of the group before
       auto read_out = [&] {  // the accumulator may be written again
@@ -468,13 +467,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         tmem_load32(g, from + 32 * q);
         if constexpr (!BACK) tmem_load32(u, from + a.bn + 32 * q);
         if (q + 1 == end) read_out();
+        const int n = min(32, width - 32 * q);
         if (row0 < a.rows) {
           if (BACK && a.sums) {
-            if (row0 + lane < a.rows)
-              gp_put_sums(g, a.sums + ((int64_t)t.split * a.rows + row0 + lane) * a.lds + c0 + 32 * q,
-                          (int)min((int64_t)32, a.cols - c0 - 32 * q));
+            if (row0 + lane < a.rows) gp_put_sums(g, a.sums + ((int64_t)t.split * a.rows + row0 + lane) * a.lds + c0 + 32 * q, n);
           } else {
-            gp_finish<T, KIND>(a, row0, c0 + 32 * q, g, u, &held, q > begin, q + 1 < end, stage);
+            gp_finish<T, KIND>(a, row0, c0 + 32 * q, n, g, u, &held, q > begin, q + 1 < end, stage);
           }
         }
         __syncwarp();
@@ -559,7 +557,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           }
         }
         uint32_t held = 0u;
-        gp_finish<T, KIND>(a, row0 + 32 * quad, (int64_t)t.n * a.bn + 32 * q, sum[0], sum[BLOCKS - 1], &held, false, false, stage);
+        gp_finish<T, KIND>(a, row0 + 32 * quad, (int64_t)t.n * a.bn + 32 * q, min(32, gp_width(a, t.n) - 32 * q), sum[0],
+                           sum[BLOCKS - 1], &held, false, false, stage);
         __syncwarp();
       }
     }
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
 // there 5.7; two of 5888 x 780, which would be copied first, 11.2, there 17.0, and
 // four 20.4 and 16.9.  SPAN: rows of weights or of x off 16-byte boundaries.
 constexpr int GP_FEW = 8;
-constexpr double GP_FEW_BYTES = 36e6;  // of weights, each row's
+constexpr double GP_FEW_BYTES = 40e6;  // of weights, each row's
 template <typename T, int KIND, bool SPAN>
 __global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu,
                                                            int64_t n, int64_t k, T* out, int64_t ldo, unsigned rows, uint32_t* diag) {
@@ -784,36 +783,44 @@ static bool gp_fits(int groups, int s, bool back) {
 // 14600 (of eight), or less for few rows; the gradient, whose sum may be long and
 // whose tiles few, may also be cut into more splits, whose sums go through the
 // workspace and cost another kernel.  Operands that half of L2 does not hold come
-// from memory, at 27 bytes a clock and SM that takes part and 3500 in all.
-static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back) {
+// from memory, at 27 bytes a clock and SM and 3500 in all.  fine: tiles may end
+// inside a group of 32 columns (those without checkpoints): 64 x 5632 x 4096 takes 19.8 us
+// in tiles of 48 columns and 22.8 in ones of 96, 17 x 11136 x 3840 29.5 in ones of 80 and
+// 30.7 in ones of 96.  Of plans that cost the same the narrower tiles are taken, which
+// copy on more SMs: 4 x 4096 x 1024 takes 6.1 us in tiles of 32 and 6.6 in ones of 48.
+static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back, bool fine) {
   GpPlan best = {};
   double least = 0.0;
   const double bytes_in = (4.0 * (double)cols + (back ? 4.0 : 2.0) * (double)rows) * (double)summed;
-  const double memory = bytes_in > 64e6 ? bytes_in / 27.0 : 0.0, all = 3500.0 / 27.0;  // clocks of one SM; the SMs that take all there is
+  const bool memory = bytes_in > 64e6;
   const double quads = rows < GP_M ? (double)ceil_div(rows, 32) : 4.0;
   const int device = current_device(), blocks = (int)ceil_div(summed, GP_K);
   for (int pair = 0; pair < (rows > GP_M ? 2 : 1); ++pair) {
     const int tm = (int)ceil_div(rows, pair ? 2 * GP_M : GP_M), workers = pair ? GP_SMS / 2 : GP_SMS, of = pair ? 2 : 1;
-    for (int bn = back ? 256 : 128; bn >= 32; bn -= 32) {
-      const int tn = (int)ceil_div(cols, bn), tiles = tm * tn, groups = bn / 32, wide = back ? bn : 2 * bn;
+    for (int bn = back ? 256 : 128; bn >= 32; bn -= fine ? 16 : 32) {
+      const int tn = (int)ceil_div(cols, bn), tiles = tm * tn, groups = (bn + 31) / 32, wide = back ? bn : 2 * bn;
       const int parts = gp_parts_of(gp_room(rows) + gp_columns(bn, pair != 0, back));
       const int steps = (back ? 2 : 1) * ((blocks + parts - 1) / parts);
       const int bytes = 2 * (gp_room(rows) + 128 * wide / of) / 128, work = bytes > 2 * wide ? bytes : 2 * wide, issue = parts == 2 ? 250 : 400;
       const double stage = parts * (work > issue ? work : issue);  // clocks
+      const auto feed = [&](int rounds, int items, int ctas) {  // clocks for the operands: of all SMs, of the one with most
+        const double most = back ? bytes_in / ((items < workers ? items : workers) * of) : rounds * 4.0 * bn * (double)summed / (tm * ctas);
+        return std::max(bytes_in / 3500.0, most / 27.0);
+      };
       for (int s = 1; s * of <= GP_CLUSTER && (s == 1 || tiles <= workers / s); ++s) {
         const int span = (steps + s - 1) / s;
         if (s > 1 && (span < 2 || (steps + span - 1) / span != s || !gp_fits(groups, s, back) || tiles > gp_clusters(device, s * of)))
           continue;
         const int rounds = (tiles * s + workers - 1) / workers;
-        const double product = rounds * span * stage, fed = memory / std::min((double)(std::min(tiles * s, workers) * of), all);
+        const double product = rounds * span * stage, fed = memory ? feed(rounds, tiles * s, s * of) : 0.0;
         const double clocks = (product > fed ? product : fed) + rounds * 3000.0 + (s > 1 ? 3500.0 + (1400.0 + 175.0 * s) * quads : 0.0);
-        if (best.bn == 0 || clocks < least) best = {pair != 0, false, bn, parts, tm, tn, s, span}, least = clocks;
+        if (best.bn == 0 || clocks <= least) best = {pair != 0, false, bn, parts, tm, tn, s, span}, least = clocks;
       }
       if (!back || tiles > workers / 2) continue;
       for (int span = 2; span < steps; span = span < 8 ? span + 1 : span * 5 / 4) {
         const int s = (steps + span - 1) / span;
         if (s < 2 || s > workers / tiles) continue;
-        const double product = span * stage, fed = memory / std::min((double)(tiles * s * of), all);
+        const double product = span * stage, fed = memory ? feed(1, tiles * s, s * of) : 0.0;
         const double clocks = (product > fed ? product : fed) + 3000.0 + 8000.0 + s * (30.0 + (double)rows * (double)cols * 0.0023);
         if (clocks < least) best = {pair != 0, true, bn, parts, tm, tn, s, span}, least = clocks;
       }
@@ -884,7 +891,7 @@ static bool launch_gp(const GpMaps& maps, const GpArgs& a, cudaStream_t s) {
   if (!ready.get(current_device(), [=] { return grant_shared(kern, GP_SHARED) ? 1 : 0; })) return false;
   constexpr int WORKERS = PAIR ? GP_SMS / 2 : GP_SMS;
   const bool joint = a.splits > 1 && !a.sums;
-  if (joint && !gp_fits(a.bn / 32, a.splits, KIND == GP_BACK)) return false;
+  if (joint && !gp_fits((a.bn + 31) / 32, a.splits, KIND == GP_BACK)) return false;
   const unsigned workers = (unsigned)(joint || a.items < WORKERS ? a.items : WORKERS);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -987,7 +994,7 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
   align_rows(copies, k, s);
   GpArgs a = {};
   a.rows = rows, a.cols = n;
-  const GpPlan p = gp_plan(rows, n, k, false);
+  const GpPlan p = gp_plan(rows, n, k, false, !gate_codes);
   set_plan(&a, p, k, false);
   a.out = out, a.ldo = ldo, a.vec = put_width(out, ldo);
   a.gcodes = gate_codes, a.ucodes = up_codes, a.gsteps = gate_steps, a.usteps = up_steps;
@@ -1042,7 +1049,7 @@ extern "C" gc_status gc_gated_proj_backward(int32_t kind, const void* dout, int6
   align_rows(weights, k, s);
   GpArgs a = {};
   a.rows = rows, a.cols = k;
-  const GpPlan p = gp_plan(rows, k, n, true);
+  const GpPlan p = gp_plan(rows, k, n, true, false);
   set_plan(&a, p, n, true);
   a.out = dx, a.ldo = lddx, a.vec = put_width(dx, lddx);
   if (p.apart) a.sums = reinterpret_cast<float*>(ws + w.sums), a.lds = gp_lds(k);

@@ -100,7 +100,8 @@ def check_held(ck, value, error):
 SHAPES = [(1, 1, 1), (1, 32, 64), (2, 33, 65), (5, 31, 7), (77, 333, 1001), (128, 128, 128), (129, 257, 320), (1, 4096, 1024),
           (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264),
           (30, 1200, 1096), (100, 64, 2000),
-          (8, 500, 300), (2, 301, 130), (6, 2000, 1500)]
+          (8, 500, 300), (2, 301, 130), (6, 2000, 1500),
+          (40, 129, 64), (100, 129, 64), (9, 1171, 2000), (40, 2344, 4096), (129, 101, 64), (129, 516, 4096), (129, 2515, 520), (300, 4867, 64)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
