@@ -812,7 +812,7 @@ static GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back, boo
         if (s > 1 && (span < 2 || (steps + span - 1) / span != s || !gp_fits(groups, s, back) || tiles > gp_clusters(device, s * of)))
           continue;
         const int rounds = (tiles * s + workers - 1) / workers;
-        const double product = rounds * span * stage, fed = memory ? feed(rounds, tiles * s, s * of) : 0.0;
+        const double product = (double)rounds * span * stage, fed = memory ? feed(rounds, tiles * s, s * of) : 0.0;
         const double clocks = (product > fed ? product : fed) + rounds * 3000.0 + (s > 1 ? 3500.0 + (1400.0 + 175.0 * s) * quads : 0.0);
         if (best.bn == 0 || clocks <= least) best = {pair != 0, false, bn, parts, tm, tn, s, span}, least = clocks;
       }
