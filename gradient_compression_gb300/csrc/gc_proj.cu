@@ -681,7 +681,7 @@ template <typename T, int KIND, bool SPAN>
 __global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu,
                                                            int64_t n, int64_t k, T* out, int64_t ldo, unsigned rows, uint32_t* diag) {
   chain_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
   x += blockIdx.x % rows * ldx, out += blockIdx.x % rows * ldo;
   const int lane = threadIdx.x & 31;
   const int64_t j = 2 * ((int64_t)(blockIdx.x / rows) * 8 + (threadIdx.x >> 5));

@@ -149,6 +149,41 @@ def test_forward_is_the_same_from_run_to_run_and_layout_to_layout(gc):
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 77, 261), (3, 129, 300), (8, 64, 515), (8, 1111, 1301), (40, 129, 67), (9, 1171, 2001), (129, 101, 68)])
+def test_what_lies_around_the_matrices_does_not_matter(gc, shape, dtype):
+    """Rows on 16-byte boundaries and rows anywhere, between zeros and between NaN: the same bits;
+    and a column of weights that is not finite spoils that one alone."""
+    rows, n, k = shape
+    dt = DT[dtype]
+    gen = torch.Generator().manual_seed(rows + n + k)
+    x, w = torch.randn(rows, k, generator=gen).to(dt), (torch.randn(2 * n, k, generator=gen) * k ** -0.5).to(dt)
+
+    def run(ld, off, around, w):
+        xb, wb = torch.full((rows, ld), around, dtype=dt, device="cuda"), torch.full((2 * n, ld), around, dtype=dt, device="cuda")
+        xb[:, off:off + k], wb[:, off:off + k] = x.cuda(), w.cuda()
+        xv, wg, wu = xb[:, off:off + k], wb[:n, off:off + k], wb[n:, off:off + k]
+        out = torch.empty(rows, n, dtype=dt, device="cuda")
+        ws = gc.gated_proj_workspace(xv, wg, wu)
+        ws.fill_(255)                                  # NaN, too, in either type
+        gc.gated_proj(0, xv, wg, wu, out, ws)
+        assert gc.get_device_status(ws).error_bits == 0
+        return out.cpu()
+
+    up = (k + 23) // 8 * 8
+    want = run(up, 8, 0.0, w)
+    assert bool(torch.isfinite(want).all())
+    for ld, off in ((up, 8), (up + 3, 1), (k, 0)):
+        assert torch.equal(run(ld, off, float("nan"), w), want), (ld, off)
+    j = n // 2
+    w[j, k - 1] = float("nan")
+    for ld, off in ((up, 8), (up + 3, 1)):
+        got = run(ld, off, 0.0, w)
+        assert bool(torch.isnan(got[:, j]).all())
+        got[:, j] = want[:, j]
+        assert torch.equal(got, want), (ld, off)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_row_that_is_not_finite_spoils_no_other(gc, bad):
     """And what is outside the matrices is zero to every row, also to that one's pads."""
