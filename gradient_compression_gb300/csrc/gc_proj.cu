@@ -631,28 +631,31 @@ struct Eight {
 };
 
 // Copies whose rows start on 16-byte boundaries, of up to three matrices of
-// 16-bit elements with as many columns each, one after another along the grid's z.
-// A thread has every gridDim.x * 256-th 8 elements, four at a time; the elements
-// past a row's end are whatever follows it (what reads the copies does not).
+// 16-bit elements with as many columns each, which have blocks in turn.  A thread
+// copies 8 elements, and 8 more half the matrix later: a call of 400 x 4097 x 1001
+// takes 16.9 us with these two, 21.0 with one and 17.7 with four; up to 16 CTAs an
+// SM, which then go round again.  The elements past a row's end are whatever follows
+// it (what reads the copies does not).
 struct GpAlign {
   const void* from[3];
   void* to[3];
   int64_t ld[3], rows[3];
+  unsigned first[4];  // block of each
   int count;
 };
 __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAlign a, int64_t cols, uint32_t chunks) {
   using B = __nv_bfloat16;  // any 16 bits
   chain_wait();
-  const int z = blockIdx.z;
+  const int z = (blockIdx.x >= a.first[1]) + (blockIdx.x >= a.first[2]);
   const B* const x = static_cast<const B*>(a.from[z]);
   uint4* const to = static_cast<uint4*>(a.to[z]);
-  const int64_t ld = a.ld[z], total = a.rows[z] * chunks, stride = (int64_t)gridDim.x * 256;
-  for (int64_t q0 = (int64_t)blockIdx.x * 256 + threadIdx.x; q0 < total; q0 += 4 * stride) {
-    Eight<B, true> v[4];
-    const B* row[4];
-    int64_t c[4];
+  const int64_t ld = a.ld[z], total = a.rows[z] * chunks, stride = (int64_t)(a.first[z + 1] - a.first[z]) * 256;
+  for (int64_t q0 = (int64_t)(blockIdx.x - a.first[z]) * 256 + threadIdx.x; q0 < total; q0 += 2 * stride) {
+    Eight<B, true> v[2];
+    const B* row[2];
+    int64_t c[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int64_t q = q0 + i * stride;
       if (q >= total) break;
       const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)q / chunks) : q / chunks;
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
       v[i].load(row[i], c[i], cols, false);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       if (q0 + i * stride < total) to[q0 + i * stride] = v[i].words(row[i], c[i]);
   }
 }
@@ -669,64 +672,91 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
 // The projection of one row reads its weights once and does little else: a warp
 // per two columns of out streams their four rows of weights, 8 elements a lane,
 // through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
-// then over the lanes.  14336 x 4096 in bf16 takes 34.6 us (6.8 TB/s) and 4096 x 1024
-// 4.0; the tensor cores' kernel, whose copies take longer to get going, 38.4 and 5.8.
-// A few rows, each by warps of its own, read the weights again from L2, 5 TB/s: two
-// rows of 4096 x 1024 take 5.4 us and three 7.1, there 6.1; eight of 1024 x 512 5.0,
-// there 5.7; two of 5888 x 780, which would be copied first, 11.2, there 17.0, and
-// four 20.4 and 16.9.  SPAN: rows of weights or of x off 16-byte boundaries.
-constexpr int GP_FEW = 8;
-constexpr double GP_FEW_BYTES = 40e6;  // of weights, each row's
-template <typename T, int KIND, bool SPAN>
-__global__ void __launch_bounds__(256, 3) k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu,
-                                                           int64_t n, int64_t k, T* out, int64_t ldo, unsigned rows, uint32_t* diag) {
+// then over the lanes, then over the warps that share the row (up to eight, where n is
+// small: 300 x 8192 takes 5.0 us, by one warp each 18.0).  14336 x 4096 in bf16 takes
+// 35.0 us from memory (6.7 TB/s) and 4096 x 1024 5.2; the tensor cores' kernel, whose copies
+// take longer to get going, 37.5 and 7.4.
+// Of more rows a warp has R = 2 at a time (one: 9.7 us for 8 x 1000 x 777, two 6.7, four, whose
+// registers leave half the loads in flight, 7.0) and what they cost is instructions: some
+// 1.25 steps of 256 k to begin and end a pair of rows by two columns, and one for each.  Two
+// rows of 4096 x 1024 take 5.4 us and four 8.2, there 7.4; 16 of 333 x 1001 6.3 and
+// 40 9.5, there 7.9; 40 of 512 x 64 6.2, there 5.5; there, too, k costs latency.
+// SPAN: rows of weights or of x off 16-byte boundaries.
+template <typename T, int KIND, bool SPAN, int R>
+__global__ void __launch_bounds__(256, R > 1 ? 2 : 3)
+    k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu, int64_t n, int64_t k, T* out,
+                     int64_t ldo, int rows, int split, uint32_t* diag) {
+  __shared__ __align__(16) float sums[8][R][4];
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
-  x += blockIdx.x % rows * ldx, out += blockIdx.x % rows * ldo;
-  const int lane = threadIdx.x & 31;
-  const int64_t j = 2 * ((int64_t)(blockIdx.x / rows) * 8 + (threadIdx.x >> 5));
-  if (j >= n) return;
-  const int64_t j1 = min(j + 1, n - 1);
-  const T* const w[4] = {wg + j * ldwg, wg + j1 * ldwg, wu + j * ldwu, wu + j1 * ldwu};
-  F2 sum[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
+  const unsigned groups = (unsigned)(rows + R - 1) / R;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = 1 << split, part = warp & (parts - 1);
+  const int row0 = R * (int)(blockIdx.x % groups);
+  const int64_t j = 2 * (((int64_t)(blockIdx.x / groups) * 8 + warp) >> split);
+  const int64_t j0 = min(j, n - 1), j1 = min(j + 1, n - 1);
+  const T* const w[4] = {wg + j0 * ldwg, wg + j1 * ldwg, wu + j0 * ldwu, wu + j1 * ldwu};
+  const T* xr[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) xr[r] = x + min(row0 + r, rows - 1) * ldx;
+  F2 sum[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[r][i] = f2(0.0f);
   constexpr int STEPS = SPAN ? 1 : 2;  // steps whose loads are in flight together
-  for (int64_t c0 = 8 * lane; c0 < k; c0 += 256 * STEPS) {
-    Eight<T, SPAN> ws[STEPS][4], xs[STEPS];
+  const int64_t step = 256 << split;     // (the same steps for each warp wherever rows start: the same bits)
+  for (int64_t c0 = 8 * lane + 256 * part; c0 < k; c0 += step * STEPS) {
+    Eight<T, SPAN> ws[STEPS][4], xs[STEPS][R];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ws[s][i].load(w[i], c0 + 256 * s, k, true);
+      for (int i = 0; i < 4; ++i) ws[s][i].load(w[i], c0 + step * s, k, true);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) xs[s].load(x, c0 + 256 * s, k, false);
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int r = 0; r < R; ++r) xs[s][r].load(xr[r], c0 + step * s, k, false);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int64_t c = c0 + 256 * s;
-      float xv[CHUNK];
-      xs[s].take(x, c, k, xv);
+      const int64_t c = c0 + step * s;
+      float xv[R][CHUNK];
+#pragma unroll
+      for (int r = 0; r < R; ++r) xs[s][r].take(xr[r], c, k, xv[r]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float wv[CHUNK];
         ws[s][i].take(w[i], c, k, wv);
 #pragma unroll
-        for (int e = 0; e < CHUNK; e += 2) sum[i] = fma2(get2(wv + e), get2(xv + e), sum[i]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < CHUNK; e += 2) sum[r][i] = fma2(get2(wv + e), get2(xv[r] + e), sum[r][i]);
       }
     }
   }
-  float v[4];
+  float v[4];  // of row row0 + lane
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float two[2];
-    put2(two, sum[i]);
-    v[i] = __fadd_rn(two[0], two[1]);
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] = __fadd_rn(v[i], __shfl_xor_sync(FULL, v[i], d));
+    for (int i = 0; i < 4; ++i) {
+      float two[2];
+      put2(two, sum[r][i]);
+      float all = __fadd_rn(two[0], two[1]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) all = __fadd_rn(all, __shfl_xor_sync(FULL, all, d));
+      if (r == 0 || lane == r) v[i] = all;
+    }
+  if (parts > 1) {
+    if (part != 0 && lane < R) *reinterpret_cast<float4*>(sums[warp][lane]) = make_float4(v[0], v[1], v[2], v[3]);
+    __syncthreads();
   }
-  if (lane == 0) {
-    F2 dp;
-    put2(v, mul2(mul2(get2(v), gate_sigmoid2<KIND>(v, &dp)), get2(v + 2)));
-    out[j] = from_f32<T>(v[0]);
-    if (j + 1 < n) out[j + 1] = from_f32<T>(v[1]);
-  }
+  if (part != 0 || lane >= R || row0 + lane >= rows || j >= n) return;
+  for (int p = 1; p < parts; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], sums[warp + p][lane][i]);
+  F2 dp;
+  put2(v, mul2(mul2(get2(v), gate_sigmoid2<KIND>(v, &dp)), get2(v + 2)));
+  T* const o = out + (row0 + lane) * ldo;
+  o[j] = from_f32<T>(v[0]);
+  if (j + 1 < n) o[j + 1] = from_f32<T>(v[1]);
 }
 
 // ---------------------------------------------------------------- host
@@ -867,21 +897,36 @@ static void add_copy(GpAlign* l, const void** x, int64_t* ld, int64_t rows, int6
   l->from[l->count] = *x, l->to[l->count] = to, l->ld[l->count] = *ld, l->rows[l->count] = rows, ++l->count;
   *x = to, *ld = gp_ld(cols);
 }
-static void align_rows(const GpAlign& l, int64_t cols, cudaStream_t s) {
+static void align_rows(GpAlign& l, int64_t cols, cudaStream_t s) {
   if (l.count == 0) return;
-  int64_t rows = 0;
-  for (int i = 0; i < l.count; ++i) rows = l.rows[i] > rows ? l.rows[i] : rows;
-  const int64_t chunks = gp_ld(cols) / CHUNK, blocks = ceil_div(rows * chunks, 256);
-  launch_chained(k_align_rows, dim3((unsigned)(blocks < GP_SMS * 16 ? blocks : GP_SMS * 16), 1, (unsigned)l.count), 256, 0, s, l, cols,
-                 (uint32_t)chunks);
+  const int64_t chunks = gp_ld(cols) / CHUNK;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t blocks = i < l.count ? ceil_div(l.rows[i] * chunks, 2 * 256) : 0;
+    l.first[i + 1] = l.first[i] + (unsigned)(blocks < GP_SMS * 16 ? blocks : GP_SMS * 16);
+  }
+  launch_chained(k_align_rows, l.first[3], 256, 0, s, l, cols, (uint32_t)chunks);
 }
 
+// Whether a call without checkpoints takes that way, by its sizes alone: the same bits wherever rows start.
+static bool gp_few(int64_t rows, int64_t n, int64_t k) {
+  const double steps = (double)ceil_div(rows, 2) * (double)(n < 16 ? 16 : n) * ((double)ceil_div(k, 256) + 1.25);
+  return rows == 1 || steps <= 24000.0 + 3.5 * (double)k;
+}
+template <typename T, int KIND, int R>
+static void launch_rows(const void* x, int64_t ldx, int64_t rows, const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int64_t n,
+                        int64_t k, void* out, int64_t ldo, bool span, uint32_t* diag, cudaStream_t s) {
+  const int64_t groups = ceil_div(rows, R);
+  int split = 0;  // warps that share a row's sum, as a power of 2: while no more than two CTAs an SM come of it
+  while (split < 3 && groups * ceil_div(n, 8 >> split) <= GP_SMS * 2 && (256 << split) < k) ++split;
+  launch_chained(span ? &k_gated_proj_row<T, KIND, true, R> : &k_gated_proj_row<T, KIND, false, R>,
+                 (unsigned)(groups * ceil_div(n, 16 >> split)), 256, 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(wg), ldwg,
+                 static_cast<const T*>(wu), ldwu, n, k, static_cast<T*>(out), ldo, (int)rows, split, diag);
+}
 template <typename T, int KIND>
 static void launch_row(const void* x, int64_t ldx, int64_t rows, const void* wg, int64_t ldwg, const void* wu, int64_t ldwu, int64_t n,
                        int64_t k, void* out, int64_t ldo, bool span, uint32_t* diag, cudaStream_t s) {
-  launch_chained(span ? &k_gated_proj_row<T, KIND, true> : &k_gated_proj_row<T, KIND, false>, (unsigned)(rows * ceil_div(n, 16)), 256, 0, s,
-                 static_cast<const T*>(x), ldx, static_cast<const T*>(wg), ldwg, static_cast<const T*>(wu), ldwu, n, k,
-                 static_cast<T*>(out), ldo, (unsigned)rows, diag);
+  const auto launch = rows > 1 ? &launch_rows<T, KIND, 2> : &launch_rows<T, KIND, 1>;
+  launch(x, ldx, rows, wg, ldwg, wu, ldwu, n, k, out, ldo, span, diag, s);
 }
 
 template <typename T, int KIND, bool PAIR, int PARTS>
@@ -981,7 +1026,7 @@ extern "C" gc_status gc_gated_proj(int32_t kind, const void* x, int64_t ldx, con
   unsigned char* const ws = static_cast<unsigned char*>(workspace);
   if (rows == 0) return zero_chained(ws, DIAG_BYTES, s) ? GC_OK : GC_ERR_CUDA;
   const bool silu = kind == GC_GATE_SILU;
-  if (!gate_codes && (rows == 1 || (rows <= GP_FEW && 4.0 * (double)rows * (double)n * (double)k <= GP_FEW_BYTES))) {
+  if (!gate_codes && gp_few(rows, n, k)) {
     const auto launch = dtype == GC_BF16 ? (silu ? &launch_row<__nv_bfloat16, GC_GATE_SILU> : &launch_row<__nv_bfloat16, GC_GATE_GELU_TANH>)
                                          : (silu ? &launch_row<__half, GC_GATE_SILU> : &launch_row<__half, GC_GATE_GELU_TANH>);
     launch(x, ldx, rows, w_gate, ldwg, w_up, ldwu, n, k, out, ldo, copied != 0, reinterpret_cast<uint32_t*>(ws), s);

@@ -101,7 +101,8 @@ SHAPES = [(1, 1, 1), (1, 32, 64), (2, 33, 65), (5, 31, 7), (77, 333, 1001), (128
           (16, 4865, 72), (300, 1000, 264), (1031, 96, 520), (48, 640, 4096), (260, 5000, 136), (3, 70, 520), (4, 4097, 264),
           (30, 1200, 1096), (100, 64, 2000),
           (8, 500, 300), (2, 301, 130), (6, 2000, 1500),
-          (40, 129, 64), (100, 129, 64), (9, 1171, 2000), (40, 2344, 4096), (129, 101, 64), (129, 516, 4096), (129, 2515, 520), (300, 4867, 64)]
+          (40, 129, 64), (100, 129, 64), (9, 1171, 2000), (40, 2344, 4096), (129, 101, 64), (129, 516, 4096), (129, 2515, 520), (300, 4867, 64),
+          (2, 300, 8192), (7, 16, 600), (40, 200, 300), (3, 640, 5120), (333, 16, 64), (5, 1, 1025)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -150,7 +151,7 @@ def test_forward_is_the_same_from_run_to_run_and_layout_to_layout(gc):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("shape", [(1, 77, 261), (3, 129, 300), (8, 64, 515), (8, 1111, 1301), (40, 129, 67), (9, 1171, 2001), (129, 101, 68)])
+@pytest.mark.parametrize("shape", [(1, 77, 261), (1, 30, 4099), (3, 129, 300), (5, 33, 2500), (8, 64, 515), (8, 1111, 1301), (40, 129, 67), (9, 1171, 2001), (129, 101, 68)])
 def test_what_lies_around_the_matrices_does_not_matter(gc, shape, dtype):
     """Rows on 16-byte boundaries and rows anywhere, between zeros and between NaN: the same bits;
     and a column of weights that is not finite spoils that one alone."""
