@@ -682,15 +682,15 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
 // rows of 4096 x 1024 take 5.4 us and four 8.2, there 7.4; 16 of 333 x 1001 6.3 and
 // 40 9.5, there 7.9; 40 of 512 x 64 6.2, there 5.5; there, too, k costs latency.
 // SPAN: rows of weights or of x off 16-byte boundaries.
-template <typename T, int KIND, bool SPAN, int R>
+template <typename T, int KIND, bool SPAN, int R, bool JOIN>
 __global__ void __launch_bounds__(256, R > 1 ? 2 : 3)
     k_gated_proj_row(const T* x, int64_t ldx, const T* wg, int64_t ldwg, const T* wu, int64_t ldwu, int64_t n, int64_t k, T* out,
-                     int64_t ldo, int rows, int split, uint32_t* diag) {
-  __shared__ __align__(16) float sums[8][R][4];
+                     int64_t ldo, int rows, int shared, uint32_t* diag) {
+  __shared__ __align__(16) float sums[JOIN ? 8 : 1][R][4];
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x <= DIAG_PATH) diag[threadIdx.x] = 0u;
   const unsigned groups = (unsigned)(rows + R - 1) / R;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = 1 << split, part = warp & (parts - 1);
+  const int split = JOIN ? shared : 0, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = 1 << split, part = warp & (parts - 1);
   const int row0 = R * (int)(blockIdx.x % groups);
   const int64_t j = 2 * (((int64_t)(blockIdx.x / groups) * 8 + warp) >> split);
   const int64_t j0 = min(j, n - 1), j1 = min(j + 1, n - 1);
@@ -744,14 +744,16 @@ __global__ void __launch_bounds__(256, R > 1 ? 2 : 3)
       for (int d = 16; d > 0; d >>= 1) all = __fadd_rn(all, __shfl_xor_sync(FULL, all, d));
       if (r == 0 || lane == r) v[i] = all;
     }
-  if (parts > 1) {
+  if constexpr (JOIN) {
     if (part != 0 && lane < R) *reinterpret_cast<float4*>(sums[warp][lane]) = make_float4(v[0], v[1], v[2], v[3]);
     __syncthreads();
   }
   if (part != 0 || lane >= R || row0 + lane >= rows || j >= n) return;
-  for (int p = 1; p < parts; ++p)
+  if constexpr (JOIN) {
+    for (int p = 1; p < parts; ++p)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], sums[warp + p][lane][i]);
+      for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], sums[warp + p][lane][i]);
+  }
   F2 dp;
   put2(v, mul2(mul2(get2(v), gate_sigmoid2<KIND>(v, &dp)), get2(v + 2)));
   T* const o = out + (row0 + lane) * ldo;
@@ -918,8 +920,9 @@ static void launch_rows(const void* x, int64_t ldx, int64_t rows, const void* wg
   const int64_t groups = ceil_div(rows, R);
   int split = 0;  // warps that share a row's sum, as a power of 2: while no more than two CTAs an SM come of it
   while (split < 3 && groups * ceil_div(n, 8 >> split) <= GP_SMS * 2 && (256 << split) < k) ++split;
-  launch_chained(span ? &k_gated_proj_row<T, KIND, true, R> : &k_gated_proj_row<T, KIND, false, R>,
-                 (unsigned)(groups * ceil_div(n, 16 >> split)), 256, 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(wg), ldwg,
+  const auto kern = split ? (span ? &k_gated_proj_row<T, KIND, true, R, true> : &k_gated_proj_row<T, KIND, false, R, true>)
+                          : (span ? &k_gated_proj_row<T, KIND, true, R, false> : &k_gated_proj_row<T, KIND, false, R, false>);
+  launch_chained(kern, (unsigned)(groups * ceil_div(n, 16 >> split)), 256, 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(wg), ldwg,
                  static_cast<const T*>(wu), ldwu, n, k, static_cast<T*>(out), ldo, (int)rows, split, diag);
 }
 template <typename T, int KIND>
