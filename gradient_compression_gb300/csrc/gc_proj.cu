@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
 // through the FMA units.  Sums are fp32, a lane's share of a row in two chains,
 // then over the lanes, then over the warps that share the row (up to eight, where n is
 // small: 300 x 8192 takes 5.0 us, by one warp each 18.0).  14336 x 4096 in bf16 takes
-// 35.0 us from memory (6.7 TB/s) and 4096 x 1024 5.2; the tensor cores' kernel, whose copies
+// 34.8 us from memory (6.7 TB/s) and 4096 x 1024 5.3; the tensor cores' kernel, whose copies
 // take longer to get going, 37.5 and 7.4.
 // Of more rows a warp has R = 2 at a time (one: 9.7 us for 8 x 1000 x 777, two 6.7, four, whose
 // registers leave half the loads in flight, 7.0) and what they cost is instructions: some
