@@ -249,6 +249,13 @@ __device__ __forceinline__ void gp_put_sums(const float (&v)[32], float* to, int
     if (8 * i < n) gp_put32(to + 8 * i, w, true);  // rows have room for whole eights
   }
 }
+// How far a CTA's copies have come: the stage that is next (past the last one: an
+// item that is not there, stage 0), its place in the ring, how many before it may not
+// have been multiplied yet.
+struct alignas(8) GpFed {
+  int i, s, slot, used;
+  uint32_t turn;
+};
 // The columns of a tile that are there; its groups of 32 of them.
 __device__ __forceinline__ int gp_width(const GpArgs& a, int n) { return (int)min((int64_t)a.bn, a.cols - (int64_t)n * a.bn); }
 __device__ __forceinline__ int gp_groups(const GpArgs& a, int n) { return (gp_width(a, n) + 31) / 32; }
@@ -290,27 +297,112 @@ __device__ __forceinline__ void gp_finish(const GpArgs& a, int64_t row0, int64_t
   gp_put(g, static_cast<T*>(a.out) + row0 * a.ldo + col, a.ldo, there, n, a.vec, stage);
 }
 
+// The barriers of a CTA, one after another: of a stage's copies (the first CTA's of a
+// pair: both CTAs' are there) and of its MMAs, of an accumulator's MMAs and (the first
+// CTA's) of its having been read out, of all MMAs after a wait that ran out, of the other
+// splits' sums.
+constexpr uint32_t GP_EMPTY = 8u * GP_SLOTS, GP_ACC_FULL = 16u * GP_SLOTS, GP_ACC_EMPTY = GP_ACC_FULL + 16u,
+                   GP_DRAINED = GP_ACC_EMPTY + 16u, GP_JOINED = GP_DRAINED + 8u;
+// The copies of a stage into its place in the ring, by a whole warp.
+template <bool BACK, bool PAIR, int PARTS>
+__device__ __forceinline__ void gp_feed(const GpMaps& maps, const GpArgs& a, const GpItem& t, int s, int slot, uint32_t base,
+                                        uint32_t bar0, int rank, int leader) {
+  const int row = t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M, cols = PAIR ? a.bn / 2 : a.bn;
+  const uint32_t full = bar0 + 8u * slot, bar = PAIR ? of_cta(full, leader) : full;
+  const int parts = PARTS > 1 && (s + 1 == a.half || s + 1 == a.steps) ? a.last : PARTS;
+  uint32_t st = base + (uint32_t)(slot * PARTS * a.part);
+  if (elected()) {
+    if (rank == 0) mbar_expect(full, (uint32_t)((PAIR ? 2 : 1) * parts * a.bytes));
+    const bool second = BACK && s >= a.half;
+    int x = (second ? s - a.half : s) * (PARTS * GP_K);
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h, x += GP_K, st += (uint32_t)a.part) {
+      if (h >= parts) break;
+      if (BACK) {
+        tma_load_2d<PAIR>(st, second ? &maps.a1 : &maps.a0, x, row, bar);
+        for (int b = 0; b < cols; b += 64)
+          tma_load_2d<PAIR>(st + a.room + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + rank * cols + b, x, bar);
+      } else {
+        tma_load_2d<PAIR>(st, &maps.a0, x, row, bar);
+        if (PAIR) {  // the first CTA has Wg's rows, the second Wu's
+          tma_load_2d<PAIR>(st + a.room, rank ? &maps.b1 : &maps.b0, x, t.n * a.bn, bar);
+        } else {
+          tma_load_2d<PAIR>(st + a.room, &maps.b0, x, t.n * a.bn, bar);
+          tma_load_2d<PAIR>(st + a.room + a.bn * (GP_K * 2), &maps.b1, x, t.n * a.bn, bar);
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+// Says that a wait ran out to all CTAs of the cluster, before it ends its role (and so
+// before the cluster's next barrier).  Out of line, as the next one, so that the common
+// path stays as short as it is.
+__device__ __noinline__ void gp_tell(const uint32_t* lost, int ctas) {
+  if ((threadIdx.x & 31) == 0)
+    for (int c = 0; c < ctas; ++c) asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(of_cta(smem_u32(lost), c)) : "memory");
+}
+// The end of a CTA of whose cluster a wait ran out: until what is on its way to its
+// shared memory is there.
+template <bool BACK, bool PAIR, int PARTS>
+__device__ __noinline__ void gp_drain(const GpMaps& maps, const GpArgs& a, const GpFed& fed, uint32_t base, uint32_t bar0) {
+  const int warp = __shfl_sync(FULL, (int)(threadIdx.x >> 5), 0);
+  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0, leader = PAIR ? cluster_rank() & ~1 : 0;
+  // MMAs in flight read the CTAs' memory, and say so on their barriers when they are
+  // done: by a barrier that nothing else completes.
+  if (warp == 1) {
+    if (rank == 0 && elected()) gp_commit<PAIR>(bar0 + GP_DRAINED, leader);
+    __syncwarp();
+    gp_wait_warp(bar0 + GP_DRAINED, 0u);
+  }
+  // Copies land on the first CTA's barriers, which are complete when both CTAs' have.  The
+  // one that gave up first issues what the other one has beyond it (whose room is free: the
+  // other one has waited for that), and every stage in flight is one that ends.
+  if (warp == 0) {
+    GpFed f = fed;
+    if (PAIR) {
+      const int stride = (int)(gridDim.x >> 1);
+      const uint32_t there = of_cta(smem_u32(&fed), leader + (rank ^ 1));
+      int i, s;
+      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(i), "=r"(s) : "r"(there) : "memory");
+      while (f.i < i || (f.i == i && f.s < s)) {
+        const GpItem t = gp_item(a, f.i);
+        gp_feed<BACK, PAIR, PARTS>(maps, a, t, f.s, f.slot, base, bar0, rank, leader);
+        if (++f.slot == a.slots) f.slot = 0, ++f.turn;
+        f.used = min(f.used + 1, a.slots);
+        if (++f.s == t.s1) f.i += stride, f.s = f.i < a.items ? gp_item(a, f.i).s0 : 0;
+      }
+    }
+    for (int j = 0; rank == 0 && j < f.used; ++j) {
+      if (--f.slot < 0) f.slot = a.slots - 1, --f.turn;
+      gp_wait_warp(bar0 + 8u * f.slot, f.turn & 1u);
+    }
+  }
+}
+
 // KIND: the activation; GP_BACK: the gradient.  PAIR: a cluster of two CTAs
 // computes a tile of 256 rows, half of them each; the first one's thread issues
 // the MMAs of both, which read each CTA's rows and half of the columns' operand out
 // of its own memory.  PARTS: of GP_K in a stage.
+// A role whose wait runs out says so to the whole cluster, whose CTAs then end
+// together: none joins its sums, and each awaits what is on its way to it, below.
 template <typename T, int KIND, bool PAIR, int PARTS>
 __global__ void __launch_bounds__(GP_THREADS, 1)
     k_gated_proj(const __grid_constant__ GpMaps maps, const __grid_constant__ GpArgs a) {
   constexpr bool BACK = KIND == GP_BACK;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[2 * GP_SLOTS + 6];
-  __shared__ uint32_t tmem_base;
+  __shared__ uint32_t tmem_base, lost;
+  __shared__ GpFed fed;
   const int warp = __shfl_sync(FULL, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (a uniform register)
   const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0, leader = PAIR ? cluster_rank() & ~1 : 0;
   const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
-  auto full = [&](int s) { return bar0 + 8u * s; };                            // of the first CTA: both CTAs' copies are there
-  auto empty = [&](int s) { return bar0 + 8u * (GP_SLOTS + s); };
-  auto acc_full = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + h); };       // an accumulator's MMAs are done
-  auto acc_empty = [&](int h) { return bar0 + 8u * (2 * GP_SLOTS + 2 + h); };  // of the first CTA: it has been read out
-  const uint32_t drained = bar0 + 8u * (2 * GP_SLOTS + 4);                     // all MMAs are done, after a wait that ran out
-  const uint32_t joined = drained + 8u;                                        // the other splits' sums are here
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + GP_EMPTY + 8u * s; };
+  auto acc_full = [&](int h) { return bar0 + GP_ACC_FULL + 8u * h; };
+  auto acc_empty = [&](int h) { return bar0 + GP_ACC_EMPTY + 8u * h; };
+  const uint32_t drained = bar0 + GP_DRAINED, joined = bar0 + GP_JOINED;
 
   if (warp == 2 && elected()) {
     for (const CUtensorMap* m : {&maps.a0, &maps.a1, &maps.b0, &maps.b1}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -319,6 +411,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     for (int s = 0; s < GP_SLOTS; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
     for (int h = 0; h < 2; ++h) mbar_init(acc_full(h), 1), mbar_init(acc_empty(h), PAIR ? 2 * GP_OUT : GP_OUT);
     mbar_init(drained, 1), mbar_init(joined, 1);
+    lost = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -333,6 +426,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   const bool joint = a.splits > 1 && !a.sums;  // a cluster's splits
+  const int ctas = (PAIR ? 2 : 1) * (joint ? a.splits : 1);
   if (PAIR || joint) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = __shfl_sync(FULL, tmem_base, 0);
@@ -342,54 +436,28 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------ operands
-    int slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
+    int i = first, at = 0, slot = 0, used = 0;  // used: the stages whose copies were issued, up to a ring's
     uint32_t turn = 0u;
-    for (int i = first; ok && i < a.items; i += stride) {
+    for (; i < a.items; i += stride) {
       const GpItem t = gp_item(a, i);
-      const int row = t.m * (PAIR ? 2 * GP_M : GP_M) + rank * GP_M, cols = PAIR ? a.bn / 2 : a.bn;
       for (int s = t.s0; s < t.s1; ++s) {
-        if (!(ok = gp_wait_warp(empty(slot), (turn & 1u) ^ 1u))) break;
-        const uint32_t bar = PAIR ? of_cta(full(slot), leader) : full(slot);
-        const int parts = PARTS > 1 && (s + 1 == a.half || s + 1 == a.steps) ? a.last : PARTS;
-        uint32_t st = base + (uint32_t)(slot * PARTS * a.part);
-        if (elected()) {
-          if (rank == 0) mbar_expect(full(slot), (uint32_t)((PAIR ? 2 : 1) * parts * a.bytes));
-          const bool second = BACK && s >= a.half;
-          int x = (second ? s - a.half : s) * (PARTS * GP_K);
-#pragma unroll
-          for (int h = 0; h < PARTS; ++h, x += GP_K, st += (uint32_t)a.part) {
-            if (h >= parts) break;
-            if (BACK) {
-              tma_load_2d<PAIR>(st, second ? &maps.a1 : &maps.a0, x, row, bar);
-              for (int b = 0; b < cols; b += 64)
-                tma_load_2d<PAIR>(st + a.room + b * (GP_K * 2), second ? &maps.b1 : &maps.b0, t.n * a.bn + rank * cols + b, x, bar);
-            } else {
-              tma_load_2d<PAIR>(st, &maps.a0, x, row, bar);
-              if (PAIR) {  // the first CTA has Wg's rows, the second Wu's
-                tma_load_2d<PAIR>(st + a.room, rank ? &maps.b1 : &maps.b0, x, t.n * a.bn, bar);
-              } else {
-                tma_load_2d<PAIR>(st + a.room, &maps.b0, x, t.n * a.bn, bar);
-                tma_load_2d<PAIR>(st + a.room + a.bn * (GP_K * 2), &maps.b1, x, t.n * a.bn, bar);
-              }
-            }
-          }
+        if (!(ok = gp_wait_warp(empty(slot), (turn & 1u) ^ 1u))) {
+          at = s;
+          break;
         }
-        __syncwarp();
+        gp_feed<BACK, PAIR, PARTS>(maps, a, t, s, slot, base, bar0, rank, leader);
         if (++slot == a.slots) slot = 0, ++turn;
         used = min(used + 1, a.slots);
       }
+      if (!ok) break;
     }
-    // Before this CTA may end: the last stages have been multiplied, and said so
-    // on its barriers; or, after a wait that ran out, its copies in flight have landed.
-    for (int j = 0; j < used; ++j) {
+    if (lane == 0) fed = {i, at, slot, used, turn};
+    // before this CTA may end: the last stages have been multiplied, and said so on its barriers
+    for (int j = 0; ok && j < used; ++j) {
       if (--slot < 0) slot = a.slots - 1, --turn;
-      if (ok)
-        ok = gp_wait_warp(empty(slot), turn & 1u);
-      else if (rank == 0)
-        gp_wait_warp(full(slot), turn & 1u);
-      else
-        __nanosleep(100000);  // they arrive on the other CTA's barrier
+      ok = gp_wait_warp(empty(slot), turn & 1u);
     }
+    if (!ok) gp_tell(&lost, ctas);
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
     if (rank == 0) {
@@ -426,11 +494,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           if (++slot == a.slots) slot = 0, ++turn;
         }
       }
-      if (!ok) {
-        // MMAs in flight read the CTAs' memory: see them end
-        if (elected()) gp_commit<PAIR>(drained, leader);
-        gp_wait_warp(drained, 0);
-      }
+      if (!ok) gp_tell(&lost, ctas);
     }
   } else if (warp >= GP_FIRST) {
     // ------------------------------------------------ result
@@ -439,7 +503,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     for (int i = first; ok && i < a.items; i += stride, ++count) {
       const GpItem t = gp_item(a, i);
       const uint32_t acc = count & 1u;
-      if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) break;
+      if (!(ok = gp_wait_warp(acc_full(acc), (count >> 1) & 1u))) {
+        gp_tell(&lost, ctas);
+        break;
+      }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t from = tmem + 256u * acc + ((uint32_t)(32 * quad) << 16);
       if (joint) break;  // the tile's only one: below
@@ -498,12 +565,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       mbar_expect(joined, (uint32_t)((groups - t.split + a.splits - 1) / a.splits * (a.splits - 1) * BLOCKS * quads) * 4096u);
     __syncwarp();
     cluster_sync();
-    const bool mine = warp >= GP_FIRST && quad < quads;
+    const bool mine = warp >= GP_FIRST && quad < quads && lost == 0u;  // (all CTAs see the same here: all send, or none)
     const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
     // where split `of` puts its sums of the owner's group q
     auto block = [&](int q, int owner, int of) { return (uint32_t)((q / a.splits) * (a.splits - 1) + of - (of > owner)) * (BLOCKS * BLOCK); };
     if (mine) {
-      for (int q = side; ok && q < groups; q += 2) {
+      for (int q = side; q < groups; q += 2) {
         const int owner = q % a.splits, cta = PAIR ? 2 * owner + rank : owner;
         if (owner == t.split) continue;
         const int sent = q - (q + a.splits - 1 - t.split) / a.splits;  // of the groups of others
@@ -526,7 +593,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           __syncwarp();
         }
       }
-      ok = gp_wait_warp(joined, 0u) && ok;  // in any case: what is on its way here lands before this CTA ends
+      ok = gp_wait_warp(joined, 0u);  // what is on its way here lands before this CTA ends
     }
     if (mine && ok) {
       const uint32_t at = base + row128;
@@ -568,6 +635,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (PAIR || joint) cluster_sync();  // none ends, or gives its tensor memory back, while another may reach it
+  if (lost != 0u) {
+    gp_drain<BACK, PAIR, PARTS>(maps, a, fed, base, bar0);
+    __syncthreads();
+    if (PAIR || joint) cluster_sync();
+  }
   if (warp == 1) {
     if (PAIR)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
