@@ -12,10 +12,14 @@
 namespace gc {
 
 // Mathematics and precision.  The operands are of 16 bits, so every product is
-// exact in the tensor cores' fp32; their sums truncate, a relative error of
-// about 1e-9 per term of the sum's length, far below the outputs' own rounding (2^-9 or
-// 2^-12).  G and U stay in fp32 from tensor memory to the activation, and the
-// checkpoints are taken of that.
+// exact in the tensor cores' fp32; their sums truncate.  A step of 16 products cuts each
+// of them two bits below the last one of the sum, or of a larger product (measured: 16
+// of 2^-2 of it are added, of 2^-3 not), and then the sum: less than 16 / 4 + 1 last bits,
+// 5 2^-23 of the sum that is reached, and half of that on average.  Of terms of one
+// sign, where nothing cancels, 6e-9 of the result per term of a chain was measured: 1.7e-4
+// for the 28672 of a gradient, a third of the output's own half step in fp16 (2^-11) and
+// a 23rd in bf16 (2^-8), so that chains are not cut.  G and U stay in fp32 from
+// tensor memory to the activation, and the checkpoints are taken of that.
 //
 // Tile.  128 rows of x by `bn` columns of out, one MMA of N = 2 bn for both
 // projections: the rows of Wg and of Wu lie one after another in shared memory, so
