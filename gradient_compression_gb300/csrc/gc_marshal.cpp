@@ -318,7 +318,7 @@ PyObject* rmsnorm_backward(Args a) {  // dy, ckpt, rstd, weight, dx, dw, workspa
 int kind_of(PyObject* o) {
   const long k = PyLong_AsLong(o);
   if (k == -1 && PyErr_Occurred()) throw Bad{};
-  return (int)k;
+  return k == (long)(int)k ? (int)k : -1;  // what is no int is no kind, not its lower half's
 }
 
 PyObject* gated_act(Args a) {  // kind, gate, up, out, ckpt_gate, ckpt_up, stream
