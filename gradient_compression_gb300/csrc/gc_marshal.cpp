@@ -424,7 +424,12 @@ gc_tensor dense(Gpu& on, const at::Tensor& t, const char* name) {
   return g;
 }
 bool same_order(const at::Tensor& a, const at::Tensor& b) {
-  return a.numel() == b.numel() && ((a.is_contiguous() && b.is_contiguous()) || (a.sizes() == b.sizes() && a.strides() == b.strides()));
+  if (a.numel() != b.numel()) return false;
+  if (a.numel() == 0 || (a.is_contiguous() && b.is_contiguous())) return true;
+  if (a.sizes() != b.sizes()) return false;
+  for (int64_t d = 0; d < a.dim(); ++d)  // (the stride of a dimension of one element means nothing)
+    if (a.size(d) > 1 && a.stride(d) != b.stride(d)) return false;
+  return true;
 }
 
 PyObject* grad_norm(Args a) {  // tensors, norm, workspace, stream
