@@ -77,7 +77,9 @@ int type_code(const at::Tensor& t, const char* name) {
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) bad("%s: a tensor is needed", name);
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.is_neg()) bad("%s: a view with the sign turned, which its memory does not have", name);
+  return t;
 }
 
 // The GPU of a call's tensors, the first one's: the others have to be there too.
