@@ -104,7 +104,9 @@ __device__ __noinline__ double gn_squares64(const void* p, int64_t n, uint32_t t
 // four chains of at most eight; where the result says that a square left fp32's
 // range, or that all are so small that what was lost may matter, again in 64
 // bits: elements below 2^-63, whose squares are rounded to multiples of 2^-149,
-// do not matter beside a sum of 2^-80.
+// do not matter beside a sum of 2^-80.  Tensors of such small elements (about 1e-12 and
+// less) are read at 0.35 TB/s in bf16 and 0.69 in fp32 instead of 7: a few instructions
+// in 64 bits for each element.
 template <typename T>
 __device__ __forceinline__ double gn_squares(const void* p, int64_t n, uint32_t tile) {
   using G = Granules<T>;
@@ -132,8 +134,9 @@ __device__ __forceinline__ double gn_squares(const void* p, int64_t n, uint32_t 
   return (double)all;
 }
 
-// The sum of squares of each CTA's tiles, in 64 bits, in an order that the sizes
-// alone set.
+// The sum of squares of each CTA's tiles, in 64 bits, in an order set by the sizes,
+// the types and where in a granule each tensor starts (which elements are summed in
+// fp32 together).
 template <int CAP>
 __global__ void __launch_bounds__(256, 6) k_grad_norm(const __grid_constant__ GnTable<CAP> t, double* part) {
   __shared__ double warps[8];

@@ -740,7 +740,8 @@ gc_status gc_grad_norm_workspace_size(int32_t count, size_t* bytes);
  * or the norm passes fp32's range.  `tensors` is a host array, done with when the
  * call returns.  Squares are summed in fp32 over at most 32 elements and in 64 bits
  * beyond (in 64 bits throughout where fp32 would overflow or lose small ones), in
- * an order set by the sizes: the same bits from run to run.  Any number of tensors
+ * an order set by the tensors' sizes, types and places in a 16-byte granule: the same bits
+ * from run to run and wherever tensors of the same offsets lie.  Any number of tensors
  * (GC_ERR_LAYOUT: over 2^42 elements in all); reads may take in the whole of a
  * 16-byte granule that holds an element.  Workspace 256-byte aligned. */
 gc_status gc_grad_norm(const gc_tensor* tensors, int32_t count, float* norm, void* workspace,
