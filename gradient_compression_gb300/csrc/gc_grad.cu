@@ -20,7 +20,9 @@ namespace gc {
 // eight, whose registers do not suffice, 2.40).  Clipping: as many CTAs as there are
 // tiles, up to 256 an SM, three at a time: 3.35e8 elements from bf16 to fp32 287 us,
 // 7.0 TB/s, where 6 and 16 an SM take 349 and 316 (a CTA that has done its range
-// makes room at once, and the ranges written at a time lie closer together).
+// makes room at once, and the ranges written at a time lie closer together).  In
+// place 3.35e8 elements in bf16 take 189 us (7.1 TB/s), and 41 where nothing is to be
+// clipped: so many CTAs' starts.
 constexpr int GN_TILE = 1024, GN_CAP = 1024, GN_CTAS = 152 * 6, GC_CTAS = 152 * 256;
 template <int CAP>
 struct GnTable {
@@ -192,7 +194,8 @@ __global__ void __launch_bounds__(256) k_grad_norm_join(const double* part, int 
 // c times a tile.  Where the output's elements lie as the granules do (all of an
 // arena's, when the sizes before them are multiples of eight), a granule is
 // written as 8, 16 or 32 bytes; else, and at a tensor's ends, element by element,
-// neighbours by neighbouring lanes.
+// neighbours by neighbouring lanes (3.35e8 elements one element off: bf16 to bf16 297 us
+// instead of 191, bf16 to fp32 360 instead of 286, fp32 to fp32 435 instead of 382).
 template <typename T, typename U>
 __device__ __forceinline__ void gc_scale(const void* p, void* out, int64_t n, uint32_t tile, float c) {
   using G = Granules<T>;

@@ -20,6 +20,11 @@ namespace gc {
 // for the 28672 of a gradient, a third of the output's own half step in fp16 (2^-11) and
 // a 23rd in bf16 (2^-8), so that chains are not cut.  G and U stay in fp32 from
 // tensor memory to the activation, and the checkpoints are taken of that.
+// The gradient's product has dgate and dup as they are rounded to 16 bits: operands in fp32
+// would be two or three terms, and as many times the MMAs.  That is what the weight
+// gradient reads, too, and what a product after gc_gated_act_backward would have; dx's error
+// against 64 bits is 1.4 times that of a sum of the fp32 values (2.4e-3 of it in bf16
+// where that is 1.7e-3, 2.9e-4 in fp16 where that is 2.1e-4).
 //
 // Tile.  128 rows of x by `bn` columns of out, one MMA of N = 2 bn for both
 // projections: the rows of Wg and of Wu lie one after another in shared memory, so
@@ -751,6 +756,12 @@ __global__ void __launch_bounds__(256) k_align_rows(const __grid_constant__ GpAl
 // small: 300 x 8192 takes 5.0 us, by one warp each 18.0).  14336 x 4096 in bf16 takes
 // 34.8 us from memory (6.7 TB/s) and 4096 x 1024 5.3; the tensor cores' kernel, whose copies
 // take longer to get going, 37.5 and 7.4.
+// One row always goes this way.  From memory, where a token's weights come from, it is
+// faster or within 3% at 37 of 41 sizes measured, and 6 to 23% slower at four whose last wave
+// of CTAs (16 columns each, 456 at a time) is mostly empty: 7448 x 4352 29.2 us, by the
+// tensor cores 23.9; 9728 x 7992 54.6 and 50.5.  Weights of 60 to 100 MB that L2 still
+// holds from the call before are read faster by the tensor cores' copies (11128 x 1664
+// 15.6 us and 11.8, 14200 x 1696 19.1 and 14.8), smaller ones slower.
 // Of more rows a warp has R = 2 at a time (one: 9.7 us for 8 x 1000 x 777, two 6.7, four, whose
 // registers leave half the loads in flight, 7.0) and what they cost is instructions: some
 // 1.25 steps of 256 k to begin and end a pair of rows by two columns, and one for each.  Two

@@ -85,7 +85,8 @@ GpPlan gp_plan(int64_t rows, int64_t cols, int64_t summed, bool back, bool fine,
   }
   return best;
 }
-// Whether a call without checkpoints goes by the FMA units, by its sizes alone: the same bits wherever rows start.
+// Whether a call without checkpoints goes by the FMA units, by its sizes alone: the same bits wherever
+// rows start.  (k_gated_proj_row says what both ways were measured to take, one row's included.)
 inline bool gp_few(int64_t rows, int64_t n, int64_t k) {
   const double steps = (double)ceil_div(rows, 2) * (double)(n < 16 ? 16 : n) * ((double)ceil_div(k, 256) + 1.25);
   return rows == 1 || steps <= 24000.0 + 3.5 * (double)k;
