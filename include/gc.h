@@ -657,7 +657,8 @@ gc_status gc_gated_act_backward(int32_t kind, const void* dout, int64_t lddo, in
  * one, and cuts the sum, so that it loses less than 5 2^-23 of the sum that is reached.
  * That is less than 3.7e-8 k S in all (S: the terms' absolute sum); where all terms have
  * one sign, so that nothing cancels, 6e-9 k S was measured, half a step of fp16 at 8e4
- * terms and of bf16 at 6e5.  Few rows of small weights are summed by units that round.
+ * terms and of bf16 at 6e5.  One row, and a few rows of small weights, are summed by units
+ * that round, unless checkpoints are asked for.
  * Products read by bulk copies need x, w_gate and w_up to start on 16-byte
  * boundaries, with row strides that are multiples of 16 bytes; those of them
  * that do not are copied into the workspace first.  n and k < 2^31, k >= 1.
